@@ -343,6 +343,50 @@ pbs_status pbs_gemm_amax(pbs_recipe recipe, pbs_layout layout, int64_t M, int64_
                          pbs_format c_fmt, float* c_amax, hipStream_t stream);
 
 /* ---------------------------------------------------------------------
+ * pbs_layernorm: y = (x - mu) r gamma + beta of every row of x [rows, cols],
+ * mu = mean(x), r = 1 / sqrt(mean((x - mu)^2) + eps): the norm whose output
+ * is a linear layer's input.  With amax_out it also returns max |y|, which
+ * pbs_scale_from_amax turns into the scale of the current-scaling and NVFP4
+ * recipes ([LP] "Interpreting results for a real model" counts the extra
+ * memory pass for that maximum among the quantization overheads).
+ *  x, y: bf16 or fp32 (x_fmt, y_fmt), last axis contiguous, rows ldx / ldy
+ *    elements apart (>= cols; any alignment of an element).  y may be x
+ *    itself (same format and stride); otherwise they do not overlap.
+ *  gamma, beta [cols]: bf16 or fp32 (w_fmt); NULL is 1 / 0.
+ *  mean, rstd [rows]: fp32, mu and r as the gradient takes them; may be NULL.
+ *  amax_out: 1 float, max |y| of the values as stored, overwritten; NULL:
+ *    not wanted.
+ *  The mean is subtracted before squaring; statistics and sums are fp32.
+ *  rows == 0 writes only amax_out (0).  cols from 1 to 2^24.
+ * ------------------------------------------------------------------- */
+pbs_status pbs_layernorm(const void* x, pbs_format x_fmt, int64_t rows, int64_t cols, int64_t ldx,
+                         const void* gamma, const void* beta, pbs_format w_fmt, float eps, void* y,
+                         pbs_format y_fmt, int64_t ldy, float* mean, float* rstd, float* amax_out,
+                         hipStream_t stream);
+
+/* ---------------------------------------------------------------------
+ * pbs_layernorm_grad: with n = (x - mu) r, u = dy gamma and means over a
+ * row's columns,
+ *   dx = r (u - mean(u) - n mean(u n)),
+ *   dgamma = sum_rows dy n,  dbeta = sum_rows dy.
+ *  dy has y's format, dx has x's; row strides as for pbs_layernorm.
+ *  mean, rstd: what pbs_layernorm returned.
+ *  dx, dgamma, dbeta: any of them may be NULL (not computed).  dgamma and
+ *    dbeta are fp32 [cols]; their sums over the rows are split and joined in
+ *    an order that depends on rows and cols alone, so identical inputs give
+ *    identical bytes.  dx may be x or dy itself (same format and stride).
+ *  workspace: pbs_layernorm_grad_bytes(rows, cols) bytes, 16-byte aligned,
+ *    for dgamma / dbeta (unused, may be NULL, if both are); its contents are
+ *    of no use afterwards.  Calls that may run at the same time need one each.
+ *  rows == 0 writes zeros to dgamma and dbeta.
+ * ------------------------------------------------------------------- */
+pbs_status pbs_layernorm_grad_bytes(int64_t rows, int64_t cols, size_t* bytes /* [host] */);
+pbs_status pbs_layernorm_grad(const void* dy, pbs_format y_fmt, int64_t lddy, const void* x, pbs_format x_fmt,
+                              int64_t ldx, int64_t rows, int64_t cols, const void* gamma, pbs_format w_fmt,
+                              const float* mean, const float* rstd, void* dx, int64_t lddx, float* dgamma,
+                              float* dbeta, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------
  * pbs_quantized_bytes [host]: bytes of the codes and of the block scales
  * of one quantized copy of a [rows, cols] tensor (not counting per-tensor
  * fp32 scalars).  For NVFP4 with 1x16 blocks this is n/2 + n/16 bytes,

@@ -25,6 +25,7 @@ __all__ = [
     "pbs_amax", "pbs_scale_from_amax", "pbs_delayed_state_bytes", "pbs_delayed_init",
     "pbs_delayed_update", "pbs_delayed_scale", "pbs_delayed_scale_inv", "pbs_cast",
     "pbs_rht_cast", "pbs_gemm", "pbs_gemm_amax", "pbs_quantized_bytes", "pbs_debug_sr_encode",
+    "pbs_layernorm", "pbs_layernorm_grad_bytes", "pbs_layernorm_grad",
     "pbs_last_error", "pbs_version",
 ]
 
@@ -59,6 +60,11 @@ SIGNATURES = {
                         _vp, _vp, _i32, _vp]),
     "pbs_gemm_amax": (_i32, [_i32, _i32, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _vp, _i32, _vp,
                              _vp, _vp, _i32, _vp, _vp]),
+    "pbs_layernorm": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _i32, _f32, _vp, _i32, _i64, _vp, _vp, _vp,
+                             _vp]),
+    "pbs_layernorm_grad_bytes": (_i32, [_i64, _i64, _c.POINTER(_c.c_size_t)]),
+    "pbs_layernorm_grad": (_i32, [_vp, _i32, _i64, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _vp, _i64,
+                                  _vp, _vp, _vp, _c.c_size_t, _vp]),
     "pbs_quantized_bytes": (_i32, [_i32, _i64, _i64, _i32, _c.POINTER(_c.c_size_t),
                                    _c.POINTER(_c.c_size_t)]),
     "pbs_last_error": (_c.c_char_p, []),
@@ -177,6 +183,25 @@ def pbs_gemm_amax(recipe, layout, M, N, K, A, a_fmt, a_scale, a_tensor_scale, B,
     _check(lib().pbs_gemm_amax(recipe, layout, M, N, K, _ptr(A), a_fmt, _ptr(a_scale), _ptr(a_tensor_scale),
                                _ptr(B), b_fmt, _ptr(b_scale), _ptr(b_tensor_scale), _ptr(C), c_fmt,
                                _ptr(c_amax), _stream(stream)))
+
+
+def pbs_layernorm(x, x_fmt, rows, cols, ldx, gamma, beta, w_fmt, eps, y, y_fmt, ldy, mean, rstd, amax_out,
+                  stream=None):
+    _check(lib().pbs_layernorm(_ptr(x), x_fmt, rows, cols, ldx, _ptr(gamma), _ptr(beta), w_fmt, eps, _ptr(y), y_fmt,
+                               ldy, _ptr(mean), _ptr(rstd), _ptr(amax_out), _stream(stream)))
+
+
+def pbs_layernorm_grad_bytes(rows, cols):
+    n = _c.c_size_t(0)
+    _check(lib().pbs_layernorm_grad_bytes(rows, cols, _c.byref(n)))
+    return n.value
+
+
+def pbs_layernorm_grad(dy, y_fmt, lddy, x, x_fmt, ldx, rows, cols, gamma, w_fmt, mean, rstd, dx, lddx, dgamma, dbeta,
+                       workspace, workspace_bytes, stream=None):
+    _check(lib().pbs_layernorm_grad(_ptr(dy), y_fmt, lddy, _ptr(x), x_fmt, ldx, rows, cols, _ptr(gamma), w_fmt,
+                                    _ptr(mean), _ptr(rstd), _ptr(dx), lddx, _ptr(dgamma), _ptr(dbeta),
+                                    _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def pbs_quantized_bytes(recipe, rows, cols, weight_2d):

@@ -21,6 +21,7 @@ to dY.
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 
 import torch
@@ -34,7 +35,8 @@ from . import (PBS_COL, PBS_DGRAD, PBS_FLAG_RHT16, PBS_FLAG_SR, PBS_FMT_BF16, PB
                PBS_RECIPE_MXFP4, PBS_RECIPE_MXFP8, PBS_RECIPE_NVFP4, PBS_ROW, PBS_WGRAD, pbs_amax,
                pbs_cast,
                pbs_delayed_init, pbs_delayed_scale, pbs_delayed_scale_inv, pbs_delayed_state_bytes,
-               pbs_delayed_update, pbs_gemm, pbs_gemm_amax, pbs_scale_from_amax)
+               pbs_delayed_update, pbs_gemm, pbs_gemm_amax, pbs_layernorm, pbs_layernorm_grad,
+               pbs_layernorm_grad_bytes, pbs_scale_from_amax)
 
 RECIPES = {
     "bf16": PBS_RECIPE_BF16,
@@ -331,3 +333,112 @@ def quantize_pass(recipe, pass_, x, w, dy, states=None, outs=None, stream=None):
     A = quantize(recipe, src[sa], sa, oa, pass_, states.get(sa), outs.get("A"), stream=stream)
     B = quantize(recipe, src[sb], sb, ob, pass_, states.get(sb), outs.get("B"), stream=stream)
     return A, B
+
+
+# ---------------------------------------------------------------------------
+# the ends of a step: the norm ahead of a linear layer
+# ---------------------------------------------------------------------------
+FMT_OF = {torch.bfloat16: PBS_FMT_BF16, torch.float32: PBS_FMT_F32}
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _matrix(name, t, shape=None):
+    """Checks a [rows, cols] operand of bf16 or fp32 whose rows are contiguous; returns (format, row stride)."""
+    _need(t.dim() == 2 and (shape is None or t.shape == shape),
+          f"{name}: want shape {tuple(shape) if shape else '[rows, cols]'}, got {tuple(t.shape)}")
+    _need(t.dtype in FMT_OF, f"{name}: want bf16 or fp32, got {t.dtype}")
+    rows, cols = t.shape
+    _need(cols <= 1 or t.stride(1) == 1, f"{name}: the last axis must be contiguous")
+    ld = t.stride(0) if rows > 1 else max(cols, 1)
+    _need(ld >= cols, f"{name}: rows overlap (row stride {ld}, {cols} columns)")
+    return FMT_OF[t.dtype], ld
+
+
+def _vector(name, t, n, dtypes, device):
+    """Checks an optional contiguous vector of n values; returns it."""
+    if t is not None:
+        _need(t.shape == (n,) and t.is_contiguous(), f"{name}: want {n} contiguous values, got shape {tuple(t.shape)}")
+        _need(t.dtype in dtypes, f"{name}: got {t.dtype}, want {' or '.join(str(d) for d in dtypes)}")
+        _need(t.device == device, f"{name}: on {t.device}, want {device}")
+    return t
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(t, stream):
+    """The context that runs a call on t's device and on `stream` (None: that
+    device's current stream), so that what the call allocates belongs there."""
+    _need(t.is_cuda, "tensors must be on the GPU")
+    if stream is None:
+        return _HERE if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=t.device)
+    _need(stream.device == t.device, f"stream of {stream.device} for tensors on {t.device}")
+    return torch.cuda.stream(stream)
+
+
+def layernorm(x, gamma=None, beta=None, eps=1e-5, out_dtype=None, y=None, amax=None, stream=None):
+    """Layer norm of the rows of ``x`` [R, C] (bf16 or fp32).  Returns (y,
+    mean [R], rstd [R]), the statistics in fp32 for ``layernorm_grad``.
+
+    ``gamma`` / ``beta`` [C]: both bf16 or both fp32 (None: 1 / 0).  ``y`` may
+    be given ([R, C], bf16 or fp32; ``x`` itself for in place), else it is
+    allocated in ``out_dtype`` (None: x's).  ``amax`` (a device fp32 of one
+    element) receives max |y| as stored: ``quantize(..., known_amax=amax)``
+    then needs no pass of its own.
+    """
+    x_fmt, ldx = _matrix("x", x)
+    R, C = x.shape
+    _need(C >= 1, "x: no columns")
+    both = tuple(FMT_OF)
+    _vector("gamma", gamma, C, both, x.device)
+    _vector("beta", beta, C, both, x.device)
+    _need(gamma is None or beta is None or gamma.dtype == beta.dtype, "gamma and beta must have the same type")
+    w = gamma if gamma is not None else beta
+    _vector("amax", amax, 1, (torch.float32,), x.device)
+    _need(y is None or out_dtype in (None, y.dtype), "out_dtype is not y's")
+    with _on(x, stream):
+        if y is None:
+            _need(out_dtype is None or out_dtype in FMT_OF, f"out_dtype: want bf16 or fp32, got {out_dtype}")
+            y = torch.empty((R, C), dtype=out_dtype or x.dtype, device=x.device)
+        _need(y.device == x.device, f"y: on {y.device}, want {x.device}")
+        y_fmt, ldy = _matrix("y", y, x.shape)
+        mean = torch.empty(R, dtype=torch.float32, device=x.device)
+        rstd = torch.empty(R, dtype=torch.float32, device=x.device)
+        pbs_layernorm(x, x_fmt, R, C, ldx, gamma, beta, PBS_FMT_F32 if w is None else FMT_OF[w.dtype], eps, y, y_fmt,
+                      ldy, mean, rstd, amax)
+    return y, mean, rstd
+
+
+def layernorm_grad(dy, x, gamma, mean, rstd, dx=None, stream=None):
+    """Gradients of ``layernorm``: returns (dx [R, C] in x's type, dgamma [C],
+    dbeta [C] in fp32) from dy [R, C] (bf16 or fp32), the forward's x, gamma
+    (None: 1) and the statistics it returned.  ``dx`` may be given, x or dy
+    itself among the choices."""
+    x_fmt, ldx = _matrix("x", x)
+    R, C = x.shape
+    _need(C >= 1, "x: no columns")
+    y_fmt, lddy = _matrix("dy", dy, x.shape)
+    _need(dy.device == x.device, f"dy: on {dy.device}, want {x.device}")
+    _vector("gamma", gamma, C, tuple(FMT_OF), x.device)
+    _need(mean is not None and rstd is not None, "mean and rstd are the forward's")
+    _vector("mean", mean, R, (torch.float32,), x.device)
+    _vector("rstd", rstd, R, (torch.float32,), x.device)
+    with _on(x, stream):
+        if dx is None:
+            dx = torch.empty((R, C), dtype=x.dtype, device=x.device)
+        _need(dx.dtype == x.dtype and dx.device == x.device, "dx: want x's type and device")
+        lddx = _matrix("dx", dx, x.shape)[1]
+        dgamma = torch.empty(C, dtype=torch.float32, device=x.device)
+        dbeta = torch.empty(C, dtype=torch.float32, device=x.device)
+        n = pbs_layernorm_grad_bytes(R, C)
+        ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+        pbs_layernorm_grad(dy, y_fmt, lddy, x, x_fmt, ldx, R, C, gamma,
+                           PBS_FMT_F32 if gamma is None else FMT_OF[gamma.dtype], mean, rstd, dx, lddx, dgamma, dbeta,
+                           ws, n)
+    return dx, dgamma, dbeta
