@@ -387,6 +387,65 @@ pbs_status pbs_layernorm_grad(const void* dy, pbs_format y_fmt, int64_t lddy, co
                               float* dbeta, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------------------
+ * Losses of a linear head, without keeping its logits.  With x [tokens,
+ * hidden] and w [vocab, hidden] in bf16 and z = x w^T / tau:
+ *   lse_t = log sum_v exp z_tv
+ *   loss_t = sum_s p_ts (log p_ts - z_t,id(t,s) + lse_t)
+ * pbs_linear_xent (softmax cross entropy): one slot, id = targets[t], p = 1,
+ *   tau = 1.  A negative target (-100, say) leaves the token out.
+ * pbs_linear_distill (Kullback-Leibler divergence from a teacher's softmax
+ *   over its `top` highest logits to the head's softmax over the whole
+ *   vocabulary): top_ids, top_logits [tokens, top] (logits bf16 or fp32),
+ *   p = softmax(top_logits / temperature) over a token's used slots, tau =
+ *   temperature.  A slot with a negative id is unused, whatever its logit
+ *   holds; an id may stand in several slots of a token, whose probabilities
+ *   then add.  A token without used slots, or whose used slots all hold
+ *   -inf, is left out.  No factor tau^2 is applied: it goes into dloss.
+ *
+ *  A token that is left out has loss 0 and lse 0, a zero row of dx and no
+ *  part in dw; its row of x may hold anything, NaN included.
+ *  An id >= vocab makes the token's loss, its row of dx and dw NaN (it is
+ *  never used as an index).
+ *  loss, lse: fp32 [tokens]; lse is an input of the gradient.
+ *
+ * pbs_linear_xent_grad / pbs_linear_distill_grad: with dloss fp32 [tokens]
+ * (1 / count for a mean, any weights),
+ *   dz_tv = dloss_t / tau (exp(z_tv - lse_t) - sum_{s: id(t,s) = v} p_ts)
+ *   dx = dz w     bf16 [tokens, hidden]
+ *   dw = dz^T x   bf16 or fp32 (dw_fmt) [vocab, hidden]
+ *  dx or dw may be NULL (not computed; not both).  z is formed again, and dz
+ *  held in the workspace, for `piece` ids of the vocabulary at a time (rounded
+ *  up to a multiple of 256; 0: the library's choice, about 1 GiB of dz).  dz
+ *  is rounded to bf16 for the two products; all sums are fp32.
+ *
+ *  workspace: the bytes that pbs_linear_loss_bytes gives for the same tokens,
+ *    vocab, hidden, top (1 for cross entropy) and piece, 256-byte aligned.
+ *    Its contents are of no use afterwards; calls that may run at the same
+ *    time need one each.
+ *  Shapes (else PBS_ERR_SHAPE): hidden a multiple of 64 up to 65536, vocab 1
+ *    to 2^22, tokens 0 to 2^24, top 1 to 1024; any number of tokens and ids.
+ *  Alignment (else PBS_ERR_INVALID_ARG): x, w, dx, dw 16 bytes, the others
+ *    their elements.  Outputs do not overlap inputs.
+ * ------------------------------------------------------------------- */
+pbs_status pbs_linear_loss_bytes(int64_t tokens, int64_t vocab, int64_t hidden, int64_t top, int64_t piece,
+                                 size_t* loss_bytes /* [host] */, size_t* grad_bytes /* [host] */);
+pbs_status pbs_linear_xent(const void* x, const void* w, int64_t tokens, int64_t vocab, int64_t hidden,
+                           const int64_t* targets, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+pbs_status pbs_linear_xent_grad(const float* dloss, const void* x, const void* w, int64_t tokens, int64_t vocab,
+                                int64_t hidden, const int64_t* targets, const float* lse, int64_t piece, void* dx,
+                                void* dw, pbs_format dw_fmt, void* workspace, size_t workspace_bytes,
+                                hipStream_t stream);
+pbs_status pbs_linear_distill(const void* x, const void* w, int64_t tokens, int64_t vocab, int64_t hidden,
+                              const int64_t* top_ids, const void* top_logits, pbs_format top_fmt, int64_t top,
+                              float temperature, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream);
+pbs_status pbs_linear_distill_grad(const float* dloss, const void* x, const void* w, int64_t tokens, int64_t vocab,
+                                   int64_t hidden, const int64_t* top_ids, const void* top_logits, pbs_format top_fmt,
+                                   int64_t top, float temperature, const float* lse, int64_t piece, void* dx, void* dw,
+                                   pbs_format dw_fmt, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------
  * pbs_quantized_bytes [host]: bytes of the codes and of the block scales
  * of one quantized copy of a [rows, cols] tensor (not counting per-tensor
  * fp32 scalars).  For NVFP4 with 1x16 blocks this is n/2 + n/16 bytes,

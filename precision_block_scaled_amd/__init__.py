@@ -25,7 +25,8 @@ __all__ = [
     "pbs_amax", "pbs_scale_from_amax", "pbs_delayed_state_bytes", "pbs_delayed_init",
     "pbs_delayed_update", "pbs_delayed_scale", "pbs_delayed_scale_inv", "pbs_cast",
     "pbs_rht_cast", "pbs_gemm", "pbs_gemm_amax", "pbs_quantized_bytes", "pbs_debug_sr_encode",
-    "pbs_layernorm", "pbs_layernorm_grad_bytes", "pbs_layernorm_grad",
+    "pbs_layernorm", "pbs_layernorm_grad_bytes", "pbs_layernorm_grad", "pbs_linear_loss_bytes",
+    "pbs_linear_xent", "pbs_linear_xent_grad", "pbs_linear_distill", "pbs_linear_distill_grad",
     "pbs_last_error", "pbs_version",
 ]
 
@@ -65,6 +66,14 @@ SIGNATURES = {
     "pbs_layernorm_grad_bytes": (_i32, [_i64, _i64, _c.POINTER(_c.c_size_t)]),
     "pbs_layernorm_grad": (_i32, [_vp, _i32, _i64, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _vp, _i64,
                                   _vp, _vp, _vp, _c.c_size_t, _vp]),
+    "pbs_linear_loss_bytes": (_i32, [_i64] * 5 + [_c.POINTER(_c.c_size_t), _c.POINTER(_c.c_size_t)]),
+    "pbs_linear_xent": (_i32, [_vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _c.c_size_t, _vp]),
+    "pbs_linear_xent_grad": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i32, _vp,
+                                    _c.c_size_t, _vp]),
+    "pbs_linear_distill": (_i32, [_vp, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _f32, _vp, _vp, _vp,
+                                  _c.c_size_t, _vp]),
+    "pbs_linear_distill_grad": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _f32, _vp, _i64, _vp,
+                                       _vp, _i32, _vp, _c.c_size_t, _vp]),
     "pbs_quantized_bytes": (_i32, [_i32, _i64, _i64, _i32, _c.POINTER(_c.c_size_t),
                                    _c.POINTER(_c.c_size_t)]),
     "pbs_last_error": (_c.c_char_p, []),
@@ -202,6 +211,38 @@ def pbs_layernorm_grad(dy, y_fmt, lddy, x, x_fmt, ldx, rows, cols, gamma, w_fmt,
     _check(lib().pbs_layernorm_grad(_ptr(dy), y_fmt, lddy, _ptr(x), x_fmt, ldx, rows, cols, _ptr(gamma), w_fmt,
                                     _ptr(mean), _ptr(rstd), _ptr(dx), lddx, _ptr(dgamma), _ptr(dbeta),
                                     _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def pbs_linear_loss_bytes(tokens, vocab, hidden, top=1, piece=0):
+    a, b = _c.c_size_t(0), _c.c_size_t(0)
+    _check(lib().pbs_linear_loss_bytes(tokens, vocab, hidden, top, piece, _c.byref(a), _c.byref(b)))
+    return a.value, b.value
+
+
+def pbs_linear_xent(x, w, tokens, vocab, hidden, targets, loss, lse, workspace, workspace_bytes, stream=None):
+    _check(lib().pbs_linear_xent(_ptr(x), _ptr(w), tokens, vocab, hidden, _ptr(targets), _ptr(loss), _ptr(lse),
+                                 _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def pbs_linear_xent_grad(dloss, x, w, tokens, vocab, hidden, targets, lse, piece, dx, dw, dw_fmt, workspace,
+                         workspace_bytes, stream=None):
+    _check(lib().pbs_linear_xent_grad(_ptr(dloss), _ptr(x), _ptr(w), tokens, vocab, hidden, _ptr(targets), _ptr(lse),
+                                      piece, _ptr(dx), _ptr(dw), dw_fmt, _ptr(workspace), workspace_bytes,
+                                      _stream(stream)))
+
+
+def pbs_linear_distill(x, w, tokens, vocab, hidden, top_ids, top_logits, top_fmt, top, temperature, loss, lse,
+                       workspace, workspace_bytes, stream=None):
+    _check(lib().pbs_linear_distill(_ptr(x), _ptr(w), tokens, vocab, hidden, _ptr(top_ids), _ptr(top_logits), top_fmt,
+                                    top, temperature, _ptr(loss), _ptr(lse), _ptr(workspace), workspace_bytes,
+                                    _stream(stream)))
+
+
+def pbs_linear_distill_grad(dloss, x, w, tokens, vocab, hidden, top_ids, top_logits, top_fmt, top, temperature, lse,
+                            piece, dx, dw, dw_fmt, workspace, workspace_bytes, stream=None):
+    _check(lib().pbs_linear_distill_grad(_ptr(dloss), _ptr(x), _ptr(w), tokens, vocab, hidden, _ptr(top_ids),
+                                         _ptr(top_logits), top_fmt, top, temperature, _ptr(lse), piece, _ptr(dx),
+                                         _ptr(dw), dw_fmt, _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def pbs_quantized_bytes(recipe, rows, cols, weight_2d):

@@ -1,0 +1,1049 @@
+// Losses of a linear head, from the hidden states and the head's weight,
+// without keeping the logits:
+//
+//   z = x W^T / tau        x [tokens, hidden], W [vocab, hidden], both bf16
+//   lse_t = log sum_v exp z_tv,   q_tv = exp(z_tv - lse_t)
+//   loss_t = sum_s p_ts (log p_ts - z_t,id(t,s) + lse_t)
+//   dz_tv = dloss_t / tau (q_tv - sum over the slots s with id(t,s) = v of p_ts)
+//   dx = dz W,   dW = dz^T x
+//
+// Cross entropy is one slot with p = 1 and tau = 1; distillation has the
+// softmax of a teacher's highest logits over tau in its slots.
+//
+// The loss multiplies x by W^T tile by tile and keeps, of each 128 (or, on the
+// small tile, 64) columns of a row, the maximum and the sum of exponentials
+// above it, and the slots' own logits; a second kernel joins them.  The
+// gradient forms z again for a piece of the vocabulary at a time, turns it
+// into dz (bf16, in the workspace) in the product's epilogue and multiplies
+// that by W and, transposed, by x.  Tokens that take no part are left out:
+// the others' rows are gathered first, so a masked token costs nothing and
+// whatever its row of x holds reaches no sum.
+//
+// The products use the tiling of the library's BF16 GEMM: 256 x 256 outputs
+// per workgroup of 4 waves, K stages of 64 values, double-buffered in LDS and
+// filled by LDS-DMA, v_mfma_f32_32x32x16_bf16.
+#include "device.hpp"
+#include "gemm_common.hpp"
+#include "host.hpp"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace pbs {
+
+enum { KMAJ = 0, MNMAJ = 1 };                    // how an operand is stored
+enum { EPI_STATS = 0, EPI_DZ = 1, EPI_DX = 2, EPI_DW = 3 };
+enum { ROW_OUT = 0, ROW_LIVE = 1, ROW_BAD = 2 }; // a token: no part, part, an id past the vocabulary
+
+struct HeadArgs {
+  const uint8_t* x;        // [tokens, hidden]
+  const uint8_t* xc;       // the live tokens' rows, used when not all are live
+  const uint8_t* w;        // first row of this piece of W
+  const int* n_live;
+  const int* row_of;       // live row -> token
+  const int* state;        // per token: ROW_*
+  const int* ids;          // [tokens][slots]: vocabulary ids, -1 unused
+  const float* p;          // [tokens][slots]
+  float* zsel;             // [tokens][slots]: the slots' logits / tau
+  float* pm;               // [parts][rows]: maximum of a part of a row
+  float* ps;               // [parts][rows]: sum of exponentials above it
+  const float* lse;        // per token
+  const float* dloss;      // per token
+  uint16_t* dz;            // [rows][dz_ld]
+  void* out;               // dx partials (fp32 [split][rows][hidden]) / dW, or its partials
+  int64_t out_split;       // elements between the partials of two splits
+  int tokens, rows, hidden, slots;   // rows: tokens, rounded up to whole tiles
+  int v0, nv;              // this piece: first id, ids in it
+  int dz_ld;
+  int splits;
+  int add;                 // the product is added to out
+  int out_bf16;
+  float inv_tau;
+};
+
+// Stage geometry for a tile of 64 TI x 64 TJ outputs: each of the 2 x 2 waves
+// holds TI x TJ 32 x 32 tiles.
+template <int T> constexpr int tile_bytes() { return 64 * T * ROWB; }
+constexpr int HEAD_PITCH_PAD = 4;                // floats: 16 rows of a 16-byte read cover every bank
+template <int TI, int TJ> constexpr int stage_rows() { return TI >= 2 ? 128 : 64; }
+template <int TI, int TJ> constexpr int head_smem() {
+  return cmax(2 * (tile_bytes<TI>() + tile_bytes<TJ>()),
+              stage_rows<TI, TJ>() * (64 * TJ + HEAD_PITCH_PAD) * 4 + 64 * TI * 8);
+}
+
+// `bytes` bytes from p as one buffer resource, and a 16-byte load from it to LDS.
+struct BufferRows {
+  __amdgpu_buffer_rsrc_t r;
+};
+__device__ __forceinline__ BufferRows buffer_rows(const uint8_t* p, uint32_t bytes) {
+  BufferRows b;
+  b.r = __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)bytes, BUF_RSRC_WORD3);
+  return b;
+}
+__device__ __forceinline__ void buffer_to_lds(const BufferRows& b, uint8_t* lds, uint32_t lane_off, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b.r, (lds_ptr_t)lds, 16, lane_off, off, 0, 0);
+}
+
+// K-major operand: load i (of 2 T) of wave w fills LDS rows 16 T w + 8 i ..
+// + 7; lane l owns row + l / 8 and the chunk that the swizzle puts at l % 8.
+// Rows past the end re-read the last one.
+template <int T>
+struct KLoad {
+  BufferRows b;
+  uint32_t off[2 * T];
+  __device__ __forceinline__ void init(const uint8_t* p, int64_t ld, int row0, int rows, int w) {
+    const int lane = threadIdx.x & 63;
+    const int64_t span = (int64_t)(rows - row0) * ld;
+    b = buffer_rows(p + (int64_t)row0 * ld, (uint32_t)(span < 0xFFFFFFFFll ? span : 0xFFFFFFFFll));
+    const int last = rows - row0 - 1;
+#pragma unroll
+    for (int i = 0; i < 2 * T; ++i) {
+      const int t = 16 * T * w + 8 * i + (lane >> 3);
+      off[i] = (uint32_t)(t < last ? t : last) * (uint32_t)ld + (uint32_t)(((lane & 7) ^ swz_key(t)) << 4);
+    }
+  }
+  __device__ __forceinline__ void load(int kt, uint8_t* tile, int w, int i) const {
+    buffer_to_lds(b, tile + (w * 2 * T + i) * 1024, off[i], (uint32_t)(kt * ROWB));
+  }
+};
+
+// MN-major operand (stored [K][MN]): a stage's 64 K rows of the tile's 64 T
+// values go to LDS as they are, 16-byte chunk c of row k at chunk c ^ 4 (k &
+// 3).  Chunks past the operand's width re-read its last one; K rows past its
+// end (krows) re-read the last row, whose products the other operand's zeros
+// take away.
+template <int T>
+struct MnLoad {
+  static constexpr int CH = 8 * T;             // chunks per row
+  static constexpr int RPL = 64 / CH;          // rows per load
+  const uint8_t* base;
+  int64_t ld;
+  int krows;
+  uint32_t off[2 * T];
+  uint32_t c[2];                               // the lane's chunk in loads of even / odd i
+  __device__ __forceinline__ void init(const uint8_t* p, int64_t ld_, int mn0, int nmn, int krows_, int w) {
+    const int lane = threadIdx.x & 63;
+    base = p + (int64_t)mn0 * 2;
+    ld = ld_;
+    krows = krows_;
+    const int lastc = (nmn - mn0 - 8) >> 3;
+#pragma unroll
+    for (int i = 0; i < 2 * T; ++i) {
+      const int row = RPL * (2 * T * w + i) + lane / CH;
+      int lc = (lane % CH) ^ (4 * (row & 3));
+      lc = lc < lastc ? lc : lastc;
+      if (i < 2) c[i] = (uint32_t)(lc << 4);
+      off[i] = (uint32_t)row * (uint32_t)ld + (uint32_t)(lc << 4);
+    }
+  }
+  __device__ __forceinline__ void load(int kt, uint8_t* tile, int w, int i) const {
+    const int left = krows - 64 * kt;
+    const uint32_t top = (uint32_t)((left < 64 ? left : 64) - 1) * (uint32_t)ld + c[i & 1];
+    buffer_to_lds(buffer_rows(base + (int64_t)kt * 64 * ld, (uint32_t)(64 * ld)), tile + (w * 2 * T + i) * 1024,
+                  off[i] < top ? off[i] : top, 0);
+  }
+};
+
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+// The restrict-qualified pointer gives the transposing read the alias
+// information by which the compiler tells it apart from LDS-DMA loads into
+// the other stage; without it every such read waits for all of them.
+__device__ __forceinline__ i16x4 head_read_tr16(const uint8_t* __restrict__ p) {
+  typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p));
+}
+
+// Fragments of one half stage (32 K values): x[tile][s] is the operand of
+// K=16 step s of the half, lane (lr, lg) holding 8 K values of its row.
+template <int T>
+struct Half {
+  i32x4 x[T][2];
+};
+
+template <int LD, int T>
+constexpr int half_reads() { return LD == KMAJ ? 2 * T : 4 * T; }
+
+template <int H, int LD, int T>
+__device__ __forceinline__ void half_read(Half<T>& f, int d, const uint8_t* base, uint32_t lb) {
+  if (LD == KMAJ) {
+    const int tile = d >> 1, part = d & 1;
+    f.x[tile][part] = *(const i32x4*)(base + tile * 4096 + (lb ^ (uint32_t)(((4 * H) ^ (2 * tile)) << 4) ^
+                                                            (uint32_t)(part << 5)));
+  } else {
+    const int tile = d >> 2, s = (d >> 1) & 1, q = d & 1;
+    const i16x4 v = head_read_tr16(base + (16 * (2 * H + s) + 4 * q) * (128 * T) + (lb ^ (uint32_t)(64 * tile)));
+    const int2 w2 = __builtin_bit_cast(int2, v);
+    if (q == 0) {
+      f.x[tile][s].x = w2.x;
+      f.x[tile][s].y = w2.y;
+    } else {
+      f.x[tile][s].z = w2.x;
+      f.x[tile][s].w = w2.y;
+    }
+  }
+}
+
+__device__ __forceinline__ constexpr int part_lo(int n, int over, int m) { return m < over ? n * m / over : n; }
+__device__ __forceinline__ constexpr int part_hi(int n, int over, int m) { return m < over ? n * (m + 1) / over : n; }
+
+constexpr float LOG2E = 1.44269504088896340736f;
+constexpr float LN2 = 0.69314718055994530942f;
+__device__ __forceinline__ float head_exp(float v) { return __builtin_amdgcn_exp2f(v * LOG2E); }
+__device__ __forceinline__ float head_log(float v) { return __builtin_amdgcn_logf(v) * LN2; }
+
+// ---------------------------------------------------------------------------
+// The product and its epilogues.
+//
+// K stage kt sits in LDS buffer (kt - first) & 1.  Phase A multiplies the
+// stage's first half while its second half is read from LDS; then the wave
+// waits for its own loads of stage kt + 1 (an explicit vmcnt(0)) and all waves
+// meet; phase C multiplies the second half while the next stage's first half
+// is read and the loads of stage kt + 2 are issued into the buffer that was
+// just read out.
+// ---------------------------------------------------------------------------
+template <int TI, int TJ, int LDA, int LDB, int EPI>
+__global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(HeadArgs g) {
+  __shared__ __align__(16) uint8_t smem[head_smem<TI, TJ>()];
+  constexpr int M_T = 64 * TI, N_T = 64 * TJ;
+
+  const int t = threadIdx.x, lane = t & 63;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = w >> 1, wn = w & 1;
+  const int n = *g.n_live;
+  const uint8_t* xs = n == g.tokens ? g.x : g.xc;
+  const int64_t ldx = (int64_t)g.hidden * 2, ldz = (int64_t)g.dz_ld * 2;
+  const int M = EPI == EPI_DW ? g.nv : n;
+  const int N = EPI <= EPI_DZ ? g.nv : g.hidden;
+  const int nk = EPI <= EPI_DZ ? g.hidden / 64 : ((EPI == EPI_DX ? g.nv : n) + 63) / 64;
+  const int tiles_m = (M + M_T - 1) / M_T, tiles_n = (N + N_T - 1) / N_T;
+  const int tiles = tiles_m * tiles_n * g.splits;
+  if ((int)blockIdx.x >= tiles) return;
+  int tm, tn;
+  tile_of(blockIdx.x, tiles_m, tiles_n * g.splits, tm, tn);
+  const int split = tn / tiles_n;
+  tn -= split * tiles_n;
+  const int m0 = tm * M_T, n0 = tn * N_T;
+  const int k0 = (int)((int64_t)nk * split / g.splits), k1 = (int)((int64_t)nk * (split + 1) / g.splits);
+
+  auto tileA = [&](int buf) { return smem + buf * (tile_bytes<TI>() + tile_bytes<TJ>()); };
+  auto tileB = [&](int buf) { return tileA(buf) + tile_bytes<TI>(); };
+
+  f32x16 acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+  typename std::conditional<LDA == KMAJ, KLoad<TI>, MnLoad<TI>>::type la;
+  typename std::conditional<LDB == KMAJ, KLoad<TJ>, MnLoad<TJ>>::type lb;
+  if constexpr (EPI <= EPI_DZ) {
+    la.init(xs, ldx, m0, n, w);
+    lb.init(g.w, ldx, n0, g.nv, w);
+  } else if constexpr (EPI == EPI_DX) {
+    la.init((const uint8_t*)g.dz, ldz, m0, n, w);
+    lb.init(g.w, ldx, n0, g.hidden, g.nv, w);
+  } else {
+    la.init((const uint8_t*)g.dz, ldz, m0, g.dz_ld, 64 * nk, w);
+    lb.init(xs, ldx, n0, g.hidden, n, w);
+  }
+
+  const int lr = lane & 31, lg = lane >> 5;
+  const int jj = (lr & 15) >> 2;
+  // per-lane part of a fragment read: K-major, the row's chunk lg under its
+  // swizzle key; MN-major, K row 8 lg + jj, the chunk swizzle 64 jj and the
+  // wave's columns
+  auto frag_base = [&](int ld, int T, int wv) {
+    if (ld == KMAJ) return (uint32_t)(lr * 128 + ((lg ^ swz_key(lr) ^ ((2 * wv * T) & 7)) << 4));
+    return (uint32_t)((8 * lg + jj) * (128 * T) + ((64 * jj) ^ (64 * T * wv)) + 32 * (lr >> 4) +
+                      16 * ((lr & 3) >> 1) + 8 * (lr & 1));
+  };
+  const uint32_t fba = frag_base(LDA, TI, wm), fbb = frag_base(LDB, TJ, wn);
+  const int offA = LDA == KMAJ ? wm * TI * 4096 : 0, offB = LDB == KMAJ ? wn * TJ * 4096 : 0;
+
+  constexpr int NMFMA = 2 * TI * TJ, HALF = NMFMA / 2;       // per half stage
+  constexpr int NVM = 2 * TI + 2 * TJ;                       // loads per stage and wave
+  constexpr int RA = half_reads<LDA, TI>(), RB = half_reads<LDB, TJ>();
+  Half<TI> a0, a1;
+  Half<TJ> b0, b1;
+
+  auto load_item = [&](int kt, int v) {
+    const int buf = (kt - k0) & 1;
+    if (v < 2 * TI) la.load(kt, tileA(buf), w, v);
+    else lb.load(kt, tileB(buf), w, v - 2 * TI);
+  };
+  auto mfma = [&](const Half<TI>& a, const Half<TJ>& b, int m) {
+    const int s = m / (TI * TJ), i = (m / TJ) % TI, j = m % TJ;
+    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a.x[i][s]),
+                                                        __builtin_bit_cast(bf16x8, b.x[j][s]), acc[i][j], 0, 0, 0);
+  };
+
+  if (k1 > k0) {
+#pragma unroll
+    for (int v = 0; v < NVM; ++v) load_item(k0, v);
+    wait_vm0();
+    __syncthreads();
+    if (k1 > k0 + 1) {
+#pragma unroll
+      for (int v = 0; v < NVM; ++v) load_item(k0 + 1, v);
+    }
+#pragma unroll
+    for (int d = 0; d < RA; ++d) half_read<0, LDA, TI>(a0, d, tileA(0) + offA, fba);
+#pragma unroll
+    for (int d = 0; d < RB; ++d) half_read<0, LDB, TJ>(b0, d, tileB(0) + offB, fbb);
+
+    auto body = [&](int kt, auto issue_c, auto next_c) {
+      constexpr bool ISSUE = decltype(issue_c)::value;
+      constexpr bool NEXT = decltype(next_c)::value;
+      const int buf = (kt - k0) & 1;
+      const uint8_t* curA = tileA(buf) + offA;
+      const uint8_t* curB = tileB(buf) + offB;
+      const uint8_t* nxtA = tileA(buf ^ 1) + offA;
+      const uint8_t* nxtB = tileB(buf ^ 1) + offB;
+#pragma unroll
+      for (int m = 0; m < NMFMA; ++m) {
+        mfma(a0, b0, m);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int d = part_lo(RA + RB, HALF, m); d < part_hi(RA + RB, HALF, m); ++d) {
+          if (d < RA) half_read<1, LDA, TI>(a1, d, curA, fba);
+          else half_read<1, LDB, TJ>(b1, d - RA, curB, fbb);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      wait_vm0();
+      __syncthreads();
+      __builtin_amdgcn_sched_barrier(0);
+      constexpr int NDS = NEXT ? RA + RB : 0;
+      constexpr int NLD = ISSUE ? NVM : 0;
+#pragma unroll
+      for (int m = 0; m < NMFMA; ++m) {
+        mfma(a1, b1, m);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int d = part_lo(NDS, HALF, m); d < part_hi(NDS, HALF, m); ++d) {
+          if (d < RA) half_read<0, LDA, TI>(a0, d, nxtA, fba);
+          else half_read<0, LDB, TJ>(b0, d - RA, nxtB, fbb);
+        }
+#pragma unroll
+        for (int v = part_lo(NLD, NMFMA, m); v < part_hi(NLD, NMFMA, m); ++v) load_item(kt + 2, v);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    using T_ = std::integral_constant<bool, true>;
+    using F_ = std::integral_constant<bool, false>;
+    for (int kt = k0; kt < k1 - 2; ++kt) body(kt, T_{}, T_{});
+    if (k1 - k0 >= 2) body(k1 - 2, F_{}, T_{});
+    body(k1 - 1, F_{}, F_{});
+  }
+  // Every LDS read of the loop finished before its last barrier, and no load
+  // is in flight: the tiles' space now stages the result, fp32, ROWS rows a
+  // pass.  Staged row s is row 32 TI (s / WR) + WR p + s % WR of the tile.
+  constexpr int ROWS = stage_rows<TI, TJ>(), PASSES = M_T / ROWS, WR = ROWS / 2;
+  constexpr int PITCH = N_T + HEAD_PITCH_PAD;
+  float* stage = (float*)smem;
+  float2* table = (float2*)(smem + ROWS * PITCH * 4);       // {lse, dloss / tau} of the tile's rows
+  auto tile_row = [&](int p, int s) { return 32 * TI * (s / WR) + WR * p + s % WR; };
+  const int ncol = N - n0 < N_T ? N - n0 : N_T;              // columns of the tile that exist
+
+  if constexpr (EPI == EPI_DZ) {
+    for (int r = t; r < M_T; r += 256) {
+      float2 e = make_float2(__builtin_inff(), 0.0f);        // rows past the last: exp(-inf) 0 = 0
+      if (m0 + r < n) {
+        const int tok = g.row_of[m0 + r];
+        e.x = g.lse[tok];
+        e.y = g.state[tok] == ROW_BAD ? __builtin_nanf("") : g.dloss[tok] * g.inv_tau;
+      }
+      table[r] = e;
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+#pragma unroll
+    for (int ii = 0; ii < WR / 32; ++ii)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int s = wm * WR + 32 * ii + 8 * (r >> 2) + 4 * lg + (r & 3);
+        float2 e;
+        if (EPI == EPI_DZ) e = table[tile_row(p, s)];
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) {
+          float v = acc[WR / 32 * p + ii][j][r];
+          if (EPI == EPI_STATS) v = v * g.inv_tau;
+          if (EPI == EPI_DZ) v = head_exp(v * g.inv_tau - e.x) * e.y;
+          stage[s * PITCH + wn * 32 * TJ + 32 * j + lr] = v;
+        }
+      }
+    __syncthreads();
+    if constexpr (EPI <= EPI_DZ) {
+      // a thread owns PW columns of a staged row
+      constexpr int PARTS = 256 / ROWS, PW = N_T / PARTS;
+      const int s = t % ROWS, part = t / ROWS;
+      float* mine = stage + s * PITCH + part * PW;
+      const int have = ncol - part * PW;                     // columns of this part that exist
+      if (ncol < N_T) {
+        for (int c = have < 0 ? 0 : have; c < PW; ++c) mine[c] = EPI == EPI_STATS ? -__builtin_inff() : 0.0f;
+      }
+      const int row = m0 + tile_row(p, s);
+      const int tok = row < n ? g.row_of[row] : -1;
+      if constexpr (EPI == EPI_STATS) {
+        float mx = -__builtin_inff(), sum = 0.0f;
+        for (int c = 0; c < PW; c += 32) {
+          float4 v[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) v[u] = *(const float4*)(mine + c + 4 * u);
+          float m1 = mx;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) m1 = fmaxf(fmaxf(m1, fmaxf(v[u].x, v[u].y)), fmaxf(v[u].z, v[u].w));
+          const float safe = m1 == -__builtin_inff() ? 0.0f : m1;   // nothing but -inf: the sum stays 0
+          float add = 0.0f;
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            add += (head_exp(v[u].x - safe) + head_exp(v[u].y - safe)) +
+                   (head_exp(v[u].z - safe) + head_exp(v[u].w - safe));
+          sum = sum * head_exp(mx - safe) + add;
+          mx = m1;
+        }
+        const int64_t at = (int64_t)(tn * PARTS + part) * g.rows + row;
+        g.pm[at] = mx;
+        g.ps[at] = sum;
+      }
+      if (tok >= 0) {
+        const int first = g.v0 + n0 + part * PW;
+        const int4* ids = (const int4*)(g.ids + (int64_t)tok * g.slots);
+        for (int q = 0; q < g.slots / 4; ++q) {
+          const int4 id4 = ids[q];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int id = u == 0 ? id4.x : u == 1 ? id4.y : u == 2 ? id4.z : id4.w;
+            const int c = id - first;
+            if (id >= 0 && c >= 0 && c < PW && c < have) {
+              const int64_t at = (int64_t)tok * g.slots + 4 * q + u;
+              if (EPI == EPI_STATS) g.zsel[at] = mine[c];
+              else mine[c] -= g.p[at] * table[tile_row(p, s)].y;
+            }
+          }
+        }
+      }
+    }
+    if constexpr (EPI == EPI_DZ) {
+      __syncthreads();
+      // 8 values a lane: N_T / 8 lanes a row
+      constexpr int LPR = N_T / 8, RPI = 256 / LPR;
+#pragma unroll 4
+      for (int s = t / LPR; s < ROWS; s += RPI) {
+        const float* q = stage + s * PITCH + (t % LPR) * 8;
+        const float4 lo = *(const float4*)q, hi = *(const float4*)(q + 4);
+        const uint4 o = make_uint4(pk_bf16(lo.x, lo.y), pk_bf16(lo.z, lo.w), pk_bf16(hi.x, hi.y), pk_bf16(hi.z, hi.w));
+        *(uint4*)(g.dz + (int64_t)(m0 + tile_row(p, s)) * g.dz_ld + n0 + (t % LPR) * 8) = o;
+      }
+    }
+    if constexpr (EPI >= EPI_DX) {
+      constexpr int LPR = N_T / 8, RPI = 256 / LPR;
+      const int col = n0 + (t % LPR) * 8;
+#pragma unroll 4
+      for (int s = t / LPR; s < ROWS; s += RPI) {
+        const float* q = stage + s * PITCH + (t % LPR) * 8;
+        float4 lo = *(const float4*)q, hi = *(const float4*)(q + 4);
+        const int row = m0 + tile_row(p, s);
+        if (row < M && col < N) {
+          const int64_t at = (int64_t)split * g.out_split + (int64_t)row * g.hidden + col;
+          if (g.out_bf16) {
+            *(uint4*)((uint16_t*)g.out + at) =
+                make_uint4(pk_bf16(lo.x, lo.y), pk_bf16(lo.z, lo.w), pk_bf16(hi.x, hi.y), pk_bf16(hi.z, hi.w));
+          } else {
+            float4* o = (float4*)((float*)g.out + at);
+            if (g.add) {
+              const float4 u = o[0], v = o[1];
+              lo = make_float4(lo.x + u.x, lo.y + u.y, lo.z + u.z, lo.w + u.w);
+              hi = make_float4(hi.x + v.x, hi.y + v.y, hi.z + v.z, hi.w + v.w);
+            }
+            o[0] = lo;
+            o[1] = hi;
+          }
+        }
+      }
+    }
+    if (p + 1 < PASSES) __syncthreads();
+  }
+}
+
+typedef void (*head_fn)(HeadArgs);
+template <int TI, int TJ, int EPI>
+static head_fn head_product() {
+  return head_gemm_kernel<TI, TJ, EPI == EPI_DW ? MNMAJ : KMAJ, EPI >= EPI_DX ? MNMAJ : KMAJ, EPI>;
+}
+
+// ---------------------------------------------------------------------------
+// Around the products.
+// ---------------------------------------------------------------------------
+struct TeacherArgs {
+  const int64_t* ids;      // [tokens][top]
+  const void* logits;      // [tokens][top]
+  int bf16, top, slots, tokens, vocab;
+  float inv_tau;
+  int* state;
+  int* ids32;
+  float* p;
+  float* ent;              // sum p log p
+};
+
+__device__ __forceinline__ float wave_max_f(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+  return v;
+}
+__device__ __forceinline__ float wave_sum_f(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// The teacher's probabilities: one wave per token.  A slot with a negative id
+// is unused, whatever its logit holds; a token without a used slot, or whose
+// used slots all hold -inf, takes no part.  The maximum is subtracted before
+// the division by tau, so the type's lowest value in every slot is a uniform
+// distribution and overflows nowhere.
+__global__ __launch_bounds__(256) void head_teacher_kernel(TeacherArgs a) {
+  const int tok = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (tok >= a.tokens) return;
+  const int64_t in = (int64_t)tok * a.top, out = (int64_t)tok * a.slots;
+  const float none = -__builtin_inff();
+  auto logit = [&](int s) {
+    if (s >= a.top || a.ids[in + s] < 0) return none;
+    return a.bf16 ? bf16_to_float(((const bf16_t*)a.logits)[in + s]) : ((const float*)a.logits)[in + s];
+  };
+  float mx = none;
+  bool bad = false, nan = false;
+  for (int s = lane; s < a.slots; s += 64) {
+    const float v = logit(s);
+    nan |= v != v;
+    bad |= s < a.top && a.ids[in + s] >= a.vocab;
+    mx = fmaxf(mx, v);
+  }
+  mx = wave_max_f(mx);
+  nan = __any(nan);
+  bad = __any(bad);
+  const bool live = mx > none || nan || bad;
+  const float safe = mx > none ? mx : 0.0f;
+  float sum = 0.0f;
+  for (int s = lane; s < a.slots; s += 64) sum += expf((logit(s) - safe) * a.inv_tau);
+  sum = wave_sum_f(sum);
+  const float ls = logf(sum);
+  float ent = 0.0f;
+  for (int s = lane; s < a.slots; s += 64) {
+    const float v = logit(s);
+    const float e = (v - safe) * a.inv_tau;
+    const float p = live ? expf(e) / sum : 0.0f;
+    if (!(p == 0.0f)) ent += p * (e - ls);
+    a.p[out + s] = p;
+    const int64_t id = s < a.top ? a.ids[in + s] : -1;
+    a.ids32[out + s] = id >= 0 && id < a.vocab ? (int)id : -1;
+  }
+  ent = wave_sum_f(ent);
+  if (lane == 0) {
+    a.ent[tok] = ent;
+    a.state[tok] = bad ? ROW_BAD : live ? ROW_LIVE : ROW_OUT;
+  }
+}
+
+struct RowsArgs {
+  const int64_t* targets;  // cross entropy; null: state is set already
+  int tokens, vocab, slots;
+  int* n_live;
+  int* row_of;
+  int* pos_of;             // token -> live row, or -1
+  int* state;
+  int* ids32;
+  float* p;
+  float* ent;
+  float* loss;             // of the tokens that take no part: 0 (null in the gradient)
+  float* lse;
+};
+
+// The live tokens in order, by one workgroup: 8 tokens a thread and step.
+constexpr int ROWS_THR = 1024, ROWS_PER = 8;
+__global__ __launch_bounds__(ROWS_THR) void head_rows_kernel(RowsArgs a) {
+  __shared__ int wave_n[ROWS_THR / 64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  int base = 0;
+  for (int64_t t0 = 0; t0 < a.tokens; t0 += ROWS_THR * ROWS_PER) {
+    const int64_t first = t0 + (int64_t)threadIdx.x * ROWS_PER;
+    int st[ROWS_PER];
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < ROWS_PER; ++i) {
+      const int64_t t = first + i;
+      st[i] = ROW_OUT;
+      if (t < a.tokens) {
+        if (a.targets) {
+          const int64_t y = a.targets[t];
+          st[i] = y < 0 ? ROW_OUT : y < a.vocab ? ROW_LIVE : ROW_BAD;
+          a.state[t] = st[i];
+          *(int4*)(a.ids32 + 4 * t) = make_int4(st[i] == ROW_LIVE ? (int)y : -1, -1, -1, -1);
+          *(float4*)(a.p + 4 * t) = make_float4(1.0f, 0.0f, 0.0f, 0.0f);
+          a.ent[t] = 0.0f;
+        } else {
+          st[i] = a.state[t];
+        }
+      }
+      mine += st[i] != ROW_OUT;
+    }
+    int before = mine;                       // inclusive scan over the wave
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(before, o, 64);
+      if (lane >= o) before += v;
+    }
+    if (lane == 63) wave_n[w] = before;
+    __syncthreads();
+    int at = base + before - mine, all = 0;
+#pragma unroll
+    for (int i = 0; i < ROWS_THR / 64; ++i) {
+      if (i < w) at += wave_n[i];
+      all += wave_n[i];
+    }
+    base += all;
+#pragma unroll
+    for (int i = 0; i < ROWS_PER; ++i) {
+      const int64_t t = first + i;
+      if (t >= a.tokens) break;
+      if (st[i] != ROW_OUT) {
+        a.row_of[at] = (int)t;
+        a.pos_of[t] = at++;
+      } else {
+        a.pos_of[t] = -1;
+        if (a.loss) {
+          a.loss[t] = 0.0f;
+          a.lse[t] = 0.0f;
+        }
+      }
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) *a.n_live = base;
+}
+
+// The live rows of x, one after the other: a wave per row.  Nothing to do when
+// every token is live (the products then read x itself).
+__global__ __launch_bounds__(256) void head_gather_kernel(const uint4* x, uint4* xc, const int* n_live,
+                                                          const int* row_of, int tokens, int chunks) {
+  const int n = *n_live;
+  if (n == tokens) return;
+  for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); i < n; i += (int64_t)gridDim.x * 4) {
+    const uint4* from = x + (int64_t)row_of[i] * chunks;
+    uint4* to = xc + i * chunks;
+    for (int c = threadIdx.x & 63; c < chunks; c += 64) to[c] = from[c];
+  }
+}
+
+struct JoinArgs {
+  const int* n_live;
+  const int* row_of;
+  const int* state;
+  const int* ids;
+  const float* p;
+  const float* ent;
+  const float* zsel;
+  const float* pm;
+  const float* ps;
+  int parts, rows, slots;
+  float* loss;
+  float* lse;
+};
+
+// lse and loss of 32 live rows: 8 threads a row share its parts.
+__global__ __launch_bounds__(256) void head_join_kernel(JoinArgs a) {
+  __shared__ float sm[8][32], ss[8][32];
+  const int r = threadIdx.x & 31, q = threadIdx.x >> 5;
+  const int row = blockIdx.x * 32 + r;
+  const bool ok = row < *a.n_live;
+  const float none = -__builtin_inff();
+  float mx = none, sum = 0.0f;
+  if (ok) {
+    for (int i = q; i < a.parts; i += 8) {
+      const float m = a.pm[(int64_t)i * a.rows + row], s = a.ps[(int64_t)i * a.rows + row];
+      const float m1 = fmaxf(mx, m), safe = m1 == none ? 0.0f : m1;
+      sum = sum * expf(mx - safe) + s * expf(m - safe);
+      mx = m1;
+    }
+  }
+  sm[q][r] = mx;
+  ss[q][r] = sum;
+  __syncthreads();
+  if (q != 0 || !ok) return;
+  for (int i = 1; i < 8; ++i) {
+    const float m = sm[i][r], m1 = fmaxf(mx, m), safe = m1 == none ? 0.0f : m1;
+    sum = sum * expf(mx - safe) + ss[i][r] * expf(m - safe);
+    mx = m1;
+  }
+  const int tok = a.row_of[row];
+  const float lse = mx + logf(sum);
+  float loss = a.ent[tok];
+  const int64_t at = (int64_t)tok * a.slots;
+  for (int s = 0; s < a.slots; ++s) {
+    const float p = a.p[at + s];
+    if (a.ids[at + s] >= 0 && !(p == 0.0f)) loss -= p * (a.zsel[at + s] - lse);
+  }
+  a.lse[tok] = lse;
+  a.loss[tok] = a.state[tok] == ROW_BAD ? __builtin_nanf("") : loss;
+}
+
+// dx [tokens, hidden] bf16 from the partial products of the live rows; zeros
+// for the tokens that take no part.  8 values a thread.
+__global__ __launch_bounds__(256) void head_dx_kernel(const float* part, int splits, int64_t split_stride,
+                                                      const int* pos_of, int64_t chunks8, int per_row,
+                                                      uint16_t* dx) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < chunks8; i += (int64_t)gridDim.x * 256) {
+    const int64_t tok = i / per_row;
+    const int c = (int)(i - tok * per_row);
+    const int pos = pos_of[tok];
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (pos >= 0) {
+      const float* q = part + ((int64_t)pos * per_row + c) * 8;
+      for (int s = 0; s < splits; ++s, q += split_stride) {
+        const float4 lo = *(const float4*)q, hi = *(const float4*)(q + 4);
+        v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+        v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+      }
+    }
+    *(uint4*)(dx + i * 8) = make_uint4(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]), pk_bf16(v[6], v[7]));
+  }
+}
+
+// dW of a piece from its splits' partial products.
+__global__ __launch_bounds__(256) void head_dw_kernel(const float* part, int splits, int64_t split_stride,
+                                                      int64_t chunks8, void* dw, int bf16) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < chunks8; i += (int64_t)gridDim.x * 256) {
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const float* q = part + i * 8;
+    for (int s = 0; s < splits; ++s, q += split_stride) {
+      const float4 lo = *(const float4*)q, hi = *(const float4*)(q + 4);
+      v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+      v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+    }
+    if (bf16) {
+      *(uint4*)((uint16_t*)dw + i * 8) =
+          make_uint4(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]), pk_bf16(v[6], v[7]));
+    } else {
+      ((float4*)dw)[2 * i] = make_float4(v[0], v[1], v[2], v[3]);
+      ((float4*)dw)[2 * i + 1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  }
+}
+
+__global__ void head_zero_kernel(uint4* p, int64_t n16) {
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n16; i += (int64_t)gridDim.x * blockDim.x)
+    p[i] = make_uint4(0, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------------------
+// Host side: the workspace's layout and the calls.
+// ---------------------------------------------------------------------------
+constexpr int HEAD_TM = 256, HEAD_TN = 256;
+constexpr int HEAD_CUS = 256;
+
+// Splits of a product's K loop over nk stages when its tiles alone leave
+// compute units idle: the number that minimises rounds of tiles times (stages
+// + a tile's fixed cost, in stages).
+static int head_splits(int64_t tiles, int64_t nk) {
+  constexpr int FIXED = 6, MOST = 16;
+  int best = 1;
+  int64_t cost = 0;
+  for (int s = 1; s <= MOST && (s == 1 || nk / s >= 8); ++s) {
+    const int64_t c = ceil_div(tiles * s, HEAD_CUS) * (ceil_div(nk, s) + FIXED);
+    if (s == 1 || c < cost) {
+      best = s;
+      cost = c;
+    }
+  }
+  return best;
+}
+
+struct HeadPlan {
+  int64_t rows, slots, parts, piece, dz_ld;
+  int dx_splits, dw_splits;
+  size_t n_live, row_of, pos_of, state, ids, p, ent, xc;
+  size_t zsel, pm, ps, loss_bytes;                       // the loss
+  size_t dz, dxp, dwp, grad_bytes;                       // the gradient
+};
+
+static HeadPlan head_plan(int64_t tokens, int64_t vocab, int64_t hidden, int64_t top, int64_t piece) {
+  HeadPlan h = {};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  h.rows = ceil_div(tokens, HEAD_TM) * HEAD_TM;
+  h.slots = ceil_div(top, 4) * 4;
+  h.parts = ceil_div(vocab, HEAD_TN) * 2;
+  h.n_live = take(4);
+  h.row_of = take(4 * tokens);
+  h.pos_of = take(4 * tokens);
+  h.state = take(4 * tokens);
+  h.ids = take(4 * tokens * h.slots);
+  h.p = take(4 * tokens * h.slots);
+  h.ent = take(4 * tokens);
+  h.xc = take(2 * tokens * hidden);
+  const size_t shared = at;
+  h.zsel = take(4 * tokens * h.slots);
+  h.pm = take(4 * h.parts * h.rows);
+  h.ps = take(4 * h.parts * h.rows);
+  h.loss_bytes = at;
+  at = shared;
+  // default piece: dz of a piece at most 1 GiB, and at least 2048 ids
+  if (piece <= 0) piece = std::max<int64_t>(2048, (1ll << 30) / (2 * std::max<int64_t>(h.rows, 1)));
+  h.piece = std::min(ceil_div(piece, HEAD_TN), ceil_div(std::max<int64_t>(vocab, 1), HEAD_TN)) * HEAD_TN;
+  h.dz_ld = h.piece;
+  const int64_t tn = ceil_div(hidden, HEAD_TN);
+  h.dx_splits = head_splits(h.rows / HEAD_TM * tn, h.piece / 64);
+  h.dw_splits = head_splits(h.piece / HEAD_TM * tn, ceil_div(tokens, 64));
+  h.dz = take(2 * h.rows * h.dz_ld);
+  h.dxp = take((size_t)4 * h.dx_splits * h.rows * hidden);
+  h.dwp = h.dw_splits > 1 ? take((size_t)4 * h.dw_splits * h.piece * hidden) : at;
+  h.grad_bytes = at;
+  return h;
+}
+
+static pbs_status head_check_dims(const char* what, int64_t tokens, int64_t vocab, int64_t hidden, int64_t top) {
+  PBS_REQUIRE(tokens >= 0 && tokens <= (1 << 24) && vocab >= 1 && vocab <= (1 << 22), PBS_ERR_SHAPE,
+              "%s: needs tokens in [0, 2^24] and vocab in [1, 2^22] (got %lld, %lld)", what, (long long)tokens,
+              (long long)vocab);
+  PBS_REQUIRE(hidden >= 64 && hidden % 64 == 0 && hidden <= (1 << 16), PBS_ERR_SHAPE,
+              "%s: hidden must be a multiple of 64 in [64, 65536] (got %lld)", what, (long long)hidden);
+  PBS_REQUIRE(top >= 1 && top <= 1024, PBS_ERR_SHAPE, "%s: top must be in [1, 1024] (got %lld)", what, (long long)top);
+  PBS_REQUIRE(ceil_div(tokens, 64) * ceil_div(vocab, 64) < (1ll << 31) / 16, PBS_ERR_SHAPE,
+              "%s: tokens x vocab is too large for one call", what);
+  return PBS_OK;
+}
+
+struct HeadCall {
+  const char* what;
+  const void* x;
+  const void* w;
+  int64_t tokens, vocab, hidden;
+  const int64_t* targets;      // cross entropy
+  const int64_t* top_ids;      // distillation
+  const void* top_logits;
+  pbs_format top_fmt;
+  int64_t top;
+  float tau;
+  float* loss;
+  float* lse;                  // the gradient reads it
+  const float* dloss;
+  int64_t piece;
+  void* dx;
+  void* dw;
+  pbs_format dw_fmt;
+  void* ws;
+  size_t ws_bytes;
+};
+
+static bool off_by(const void* p, int bytes) { return ((uintptr_t)p & (bytes - 1)) != 0; }
+
+static pbs_status head_check(const HeadCall& c, bool grad, HeadPlan* plan) {
+  const pbs_status st = head_check_dims(c.what, c.tokens, c.vocab, c.hidden, c.top);
+  if (st != PBS_OK) return st;
+  PBS_REQUIRE(c.tau > 0.0f && c.tau <= 1e30f && c.tau >= 1e-30f, PBS_ERR_INVALID_ARG,
+              "%s: temperature must be in [1e-30, 1e30]", c.what);
+  PBS_REQUIRE(c.targets || c.tokens == 0 || (c.top_ids && c.top_logits), PBS_ERR_INVALID_ARG,
+              "%s: null targets", c.what);
+  PBS_REQUIRE(!c.top_logits || c.top_fmt == PBS_FMT_F32 || c.top_fmt == PBS_FMT_BF16, PBS_ERR_UNSUPPORTED,
+              "%s: teacher logits must be BF16 or F32", c.what);
+  PBS_REQUIRE(!off_by(c.targets, 8) && !off_by(c.top_ids, 8) &&
+                  !off_by(c.top_logits, c.top_fmt == PBS_FMT_BF16 ? 2 : 4),
+              PBS_ERR_INVALID_ARG, "%s: targets not aligned to their elements", c.what);
+  PBS_REQUIRE(c.w && !off_by(c.w, 16) && !off_by(c.x, 16), PBS_ERR_INVALID_ARG,
+              "%s: x and w must be 16-byte aligned, w not null", c.what);
+  PBS_REQUIRE(c.tokens == 0 || (c.x && c.lse), PBS_ERR_INVALID_ARG, "%s: x or lse is null", c.what);
+  PBS_REQUIRE(!off_by(c.lse, 4) && !off_by(c.loss, 4) && !off_by(c.dloss, 4), PBS_ERR_INVALID_ARG,
+              "%s: loss, lse and dloss must be 4-byte aligned", c.what);
+  if (grad) {
+    PBS_REQUIRE(c.tokens == 0 || c.dloss, PBS_ERR_INVALID_ARG, "%s: dloss is null", c.what);
+    PBS_REQUIRE(c.piece >= 0, PBS_ERR_INVALID_ARG, "%s: piece is negative", c.what);
+    PBS_REQUIRE(c.dx || c.dw || c.tokens == 0, PBS_ERR_INVALID_ARG, "%s: dx and dw are both null", c.what);
+    PBS_REQUIRE(!off_by(c.dx, 16) && !off_by(c.dw, 16), PBS_ERR_INVALID_ARG, "%s: dx and dw must be 16-byte aligned",
+                c.what);
+    PBS_REQUIRE(!c.dw || c.dw_fmt == PBS_FMT_F32 || c.dw_fmt == PBS_FMT_BF16, PBS_ERR_UNSUPPORTED,
+                "%s: dw must be F32 or BF16", c.what);
+  } else {
+    PBS_REQUIRE(c.tokens == 0 || c.loss, PBS_ERR_INVALID_ARG, "%s: loss is null", c.what);
+  }
+  *plan = head_plan(c.tokens, c.vocab, c.hidden, c.top, c.piece);
+  const size_t need = grad ? plan->grad_bytes : plan->loss_bytes;
+  PBS_REQUIRE(c.tokens == 0 || (c.ws && !off_by(c.ws, 256)), PBS_ERR_INVALID_ARG,
+              "%s: the workspace is null or not 256-byte aligned", c.what);
+  PBS_REQUIRE(c.tokens == 0 || c.ws_bytes >= need, PBS_ERR_INVALID_ARG,
+              "%s: the workspace holds %zu bytes, pbs_linear_loss_bytes asks for %zu", c.what, c.ws_bytes, need);
+  return PBS_OK;
+}
+
+// The live rows, their slots, and the products' common arguments.
+static HeadArgs head_rows(const HeadCall& c, const HeadPlan& h, hipStream_t stream) {
+  uint8_t* ws = (uint8_t*)c.ws;
+  if (!c.targets) {
+    TeacherArgs a = {};
+    a.ids = c.top_ids; a.logits = c.top_logits; a.bf16 = c.top_fmt == PBS_FMT_BF16;
+    a.top = (int)c.top; a.slots = (int)h.slots; a.tokens = (int)c.tokens; a.vocab = (int)c.vocab;
+    a.inv_tau = 1.0f / c.tau;
+    a.state = (int*)(ws + h.state); a.ids32 = (int*)(ws + h.ids); a.p = (float*)(ws + h.p);
+    a.ent = (float*)(ws + h.ent);
+    hipLaunchKernelGGL(head_teacher_kernel, dim3((unsigned)ceil_div(c.tokens, 4)), dim3(256), 0, stream, a);
+  }
+  RowsArgs r = {};
+  r.targets = c.targets; r.tokens = (int)c.tokens; r.vocab = (int)c.vocab; r.slots = (int)h.slots;
+  r.n_live = (int*)(ws + h.n_live); r.row_of = (int*)(ws + h.row_of); r.pos_of = (int*)(ws + h.pos_of);
+  r.state = (int*)(ws + h.state); r.ids32 = (int*)(ws + h.ids); r.p = (float*)(ws + h.p);
+  r.ent = (float*)(ws + h.ent); r.loss = c.loss; r.lse = c.loss ? c.lse : nullptr;
+  hipLaunchKernelGGL(head_rows_kernel, dim3(1), dim3(ROWS_THR), 0, stream, r);
+  hipLaunchKernelGGL(head_gather_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(c.tokens, 4), 2048)), dim3(256), 0,
+                     stream, (const uint4*)c.x, (uint4*)(ws + h.xc), r.n_live, r.row_of, (int)c.tokens,
+                     (int)(c.hidden / 8));
+  HeadArgs g = {};
+  g.x = (const uint8_t*)c.x; g.xc = ws + h.xc; g.w = (const uint8_t*)c.w;
+  g.n_live = r.n_live; g.row_of = r.row_of; g.state = r.state; g.ids = r.ids32; g.p = r.p;
+  g.tokens = (int)c.tokens; g.rows = (int)h.rows; g.hidden = (int)c.hidden; g.slots = (int)h.slots;
+  g.nv = (int)c.vocab; g.splits = 1; g.inv_tau = 1.0f / c.tau;
+  return g;
+}
+
+static pbs_status head_loss(const HeadCall& c, hipStream_t stream) {
+  HeadPlan h;
+  const pbs_status st = head_check(c, false, &h);
+  if (st != PBS_OK || c.tokens == 0) return st;
+  uint8_t* ws = (uint8_t*)c.ws;
+  HeadArgs g = head_rows(c, h, stream);
+  g.zsel = (float*)(ws + h.zsel); g.pm = (float*)(ws + h.pm); g.ps = (float*)(ws + h.ps);
+  const int64_t grid = h.rows / HEAD_TM * ceil_div(c.vocab, HEAD_TN);
+  log_dispatch("%s tokens=%lld vocab=%lld hidden=%lld top=%lld tiles=%lld", c.what, (long long)c.tokens,
+               (long long)c.vocab, (long long)c.hidden, (long long)c.top, (long long)grid);
+  hipLaunchKernelGGL((head_product<4, 4, EPI_STATS>()), dim3((unsigned)grid), dim3(256), 0, stream, g);
+  JoinArgs j = {};
+  j.n_live = g.n_live; j.row_of = g.row_of; j.state = g.state; j.ids = g.ids; j.p = g.p;
+  j.ent = (float*)(ws + h.ent); j.zsel = g.zsel; j.pm = g.pm; j.ps = g.ps;
+  j.parts = (int)h.parts; j.rows = g.rows; j.slots = g.slots; j.loss = c.loss; j.lse = c.lse;
+  hipLaunchKernelGGL(head_join_kernel, dim3((unsigned)ceil_div(c.tokens, 32)), dim3(256), 0, stream, j);
+  return check_launch(c.what);
+}
+
+static pbs_status head_grad(const HeadCall& c, hipStream_t stream) {
+  HeadPlan h;
+  const pbs_status st = head_check(c, true, &h);
+  if (st != PBS_OK) return st;
+  const int dwb = c.dw_fmt == PBS_FMT_BF16 ? 2 : 4;
+  if (c.tokens == 0) {
+    if (c.dw)
+      hipLaunchKernelGGL(head_zero_kernel, dim3(1024), dim3(256), 0, stream, (uint4*)c.dw, c.vocab * c.hidden * dwb / 16);
+    return check_launch(c.what);
+  }
+  uint8_t* ws = (uint8_t*)c.ws;
+  HeadArgs g = head_rows(c, h, stream);
+  g.lse = c.lse; g.dloss = c.dloss; g.dz = (uint16_t*)(ws + h.dz); g.dz_ld = (int)h.dz_ld;
+  log_dispatch("%s tokens=%lld vocab=%lld hidden=%lld top=%lld piece=%lld splits=%d,%d", c.what, (long long)c.tokens,
+               (long long)c.vocab, (long long)c.hidden, (long long)c.top, (long long)h.piece, h.dx_splits, h.dw_splits);
+  const int64_t tm = h.rows / HEAD_TM, tn = ceil_div(c.hidden, HEAD_TN);
+  for (int64_t v0 = 0; v0 < c.vocab; v0 += h.piece) {
+    const int64_t nv = std::min(h.piece, c.vocab - v0);
+    g.v0 = (int)v0;
+    g.nv = (int)nv;
+    g.w = (const uint8_t*)c.w + v0 * c.hidden * 2;
+    g.splits = 1;
+    hipLaunchKernelGGL((head_product<4, 4, EPI_DZ>()), dim3((unsigned)(tm * ceil_div(nv, HEAD_TN))),
+                       dim3(256), 0, stream, g);
+    if (c.dx) {
+      HeadArgs d = g;
+      d.out = ws + h.dxp; d.out_split = h.rows * c.hidden; d.splits = h.dx_splits; d.add = v0 > 0;
+      hipLaunchKernelGGL((head_product<4, 4, EPI_DX>()), dim3((unsigned)(tm * tn * d.splits)), dim3(256),
+                         0, stream, d);
+    }
+    if (c.dw) {
+      HeadArgs d = g;
+      uint8_t* to = (uint8_t*)c.dw + v0 * c.hidden * dwb;
+      d.splits = h.dw_splits;
+      if (d.splits == 1) {
+        d.out = to; d.out_bf16 = dwb == 2;
+      } else {
+        d.out = ws + h.dwp; d.out_split = h.piece * c.hidden;
+      }
+      hipLaunchKernelGGL((head_product<4, 4, EPI_DW>()),
+                         dim3((unsigned)(ceil_div(nv, HEAD_TM) * tn * d.splits)), dim3(256), 0, stream, d);
+      if (d.splits > 1)
+        hipLaunchKernelGGL(head_dw_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(nv * c.hidden / 8, 256), 4096)),
+                           dim3(256), 0, stream, (const float*)d.out, d.splits, d.out_split, nv * c.hidden / 8, to,
+                           (int)(dwb == 2));
+    }
+  }
+  if (c.dx)
+    hipLaunchKernelGGL(head_dx_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(c.tokens * c.hidden / 8, 256), 4096)),
+                       dim3(256), 0, stream, (const float*)(ws + h.dxp), h.dx_splits, h.rows * c.hidden,
+                       (const int*)(ws + h.pos_of), c.tokens * c.hidden / 8, (int)(c.hidden / 8), (uint16_t*)c.dx);
+  return check_launch(c.what);
+}
+
+}  // namespace pbs
+
+using namespace pbs;
+
+extern "C" {
+
+pbs_status pbs_linear_loss_bytes(int64_t tokens, int64_t vocab, int64_t hidden, int64_t top, int64_t piece,
+                                 size_t* loss_bytes, size_t* grad_bytes) {
+  PBS_REQUIRE(loss_bytes && grad_bytes, PBS_ERR_INVALID_ARG, "pbs_linear_loss_bytes: null output pointer");
+  const pbs_status st = head_check_dims("pbs_linear_loss_bytes", tokens, vocab, hidden, top);
+  if (st != PBS_OK) return st;
+  PBS_REQUIRE(piece >= 0, PBS_ERR_INVALID_ARG, "pbs_linear_loss_bytes: piece is negative");
+  const HeadPlan h = head_plan(tokens, vocab, hidden, top, piece);
+  *loss_bytes = h.loss_bytes;
+  *grad_bytes = h.grad_bytes;
+  return PBS_OK;
+}
+
+pbs_status pbs_linear_xent(const void* x, const void* w, int64_t tokens, int64_t vocab, int64_t hidden,
+                           const int64_t* targets, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream) {
+  HeadCall c = {};
+  c.what = "pbs_linear_xent"; c.x = x; c.w = w; c.tokens = tokens; c.vocab = vocab; c.hidden = hidden;
+  c.targets = targets; c.top = 1; c.tau = 1.0f; c.loss = loss; c.lse = lse; c.ws = workspace;
+  c.ws_bytes = workspace_bytes;
+  return head_loss(c, stream);
+}
+
+pbs_status pbs_linear_xent_grad(const float* dloss, const void* x, const void* w, int64_t tokens, int64_t vocab,
+                                int64_t hidden, const int64_t* targets, const float* lse, int64_t piece, void* dx,
+                                void* dw, pbs_format dw_fmt, void* workspace, size_t workspace_bytes,
+                                hipStream_t stream) {
+  HeadCall c = {};
+  c.what = "pbs_linear_xent_grad"; c.x = x; c.w = w; c.tokens = tokens; c.vocab = vocab; c.hidden = hidden;
+  c.targets = targets; c.top = 1; c.tau = 1.0f; c.lse = (float*)lse; c.dloss = dloss; c.piece = piece; c.dx = dx;
+  c.dw = dw; c.dw_fmt = dw_fmt; c.ws = workspace; c.ws_bytes = workspace_bytes;
+  return head_grad(c, stream);
+}
+
+pbs_status pbs_linear_distill(const void* x, const void* w, int64_t tokens, int64_t vocab, int64_t hidden,
+                              const int64_t* top_ids, const void* top_logits, pbs_format top_fmt, int64_t top,
+                              float temperature, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream) {
+  HeadCall c = {};
+  c.what = "pbs_linear_distill"; c.x = x; c.w = w; c.tokens = tokens; c.vocab = vocab; c.hidden = hidden;
+  c.top_ids = top_ids; c.top_logits = top_logits; c.top_fmt = top_fmt; c.top = top; c.tau = temperature;
+  c.loss = loss; c.lse = lse; c.ws = workspace; c.ws_bytes = workspace_bytes;
+  return head_loss(c, stream);
+}
+
+pbs_status pbs_linear_distill_grad(const float* dloss, const void* x, const void* w, int64_t tokens, int64_t vocab,
+                                   int64_t hidden, const int64_t* top_ids, const void* top_logits, pbs_format top_fmt,
+                                   int64_t top, float temperature, const float* lse, int64_t piece, void* dx, void* dw,
+                                   pbs_format dw_fmt, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  HeadCall c = {};
+  c.what = "pbs_linear_distill_grad"; c.x = x; c.w = w; c.tokens = tokens; c.vocab = vocab; c.hidden = hidden;
+  c.top_ids = top_ids; c.top_logits = top_logits; c.top_fmt = top_fmt; c.top = top; c.tau = temperature;
+  c.lse = (float*)lse; c.dloss = dloss; c.piece = piece; c.dx = dx; c.dw = dw; c.dw_fmt = dw_fmt; c.ws = workspace;
+  c.ws_bytes = workspace_bytes;
+  return head_grad(c, stream);
+}
+
+}  // extern "C"

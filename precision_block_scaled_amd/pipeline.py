@@ -36,7 +36,8 @@ from . import (PBS_COL, PBS_DGRAD, PBS_FLAG_RHT16, PBS_FLAG_SR, PBS_FMT_BF16, PB
                pbs_cast,
                pbs_delayed_init, pbs_delayed_scale, pbs_delayed_scale_inv, pbs_delayed_state_bytes,
                pbs_delayed_update, pbs_gemm, pbs_gemm_amax, pbs_layernorm, pbs_layernorm_grad,
-               pbs_layernorm_grad_bytes, pbs_scale_from_amax)
+               pbs_layernorm_grad_bytes, pbs_linear_distill, pbs_linear_distill_grad, pbs_linear_loss_bytes,
+               pbs_linear_xent, pbs_linear_xent_grad, pbs_scale_from_amax)
 
 RECIPES = {
     "bf16": PBS_RECIPE_BF16,
@@ -336,7 +337,7 @@ def quantize_pass(recipe, pass_, x, w, dy, states=None, outs=None, stream=None):
 
 
 # ---------------------------------------------------------------------------
-# the ends of a step: the norm ahead of a linear layer
+# the ends of a step: the norm ahead of a linear layer, the losses of the head
 # ---------------------------------------------------------------------------
 FMT_OF = {torch.bfloat16: PBS_FMT_BF16, torch.float32: PBS_FMT_F32}
 
@@ -442,3 +443,101 @@ def layernorm_grad(dy, x, gamma, mean, rstd, dx=None, stream=None):
                            PBS_FMT_F32 if gamma is None else FMT_OF[gamma.dtype], mean, rstd, dx, lddx, dgamma, dbeta,
                            ws, n)
     return dx, dgamma, dbeta
+
+
+def _head(x, w):
+    """Checks the head's operands; returns (tokens, vocab, hidden)."""
+    for name, t in (("x", x), ("w", w)):
+        _need(t.dim() == 2 and t.dtype == torch.bfloat16 and t.is_contiguous(),
+              f"{name}: want a contiguous bf16 matrix, got {t.dtype} {tuple(t.shape)}")
+    _need(w.device == x.device, f"w: on {w.device}, want {x.device}")
+    _need(w.shape[1] == x.shape[1], f"w {tuple(w.shape)} does not fit x {tuple(x.shape)}")
+    return x.shape[0], w.shape[0], x.shape[1]
+
+
+def _teacher(top_ids, top_logits, T, device):
+    _need(top_ids.dim() == 2 and top_ids.shape[0] == T and top_ids.shape[1] >= 1 and top_ids.is_contiguous() and
+          top_ids.dtype == torch.int64, f"top_ids: want contiguous int64 [{T}, top], got {top_ids.dtype} "
+          f"{tuple(top_ids.shape)}")
+    _need(top_logits.shape == top_ids.shape and top_logits.is_contiguous() and top_logits.dtype in FMT_OF,
+          f"top_logits: want contiguous bf16 or fp32 {tuple(top_ids.shape)}, got {top_logits.dtype} "
+          f"{tuple(top_logits.shape)}")
+    _need(top_ids.device == device and top_logits.device == device, f"the teacher's tensors must be on {device}")
+    return top_ids.shape[1]
+
+
+def _loss_outputs(T, V, H, top, x):
+    n = pbs_linear_loss_bytes(T, V, H, top)[0]
+    return (torch.empty(T, dtype=torch.float32, device=x.device), torch.empty(T, dtype=torch.float32, device=x.device),
+            torch.empty(n, dtype=torch.uint8, device=x.device), n)
+
+
+def _grad_outputs(T, V, H, top, piece, x, need_dx, need_dw, dw_dtype):
+    _need(need_dx or need_dw, "neither dx nor dw is wanted")
+    _need(dw_dtype in FMT_OF, f"dw_dtype: want bf16 or fp32, got {dw_dtype}")
+    n = pbs_linear_loss_bytes(T, V, H, top, piece)[1]
+    return (torch.empty((T, H), dtype=torch.bfloat16, device=x.device) if need_dx else None,
+            torch.empty((V, H), dtype=dw_dtype, device=x.device) if need_dw else None,
+            torch.empty(n, dtype=torch.uint8, device=x.device), n)
+
+
+def linear_xent(x, w, targets, stream=None):
+    """Softmax cross entropy of the logits x w^T, which are never kept: x
+    [T, H] and w [V, H] bf16, ``targets`` [T] int64 (negative: the token is
+    left out, its loss and lse are 0).  Returns (loss [T], lse [T]) in fp32;
+    lse = log sum exp of a token's logits is what ``linear_xent_grad`` takes.
+    """
+    T, V, H = _head(x, w)
+    _need(targets is not None, "targets are missing")
+    _vector("targets", targets, T, (torch.int64,), x.device)
+    with _on(x, stream):
+        loss, lse, ws, n = _loss_outputs(T, V, H, 1, x)
+        pbs_linear_xent(x, w, T, V, H, targets, loss, lse, ws, n)
+    return loss, lse
+
+
+def linear_xent_grad(dloss, x, w, targets, lse, piece=0, need_dx=True, need_dw=True, dw_dtype=torch.bfloat16,
+                     stream=None):
+    """Gradients of sum(dloss * loss) of ``linear_xent``: (dx [T, H] bf16, dw
+    [V, H] in ``dw_dtype``), None for one that is not needed.  The workspace
+    holds the logits' gradient for ``piece`` ids at a time (0: about 1 GiB)."""
+    T, V, H = _head(x, w)
+    _need(dloss is not None and targets is not None and lse is not None, "dloss, targets or lse is missing")
+    _vector("targets", targets, T, (torch.int64,), x.device)
+    _vector("dloss", dloss, T, (torch.float32,), x.device)
+    _vector("lse", lse, T, (torch.float32,), x.device)
+    with _on(x, stream):
+        dx, dw, ws, n = _grad_outputs(T, V, H, 1, piece, x, need_dx, need_dw, dw_dtype)
+        pbs_linear_xent_grad(dloss, x, w, T, V, H, targets, lse, piece, dx, dw, FMT_OF[dw_dtype], ws, n)
+    return dx, dw
+
+
+def linear_distill(x, w, top_ids, top_logits, temperature=1.0, stream=None):
+    """Kullback-Leibler divergence from softmax(top_logits / temperature) over
+    a teacher's stored logits to softmax(x w^T / temperature) over the whole
+    vocabulary.  ``top_ids`` [T, k] int64 (negative: unused slot), ``top_logits``
+    [T, k] bf16 or fp32.  Returns (loss [T], lse [T]) in fp32, both 0 for a
+    token without used slots; no factor temperature^2 is applied."""
+    T, V, H = _head(x, w)
+    top = _teacher(top_ids, top_logits, T, x.device)
+    with _on(x, stream):
+        loss, lse, ws, n = _loss_outputs(T, V, H, top, x)
+        pbs_linear_distill(x, w, T, V, H, top_ids, top_logits, FMT_OF[top_logits.dtype], top, temperature, loss, lse,
+                           ws, n)
+    return loss, lse
+
+
+def linear_distill_grad(dloss, x, w, top_ids, top_logits, temperature, lse, piece=0, need_dx=True, need_dw=True,
+                        dw_dtype=torch.bfloat16, stream=None):
+    """Gradients of sum(dloss * loss) of ``linear_distill``, as
+    ``linear_xent_grad`` returns them."""
+    T, V, H = _head(x, w)
+    top = _teacher(top_ids, top_logits, T, x.device)
+    _need(dloss is not None and lse is not None, "dloss or lse is missing")
+    _vector("dloss", dloss, T, (torch.float32,), x.device)
+    _vector("lse", lse, T, (torch.float32,), x.device)
+    with _on(x, stream):
+        dx, dw, ws, n = _grad_outputs(T, V, H, top, piece, x, need_dx, need_dw, dw_dtype)
+        pbs_linear_distill_grad(dloss, x, w, T, V, H, top_ids, top_logits, FMT_OF[top_logits.dtype], top, temperature,
+                                lse, piece, dx, dw, FMT_OF[dw_dtype], ws, n)
+    return dx, dw
