@@ -171,16 +171,354 @@ __global__ __launch_bounds__(WIDE_THR) void layernorm_dw_wide_kernel(NormArgs a)
   a.part[(int64_t)(a.strips + blockIdx.y) * a.cols + c] = sb;
 }
 
-// dgamma / dbeta from the strips' partial sums, in the strips' order.
-__global__ __launch_bounds__(WIDE_THR) void layernorm_dw_join_kernel(const float* part, int strips, int cols,
+// ---------------------------------------------------------------------------
+// Rows held in registers: a row is read once.
+//
+// TPR threads share a row (16 or 64: part of a wave or one wave, no barrier;
+// 256 and more: a workgroup), each with NCH chunks of 8 consecutive values, so
+// a lane's loads and stores are 16 bytes (32 in fp32) at any element address.
+// Workgroups stay and walk over the rows, the next row's loads in flight while
+// a row is reduced; the weights stay in registers.
+// ---------------------------------------------------------------------------
+typedef uint32_t u32x4a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4a4 __attribute__((ext_vector_type(4), aligned(4)));
+
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<bf16_t> {
+  u32x4 w;
+  __device__ __forceinline__ void zero() { w = u32x4{0, 0, 0, 0}; }
+  // the values, as something the compiler knows nothing about
+  __device__ __forceinline__ void opaque() { asm volatile("" : "+v"(w)); }
+  __device__ __forceinline__ void load(const void* p, int64_t i) { w = *(const u32x4a2*)((const bf16_t*)p + i); }
+  __device__ __forceinline__ void set(int k, const void* p, int64_t i) {
+    const uint32_t v = ((const bf16_t*)p)[i];
+    w[k >> 1] = (k & 1) ? (w[k >> 1] & 0xFFFFu) | (v << 16) : (w[k >> 1] & 0xFFFF0000u) | v;
+  }
+  __device__ __forceinline__ float get(int k) const {
+    return __uint_as_float((k & 1) ? (w[k >> 1] & 0xFFFF0000u) : (w[k >> 1] << 16));
+  }
+};
+template <>
+struct Raw8<float> {
+  f32x4a4 a, b;
+  __device__ __forceinline__ void zero() { a = b = f32x4a4{0, 0, 0, 0}; }
+  __device__ __forceinline__ void opaque() { asm volatile("" : "+v"(a), "+v"(b)); }
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    const float* q = (const float*)p + i;
+    a = *(const f32x4a4*)q;
+    b = *(const f32x4a4*)(q + 4);
+  }
+  __device__ __forceinline__ void set(int k, const void* p, int64_t i) {
+    const float v = ((const float*)p)[i];
+    if (k < 4) a[k & 3] = v;
+    else b[k & 3] = v;
+  }
+  __device__ __forceinline__ float get(int k) const { return k < 4 ? a[k & 3] : b[k & 3]; }
+};
+
+// Chunk of 8 values from column c of a row of `cols`; columns past the end are 0.
+template <typename T>
+__device__ __forceinline__ void row_load8(Raw8<T>& r, const void* p, int64_t row0, int c, int cols) {
+  if (c + 8 <= cols) {
+    r.load(p, row0 + c);
+  } else {
+    r.zero();
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (c + k < cols) r.set(k, p, row0 + c + k);
+  }
+}
+
+__device__ __forceinline__ uint32_t pk2(float lo, float hi) { return bf16_bits(lo) | (bf16_bits(hi) << 16); }
+
+// Stores 8 values; returns the bits of the largest |v| as stored, in fp32.
+template <typename T>
+__device__ __forceinline__ uint32_t row_store8(void* p, int64_t row0, int c, int cols, const float (&v)[8], bool want) {
+  uint32_t mx = 0;
+  if (c + 8 <= cols) {
+    if (sizeof(T) == 2) {
+      const u32x4 w = {pk2(v[0], v[1]), pk2(v[2], v[3]), pk2(v[4], v[5]), pk2(v[6], v[7])};
+      *(u32x4a2*)((bf16_t*)p + row0 + c) = w;
+      if (want) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t lo = (w[k] & 0x7FFFu) << 16, hi = w[k] & 0x7FFF0000u;
+          mx = mx > lo ? mx : lo;
+          mx = mx > hi ? mx : hi;
+        }
+      }
+    } else {
+      float* q = (float*)p + row0 + c;
+      *(f32x4a4*)q = f32x4a4{v[0], v[1], v[2], v[3]};
+      *(f32x4a4*)(q + 4) = f32x4a4{v[4], v[5], v[6], v[7]};
+      if (want) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t b = __float_as_uint(v[k]) & 0x7FFFFFFFu;
+          mx = mx > b ? mx : b;
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (c + k < cols) {
+        const uint32_t b = st1<T>(p, row0 + c + k, v[k]);
+        mx = mx > b ? mx : b;
+      }
+  }
+  return mx;
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float lane_value(float v, int l) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), l));
+}
+// Sum over 16 consecutive lanes, to each of them (row rotations by 8, 4, 2, 1).
+__device__ __forceinline__ float sum16(float v) { return dpp_add<0x121>(dpp_add<0x122>(dpp_add<0x124>(dpp_add<0x128>(v)))); }
+__device__ __forceinline__ float sum64(float v) {
+  v = sum16(v);
+  return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+}
+// Sum over the TPR threads of a row; `part`: TPR / 64 floats of this reduction's own.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* part) {
+  if (TPR == 16) return sum16(v);
+  v = sum64(v);
+  if (TPR == 64) return v;
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < TPR / 64; ++i) s += part[i];
+  return s;
+}
+// The same for two sums with one barrier.
+template <int TPR>
+__device__ __forceinline__ void row_sum2(float& a, float& b, float2* part) {
+  if (TPR == 16) {
+    a = sum16(a);
+    b = sum16(b);
+    return;
+  }
+  a = sum64(a);
+  b = sum64(b);
+  if (TPR == 64) return;
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = make_float2(a, b);
+  __syncthreads();
+  a = b = 0.0f;
+#pragma unroll
+  for (int i = 0; i < TPR / 64; ++i) {
+    const float2 u = part[i];
+    a += u.x;
+    b += u.y;
+  }
+}
+
+// 8 weights from column c; columns past the end, and all where there are none: `none` / 0.
+__device__ __forceinline__ void weights8(float (&v)[8], const void* p, int w_bf16, int c, int cols, float none) {
+  if (p && w_bf16) {
+    Raw8<bf16_t> r;
+    row_load8(r, p, 0, c, cols);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = r.get(k);
+  } else if (p) {
+    Raw8<float> r;
+    row_load8(r, p, 0, c, cols);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = r.get(k);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = none;
+  }
+}
+
+constexpr int norm_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
+
+template <typename TX, typename TY, int TPR, int NCH>
+__global__ __launch_bounds__(norm_threads(TPR)) void layernorm_kernel(NormArgs a) {
+  constexpr int THR = norm_threads(TPR), RPW = THR / TPR;
+  __shared__ float part[3][THR / 64];
+  const int sub = threadIdx.x % TPR;
+  const int64_t step = (int64_t)gridDim.x * RPW;
+  const float inv = 1.0f / (float)a.cols;
+  float gam[NCH][8], bet[NCH][8];
+  uint32_t mx = 0;
+  int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / TPR;
+  Raw8<TX> next[NCH];
+  if (row < a.rows) {
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) row_load8(next[j], a.x, row * a.ldx, (sub + j * TPR) * 8, a.cols);
+  }
+#pragma unroll
+  for (int j = 0; j < NCH; ++j) {
+    weights8(gam[j], a.gamma, a.w_bf16, (sub + j * TPR) * 8, a.cols, 1.0f);
+    weights8(bet[j], a.beta, a.w_bf16, (sub + j * TPR) * 8, a.cols, 0.0f);
+  }
+  for (; row < a.rows; row += step) {
+    float x[NCH][8];
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NCH; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        x[j][k] = next[j].get(k);
+        s += x[j][k];
+      }
+    if (row + step < a.rows) {
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) row_load8(next[j], a.x, (row + step) * a.ldx, (sub + j * TPR) * 8, a.cols);
+    }
+    const float mu = row_sum<TPR>(s, part[0]) * inv;
+    s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NCH; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        x[j][k] = (sub + j * TPR) * 8 + k < a.cols ? x[j][k] - mu : 0.0f;
+        s = __builtin_fmaf(x[j][k], x[j][k], s);
+      }
+    const float r = 1.0f / sqrtf(__builtin_fmaf(row_sum<TPR>(s, part[1]), inv, a.eps));
+    if (sub == 0) {
+      if (a.mean) a.mean[row] = mu;
+      if (a.rstd) a.rstd[row] = r;
+    }
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      float y[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = __builtin_fmaf(x[j][k] * r, gam[j][k], bet[j][k]);
+      const uint32_t b = row_store8<TY>(a.y, row * a.ldy, (sub + j * TPR) * 8, a.cols, y, a.amax != nullptr);
+      mx = mx > b ? mx : b;
+    }
+  }
+  if (a.amax) block_amax(mx, a.amax, (uint32_t*)part[2]);
+}
+
+template <typename TX, typename TY, int TPR, int NCH>
+__global__ __launch_bounds__(norm_threads(TPR)) void layernorm_grad_kernel(NormArgs a) {
+  constexpr int THR = norm_threads(TPR), RPW = THR / TPR;
+  __shared__ float2 part[2][THR / 64];
+  __shared__ float fold[RPW > 1 ? THR * 8 : 1];
+  const int sub = threadIdx.x % TPR;
+  const int64_t step = (int64_t)gridDim.x * RPW;
+  const float inv = 1.0f / (float)a.cols;
+  float gam[NCH][8], sg[NCH][8], sb[NCH][8];
+  int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / TPR;
+  Raw8<TX> x[NCH], nx[NCH];
+  Raw8<TY> dy[NCH], ndy[NCH];
+  float nmu = 0.0f, nr = 0.0f;
+  auto fetch = [&](int64_t at) {
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      row_load8(nx[j], a.x, at * a.ldx, (sub + j * TPR) * 8, a.cols);
+      row_load8(ndy[j], a.dy, at * a.ldy, (sub + j * TPR) * 8, a.cols);
+    }
+    nmu = a.mean[at];
+    nr = a.rstd[at];
+  };
+  // 1024 threads have 128 registers each: the next row's values would spill
+  // (8192 x 16384, fp32 in and bf16 dy: 483 us with them, 293 without, unpacking again for dx)
+  constexpr bool AHEAD = TPR < 1024;
+  if (AHEAD && row < a.rows) fetch(row);
+#pragma unroll
+  for (int j = 0; j < NCH; ++j) {
+    weights8(gam[j], a.gamma, a.w_bf16, (sub + j * TPR) * 8, a.cols, 1.0f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sg[j][k] = sb[j][k] = 0.0f;
+  }
+  int slot = 0;
+  for (; row < a.rows; row += step, slot ^= 1) {
+    if (!AHEAD) fetch(row);
+    const float mu = nmu, r = nr;
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      x[j] = nx[j];
+      dy[j] = ndy[j];
+    }
+    if (AHEAD && row + step < a.rows) fetch(row + step);
+    float su = 0.0f, sn = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NCH; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float d = dy[j].get(k);                  // 0 past the last column, which keeps n out of every sum
+        const float n = (x[j].get(k) - mu) * r, u = d * gam[j][k];
+        sg[j][k] = __builtin_fmaf(d, n, sg[j][k]);
+        sb[j][k] += d;
+        su += u;
+        sn = __builtin_fmaf(u, n, sn);
+      }
+    if (a.dx) {
+      row_sum2<TPR>(su, sn, part[slot]);
+      su *= inv;
+      sn *= inv;
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        if (!AHEAD) {
+          x[j].opaque();
+          dy[j].opaque();
+        }
+        float d[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          d[k] = r * (__builtin_fmaf(-((x[j].get(k) - mu) * r), sn, dy[j].get(k) * gam[j][k]) - su);
+        row_store8<TX>(a.dx, row * a.lddx, (sub + j * TPR) * 8, a.cols, d, false);
+      }
+    }
+  }
+  if (!a.part) return;
+  // the workgroup's sums: one strip
+  float* pg = a.part + (int64_t)blockIdx.x * a.cols;
+  float* pb = pg + (int64_t)a.strips * a.cols;
+#pragma unroll
+  for (int j = 0; j < NCH; ++j)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = h ? sb[j][k] : sg[j][k];
+      if constexpr (RPW > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) fold[k * THR + threadIdx.x] = v[k];
+        __syncthreads();
+        if (threadIdx.x >= TPR) continue;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          for (int q = 1; q < RPW; ++q) v[k] += fold[k * THR + q * TPR + sub];
+      }
+      row_store8<float>(h ? pb : pg, 0, (sub + j * TPR) * 8, a.cols, v, false);
+    }
+}
+
+// dgamma / dbeta from the strips' partial sums: 32 columns a workgroup, 32
+// threads a column, in the strips' order.
+constexpr int JOIN_THR = 1024;
+__global__ __launch_bounds__(JOIN_THR) void layernorm_dw_join_kernel(const float* part, int strips, int cols,
                                                                      float* dgamma, float* dbeta) {
-  const int c = blockIdx.x * WIDE_THR + threadIdx.x;
+  __shared__ float sums[32][33];
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), q = threadIdx.x >> 5;
   float* out = blockIdx.y ? dbeta : dgamma;
-  if (c >= cols || !out) return;
+  if (!out) return;
   const float* p = part + (int64_t)blockIdx.y * strips * cols + c;
   float s = 0.0f;
-  for (int i = 0; i < strips; ++i) s += p[(int64_t)i * cols];
-  out[c] = s;
+  if (c < cols) {
+#pragma unroll 8
+    for (int i = q; i < strips; i += 32) s += p[(int64_t)i * cols];
+  }
+  sums[q][threadIdx.x & 31] = s;
+  __syncthreads();
+  if (threadIdx.x < 32 && c < cols) {
+    s = 0.0f;
+    for (int i = 0; i < 32; ++i) s += sums[i][threadIdx.x];
+    out[c] = s;
+  }
 }
 
 __global__ void norm_fill_kernel(uint32_t* p, int64_t n) {
@@ -188,7 +526,37 @@ __global__ void norm_fill_kernel(uint32_t* p, int64_t n) {
     p[i] = 0u;
 }
 
-static int norm_strips(int64_t rows) { return (int)std::min<int64_t>(std::max<int64_t>(rows, 1), 512); }
+// Threads a row and chunks of 8 values a thread; 0: the row is too wide for
+// registers.  Workgroups are few enough that their start (weights, the first
+// row's latency) is paid over several rows, and many enough to fill memory's
+// queues: 256-thread workgroups at 512 / 768 / 1024 / 2048 of them took 49.6 /
+// 50.2 / 50.6 / 51.8 us on 15872 x 4096 bf16.  The gradient, which keeps two
+// sums a column in registers, takes a row of 4096 by 512 threads (74.6 us on
+// the same rows; 78.7 with 256 threads of two chunks each), the forward pass,
+// which has one more barrier a row, by 256 (50 us; 51 to 62 with 512).
+struct NormShape {
+  int tpr, nch, cap;
+};
+static NormShape norm_shape(int64_t cols, bool grad) {
+  if (cols <= 128) return {16, 1, 768};
+  if (cols <= 512) return {64, 1, grad ? 512 : 768};
+  if (cols <= 1024) return {64, 2, grad ? 512 : 768};
+  if (cols <= 2048) return {256, 1, 768};
+  if (cols <= 4096 && !grad) return {256, 2, 768};
+  if (cols <= 4096) return {512, 1, 256};
+  if (cols <= 8192) return {512, 2, 256};
+  if (cols <= 16384) return {1024, 2, grad ? 256 : 512};
+  return {0, 0, grad ? 512 : 2048};
+}
+
+static int norm_grid(const NormShape& f, int64_t rows) {
+  const int64_t groups = ceil_div(std::max<int64_t>(rows, 1), f.tpr && f.tpr < 256 ? 256 / f.tpr : 1);
+  return (int)std::min<int64_t>(groups, f.cap);
+}
+
+// Strips of rows that leave partial column sums, one for each workgroup of the
+// gradient's pass.
+static int norm_strips(int64_t rows, int64_t cols) { return norm_grid(norm_shape(cols, true), rows); }
 
 }  // namespace pbs
 
@@ -214,15 +582,29 @@ static pbs_status norm_check(const char* what, pbs_format x_fmt, pbs_format y_fm
 
 static bool norm_misaligned(const void* p, int bytes) { return ((uintptr_t)p & (bytes - 1)) != 0; }
 
-#define PBS_NORM_LAUNCH(kernel, grid, thr, a)                                                       \
+// One launch of kernel<TX, TY ...> for the call's formats.
+#define PBS_NORM_LAUNCH(kernel, grid, thr, a, ...)                                                  \
   do {                                                                                              \
     if (x_fmt == PBS_FMT_BF16) {                                                                    \
-      if (y_fmt == PBS_FMT_BF16) hipLaunchKernelGGL((kernel<bf16_t, bf16_t>), grid, dim3(thr), 0, stream, a); \
-      else hipLaunchKernelGGL((kernel<bf16_t, float>), grid, dim3(thr), 0, stream, a);              \
+      if (y_fmt == PBS_FMT_BF16) hipLaunchKernelGGL((kernel<bf16_t, bf16_t __VA_ARGS__>), grid, dim3(thr), 0, stream, a); \
+      else hipLaunchKernelGGL((kernel<bf16_t, float __VA_ARGS__>), grid, dim3(thr), 0, stream, a);              \
     } else {                                                                                        \
-      if (y_fmt == PBS_FMT_BF16) hipLaunchKernelGGL((kernel<float, bf16_t>), grid, dim3(thr), 0, stream, a); \
-      else hipLaunchKernelGGL((kernel<float, float>), grid, dim3(thr), 0, stream, a);               \
+      if (y_fmt == PBS_FMT_BF16) hipLaunchKernelGGL((kernel<float, bf16_t __VA_ARGS__>), grid, dim3(thr), 0, stream, a); \
+      else hipLaunchKernelGGL((kernel<float, float __VA_ARGS__>), grid, dim3(thr), 0, stream, a);               \
     }                                                                                               \
+  } while (0)
+
+#define PBS_NORM_COMMA ,
+#define PBS_NORM_SHAPED(kernel, f, grid, a, T4096, N4096)                                           \
+  do {                                                                                              \
+    if (f.tpr == 16) PBS_NORM_LAUNCH(kernel, grid, 256, a, PBS_NORM_COMMA 16, 1);                    \
+    else if (f.tpr == 64 && f.nch == 1) PBS_NORM_LAUNCH(kernel, grid, 256, a, PBS_NORM_COMMA 64, 1); \
+    else if (f.tpr == 64) PBS_NORM_LAUNCH(kernel, grid, 256, a, PBS_NORM_COMMA 64, 2);               \
+    else if (f.tpr == 256 && f.nch == 1) PBS_NORM_LAUNCH(kernel, grid, 256, a, PBS_NORM_COMMA 256, 1); \
+    else if (f.tpr == T4096 && f.nch == N4096)                                                      \
+      PBS_NORM_LAUNCH(kernel, grid, T4096, a, PBS_NORM_COMMA T4096, N4096);                          \
+    else if (f.tpr == 512) PBS_NORM_LAUNCH(kernel, grid, 512, a, PBS_NORM_COMMA 512, 2);             \
+    else PBS_NORM_LAUNCH(kernel, grid, 1024, a, PBS_NORM_COMMA 1024, 2);                             \
   } while (0)
 
 extern "C" {
@@ -244,9 +626,12 @@ pbs_status pbs_layernorm(const void* x, pbs_format x_fmt, int64_t rows, int64_t 
     a.x = x; a.gamma = gamma; a.beta = beta; a.w_bf16 = wb == 2;
     a.rows = rows; a.cols = (int)cols; a.ldx = ldx; a.ldy = ldy; a.eps = eps;
     a.y = y; a.mean = mean; a.rstd = rstd; a.amax = (uint32_t*)amax_out;
-    const int grid = (int)std::min<int64_t>(rows, 2048);
-    log_dispatch("layernorm_wide rows=%lld cols=%lld grid=%d", (long long)rows, (long long)cols, grid);
-    PBS_NORM_LAUNCH(layernorm_wide_kernel, dim3(grid), WIDE_THR, a);
+    const NormShape f = norm_shape(cols, false);
+    const unsigned grid = (unsigned)norm_grid(f, rows);
+    log_dispatch("layernorm rows=%lld cols=%lld threads/row=%d chunks=%d grid=%u", (long long)rows, (long long)cols,
+                 f.tpr, f.nch, grid);
+    if (f.tpr) PBS_NORM_SHAPED(layernorm_kernel, f, dim3(grid), a, 256, 2);
+    else PBS_NORM_LAUNCH(layernorm_wide_kernel, dim3(grid), WIDE_THR, a);
   }
   return check_launch("pbs_layernorm");
 }
@@ -256,7 +641,7 @@ pbs_status pbs_layernorm_grad_bytes(int64_t rows, int64_t cols, size_t* bytes) {
   PBS_REQUIRE(rows >= 0 && cols >= 1 && cols <= (1 << 24) && rows <= (1ll << 40), PBS_ERR_SHAPE,
               "pbs_layernorm_grad_bytes: needs rows in [0, 2^40] and cols in [1, 2^24] (got %lld x %lld)",
               (long long)rows, (long long)cols);
-  *bytes = (size_t)norm_strips(rows) * 2 * (size_t)cols * 4;
+  *bytes = (size_t)norm_strips(rows, cols) * 2 * (size_t)cols * 4;
   return PBS_OK;
 }
 
@@ -279,7 +664,7 @@ pbs_status pbs_layernorm_grad(const void* dy, pbs_format y_fmt, int64_t lddy, co
     return check_launch("pbs_layernorm_grad");
   }
   NormArgs a = {};
-  a.strips = norm_strips(rows);
+  a.strips = norm_strips(rows, cols);
   const bool sums = dgamma || dbeta;
   if (sums) {
     PBS_REQUIRE(workspace && ((uintptr_t)workspace & 15) == 0, PBS_ERR_INVALID_ARG,
@@ -291,15 +676,21 @@ pbs_status pbs_layernorm_grad(const void* dy, pbs_format y_fmt, int64_t lddy, co
   a.x = x; a.dy = dy; a.gamma = gamma; a.w_bf16 = w_fmt == PBS_FMT_BF16;
   a.rows = rows; a.cols = (int)cols; a.ldx = ldx; a.ldy = lddy; a.lddx = lddx;
   a.mean = (float*)mean; a.rstd = (float*)rstd; a.dx = dx; a.part = (float*)workspace;
-  const unsigned cb = (unsigned)ceil_div(cols, WIDE_THR);
-  log_dispatch("layernorm_grad_wide rows=%lld cols=%lld strips=%d", (long long)rows, (long long)cols, a.strips);
-  if (sums) {
-    PBS_NORM_LAUNCH(layernorm_dw_wide_kernel, dim3(cb, a.strips), WIDE_THR, a);
-    hipLaunchKernelGGL(layernorm_dw_join_kernel, dim3(cb, 2), dim3(WIDE_THR), 0, stream, a.part, a.strips, a.cols,
-                       dgamma, dbeta);
+  const NormShape f = norm_shape(cols, true);
+  log_dispatch("layernorm_grad rows=%lld cols=%lld threads/row=%d chunks=%d strips=%d", (long long)rows,
+               (long long)cols, f.tpr, f.nch, a.strips);
+  if (!sums) a.part = nullptr;
+  if (f.tpr) {
+    PBS_NORM_SHAPED(layernorm_grad_kernel, f, dim3(a.strips), a, 512, 1);
+  } else if (sums) {
+    PBS_NORM_LAUNCH(layernorm_dw_wide_kernel, dim3((unsigned)ceil_div(cols, WIDE_THR), a.strips), WIDE_THR, a);
   }
+  if (sums)
+    hipLaunchKernelGGL(layernorm_dw_join_kernel, dim3((unsigned)ceil_div(cols, 32), 2), dim3(JOIN_THR), 0, stream,
+                       a.part, a.strips, a.cols, dgamma, dbeta);
   // last: dx may take the place of x or dy
-  if (dx) PBS_NORM_LAUNCH(layernorm_dx_wide_kernel, dim3((unsigned)std::min<int64_t>(rows, 2048)), WIDE_THR, a);
+  if (!f.tpr && dx)
+    PBS_NORM_LAUNCH(layernorm_dx_wide_kernel, dim3((unsigned)std::min<int64_t>(rows, 2048)), WIDE_THR, a);
   return check_launch("pbs_layernorm_grad");
 }
 

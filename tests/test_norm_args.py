@@ -49,7 +49,7 @@ def test_layernorm_refuses(status, change):
     (2, dict(rows=-1)), (2, dict(cols=0)), (2, dict(lddy=63)), (2, dict(ldx=1)), (2, dict(lddx=63)),
     (1, dict(dy=None)), (1, dict(x=None)), (1, dict(mean=None)), (1, dict(rstd=None)),
     (1, dict(dy=FAKE + 1)), (1, dict(dx=FAKE + 1)), (1, dict(dgamma=FAKE + 2)), (1, dict(dbeta=FAKE + 2)),
-    (1, dict(ws=None)), (1, dict(ws=FAKE + 8)), (1, dict(n=0)), (1, dict(n=4 * 2 * 64 * 4 - 1))])
+    (1, dict(ws=None)), (1, dict(ws=FAKE + 8)), (1, dict(n=0)), (1, dict(n=2 * 64 * 4 - 1))])
 def test_layernorm_grad_refuses(status, change):
     _expect(status, P.pbs_layernorm_grad, *grad(**change))
 
