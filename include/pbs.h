@@ -419,7 +419,7 @@ pbs_status pbs_layernorm_grad(const void* dy, pbs_format y_fmt, int64_t lddy, co
  *  is rounded to bf16 for the two products; all sums are fp32.
  *
  *  workspace: the bytes that pbs_linear_loss_bytes gives for the same tokens,
- *    vocab, hidden, top (1 for cross entropy) and piece, 256-byte aligned.
+ *    vocab, hidden, top (0 for cross entropy) and piece, 256-byte aligned.
  *    Its contents are of no use afterwards; calls that may run at the same
  *    time need one each.
  *  Shapes (else PBS_ERR_SHAPE): hidden a multiple of 64 up to 65536, vocab 1

@@ -213,7 +213,7 @@ def pbs_layernorm_grad(dy, y_fmt, lddy, x, x_fmt, ldx, rows, cols, gamma, w_fmt,
                                     _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
-def pbs_linear_loss_bytes(tokens, vocab, hidden, top=1, piece=0):
+def pbs_linear_loss_bytes(tokens, vocab, hidden, top=0, piece=0):
     a, b = _c.c_size_t(0), _c.c_size_t(0)
     _check(lib().pbs_linear_loss_bytes(tokens, vocab, hidden, top, piece, _c.byref(a), _c.byref(b)))
     return a.value, b.value

@@ -39,23 +39,23 @@ struct HeadArgs {
   const uint8_t* x;        // [tokens, hidden]
   const uint8_t* xc;       // the live tokens' rows, used when not all are live
   const uint8_t* w;        // first row of this piece of W
-  const int* n_live;
+  const int* live;         // {live rows, splits of dx, splits of dW}
   const int* row_of;       // live row -> token
-  const int* state;        // per token: ROW_*
-  const int* ids;          // [tokens][slots]: vocabulary ids, -1 unused
-  const float* p;          // [tokens][slots]
+  const int64_t* targets;  // cross entropy: the token's one slot, p = 1; else null and
+  const int* state;        //   per token: ROW_*
+  const int* ids;          //   [tokens][slots]: vocabulary ids, -1 unused
+  const float* p;          //   [tokens][slots]
   float* zsel;             // [tokens][slots]: the slots' logits / tau
-  float* pm;               // [parts][rows]: maximum of a part of a row
-  float* ps;               // [parts][rows]: sum of exponentials above it
+  float2* stats;           // [parts][rows]: maximum of a part of a row, sum of exponentials above it
   const float* lse;        // per token
   const float* dloss;      // per token
   uint16_t* dz;            // [rows][dz_ld]
-  void* out;               // dx partials (fp32 [split][rows][hidden]) / dW, or its partials
-  int64_t out_split;       // elements between the partials of two splits
+  float* part;             // partial products of dx, or of dW
+  void* dw;                // this piece of dW
   int tokens, rows, hidden, slots;   // rows: tokens, rounded up to whole tiles
   int v0, nv;              // this piece: first id, ids in it
   int dz_ld;
-  int splits;
+  int vocab;
   int add;                 // the product is added to out
   int out_bf16;
   float inv_tau;
@@ -209,21 +209,21 @@ __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(H
   const int t = threadIdx.x, lane = t & 63;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = w >> 1, wn = w & 1;
-  const int n = *g.n_live;
+  const int n = g.live[0], splits = EPI <= EPI_DZ ? 1 : g.live[EPI == EPI_DX ? 1 : 2];
   const uint8_t* xs = n == g.tokens ? g.x : g.xc;
   const int64_t ldx = (int64_t)g.hidden * 2, ldz = (int64_t)g.dz_ld * 2;
   const int M = EPI == EPI_DW ? g.nv : n;
   const int N = EPI <= EPI_DZ ? g.nv : g.hidden;
   const int nk = EPI <= EPI_DZ ? g.hidden / 64 : ((EPI == EPI_DX ? g.nv : n) + 63) / 64;
   const int tiles_m = (M + M_T - 1) / M_T, tiles_n = (N + N_T - 1) / N_T;
-  const int tiles = tiles_m * tiles_n * g.splits;
+  const int tiles = tiles_m * tiles_n * splits;
   if ((int)blockIdx.x >= tiles) return;
   int tm, tn;
-  tile_of(blockIdx.x, tiles_m, tiles_n * g.splits, tm, tn);
+  tile_of(blockIdx.x, tiles_m, tiles_n * splits, tm, tn);
   const int split = tn / tiles_n;
   tn -= split * tiles_n;
   const int m0 = tm * M_T, n0 = tn * N_T;
-  const int k0 = (int)((int64_t)nk * split / g.splits), k1 = (int)((int64_t)nk * (split + 1) / g.splits);
+  const int k0 = (int)((int64_t)nk * split / splits), k1 = (int)((int64_t)nk * (split + 1) / splits);
 
   auto tileA = [&](int buf) { return smem + buf * (tile_bytes<TI>() + tile_bytes<TJ>()); };
   auto tileB = [&](int buf) { return tileA(buf) + tile_bytes<TI>(); };
@@ -353,7 +353,8 @@ __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(H
       if (m0 + r < n) {
         const int tok = g.row_of[m0 + r];
         e.x = g.lse[tok];
-        e.y = g.state[tok] == ROW_BAD ? __builtin_nanf("") : g.dloss[tok] * g.inv_tau;
+        const bool bad = g.targets ? g.targets[tok] >= g.vocab : g.state[tok] == ROW_BAD;
+        e.y = bad ? __builtin_nanf("") : g.dloss[tok] * g.inv_tau;
       }
       table[r] = e;
     }
@@ -406,24 +407,29 @@ __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(H
           sum = sum * head_exp(mx - safe) + add;
           mx = m1;
         }
-        const int64_t at = (int64_t)(tn * PARTS + part) * g.rows + row;
-        g.pm[at] = mx;
-        g.ps[at] = sum;
+        g.stats[(int64_t)(tn * PARTS + part) * g.rows + row] = make_float2(mx, sum);
       }
       if (tok >= 0) {
-        const int first = g.v0 + n0 + part * PW;
-        const int4* ids = (const int4*)(g.ids + (int64_t)tok * g.slots);
-        for (int q = 0; q < g.slots / 4; ++q) {
-          const int4 id4 = ids[q];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int id = u == 0 ? id4.x : u == 1 ? id4.y : u == 2 ? id4.z : id4.w;
-            const int c = id - first;
-            if (id >= 0 && c >= 0 && c < PW && c < have) {
-              const int64_t at = (int64_t)tok * g.slots + 4 * q + u;
-              if (EPI == EPI_STATS) g.zsel[at] = mine[c];
-              else mine[c] -= g.p[at] * table[tile_row(p, s)].y;
-            }
+        // the token's slots that lie in this part
+        const int64_t first = g.v0 + n0 + part * PW;
+        const int mineN = have < PW ? have : PW;
+        auto slot = [&](int64_t id, int64_t at, bool one) {
+          const int64_t c = id - first;
+          if (id < 0 || c < 0 || c >= mineN) return;
+          if (EPI == EPI_STATS) g.zsel[at] = mine[c];
+          else mine[c] -= one ? table[tile_row(p, s)].y : g.p[at] * table[tile_row(p, s)].y;
+        };
+        if (g.targets) {
+          slot(g.targets[tok], tok, true);
+        } else {
+          const int64_t at = (int64_t)tok * g.slots;
+          const int4* ids = (const int4*)(g.ids + at);
+          for (int q = 0; q < g.slots / 4; ++q) {
+            const int4 id4 = ids[q];
+            slot(id4.x, at + 4 * q, false);
+            slot(id4.y, at + 4 * q + 1, false);
+            slot(id4.z, at + 4 * q + 2, false);
+            slot(id4.w, at + 4 * q + 3, false);
           }
         }
       }
@@ -449,13 +455,16 @@ __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(H
         float4 lo = *(const float4*)q, hi = *(const float4*)(q + 4);
         const int row = m0 + tile_row(p, s);
         if (row < M && col < N) {
-          const int64_t at = (int64_t)split * g.out_split + (int64_t)row * g.hidden + col;
-          if (g.out_bf16) {
-            *(uint4*)((uint16_t*)g.out + at) =
+          // dx partials: the splits' live rows, in whole tiles, one after the other; dW itself, or its partials
+          const int64_t at = (int64_t)split * (EPI == EPI_DX ? tiles_m * M_T : g.dz_ld) * g.hidden +
+                             (int64_t)row * g.hidden + col;
+          void* out = EPI == EPI_DW && splits == 1 ? g.dw : g.part;
+          if (EPI == EPI_DW && splits == 1 && g.out_bf16) {
+            *(uint4*)((uint16_t*)out + at) =
                 make_uint4(pk_bf16(lo.x, lo.y), pk_bf16(lo.z, lo.w), pk_bf16(hi.x, hi.y), pk_bf16(hi.z, hi.w));
           } else {
-            float4* o = (float4*)((float*)g.out + at);
-            if (g.add) {
+            float4* o = (float4*)((float*)out + at);
+            if (EPI == EPI_DX && g.add) {
               const float4 u = o[0], v = o[1];
               lo = make_float4(lo.x + u.x, lo.y + u.y, lo.z + u.z, lo.w + u.w);
               hi = make_float4(hi.x + v.x, hi.y + v.y, hi.z + v.z, hi.w + v.w);
@@ -549,90 +558,99 @@ __global__ __launch_bounds__(256) void head_teacher_kernel(TeacherArgs a) {
   }
 }
 
+// Splits of a product's K loop over nk stages when its tiles alone leave
+// workgroup slots idle: the number that minimises rounds of tiles times
+// (stages + a tile's fixed cost) plus the partial products' traffic, all in
+// stages.  Never more than 2 x 256 tiles' worth of partial products.
+constexpr int HEAD_FIXED = 6, HEAD_LEAST_STAGES = 8, HEAD_MOST_SPLITS = 16, HEAD_SPLIT_TILES = 512;
+__host__ __device__ inline int head_splits(int64_t tiles, int64_t nk, int slots) {
+  int best = 1;
+  int64_t cost = 0;
+  for (int s = 1; s <= HEAD_MOST_SPLITS && (s == 1 || (nk / s >= HEAD_LEAST_STAGES && tiles * s <= HEAD_SPLIT_TILES)); ++s) {
+    const int64_t c = (tiles * s + slots - 1) / slots * ((nk + s - 1) / s + HEAD_FIXED) + (s > 1 ? tiles * s / 23 : 0);
+    if (s == 1 || c < cost) {
+      best = s;
+      cost = c;
+    }
+  }
+  return best;
+}
+
 struct RowsArgs {
-  const int64_t* targets;  // cross entropy; null: state is set already
-  int tokens, vocab, slots;
-  int* n_live;
+  const int64_t* targets;  // cross entropy; null: state is set
+  const int* state;
+  int tokens;
+  int* live;               // out: {live rows, splits of dx, splits of dW}
   int* row_of;
   int* pos_of;             // token -> live row, or -1
-  int* state;
-  int* ids32;
-  float* p;
-  float* ent;
   float* loss;             // of the tokens that take no part: 0 (null in the gradient)
   float* lse;
+  int tile_m, dx_tn, dx_nk, dw_tiles, slots;     // the gradient's products, for their splits
 };
 
-// The live tokens in order, by one workgroup: 8 tokens a thread and step.
+// The live tokens in order, by one workgroup: a wave takes 8 x 64 consecutive
+// tokens a step, ranks them by ballots, and the waves' counts are added up in LDS.
 constexpr int ROWS_THR = 1024, ROWS_PER = 8;
 __global__ __launch_bounds__(ROWS_THR) void head_rows_kernel(RowsArgs a) {
-  __shared__ int wave_n[ROWS_THR / 64];
+  __shared__ int wave_n[2][ROWS_THR / 64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  int base = 0;
-  for (int64_t t0 = 0; t0 < a.tokens; t0 += ROWS_THR * ROWS_PER) {
-    const int64_t first = t0 + (int64_t)threadIdx.x * ROWS_PER;
-    int st[ROWS_PER];
+  int base = 0, buf = 0;
+  for (int64_t t0 = 0; t0 < a.tokens; t0 += ROWS_THR * ROWS_PER, buf ^= 1) {
+    const int64_t first = t0 + w * 64 * ROWS_PER + lane;
+    bool on[ROWS_PER];
+#pragma unroll
+    for (int i = 0; i < ROWS_PER; ++i) {
+      const int64_t t = first + 64 * i;
+      on[i] = t < a.tokens && (a.targets ? a.targets[t] >= 0 : a.state[t] != ROW_OUT);
+    }
+    uint64_t mask[ROWS_PER];
     int mine = 0;
 #pragma unroll
     for (int i = 0; i < ROWS_PER; ++i) {
-      const int64_t t = first + i;
-      st[i] = ROW_OUT;
-      if (t < a.tokens) {
-        if (a.targets) {
-          const int64_t y = a.targets[t];
-          st[i] = y < 0 ? ROW_OUT : y < a.vocab ? ROW_LIVE : ROW_BAD;
-          a.state[t] = st[i];
-          *(int4*)(a.ids32 + 4 * t) = make_int4(st[i] == ROW_LIVE ? (int)y : -1, -1, -1, -1);
-          *(float4*)(a.p + 4 * t) = make_float4(1.0f, 0.0f, 0.0f, 0.0f);
-          a.ent[t] = 0.0f;
-        } else {
-          st[i] = a.state[t];
-        }
-      }
-      mine += st[i] != ROW_OUT;
+      mask[i] = __ballot(on[i]);
+      mine += __popcll(mask[i]);
     }
-    int before = mine;                       // inclusive scan over the wave
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(before, o, 64);
-      if (lane >= o) before += v;
-    }
-    if (lane == 63) wave_n[w] = before;
+    if (lane == 0) wave_n[buf][w] = mine;
     __syncthreads();
-    int at = base + before - mine, all = 0;
+    int at = base;
 #pragma unroll
     for (int i = 0; i < ROWS_THR / 64; ++i) {
-      if (i < w) at += wave_n[i];
-      all += wave_n[i];
+      const int c = wave_n[buf][i];
+      at += i < w ? c : 0;
+      base += c;
     }
-    base += all;
 #pragma unroll
     for (int i = 0; i < ROWS_PER; ++i) {
-      const int64_t t = first + i;
-      if (t >= a.tokens) break;
-      if (st[i] != ROW_OUT) {
-        a.row_of[at] = (int)t;
-        a.pos_of[t] = at++;
-      } else {
-        a.pos_of[t] = -1;
-        if (a.loss) {
-          a.loss[t] = 0.0f;
-          a.lse[t] = 0.0f;
-        }
+      const int64_t t = first + 64 * i;
+      const int pos = at + __popcll(mask[i] & ((1ull << lane) - 1));
+      at += __popcll(mask[i]);
+      if (t >= a.tokens) continue;
+      a.pos_of[t] = on[i] ? pos : -1;
+      if (on[i]) a.row_of[pos] = (int)t;
+      if (!on[i] && a.loss) {
+        a.loss[t] = 0.0f;
+        a.lse[t] = 0.0f;
       }
     }
-    __syncthreads();
   }
-  if (threadIdx.x == 0) *a.n_live = base;
+  if (threadIdx.x == 0) {
+    a.live[0] = base;
+    if (!a.loss) {
+      a.live[1] = head_splits((int64_t)((base + a.tile_m - 1) / a.tile_m) * a.dx_tn, a.dx_nk, a.slots);
+      a.live[2] = head_splits(a.dw_tiles, (base + 63) / 64, a.slots);
+    }
+  }
 }
 
 // The live rows of x, one after the other: a wave per row.  Nothing to do when
 // every token is live (the products then read x itself).
-__global__ __launch_bounds__(256) void head_gather_kernel(const uint4* x, uint4* xc, const int* n_live,
-                                                          const int* row_of, int tokens, int chunks) {
-  const int n = *n_live;
+constexpr int GATHER_THR = 512;
+__global__ __launch_bounds__(GATHER_THR) void head_gather_kernel(const uint4* x, uint4* xc, const int* live,
+                                                                 const int* row_of, int tokens, int chunks) {
+  constexpr int PER = GATHER_THR / 64;
+  const int n = *live;
   if (n == tokens) return;
-  for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); i < n; i += (int64_t)gridDim.x * 4) {
+  for (int64_t i = (int64_t)blockIdx.x * PER + (threadIdx.x >> 6); i < n; i += (int64_t)gridDim.x * PER) {
     const uint4* from = x + (int64_t)row_of[i] * chunks;
     uint4* to = xc + i * chunks;
     for (int c = threadIdx.x & 63; c < chunks; c += 64) to[c] = from[c];
@@ -640,62 +658,87 @@ __global__ __launch_bounds__(256) void head_gather_kernel(const uint4* x, uint4*
 }
 
 struct JoinArgs {
-  const int* n_live;
+  const int* live;
   const int* row_of;
+  const int64_t* targets;  // cross entropy, or null and
   const int* state;
   const int* ids;
   const float* p;
   const float* ent;
   const float* zsel;
-  const float* pm;
-  const float* ps;
-  int parts, rows, slots;
+  const float2* stats;
+  int parts, rows, slots, vocab;
   float* loss;
   float* lse;
 };
 
-// lse and loss of 32 live rows: 8 threads a row share its parts.
-__global__ __launch_bounds__(256) void head_join_kernel(JoinArgs a) {
-  __shared__ float sm[8][32], ss[8][32];
-  const int r = threadIdx.x & 31, q = threadIdx.x >> 5;
-  const int row = blockIdx.x * 32 + r;
-  const bool ok = row < *a.n_live;
+// lse and loss of 32 live rows: 32 threads a row share its parts, then its slots.
+constexpr int JOIN_ROWS = 32, JOIN_Q = 32;
+__global__ __launch_bounds__(JOIN_ROWS * JOIN_Q) void head_join_kernel(JoinArgs a) {
+  __shared__ float2 sm[JOIN_Q][JOIN_ROWS + 1];
+  const int r = threadIdx.x % JOIN_ROWS, q = threadIdx.x / JOIN_ROWS;
+  const int row = blockIdx.x * JOIN_ROWS + r;
+  const int n = a.live[0];
+  if ((int)blockIdx.x * JOIN_ROWS >= n) return;
+  const bool ok = row < n;
   const float none = -__builtin_inff();
-  float mx = none, sum = 0.0f;
+  float2 u = make_float2(none, 0.0f);
+  auto add = [&](float2 v) {
+    const float m1 = fmaxf(u.x, v.x), safe = m1 == none ? 0.0f : m1;
+    u = make_float2(m1, u.y * head_exp(u.x - safe) + v.y * head_exp(v.x - safe));
+  };
   if (ok) {
-    for (int i = q; i < a.parts; i += 8) {
-      const float m = a.pm[(int64_t)i * a.rows + row], s = a.ps[(int64_t)i * a.rows + row];
-      const float m1 = fmaxf(mx, m), safe = m1 == none ? 0.0f : m1;
-      sum = sum * expf(mx - safe) + s * expf(m - safe);
-      mx = m1;
+    const float2* st = a.stats + row;
+    int i = q;
+    for (; i + 3 * JOIN_Q < a.parts; i += 4 * JOIN_Q) {
+      const float2 v0 = st[(int64_t)i * a.rows], v1 = st[(int64_t)(i + JOIN_Q) * a.rows];
+      const float2 v2 = st[(int64_t)(i + 2 * JOIN_Q) * a.rows], v3 = st[(int64_t)(i + 3 * JOIN_Q) * a.rows];
+      const float m1 = fmaxf(fmaxf(u.x, fmaxf(v0.x, v1.x)), fmaxf(v2.x, v3.x)), safe = m1 == none ? 0.0f : m1;
+      u = make_float2(m1, (u.y * head_exp(u.x - safe) + v0.y * head_exp(v0.x - safe)) +
+                              (v1.y * head_exp(v1.x - safe) + v2.y * head_exp(v2.x - safe)) +
+                              v3.y * head_exp(v3.x - safe));
+    }
+    for (; i < a.parts; i += JOIN_Q) add(st[(int64_t)i * a.rows]);
+  }
+  sm[q][r] = u;
+  __syncthreads();
+  // every thread of the row joins the 32 sums, in the same order
+  u = sm[0][r];
+#pragma unroll 4
+  for (int i = 1; i < JOIN_Q; ++i) add(sm[i][r]);
+  const float lse = u.x + head_log(u.y);
+  const int tok = ok ? a.row_of[row] : 0;
+  if (a.targets) {
+    if (q == 0 && ok) {
+      a.lse[tok] = lse;
+      a.loss[tok] = a.targets[tok] >= a.vocab ? __builtin_nanf("") : lse - a.zsel[tok];
+    }
+    return;
+  }
+  float loss = 0.0f;
+  if (ok) {
+    const int64_t at = (int64_t)tok * a.slots;
+    for (int s = q; s < a.slots; s += JOIN_Q) {
+      const float p = a.p[at + s];
+      if (a.ids[at + s] >= 0 && !(p == 0.0f)) loss -= p * (a.zsel[at + s] - lse);
     }
   }
-  sm[q][r] = mx;
-  ss[q][r] = sum;
+  __syncthreads();
+  sm[q][r].x = loss;
   __syncthreads();
   if (q != 0 || !ok) return;
-  for (int i = 1; i < 8; ++i) {
-    const float m = sm[i][r], m1 = fmaxf(mx, m), safe = m1 == none ? 0.0f : m1;
-    sum = sum * expf(mx - safe) + ss[i][r] * expf(m - safe);
-    mx = m1;
-  }
-  const int tok = a.row_of[row];
-  const float lse = mx + logf(sum);
-  float loss = a.ent[tok];
-  const int64_t at = (int64_t)tok * a.slots;
-  for (int s = 0; s < a.slots; ++s) {
-    const float p = a.p[at + s];
-    if (a.ids[at + s] >= 0 && !(p == 0.0f)) loss -= p * (a.zsel[at + s] - lse);
-  }
+  for (int i = 1; i < JOIN_Q; ++i) loss += sm[i][r].x;
   a.lse[tok] = lse;
-  a.loss[tok] = a.state[tok] == ROW_BAD ? __builtin_nanf("") : loss;
+  a.loss[tok] = a.state[tok] == ROW_BAD ? __builtin_nanf("") : loss + a.ent[tok];
 }
 
 // dx [tokens, hidden] bf16 from the partial products of the live rows; zeros
 // for the tokens that take no part.  8 values a thread.
-__global__ __launch_bounds__(256) void head_dx_kernel(const float* part, int splits, int64_t split_stride,
+__global__ __launch_bounds__(256) void head_dx_kernel(const float* part, const int* live, int tile_m, int hidden,
                                                       const int* pos_of, int64_t chunks8, int per_row,
                                                       uint16_t* dx) {
+  const int splits = live[1];
+  const int64_t split_stride = (int64_t)((live[0] + tile_m - 1) / tile_m) * tile_m * hidden;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < chunks8; i += (int64_t)gridDim.x * 256) {
     const int64_t tok = i / per_row;
     const int c = (int)(i - tok * per_row);
@@ -714,8 +757,10 @@ __global__ __launch_bounds__(256) void head_dx_kernel(const float* part, int spl
 }
 
 // dW of a piece from its splits' partial products.
-__global__ __launch_bounds__(256) void head_dw_kernel(const float* part, int splits, int64_t split_stride,
+__global__ __launch_bounds__(256) void head_dw_kernel(const float* part, const int* live, int64_t split_stride,
                                                       int64_t chunks8, void* dw, int bf16) {
+  const int splits = live[2];
+  if (splits == 1) return;                     // the product stored dW itself
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < chunks8; i += (int64_t)gridDim.x * 256) {
     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     const float* q = part + i * 8;
@@ -742,35 +787,24 @@ __global__ void head_zero_kernel(uint4* p, int64_t n16) {
 // ---------------------------------------------------------------------------
 // Host side: the workspace's layout and the calls.
 // ---------------------------------------------------------------------------
-constexpr int HEAD_TM = 256, HEAD_TN = 256;
-constexpr int HEAD_CUS = 256;
-
-// Splits of a product's K loop over nk stages when its tiles alone leave
-// compute units idle: the number that minimises rounds of tiles times (stages
-// + a tile's fixed cost, in stages).
-static int head_splits(int64_t tiles, int64_t nk) {
-  constexpr int FIXED = 6, MOST = 16;
-  int best = 1;
-  int64_t cost = 0;
-  for (int s = 1; s <= MOST && (s == 1 || nk / s >= 8); ++s) {
-    const int64_t c = ceil_div(tiles * s, HEAD_CUS) * (ceil_div(nk, s) + FIXED);
-    if (s == 1 || c < cost) {
-      best = s;
-      cost = c;
-    }
-  }
-  return best;
-}
+// Tiles: 256 x 256, one workgroup per compute unit, or 128 x 128, two.
+constexpr int HEAD_TILE = 256, HEAD_SMALL = 128, HEAD_CUS = 256;
 
 struct HeadPlan {
-  int64_t rows, slots, parts, piece, dz_ld;
-  int dx_splits, dw_splits;
-  size_t n_live, row_of, pos_of, state, ids, p, ent, xc;
-  size_t zsel, pm, ps, loss_bytes;                       // the loss
+  int64_t rows, slots, parts, piece;
+  int loss_tile, grad_tile, wg_slots;                    // the gradient's workgroups at a time
+  int64_t dx_grid, dw_grid;                              // most tiles, splits included
+  bool dw_can_split;
+  size_t live, row_of, pos_of, state, ids, p, ent, xc;
+  size_t zsel, stats, loss_bytes;                        // the loss
   size_t dz, dxp, dwp, grad_bytes;                       // the gradient
 };
 
-static HeadPlan head_plan(int64_t tokens, int64_t vocab, int64_t hidden, int64_t top, int64_t piece) {
+// The tile of products whose 256 x 256 tiles are `tiles`: while these leave
+// most compute units idle, four times as many small ones.
+static int head_tile(int64_t tiles) { return tiles < HEAD_CUS ? HEAD_SMALL : HEAD_TILE; }
+
+static HeadPlan head_plan(int64_t tokens, int64_t vocab, int64_t hidden, int64_t top, bool xent, int64_t piece) {
   HeadPlan h = {};
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -778,44 +812,51 @@ static HeadPlan head_plan(int64_t tokens, int64_t vocab, int64_t hidden, int64_t
     at += (bytes + 255) / 256 * 256;
     return here;
   };
-  h.rows = ceil_div(tokens, HEAD_TM) * HEAD_TM;
-  h.slots = ceil_div(top, 4) * 4;
-  h.parts = ceil_div(vocab, HEAD_TN) * 2;
-  h.n_live = take(4);
+  const int64_t tm = ceil_div(tokens, HEAD_TILE), tv = ceil_div(vocab, HEAD_TILE), th = ceil_div(hidden, HEAD_TILE);
+  h.rows = tm * HEAD_TILE;
+  h.slots = xent ? 1 : ceil_div(top, 4) * 4;
+  h.loss_tile = head_tile(tm * tv);
+  h.parts = ceil_div(vocab, h.loss_tile) * 2;
+  h.live = take(12);
   h.row_of = take(4 * tokens);
   h.pos_of = take(4 * tokens);
-  h.state = take(4 * tokens);
-  h.ids = take(4 * tokens * h.slots);
-  h.p = take(4 * tokens * h.slots);
-  h.ent = take(4 * tokens);
+  h.state = take(xent ? 0 : 4 * tokens);
+  h.ids = take(xent ? 0 : 4 * tokens * h.slots);
+  h.p = take(xent ? 0 : 4 * tokens * h.slots);
+  h.ent = take(xent ? 0 : 4 * tokens);
   h.xc = take(2 * tokens * hidden);
   const size_t shared = at;
   h.zsel = take(4 * tokens * h.slots);
-  h.pm = take(4 * h.parts * h.rows);
-  h.ps = take(4 * h.parts * h.rows);
+  h.stats = take(8 * h.parts * h.rows);
   h.loss_bytes = at;
   at = shared;
   // default piece: dz of a piece at most 1 GiB, and at least 2048 ids
   if (piece <= 0) piece = std::max<int64_t>(2048, (1ll << 30) / (2 * std::max<int64_t>(h.rows, 1)));
-  h.piece = std::min(ceil_div(piece, HEAD_TN), ceil_div(std::max<int64_t>(vocab, 1), HEAD_TN)) * HEAD_TN;
-  h.dz_ld = h.piece;
-  const int64_t tn = ceil_div(hidden, HEAD_TN);
-  h.dx_splits = head_splits(h.rows / HEAD_TM * tn, h.piece / 64);
-  h.dw_splits = head_splits(h.piece / HEAD_TM * tn, ceil_div(tokens, 64));
-  h.dz = take(2 * h.rows * h.dz_ld);
-  h.dxp = take((size_t)4 * h.dx_splits * h.rows * hidden);
-  h.dwp = h.dw_splits > 1 ? take((size_t)4 * h.dw_splits * h.piece * hidden) : at;
+  h.piece = std::min(ceil_div(piece, HEAD_TILE), tv) * HEAD_TILE;
+  h.grad_tile = head_tile(tm * (h.piece / HEAD_TILE));
+  h.wg_slots = h.grad_tile == HEAD_TILE ? HEAD_CUS : 2 * HEAD_CUS;
+  const int64_t hn = ceil_div(hidden, h.grad_tile);
+  h.dx_grid = std::max<int64_t>(ceil_div(tokens, h.grad_tile) * hn, HEAD_SPLIT_TILES);
+  h.dw_grid = std::max<int64_t>(h.piece / h.grad_tile * hn, HEAD_SPLIT_TILES);
+  h.dz = take(2 * h.rows * h.piece);
+  // partial products: the tiles of one product, or of all splits of one that is split
+  const int64_t tile_values = (int64_t)h.grad_tile * hidden;
+  h.dxp = take(4 * tile_values * std::max(ceil_div(tokens, h.grad_tile), HEAD_SPLIT_TILES / hn));
+  // as head_splits decides for any number of live rows
+  h.dw_can_split = h.piece / h.grad_tile * hn * 2 <= HEAD_SPLIT_TILES && ceil_div(tokens, 64) / 2 >= HEAD_LEAST_STAGES;
+  h.dwp = take(h.dw_can_split ? 4 * tile_values * (HEAD_SPLIT_TILES / hn) : 0);
   h.grad_bytes = at;
   return h;
 }
 
+// top: 0 for cross entropy
 static pbs_status head_check_dims(const char* what, int64_t tokens, int64_t vocab, int64_t hidden, int64_t top) {
   PBS_REQUIRE(tokens >= 0 && tokens <= (1 << 24) && vocab >= 1 && vocab <= (1 << 22), PBS_ERR_SHAPE,
               "%s: needs tokens in [0, 2^24] and vocab in [1, 2^22] (got %lld, %lld)", what, (long long)tokens,
               (long long)vocab);
   PBS_REQUIRE(hidden >= 64 && hidden % 64 == 0 && hidden <= (1 << 16), PBS_ERR_SHAPE,
               "%s: hidden must be a multiple of 64 in [64, 65536] (got %lld)", what, (long long)hidden);
-  PBS_REQUIRE(top >= 1 && top <= 1024, PBS_ERR_SHAPE, "%s: top must be in [1, 1024] (got %lld)", what, (long long)top);
+  PBS_REQUIRE(top >= 0 && top <= 1024, PBS_ERR_SHAPE, "%s: top must be in [1, 1024] (got %lld)", what, (long long)top);
   PBS_REQUIRE(ceil_div(tokens, 64) * ceil_div(vocab, 64) < (1ll << 31) / 16, PBS_ERR_SHAPE,
               "%s: tokens x vocab is too large for one call", what);
   return PBS_OK;
@@ -823,6 +864,7 @@ static pbs_status head_check_dims(const char* what, int64_t tokens, int64_t voca
 
 struct HeadCall {
   const char* what;
+  bool xent;
   const void* x;
   const void* w;
   int64_t tokens, vocab, hidden;
@@ -848,9 +890,10 @@ static bool off_by(const void* p, int bytes) { return ((uintptr_t)p & (bytes - 1
 static pbs_status head_check(const HeadCall& c, bool grad, HeadPlan* plan) {
   const pbs_status st = head_check_dims(c.what, c.tokens, c.vocab, c.hidden, c.top);
   if (st != PBS_OK) return st;
+  PBS_REQUIRE(c.xent || c.top >= 1, PBS_ERR_SHAPE, "%s: top must be in [1, 1024] (got 0)", c.what);
   PBS_REQUIRE(c.tau > 0.0f && c.tau <= 1e30f && c.tau >= 1e-30f, PBS_ERR_INVALID_ARG,
               "%s: temperature must be in [1e-30, 1e30]", c.what);
-  PBS_REQUIRE(c.targets || c.tokens == 0 || (c.top_ids && c.top_logits), PBS_ERR_INVALID_ARG,
+  PBS_REQUIRE(c.tokens == 0 || (c.xent ? c.targets != nullptr : c.top_ids && c.top_logits), PBS_ERR_INVALID_ARG,
               "%s: null targets", c.what);
   PBS_REQUIRE(!c.top_logits || c.top_fmt == PBS_FMT_F32 || c.top_fmt == PBS_FMT_BF16, PBS_ERR_UNSUPPORTED,
               "%s: teacher logits must be BF16 or F32", c.what);
@@ -873,7 +916,7 @@ static pbs_status head_check(const HeadCall& c, bool grad, HeadPlan* plan) {
   } else {
     PBS_REQUIRE(c.tokens == 0 || c.loss, PBS_ERR_INVALID_ARG, "%s: loss is null", c.what);
   }
-  *plan = head_plan(c.tokens, c.vocab, c.hidden, c.top, c.piece);
+  *plan = head_plan(c.tokens, c.vocab, c.hidden, c.top, c.xent, c.piece);
   const size_t need = grad ? plan->grad_bytes : plan->loss_bytes;
   PBS_REQUIRE(c.tokens == 0 || (c.ws && !off_by(c.ws, 256)), PBS_ERR_INVALID_ARG,
               "%s: the workspace is null or not 256-byte aligned", c.what);
@@ -885,7 +928,7 @@ static pbs_status head_check(const HeadCall& c, bool grad, HeadPlan* plan) {
 // The live rows, their slots, and the products' common arguments.
 static HeadArgs head_rows(const HeadCall& c, const HeadPlan& h, hipStream_t stream) {
   uint8_t* ws = (uint8_t*)c.ws;
-  if (!c.targets) {
+  if (!c.xent) {
     TeacherArgs a = {};
     a.ids = c.top_ids; a.logits = c.top_logits; a.bf16 = c.top_fmt == PBS_FMT_BF16;
     a.top = (int)c.top; a.slots = (int)h.slots; a.tokens = (int)c.tokens; a.vocab = (int)c.vocab;
@@ -895,20 +938,27 @@ static HeadArgs head_rows(const HeadCall& c, const HeadPlan& h, hipStream_t stre
     hipLaunchKernelGGL(head_teacher_kernel, dim3((unsigned)ceil_div(c.tokens, 4)), dim3(256), 0, stream, a);
   }
   RowsArgs r = {};
-  r.targets = c.targets; r.tokens = (int)c.tokens; r.vocab = (int)c.vocab; r.slots = (int)h.slots;
-  r.n_live = (int*)(ws + h.n_live); r.row_of = (int*)(ws + h.row_of); r.pos_of = (int*)(ws + h.pos_of);
-  r.state = (int*)(ws + h.state); r.ids32 = (int*)(ws + h.ids); r.p = (float*)(ws + h.p);
-  r.ent = (float*)(ws + h.ent); r.loss = c.loss; r.lse = c.loss ? c.lse : nullptr;
+  r.targets = c.targets; r.state = (const int*)(ws + h.state); r.tokens = (int)c.tokens;
+  r.live = (int*)(ws + h.live); r.row_of = (int*)(ws + h.row_of); r.pos_of = (int*)(ws + h.pos_of);
+  r.loss = c.loss; r.lse = c.loss ? c.lse : nullptr;
+  r.tile_m = h.grad_tile; r.dx_tn = (int)ceil_div(c.hidden, h.grad_tile); r.dx_nk = (int)(h.piece / 64);
+  r.dw_tiles = (int)(h.piece / h.grad_tile) * r.dx_tn; r.slots = h.wg_slots;
   hipLaunchKernelGGL(head_rows_kernel, dim3(1), dim3(ROWS_THR), 0, stream, r);
-  hipLaunchKernelGGL(head_gather_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(c.tokens, 4), 2048)), dim3(256), 0,
-                     stream, (const uint4*)c.x, (uint4*)(ws + h.xc), r.n_live, r.row_of, (int)c.tokens,
-                     (int)(c.hidden / 8));
+  hipLaunchKernelGGL(head_gather_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(c.tokens, GATHER_THR / 64), 512)),
+                     dim3(GATHER_THR), 0, stream, (const uint4*)c.x, (uint4*)(ws + h.xc), r.live, r.row_of,
+                     (int)c.tokens, (int)(c.hidden / 8));
   HeadArgs g = {};
-  g.x = (const uint8_t*)c.x; g.xc = ws + h.xc; g.w = (const uint8_t*)c.w;
-  g.n_live = r.n_live; g.row_of = r.row_of; g.state = r.state; g.ids = r.ids32; g.p = r.p;
-  g.tokens = (int)c.tokens; g.rows = (int)h.rows; g.hidden = (int)c.hidden; g.slots = (int)h.slots;
-  g.nv = (int)c.vocab; g.splits = 1; g.inv_tau = 1.0f / c.tau;
+  g.x = (const uint8_t*)c.x; g.xc = ws + h.xc; g.w = (const uint8_t*)c.w; g.targets = c.targets;
+  g.live = r.live; g.row_of = r.row_of; g.state = r.state; g.ids = (const int*)(ws + h.ids);
+  g.p = (const float*)(ws + h.p); g.tokens = (int)c.tokens; g.rows = (int)h.rows; g.hidden = (int)c.hidden;
+  g.slots = (int)h.slots; g.nv = g.vocab = (int)c.vocab; g.inv_tau = 1.0f / c.tau;
   return g;
+}
+
+template <int EPI>
+static void head_launch(int tile, int64_t grid, const HeadArgs& g, hipStream_t stream) {
+  hipLaunchKernelGGL((tile == HEAD_TILE ? head_product<4, 4, EPI>() : head_product<2, 2, EPI>()), dim3((unsigned)grid),
+                     dim3(256), 0, stream, g);
 }
 
 static pbs_status head_loss(const HeadCall& c, hipStream_t stream) {
@@ -917,16 +967,17 @@ static pbs_status head_loss(const HeadCall& c, hipStream_t stream) {
   if (st != PBS_OK || c.tokens == 0) return st;
   uint8_t* ws = (uint8_t*)c.ws;
   HeadArgs g = head_rows(c, h, stream);
-  g.zsel = (float*)(ws + h.zsel); g.pm = (float*)(ws + h.pm); g.ps = (float*)(ws + h.ps);
-  const int64_t grid = h.rows / HEAD_TM * ceil_div(c.vocab, HEAD_TN);
-  log_dispatch("%s tokens=%lld vocab=%lld hidden=%lld top=%lld tiles=%lld", c.what, (long long)c.tokens,
-               (long long)c.vocab, (long long)c.hidden, (long long)c.top, (long long)grid);
-  hipLaunchKernelGGL((head_product<4, 4, EPI_STATS>()), dim3((unsigned)grid), dim3(256), 0, stream, g);
+  g.zsel = (float*)(ws + h.zsel); g.stats = (float2*)(ws + h.stats);
+  const int64_t grid = ceil_div(c.tokens, h.loss_tile) * ceil_div(c.vocab, h.loss_tile);
+  log_dispatch("%s tokens=%lld vocab=%lld hidden=%lld top=%lld tile=%d tiles=%lld", c.what, (long long)c.tokens,
+               (long long)c.vocab, (long long)c.hidden, (long long)c.top, h.loss_tile, (long long)grid);
+  head_launch<EPI_STATS>(h.loss_tile, grid, g, stream);
   JoinArgs j = {};
-  j.n_live = g.n_live; j.row_of = g.row_of; j.state = g.state; j.ids = g.ids; j.p = g.p;
-  j.ent = (float*)(ws + h.ent); j.zsel = g.zsel; j.pm = g.pm; j.ps = g.ps;
-  j.parts = (int)h.parts; j.rows = g.rows; j.slots = g.slots; j.loss = c.loss; j.lse = c.lse;
-  hipLaunchKernelGGL(head_join_kernel, dim3((unsigned)ceil_div(c.tokens, 32)), dim3(256), 0, stream, j);
+  j.live = g.live; j.row_of = g.row_of; j.targets = g.targets; j.state = g.state; j.ids = g.ids; j.p = g.p;
+  j.ent = (const float*)(ws + h.ent); j.zsel = g.zsel; j.stats = g.stats;
+  j.parts = (int)h.parts; j.rows = g.rows; j.slots = g.slots; j.vocab = g.vocab; j.loss = c.loss; j.lse = c.lse;
+  hipLaunchKernelGGL(head_join_kernel, dim3((unsigned)ceil_div(c.tokens, JOIN_ROWS)), dim3(JOIN_ROWS * JOIN_Q), 0,
+                     stream, j);
   return check_launch(c.what);
 }
 
@@ -942,44 +993,33 @@ static pbs_status head_grad(const HeadCall& c, hipStream_t stream) {
   }
   uint8_t* ws = (uint8_t*)c.ws;
   HeadArgs g = head_rows(c, h, stream);
-  g.lse = c.lse; g.dloss = c.dloss; g.dz = (uint16_t*)(ws + h.dz); g.dz_ld = (int)h.dz_ld;
-  log_dispatch("%s tokens=%lld vocab=%lld hidden=%lld top=%lld piece=%lld splits=%d,%d", c.what, (long long)c.tokens,
-               (long long)c.vocab, (long long)c.hidden, (long long)c.top, (long long)h.piece, h.dx_splits, h.dw_splits);
-  const int64_t tm = h.rows / HEAD_TM, tn = ceil_div(c.hidden, HEAD_TN);
+  g.lse = c.lse; g.dloss = c.dloss; g.dz = (uint16_t*)(ws + h.dz); g.dz_ld = (int)h.piece; g.out_bf16 = dwb == 2;
+  log_dispatch("%s tokens=%lld vocab=%lld hidden=%lld top=%lld piece=%lld tile=%d", c.what, (long long)c.tokens,
+               (long long)c.vocab, (long long)c.hidden, (long long)c.top, (long long)h.piece, h.grad_tile);
   for (int64_t v0 = 0; v0 < c.vocab; v0 += h.piece) {
     const int64_t nv = std::min(h.piece, c.vocab - v0);
     g.v0 = (int)v0;
     g.nv = (int)nv;
     g.w = (const uint8_t*)c.w + v0 * c.hidden * 2;
-    g.splits = 1;
-    hipLaunchKernelGGL((head_product<4, 4, EPI_DZ>()), dim3((unsigned)(tm * ceil_div(nv, HEAD_TN))),
-                       dim3(256), 0, stream, g);
+    head_launch<EPI_DZ>(h.grad_tile, ceil_div(c.tokens, h.grad_tile) * ceil_div(nv, h.grad_tile), g, stream);
     if (c.dx) {
-      HeadArgs d = g;
-      d.out = ws + h.dxp; d.out_split = h.rows * c.hidden; d.splits = h.dx_splits; d.add = v0 > 0;
-      hipLaunchKernelGGL((head_product<4, 4, EPI_DX>()), dim3((unsigned)(tm * tn * d.splits)), dim3(256),
-                         0, stream, d);
+      g.part = (float*)(ws + h.dxp);
+      g.add = v0 > 0;
+      head_launch<EPI_DX>(h.grad_tile, h.dx_grid, g, stream);
     }
     if (c.dw) {
-      HeadArgs d = g;
-      uint8_t* to = (uint8_t*)c.dw + v0 * c.hidden * dwb;
-      d.splits = h.dw_splits;
-      if (d.splits == 1) {
-        d.out = to; d.out_bf16 = dwb == 2;
-      } else {
-        d.out = ws + h.dwp; d.out_split = h.piece * c.hidden;
-      }
-      hipLaunchKernelGGL((head_product<4, 4, EPI_DW>()),
-                         dim3((unsigned)(ceil_div(nv, HEAD_TM) * tn * d.splits)), dim3(256), 0, stream, d);
-      if (d.splits > 1)
-        hipLaunchKernelGGL(head_dw_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(nv * c.hidden / 8, 256), 4096)),
-                           dim3(256), 0, stream, (const float*)d.out, d.splits, d.out_split, nv * c.hidden / 8, to,
-                           (int)(dwb == 2));
+      g.part = (float*)(ws + h.dwp);
+      g.dw = (uint8_t*)c.dw + v0 * c.hidden * dwb;
+      head_launch<EPI_DW>(h.grad_tile, h.dw_grid, g, stream);
+      if (h.dw_can_split)
+        hipLaunchKernelGGL(head_dw_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(nv * c.hidden / 8, 256), 2048)),
+                           dim3(256), 0, stream, g.part, g.live, h.piece * c.hidden, nv * c.hidden / 8, g.dw,
+                           g.out_bf16);
     }
   }
   if (c.dx)
-    hipLaunchKernelGGL(head_dx_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(c.tokens * c.hidden / 8, 256), 4096)),
-                       dim3(256), 0, stream, (const float*)(ws + h.dxp), h.dx_splits, h.rows * c.hidden,
+    hipLaunchKernelGGL(head_dx_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(c.tokens * c.hidden / 8, 256), 2048)),
+                       dim3(256), 0, stream, (const float*)(ws + h.dxp), g.live, h.grad_tile, g.hidden,
                        (const int*)(ws + h.pos_of), c.tokens * c.hidden / 8, (int)(c.hidden / 8), (uint16_t*)c.dx);
   return check_launch(c.what);
 }
@@ -996,7 +1036,7 @@ pbs_status pbs_linear_loss_bytes(int64_t tokens, int64_t vocab, int64_t hidden, 
   const pbs_status st = head_check_dims("pbs_linear_loss_bytes", tokens, vocab, hidden, top);
   if (st != PBS_OK) return st;
   PBS_REQUIRE(piece >= 0, PBS_ERR_INVALID_ARG, "pbs_linear_loss_bytes: piece is negative");
-  const HeadPlan h = head_plan(tokens, vocab, hidden, top, piece);
+  const HeadPlan h = head_plan(tokens, vocab, hidden, top, top == 0, piece);
   *loss_bytes = h.loss_bytes;
   *grad_bytes = h.grad_bytes;
   return PBS_OK;
@@ -1007,7 +1047,7 @@ pbs_status pbs_linear_xent(const void* x, const void* w, int64_t tokens, int64_t
                            hipStream_t stream) {
   HeadCall c = {};
   c.what = "pbs_linear_xent"; c.x = x; c.w = w; c.tokens = tokens; c.vocab = vocab; c.hidden = hidden;
-  c.targets = targets; c.top = 1; c.tau = 1.0f; c.loss = loss; c.lse = lse; c.ws = workspace;
+  c.xent = true; c.targets = targets; c.tau = 1.0f; c.loss = loss; c.lse = lse; c.ws = workspace;
   c.ws_bytes = workspace_bytes;
   return head_loss(c, stream);
 }
@@ -1018,7 +1058,7 @@ pbs_status pbs_linear_xent_grad(const float* dloss, const void* x, const void* w
                                 hipStream_t stream) {
   HeadCall c = {};
   c.what = "pbs_linear_xent_grad"; c.x = x; c.w = w; c.tokens = tokens; c.vocab = vocab; c.hidden = hidden;
-  c.targets = targets; c.top = 1; c.tau = 1.0f; c.lse = (float*)lse; c.dloss = dloss; c.piece = piece; c.dx = dx;
+  c.xent = true; c.targets = targets; c.tau = 1.0f; c.lse = (float*)lse; c.dloss = dloss; c.piece = piece; c.dx = dx;
   c.dw = dw; c.dw_fmt = dw_fmt; c.ws = workspace; c.ws_bytes = workspace_bytes;
   return head_grad(c, stream);
 }

@@ -491,7 +491,7 @@ def linear_xent(x, w, targets, stream=None):
     _need(targets is not None, "targets are missing")
     _vector("targets", targets, T, (torch.int64,), x.device)
     with _on(x, stream):
-        loss, lse, ws, n = _loss_outputs(T, V, H, 1, x)
+        loss, lse, ws, n = _loss_outputs(T, V, H, 0, x)
         pbs_linear_xent(x, w, T, V, H, targets, loss, lse, ws, n)
     return loss, lse
 
@@ -507,7 +507,7 @@ def linear_xent_grad(dloss, x, w, targets, lse, piece=0, need_dx=True, need_dw=T
     _vector("dloss", dloss, T, (torch.float32,), x.device)
     _vector("lse", lse, T, (torch.float32,), x.device)
     with _on(x, stream):
-        dx, dw, ws, n = _grad_outputs(T, V, H, 1, piece, x, need_dx, need_dw, dw_dtype)
+        dx, dw, ws, n = _grad_outputs(T, V, H, 0, piece, x, need_dx, need_dw, dw_dtype)
         pbs_linear_xent_grad(dloss, x, w, T, V, H, targets, lse, piece, dx, dw, FMT_OF[dw_dtype], ws, n)
     return dx, dw
 

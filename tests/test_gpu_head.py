@@ -11,10 +11,12 @@ pytestmark = pytest.mark.gpu
 
 BF, F32 = torch.bfloat16, torch.float32
 # one token, one id, tile edges on either side, products whose K loop is split (few tokens against a long
-# vocabulary; a small vocabulary against many tokens), one to several stages of K
+# vocabulary; a small vocabulary against many tokens), one to several stages of K; the last three fill the GPU with
+# 256 x 256 tiles, the others take 128 x 128
 SHAPES = [(1, 1, 64), (1, 257, 64), (2, 256, 128), (37, 300, 64), (63, 1000, 192), (64, 64, 64), (65, 129, 128),
           (128, 128, 256), (255, 1000, 192), (256, 512, 64), (257, 513, 128), (300, 2003, 320), (513, 131, 64),
-          (70, 9001, 512), (2100, 300, 64), (1500, 17, 128)]
+          (70, 9001, 512), (2100, 300, 64), (1500, 17, 128),
+          (300, 33001, 192), (1100, 14001, 64), (4100, 4100, 128)]
 
 
 def make(T, V, H, seed=0, masked=0.0):
@@ -85,15 +87,16 @@ def test_distillation(T, V, H, k, tau, dtype):
     assert same(got, distill(x, w, ids, logits, tau, dloss))
 
 
-@pytest.mark.parametrize("piece", [1, 256, 700, 1024, 100000])
-def test_pieces_of_the_vocabulary(piece):
-    x, w, targets, dloss = make(300, 2003, 320, seed=8, masked=0.2)
+@pytest.mark.parametrize("T,V,H,piece", [(300, 2003, 320, 1), (300, 2003, 320, 256), (300, 2003, 320, 700),
+                                         (300, 2003, 320, 1024), (300, 2003, 320, 100000), (4200, 9000, 64, 4096)])
+def test_pieces_of_the_vocabulary(T, V, H, piece):
+    x, w, targets, dloss = make(T, V, H, seed=8, masked=0.2)
     want = head_ref(x.double(), w.double(), slots_of(targets), 1.0, dloss.double())
     for dtype in (BF, F32):
         got = xent(x, w, targets, dloss, piece=piece, dw_dtype=dtype)
         assert got["dw"].dtype == dtype
         check(got, want, dtype)
-    ids, logits = teacher(300, 2003, 9, targets)
+    ids, logits = teacher(T, V, 9, targets)
     want = head_ref(x.double(), w.double(), slots_of(None, ids, logits, 2.0), 2.0, dloss.double())
     check(distill(x, w, ids, logits, 2.0, dloss, piece=piece), want)
 

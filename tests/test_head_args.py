@@ -74,14 +74,14 @@ def test_distill_grad_refuses(status, change):
 
 @needs_lib
 def test_workspace_bytes():
-    for status, change in SIZES + [(2, dict(top=0)), (1, dict(piece=-5))]:
+    for status, change in SIZES + [(2, dict(top=-1)), (2, dict(top=1025)), (1, dict(piece=-5))]:
         a = args(change)
         refused(status, P.pbs_linear_loss_bytes, a["tokens"], a["vocab"], a["hidden"], a["top"], a["piece"])
     loss, grad = P.pbs_linear_loss_bytes(8192, 131072, 4096)
     # the loss keeps two numbers per 64 to 128 logits, and a gathered x
     assert loss < 8192 * 131072 * 8 / 64 + 2 * 8192 * 4096 + (1 << 20)
     # a piece of 4096 ids at a time: its dz, dx sums, a gathered x and what splits may take
-    small = P.pbs_linear_loss_bytes(8192, 131072, 4096, 1, 4096)[1]
+    small = P.pbs_linear_loss_bytes(8192, 131072, 4096, 0, 4096)[1]
     assert small < grad and small < 8192 * 4096 * (2 + 2 + 4 * 4)
     # one byte short is refused
     a = args(dict(n=P.pbs_linear_loss_bytes(8, 100, 64)[0] - 1))
