@@ -46,7 +46,7 @@ struct HeadArgs {
   const int* ids;          //   [tokens][slots]: vocabulary ids, -1 unused
   const float* p;          //   [tokens][slots]
   float* zsel;             // [tokens][slots]: the slots' logits / tau
-  float2* stats;           // [parts][rows]: maximum of a part of a row, sum of exponentials above it
+  float2* stats;           // [parts][rows]: maximum of a part of a row over log 2, sum of exponentials above it
   const float* lse;        // per token
   const float* dloss;      // per token
   uint16_t* dz;            // [rows][dz_ld]
@@ -64,11 +64,14 @@ struct HeadArgs {
 // Stage geometry for a tile of 64 TI x 64 TJ outputs: each of the 2 x 2 waves
 // holds TI x TJ 32 x 32 tiles.
 template <int T> constexpr int tile_bytes() { return 64 * T * ROWB; }
-constexpr int HEAD_PITCH_PAD = 4;                // floats: 16 rows of a 16-byte read cover every bank
-template <int TI, int TJ> constexpr int stage_rows() { return TI >= 2 ? 128 : 64; }
+// Staging of a result tile in LDS: fp32, 128 rows a pass, or bf16, all rows at
+// once.  16 bytes of padding a row: 16 lanes' 16-byte (32 lanes' 8-byte)
+// accesses to consecutive rows then cover every bank.
+constexpr int STAGE_ROWS = 128, STAGE_PAD = 16;
 template <int TI, int TJ> constexpr int head_smem() {
-  return cmax(2 * (tile_bytes<TI>() + tile_bytes<TJ>()),
-              stage_rows<TI, TJ>() * (64 * TJ + HEAD_PITCH_PAD) * 4 + 64 * TI * 8);
+  return cmax(cmax(2 * (tile_bytes<TI>() + tile_bytes<TJ>()),
+                   STAGE_ROWS * (64 * cmax(TI, TJ) * 4 + STAGE_PAD) + 64 * TJ * 4),
+              64 * TJ * (64 * TI * 2 + STAGE_PAD));
 }
 
 // `bytes` bytes from p as one buffer resource, and a 16-byte load from it to LDS.
@@ -188,8 +191,6 @@ __device__ __forceinline__ constexpr int part_hi(int n, int over, int m) { retur
 
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float LN2 = 0.69314718055994530942f;
-__device__ __forceinline__ float head_exp(float v) { return __builtin_amdgcn_exp2f(v * LOG2E); }
-__device__ __forceinline__ float head_log(float v) { return __builtin_amdgcn_logf(v) * LN2; }
 
 // ---------------------------------------------------------------------------
 // The product and its epilogues.
@@ -201,7 +202,7 @@ __device__ __forceinline__ float head_log(float v) { return __builtin_amdgcn_log
 // is read and the loads of stage kt + 2 are issued into the buffer that was
 // just read out.
 // ---------------------------------------------------------------------------
-template <int TI, int TJ, int LDA, int LDB, int EPI>
+template <int TI, int TJ, int LDA, int LDB, int EPI, bool MULTI>
 __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(HeadArgs g) {
   __shared__ __align__(16) uint8_t smem[head_smem<TI, TJ>()];
   constexpr int M_T = 64 * TI, N_T = 64 * TJ;
@@ -212,8 +213,11 @@ __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(H
   const int n = g.live[0], splits = EPI <= EPI_DZ ? 1 : g.live[EPI == EPI_DX ? 1 : 2];
   const uint8_t* xs = n == g.tokens ? g.x : g.xc;
   const int64_t ldx = (int64_t)g.hidden * 2, ldz = (int64_t)g.dz_ld * 2;
-  const int M = EPI == EPI_DW ? g.nv : n;
-  const int N = EPI <= EPI_DZ ? g.nv : g.hidden;
+  // the logits are formed transposed, vocabulary x tokens: a lane then holds
+  // 16 TI values of each of its TJ tokens, and a token's maximum, sum and
+  // gradient need no other lane but one
+  const int M = EPI == EPI_DX ? n : g.nv;
+  const int N = EPI <= EPI_DZ ? n : g.hidden;
   const int nk = EPI <= EPI_DZ ? g.hidden / 64 : ((EPI == EPI_DX ? g.nv : n) + 63) / 64;
   const int tiles_m = (M + M_T - 1) / M_T, tiles_n = (N + N_T - 1) / N_T;
   const int tiles = tiles_m * tiles_n * splits;
@@ -239,8 +243,8 @@ __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(H
   typename std::conditional<LDA == KMAJ, KLoad<TI>, MnLoad<TI>>::type la;
   typename std::conditional<LDB == KMAJ, KLoad<TJ>, MnLoad<TJ>>::type lb;
   if constexpr (EPI <= EPI_DZ) {
-    la.init(xs, ldx, m0, n, w);
-    lb.init(g.w, ldx, n0, g.nv, w);
+    la.init(g.w, ldx, m0, g.nv, w);
+    lb.init(xs, ldx, n0, n, w);
   } else if constexpr (EPI == EPI_DX) {
     la.init((const uint8_t*)g.dz, ldz, m0, n, w);
     lb.init(g.w, ldx, n0, g.hidden, g.nv, w);
@@ -338,132 +342,207 @@ __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(H
     body(k1 - 1, F_{}, F_{});
   }
   // Every LDS read of the loop finished before its last barrier, and no load
-  // is in flight: the tiles' space now stages the result, fp32, ROWS rows a
-  // pass.  Staged row s is row 32 TI (s / WR) + WR p + s % WR of the tile.
-  constexpr int ROWS = stage_rows<TI, TJ>(), PASSES = M_T / ROWS, WR = ROWS / 2;
-  constexpr int PITCH = N_T + HEAD_PITCH_PAD;
-  float* stage = (float*)smem;
-  float2* table = (float2*)(smem + ROWS * PITCH * 4);       // {lse, dloss / tau} of the tile's rows
-  auto tile_row = [&](int p, int s) { return 32 * TI * (s / WR) + WR * p + s % WR; };
-  const int ncol = N - n0 < N_T ? N - n0 : N_T;              // columns of the tile that exist
-
-  if constexpr (EPI == EPI_DZ) {
-    for (int r = t; r < M_T; r += 256) {
-      float2 e = make_float2(__builtin_inff(), 0.0f);        // rows past the last: exp(-inf) 0 = 0
-      if (m0 + r < n) {
-        const int tok = g.row_of[m0 + r];
-        e.x = g.lse[tok];
-        const bool bad = g.targets ? g.targets[tok] >= g.vocab : g.state[tok] == ROW_BAD;
-        e.y = bad ? __builtin_nanf("") : g.dloss[tok] * g.inv_tau;
-      }
-      table[r] = e;
+  // is in flight: the tiles' space may now stage the result.  Lane (lr, lg)
+  // holds, in acc[i][j][4 q + r], row 32 TI wm + 32 i + 8 q + 4 lg + r of column
+  // 32 TJ wn + 32 j + lr.
+  const float none = -__builtin_inff();
+  if constexpr (EPI <= EPI_DZ) {
+    constexpr int PITCH = M_T + STAGE_PAD / 4, PITCHB = M_T * 2 + STAGE_PAD;
+    float* stage = (float*)smem;                               // MULTI: [STAGE_ROWS tokens][PITCH ids]
+    float* scale = (float*)(smem + STAGE_ROWS * PITCH * 4);     // MULTI: dloss / tau of the tile's tokens
+    const int have = g.nv - m0 < M_T ? g.nv - m0 : M_T;        // ids of the tile that exist
+    const int row0 = wm * 32 * TI;
+    if (have < M_T) {
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const bool past = row0 + 32 * i + 8 * (r >> 2) + 4 * lg + (r & 3) >= have;
+#pragma unroll
+          for (int j = 0; j < TJ; ++j) acc[i][j][r] = past ? none : acc[i][j][r];
+        }
     }
-    __syncthreads();
-  }
+    const float c2 = g.inv_tau * LOG2E;
+    int tok[TJ], want[TJ];                                     // token, and its target less this lane's first row
 #pragma unroll
-  for (int p = 0; p < PASSES; ++p) {
+    for (int j = 0; j < TJ; ++j) {
+      const int col = n0 + wn * 32 * TJ + 32 * j + lr;
+      tok[j] = col < n ? g.row_of[col] : -1;
+      want[j] = -1;
+      if (!MULTI && tok[j] >= 0) {
+        const int64_t local = g.targets[tok[j]] - (g.v0 + m0 + row0);
+        if (local >= 0 && local < 32 * TI) want[j] = (int)local - 4 * lg;
+        if (local >= have - row0) want[j] = -1;
+      }
+    }
+    if constexpr (EPI == EPI_STATS) {
 #pragma unroll
-    for (int ii = 0; ii < WR / 32; ++ii)
+      for (int j = 0; j < TJ; ++j) {
+        float mx = none;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int s = wm * WR + 32 * ii + 8 * (r >> 2) + 4 * lg + (r & 3);
-        float2 e;
-        if (EPI == EPI_DZ) e = table[tile_row(p, s)];
+        for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) {
-          float v = acc[WR / 32 * p + ii][j][r];
-          if (EPI == EPI_STATS) v = v * g.inv_tau;
-          if (EPI == EPI_DZ) v = head_exp(v * g.inv_tau - e.x) * e.y;
-          stage[s * PITCH + wn * 32 * TJ + 32 * j + lr] = v;
+          for (int r = 0; r < 16; ++r) mx = fmaxf(mx, acc[i][j][r]);
+        mx *= c2;                                              // everything in units of log 2 from here
+        const float safe = mx == none ? 0.0f : mx;             // nothing but -inf: the sum stays 0
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], c2, -safe));
+        const float mo = __shfl_xor(mx, 32, 64), so = __shfl_xor(sum, 32, 64);
+        const float m1 = fmaxf(mx, mo), safe1 = m1 == none ? 0.0f : m1;
+        sum = sum * __builtin_amdgcn_exp2f(mx - safe1) + so * __builtin_amdgcn_exp2f(mo - safe1);
+        if (lg == 0)
+          g.stats[(int64_t)(tm * 2 + wm) * g.rows + n0 + wn * 32 * TJ + 32 * j + lr] = make_float2(m1, sum);
+        if (!MULTI && __any(want[j] >= 0)) {
+          float z = 0.0f;
+          bool mine = false;
+#pragma unroll
+          for (int i = 0; i < TI; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const bool hit = want[j] == 32 * i + 8 * (r >> 2) + (r & 3);
+              z = hit ? acc[i][j][r] : z;
+              mine |= hit;
+            }
+          if (mine) g.zsel[tok[j]] = z * g.inv_tau;
         }
       }
-    __syncthreads();
-    if constexpr (EPI <= EPI_DZ) {
-      // a thread owns PW columns of a staged row
-      constexpr int PARTS = 256 / ROWS, PW = N_T / PARTS;
-      const int s = t % ROWS, part = t / ROWS;
-      float* mine = stage + s * PITCH + part * PW;
-      const int have = ncol - part * PW;                     // columns of this part that exist
-      if (ncol < N_T) {
-        for (int c = have < 0 ? 0 : have; c < PW; ++c) mine[c] = EPI == EPI_STATS ? -__builtin_inff() : 0.0f;
-      }
-      const int row = m0 + tile_row(p, s);
-      const int tok = row < n ? g.row_of[row] : -1;
-      if constexpr (EPI == EPI_STATS) {
-        float mx = -__builtin_inff(), sum = 0.0f;
-        for (int c = 0; c < PW; c += 32) {
-          float4 v[8];
+    }
+    float cz[TJ];
+    if constexpr (EPI == EPI_DZ) {
 #pragma unroll
-          for (int u = 0; u < 8; ++u) v[u] = *(const float4*)(mine + c + 4 * u);
-          float m1 = mx;
-#pragma unroll
-          for (int u = 0; u < 8; ++u) m1 = fmaxf(fmaxf(m1, fmaxf(v[u].x, v[u].y)), fmaxf(v[u].z, v[u].w));
-          const float safe = m1 == -__builtin_inff() ? 0.0f : m1;   // nothing but -inf: the sum stays 0
-          float add = 0.0f;
-#pragma unroll
-          for (int u = 0; u < 8; ++u)
-            add += (head_exp(v[u].x - safe) + head_exp(v[u].y - safe)) +
-                   (head_exp(v[u].z - safe) + head_exp(v[u].w - safe));
-          sum = sum * head_exp(mx - safe) + add;
-          mx = m1;
+      for (int j = 0; j < TJ; ++j) {
+        float lse2 = __builtin_inff();                         // rows past the last: exp(-inf) 0 = 0
+        cz[j] = 0.0f;
+        if (tok[j] >= 0) {
+          lse2 = g.lse[tok[j]] * LOG2E;
+          const bool bad = MULTI ? g.state[tok[j]] == ROW_BAD : g.targets[tok[j]] >= g.vocab;
+          cz[j] = bad ? __builtin_nanf("") : g.dloss[tok[j]] * g.inv_tau;
         }
-        g.stats[(int64_t)(tn * PARTS + part) * g.rows + row] = make_float2(mx, sum);
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            acc[i][j][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], c2, -lse2)) * cz[j];
+        if (!MULTI && __any(want[j] >= 0)) {
+#pragma unroll
+          for (int i = 0; i < TI; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              acc[i][j][r] -= want[j] == 32 * i + 8 * (r >> 2) + (r & 3) ? cz[j] : 0.0f;
+        }
       }
-      if (tok >= 0) {
-        // the token's slots that lie in this part
-        const int64_t first = g.v0 + n0 + part * PW;
-        const int mineN = have < PW ? have : PW;
-        auto slot = [&](int64_t id, int64_t at, bool one) {
-          const int64_t c = id - first;
-          if (id < 0 || c < 0 || c >= mineN) return;
-          if (EPI == EPI_STATS) g.zsel[at] = mine[c];
-          else mine[c] -= one ? table[tile_row(p, s)].y : g.p[at] * table[tile_row(p, s)].y;
-        };
-        if (g.targets) {
-          slot(g.targets[tok], tok, true);
-        } else {
-          const int64_t at = (int64_t)tok * g.slots;
+    }
+    if constexpr (!MULTI && EPI == EPI_DZ) {
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *(uint2*)(smem + (wn * 32 * TJ + 32 * j + lr) * PITCHB + (row0 + 32 * i + 8 * q + 4 * lg) * 2) =
+                make_uint2(pk_bf16(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
+                           pk_bf16(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]));
+      __syncthreads();
+      constexpr int LPR = M_T / 8;                             // lanes a row, 8 values each
+#pragma unroll 4
+      for (int s = t / LPR; s < N_T; s += 256 / LPR)
+        *(uint4*)(g.dz + (int64_t)(n0 + s) * g.dz_ld + m0 + (t % LPR) * 8) =
+            *(const uint4*)(smem + s * PITCHB + (t % LPR) * 16);
+    }
+    if constexpr (MULTI) {
+      // fp32, 128 tokens a pass: staged row s is token 32 TJ (s / 64) + 64 p + s % 64
+      if (EPI == EPI_DZ && wm == 0 && lg == 0) {
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) scale[wn * 32 * TJ + 32 * j + lr] = cz[j];
+      }
+#pragma unroll
+      for (int p = 0; p < N_T / STAGE_ROWS; ++p) {
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+          for (int i = 0; i < TI; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int j = 2 * p + jj;
+              const float f = EPI == EPI_STATS ? g.inv_tau : 1.0f;
+              *(float4*)(stage + (wn * 64 + 32 * jj + lr) * PITCH + row0 + 32 * i + 8 * q + 4 * lg) =
+                  make_float4(acc[i][j][4 * q] * f, acc[i][j][4 * q + 1] * f, acc[i][j][4 * q + 2] * f,
+                              acc[i][j][4 * q + 3] * f);
+            }
+        __syncthreads();
+        // the slots: thread (s, part) looks for those of its token in its half of the ids
+        constexpr int PW = M_T / 2;
+        const int s = t % STAGE_ROWS, part = t / STAGE_ROWS;
+        const int at_tile = 32 * TJ * (s / 64) + 64 * p + s % 64;
+        if (n0 + at_tile < n) {
+          const int token = g.row_of[n0 + at_tile];
+          float* mine = stage + s * PITCH + part * PW;
+          const int first = g.v0 + m0 + part * PW;
+          const int some = have - part * PW < PW ? have - part * PW : PW;
+          const int64_t at = (int64_t)token * g.slots;
           const int4* ids = (const int4*)(g.ids + at);
+          auto slot = [&](int id, int64_t k) {
+            const int c = id - first;
+            if (id < 0 || c < 0 || c >= some) return;
+            if (EPI == EPI_STATS) g.zsel[k] = mine[c];
+            else mine[c] -= g.p[k] * scale[at_tile];
+          };
           for (int q = 0; q < g.slots / 4; ++q) {
             const int4 id4 = ids[q];
-            slot(id4.x, at + 4 * q, false);
-            slot(id4.y, at + 4 * q + 1, false);
-            slot(id4.z, at + 4 * q + 2, false);
-            slot(id4.w, at + 4 * q + 3, false);
+            slot(id4.x, at + 4 * q);
+            slot(id4.y, at + 4 * q + 1);
+            slot(id4.z, at + 4 * q + 2);
+            slot(id4.w, at + 4 * q + 3);
           }
+        }
+        __syncthreads();
+        if (EPI == EPI_DZ) {
+          constexpr int LPR = M_T / 8;
+#pragma unroll 4
+          for (int s2 = t / LPR; s2 < STAGE_ROWS; s2 += 256 / LPR) {
+            const float* q = stage + s2 * PITCH + (t % LPR) * 8;
+            const float4 lo = *(const float4*)q, hi = *(const float4*)(q + 4);
+            *(uint4*)(g.dz + (int64_t)(n0 + 32 * TJ * (s2 / 64) + 64 * p + s2 % 64) * g.dz_ld + m0 + (t % LPR) * 8) =
+                make_uint4(pk_bf16(lo.x, lo.y), pk_bf16(lo.z, lo.w), pk_bf16(hi.x, hi.y), pk_bf16(hi.z, hi.w));
+          }
+          if (p + 1 < N_T / STAGE_ROWS) __syncthreads();
         }
       }
     }
-    if constexpr (EPI == EPI_DZ) {
+  } else {
+    // fp32, 128 rows a pass: staged row s is row 32 TI (s / 64) + 64 p + s % 64 of the tile
+    constexpr int PITCH = N_T + STAGE_PAD / 4;
+    constexpr int LPR = N_T / 8, RPI = 256 / LPR;
+    float* stage = (float*)smem;
+    const int col = n0 + (t % LPR) * 8;
+#pragma unroll
+    for (int p = 0; p < M_T / STAGE_ROWS; ++p) {
+#pragma unroll
+      for (int ii = 0; ii < 2; ++ii)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+#pragma unroll
+          for (int j = 0; j < TJ; ++j)
+            stage[(wm * 64 + 32 * ii + 8 * (r >> 2) + 4 * lg + (r & 3)) * PITCH + wn * 32 * TJ + 32 * j + lr] =
+                acc[2 * p + ii][j][r];
       __syncthreads();
-      // 8 values a lane: N_T / 8 lanes a row
-      constexpr int LPR = N_T / 8, RPI = 256 / LPR;
 #pragma unroll 4
-      for (int s = t / LPR; s < ROWS; s += RPI) {
-        const float* q = stage + s * PITCH + (t % LPR) * 8;
-        const float4 lo = *(const float4*)q, hi = *(const float4*)(q + 4);
-        const uint4 o = make_uint4(pk_bf16(lo.x, lo.y), pk_bf16(lo.z, lo.w), pk_bf16(hi.x, hi.y), pk_bf16(hi.z, hi.w));
-        *(uint4*)(g.dz + (int64_t)(m0 + tile_row(p, s)) * g.dz_ld + n0 + (t % LPR) * 8) = o;
-      }
-    }
-    if constexpr (EPI >= EPI_DX) {
-      constexpr int LPR = N_T / 8, RPI = 256 / LPR;
-      const int col = n0 + (t % LPR) * 8;
-#pragma unroll 4
-      for (int s = t / LPR; s < ROWS; s += RPI) {
+      for (int s = t / LPR; s < STAGE_ROWS; s += RPI) {
         const float* q = stage + s * PITCH + (t % LPR) * 8;
         float4 lo = *(const float4*)q, hi = *(const float4*)(q + 4);
-        const int row = m0 + tile_row(p, s);
+        const int row = m0 + 32 * TI * (s / 64) + 64 * p + s % 64;
         if (row < M && col < N) {
           // dx partials: the splits' live rows, in whole tiles, one after the other; dW itself, or its partials
           const int64_t at = (int64_t)split * (EPI == EPI_DX ? tiles_m * M_T : g.dz_ld) * g.hidden +
                              (int64_t)row * g.hidden + col;
-          void* out = EPI == EPI_DW && splits == 1 ? g.dw : g.part;
           if (EPI == EPI_DW && splits == 1 && g.out_bf16) {
-            *(uint4*)((uint16_t*)out + at) =
+            *(uint4*)((uint16_t*)g.dw + at) =
                 make_uint4(pk_bf16(lo.x, lo.y), pk_bf16(lo.z, lo.w), pk_bf16(hi.x, hi.y), pk_bf16(hi.z, hi.w));
           } else {
-            float4* o = (float4*)((float*)out + at);
+            float4* o = (float4*)((EPI == EPI_DW && splits == 1 ? (float*)g.dw : g.part) + at);
             if (EPI == EPI_DX && g.add) {
               const float4 u = o[0], v = o[1];
               lo = make_float4(lo.x + u.x, lo.y + u.y, lo.z + u.z, lo.w + u.w);
@@ -474,15 +553,15 @@ __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(H
           }
         }
       }
+      if (p + 1 < M_T / STAGE_ROWS) __syncthreads();
     }
-    if (p + 1 < PASSES) __syncthreads();
   }
 }
 
 typedef void (*head_fn)(HeadArgs);
-template <int TI, int TJ, int EPI>
+template <int TI, int TJ, int EPI, bool MULTI>
 static head_fn head_product() {
-  return head_gemm_kernel<TI, TJ, EPI == EPI_DW ? MNMAJ : KMAJ, EPI >= EPI_DX ? MNMAJ : KMAJ, EPI>;
+  return head_gemm_kernel<TI, TJ, EPI == EPI_DW ? MNMAJ : KMAJ, EPI >= EPI_DX ? MNMAJ : KMAJ, EPI, MULTI>;
 }
 
 // ---------------------------------------------------------------------------
@@ -685,7 +764,7 @@ __global__ __launch_bounds__(JOIN_ROWS * JOIN_Q) void head_join_kernel(JoinArgs 
   float2 u = make_float2(none, 0.0f);
   auto add = [&](float2 v) {
     const float m1 = fmaxf(u.x, v.x), safe = m1 == none ? 0.0f : m1;
-    u = make_float2(m1, u.y * head_exp(u.x - safe) + v.y * head_exp(v.x - safe));
+    u = make_float2(m1, u.y * __builtin_amdgcn_exp2f(u.x - safe) + v.y * __builtin_amdgcn_exp2f(v.x - safe));
   };
   if (ok) {
     const float2* st = a.stats + row;
@@ -694,9 +773,9 @@ __global__ __launch_bounds__(JOIN_ROWS * JOIN_Q) void head_join_kernel(JoinArgs 
       const float2 v0 = st[(int64_t)i * a.rows], v1 = st[(int64_t)(i + JOIN_Q) * a.rows];
       const float2 v2 = st[(int64_t)(i + 2 * JOIN_Q) * a.rows], v3 = st[(int64_t)(i + 3 * JOIN_Q) * a.rows];
       const float m1 = fmaxf(fmaxf(u.x, fmaxf(v0.x, v1.x)), fmaxf(v2.x, v3.x)), safe = m1 == none ? 0.0f : m1;
-      u = make_float2(m1, (u.y * head_exp(u.x - safe) + v0.y * head_exp(v0.x - safe)) +
-                              (v1.y * head_exp(v1.x - safe) + v2.y * head_exp(v2.x - safe)) +
-                              v3.y * head_exp(v3.x - safe));
+      u = make_float2(m1, (u.y * __builtin_amdgcn_exp2f(u.x - safe) + v0.y * __builtin_amdgcn_exp2f(v0.x - safe)) +
+                              (v1.y * __builtin_amdgcn_exp2f(v1.x - safe) + v2.y * __builtin_amdgcn_exp2f(v2.x - safe)) +
+                              v3.y * __builtin_amdgcn_exp2f(v3.x - safe));
     }
     for (; i < a.parts; i += JOIN_Q) add(st[(int64_t)i * a.rows]);
   }
@@ -706,7 +785,7 @@ __global__ __launch_bounds__(JOIN_ROWS * JOIN_Q) void head_join_kernel(JoinArgs 
   u = sm[0][r];
 #pragma unroll 4
   for (int i = 1; i < JOIN_Q; ++i) add(sm[i][r]);
-  const float lse = u.x + head_log(u.y);
+  const float lse = (u.x + __builtin_amdgcn_logf(u.y)) * LN2;
   const int tok = ok ? a.row_of[row] : 0;
   if (a.targets) {
     if (q == 0 && ok) {
@@ -957,8 +1036,11 @@ static HeadArgs head_rows(const HeadCall& c, const HeadPlan& h, hipStream_t stre
 
 template <int EPI>
 static void head_launch(int tile, int64_t grid, const HeadArgs& g, hipStream_t stream) {
-  hipLaunchKernelGGL((tile == HEAD_TILE ? head_product<4, 4, EPI>() : head_product<2, 2, EPI>()), dim3((unsigned)grid),
-                     dim3(256), 0, stream, g);
+  constexpr bool SLOTS = EPI <= EPI_DZ;             // the products of dz know no slots
+  const bool multi = SLOTS && !g.targets;
+  head_fn fn = tile == HEAD_TILE ? head_product<4, 4, EPI, false>() : head_product<2, 2, EPI, false>();
+  if (multi) fn = tile == HEAD_TILE ? head_product<4, 4, EPI, SLOTS>() : head_product<2, 2, EPI, SLOTS>();
+  hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(256), 0, stream, g);
 }
 
 static pbs_status head_loss(const HeadCall& c, hipStream_t stream) {
