@@ -69,7 +69,7 @@ template <int T> constexpr int tile_bytes() { return 64 * T * ROWB; }
 // accesses to consecutive rows then cover every bank.
 constexpr int STAGE_ROWS = 128, STAGE_PAD = 16;
 template <int TI, int TJ> constexpr int head_smem() {
-  return cmax(cmax(2 * (tile_bytes<TI>() + tile_bytes<TJ>()),
+  return cmax(cmax(2 * tile_bytes<TI>() + 3 * tile_bytes<TJ>(),
                    STAGE_ROWS * (64 * cmax(TI, TJ) * 4 + STAGE_PAD) + 64 * TJ * 4),
               64 * TJ * (64 * TI * 2 + STAGE_PAD));
 }
@@ -186,6 +186,17 @@ __device__ __forceinline__ void half_read(Half<T>& f, int d, const uint8_t* base
   }
 }
 
+// Waits for all but this wave's last N loads and for its LDS reads, then for
+// every wave.  (__syncthreads would wait for every load.)
+template <int N>
+__device__ __forceinline__ void stage_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 __device__ __forceinline__ constexpr int part_lo(int n, int over, int m) { return m < over ? n * m / over : n; }
 __device__ __forceinline__ constexpr int part_hi(int n, int over, int m) { return m < over ? n * (m + 1) / over : n; }
 
@@ -195,12 +206,15 @@ constexpr float LN2 = 0.69314718055994530942f;
 // ---------------------------------------------------------------------------
 // The product and its epilogues.
 //
-// K stage kt sits in LDS buffer (kt - first) & 1.  Phase A multiplies the
-// stage's first half while its second half is read from LDS; then the wave
-// waits for its own loads of stage kt + 1 (an explicit vmcnt(0)) and all waves
-// meet; phase C multiplies the second half while the next stage's first half
-// is read and the loads of stage kt + 2 are issued into the buffer that was
-// just read out.
+// A's K stages go through two LDS buffers, B's through three.  Phase A of
+// stage kt multiplies its first half while its second half is read from LDS
+// and the loads of B's stage kt + 2 are issued; then the wave waits for its
+// own loads of stage kt + 1 (all but those just issued, an explicit vmcnt) and
+// all waves meet; phase C multiplies the second half while the first half of
+// stage kt + 1 is read and the loads of A's stage kt + 2 go into the buffer
+// that was just read out.  The third B buffer is what lets the loads spread
+// over the whole stage: issued over phase C alone, they fill the address
+// unit's time there and hold up the wave.
 // ---------------------------------------------------------------------------
 template <int TI, int TJ, int LDA, int LDB, int EPI, bool MULTI>
 __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(HeadArgs g) {
@@ -213,11 +227,12 @@ __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(H
   const int n = g.live[0], splits = EPI <= EPI_DZ ? 1 : g.live[EPI == EPI_DX ? 1 : 2];
   const uint8_t* xs = n == g.tokens ? g.x : g.xc;
   const int64_t ldx = (int64_t)g.hidden * 2, ldz = (int64_t)g.dz_ld * 2;
-  // the logits are formed transposed, vocabulary x tokens: a lane then holds
-  // 16 TI values of each of its TJ tokens, and a token's maximum, sum and
-  // gradient need no other lane but one
-  const int M = EPI == EPI_DX ? n : g.nv;
-  const int N = EPI <= EPI_DZ ? n : g.hidden;
+  // every product is formed transposed: M is the result's contiguous axis (ids
+  // of z and dz, hidden of dx and dW), N its rows.  A lane then holds 16 TI
+  // values of each of TJ rows, four consecutive ones at a time: a token's
+  // maximum, sum and gradient need one other lane, and stores are wide.
+  const int M = EPI <= EPI_DZ ? g.nv : g.hidden;
+  const int N = EPI == EPI_DW ? g.nv : n;
   const int nk = EPI <= EPI_DZ ? g.hidden / 64 : ((EPI == EPI_DX ? g.nv : n) + 63) / 64;
   const int tiles_m = (M + M_T - 1) / M_T, tiles_n = (N + N_T - 1) / N_T;
   const int tiles = tiles_m * tiles_n * splits;
@@ -229,8 +244,8 @@ __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(H
   const int m0 = tm * M_T, n0 = tn * N_T;
   const int k0 = (int)((int64_t)nk * split / splits), k1 = (int)((int64_t)nk * (split + 1) / splits);
 
-  auto tileA = [&](int buf) { return smem + buf * (tile_bytes<TI>() + tile_bytes<TJ>()); };
-  auto tileB = [&](int buf) { return tileA(buf) + tile_bytes<TI>(); };
+  auto tileA = [&](int kt) { return smem + ((kt - k0) & 1) * tile_bytes<TI>(); };
+  auto tileB = [&](int kt) { return smem + 2 * tile_bytes<TI>() + (kt - k0) % 3 * tile_bytes<TJ>(); };
 
   f32x16 acc[TI][TJ];
 #pragma unroll
@@ -246,11 +261,11 @@ __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(H
     la.init(g.w, ldx, m0, g.nv, w);
     lb.init(xs, ldx, n0, n, w);
   } else if constexpr (EPI == EPI_DX) {
-    la.init((const uint8_t*)g.dz, ldz, m0, n, w);
-    lb.init(g.w, ldx, n0, g.hidden, g.nv, w);
+    la.init(g.w, ldx, m0, g.hidden, g.nv, w);
+    lb.init((const uint8_t*)g.dz, ldz, n0, n, w);
   } else {
-    la.init((const uint8_t*)g.dz, ldz, m0, g.dz_ld, 64 * nk, w);
-    lb.init(xs, ldx, n0, g.hidden, n, w);
+    la.init(xs, ldx, m0, g.hidden, n, w);
+    lb.init((const uint8_t*)g.dz, ldz, n0, g.dz_ld, 64 * nk, w);
   }
 
   const int lr = lane & 31, lg = lane >> 5;
@@ -266,79 +281,112 @@ __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(H
   const uint32_t fba = frag_base(LDA, TI, wm), fbb = frag_base(LDB, TJ, wn);
   const int offA = LDA == KMAJ ? wm * TI * 4096 : 0, offB = LDB == KMAJ ? wn * TJ * 4096 : 0;
 
-  constexpr int NMFMA = 2 * TI * TJ, HALF = NMFMA / 2;       // per half stage
-  constexpr int NVM = 2 * TI + 2 * TJ;                       // loads per stage and wave
+  constexpr int NMFMA = 2 * TI * TJ;                         // per half stage
+  constexpr int OVER = NMFMA * 3 / 4;                        // MFMAs that a half stage's fragment reads are spread over
+  constexpr int NA = 2 * TI, NB = 2 * TJ;                    // loads per stage and wave
   constexpr int RA = half_reads<LDA, TI>(), RB = half_reads<LDB, TJ>();
   Half<TI> a0, a1;
   Half<TJ> b0, b1;
 
-  auto load_item = [&](int kt, int v) {
-    const int buf = (kt - k0) & 1;
-    if (v < 2 * TI) la.load(kt, tileA(buf), w, v);
-    else lb.load(kt, tileB(buf), w, v - 2 * TI);
-  };
   auto mfma = [&](const Half<TI>& a, const Half<TJ>& b, int m) {
     const int s = m / (TI * TJ), i = (m / TJ) % TI, j = m % TJ;
     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a.x[i][s]),
                                                         __builtin_bit_cast(bf16x8, b.x[j][s]), acc[i][j], 0, 0, 0);
   };
 
+  // What the epilogue needs of the lane's tokens: loaded behind the last two
+  // stages' products.
+  int tok[TJ], state[TJ];
+  int64_t target[TJ];
+  float lse[TJ], dloss[TJ];
+  auto token_rows = [&]() {
+    if constexpr (EPI <= EPI_DZ) {
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        const int col = n0 + wn * 32 * TJ + 32 * j + lr;
+        tok[j] = g.row_of[col < n ? col : n - 1];
+      }
+    }
+  };
+  auto token_data = [&]() {
+    if constexpr (EPI <= EPI_DZ) {
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        if (!MULTI) target[j] = g.targets[tok[j]];
+        if (EPI == EPI_DZ) {
+          if (MULTI) state[j] = g.state[tok[j]];
+          lse[j] = g.lse[tok[j]];
+          dloss[j] = g.dloss[tok[j]];
+        }
+      }
+    }
+  };
+
   if (k1 > k0) {
 #pragma unroll
-    for (int v = 0; v < NVM; ++v) load_item(k0, v);
-    wait_vm0();
-    __syncthreads();
+    for (int v = 0; v < NA; ++v) la.load(k0, tileA(k0), w, v);
+#pragma unroll
+    for (int v = 0; v < NB; ++v) lb.load(k0, tileB(k0), w, v);
     if (k1 > k0 + 1) {
 #pragma unroll
-      for (int v = 0; v < NVM; ++v) load_item(k0 + 1, v);
+      for (int v = 0; v < NA; ++v) la.load(k0 + 1, tileA(k0 + 1), w, v);
+#pragma unroll
+      for (int v = 0; v < NB; ++v) lb.load(k0 + 1, tileB(k0 + 1), w, v);
+      stage_barrier<NA + NB>();
+    } else {
+      stage_barrier<0>();
     }
 #pragma unroll
-    for (int d = 0; d < RA; ++d) half_read<0, LDA, TI>(a0, d, tileA(0) + offA, fba);
+    for (int d = 0; d < RA; ++d) half_read<0, LDA, TI>(a0, d, tileA(k0) + offA, fba);
 #pragma unroll
-    for (int d = 0; d < RB; ++d) half_read<0, LDB, TJ>(b0, d, tileB(0) + offB, fbb);
+    for (int d = 0; d < RB; ++d) half_read<0, LDB, TJ>(b0, d, tileB(k0) + offB, fbb);
 
     auto body = [&](int kt, auto issue_c, auto next_c) {
       constexpr bool ISSUE = decltype(issue_c)::value;
       constexpr bool NEXT = decltype(next_c)::value;
-      const int buf = (kt - k0) & 1;
-      const uint8_t* curA = tileA(buf) + offA;
-      const uint8_t* curB = tileB(buf) + offB;
-      const uint8_t* nxtA = tileA(buf ^ 1) + offA;
-      const uint8_t* nxtB = tileB(buf ^ 1) + offB;
+      const uint8_t* curA = tileA(kt) + offA;
+      const uint8_t* curB = tileB(kt) + offB;
+      const uint8_t* nxtA = tileA(kt + 1) + offA;
+      const uint8_t* nxtB = tileB(kt + 1) + offB;
 #pragma unroll
       for (int m = 0; m < NMFMA; ++m) {
         mfma(a0, b0, m);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int d = part_lo(RA + RB, HALF, m); d < part_hi(RA + RB, HALF, m); ++d) {
+        for (int d = part_lo(RA + RB, OVER, m); d < part_hi(RA + RB, OVER, m); ++d) {
           if (d < RA) half_read<1, LDA, TI>(a1, d, curA, fba);
           else half_read<1, LDB, TJ>(b1, d - RA, curB, fbb);
         }
+        if (ISSUE) {
+#pragma unroll
+          for (int v = part_lo(NB, NMFMA, m); v < part_hi(NB, NMFMA, m); ++v) lb.load(kt + 2, tileB(kt + 2), w, v);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
-      wait_vm0();
-      __syncthreads();
-      __builtin_amdgcn_sched_barrier(0);
+      stage_barrier<ISSUE ? NB : 0>();
       constexpr int NDS = NEXT ? RA + RB : 0;
-      constexpr int NLD = ISSUE ? NVM : 0;
 #pragma unroll
       for (int m = 0; m < NMFMA; ++m) {
         mfma(a1, b1, m);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int d = part_lo(NDS, HALF, m); d < part_hi(NDS, HALF, m); ++d) {
+        for (int d = part_lo(NDS, OVER, m); d < part_hi(NDS, OVER, m); ++d) {
           if (d < RA) half_read<0, LDA, TI>(a0, d, nxtA, fba);
           else half_read<0, LDB, TJ>(b0, d - RA, nxtB, fbb);
         }
+        if (ISSUE) {
 #pragma unroll
-        for (int v = part_lo(NLD, NMFMA, m); v < part_hi(NLD, NMFMA, m); ++v) load_item(kt + 2, v);
+          for (int v = part_lo(NA, NMFMA, m); v < part_hi(NA, NMFMA, m); ++v) la.load(kt + 2, tileA(kt + 2), w, v);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
     };
     using T_ = std::integral_constant<bool, true>;
     using F_ = std::integral_constant<bool, false>;
     for (int kt = k0; kt < k1 - 2; ++kt) body(kt, T_{}, T_{});
+    token_rows();
     if (k1 - k0 >= 2) body(k1 - 2, F_{}, T_{});
+    token_data();
     body(k1 - 1, F_{}, F_{});
   }
   // Every LDS read of the loop finished before its last barrier, and no load
@@ -346,105 +394,113 @@ __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(H
   // holds, in acc[i][j][4 q + r], row 32 TI wm + 32 i + 8 q + 4 lg + r of column
   // 32 TJ wn + 32 j + lr.
   const float none = -__builtin_inff();
-  if constexpr (EPI <= EPI_DZ) {
-    constexpr int PITCH = M_T + STAGE_PAD / 4, PITCHB = M_T * 2 + STAGE_PAD;
-    float* stage = (float*)smem;                               // MULTI: [STAGE_ROWS tokens][PITCH ids]
-    float* scale = (float*)(smem + STAGE_ROWS * PITCH * 4);     // MULTI: dloss / tau of the tile's tokens
-    const int have = g.nv - m0 < M_T ? g.nv - m0 : M_T;        // ids of the tile that exist
-    const int row0 = wm * 32 * TI;
-    if (have < M_T) {
+  constexpr int PITCH = M_T + STAGE_PAD / 4, PITCHB = M_T * 2 + STAGE_PAD;
+  float* stage = (float*)smem;                                 // [STAGE_ROWS][PITCH], or bf16 [N_T][PITCHB]
+  const int row0 = wm * 32 * TI;                               // the wave's first value of the tile's rows
+  auto stage_bf16 = [&](int j) {
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *(uint2*)(smem + (wn * 32 * TJ + 32 * j + lr) * PITCHB + (row0 + 32 * i + 8 * q + 4 * lg) * 2) = make_uint2(
+            pk_bf16(acc[i][j][4 * q], acc[i][j][4 * q + 1]), pk_bf16(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]));
+  };
+  // rows 32 TJ wn + 64 p .. of the wave's columns, to staged rows 64 wn ..: a
+  // pass p stages row s of the tile's row 32 TJ (s / 64) + 64 p + s % 64
+  auto stage_f32 = [&](int p, float f) {
+#pragma unroll
+    for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
       for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const bool past = row0 + 32 * i + 8 * (r >> 2) + 4 * lg + (r & 3) >= have;
-#pragma unroll
-          for (int j = 0; j < TJ; ++j) acc[i][j][r] = past ? none : acc[i][j][r];
+        for (int q = 0; q < 4; ++q) {
+          const int j = 2 * p + jj;
+          *(float4*)(stage + (wn * 64 + 32 * jj + lr) * PITCH + row0 + 32 * i + 8 * q + 4 * lg) =
+              make_float4(acc[i][j][4 * q] * f, acc[i][j][4 * q + 1] * f, acc[i][j][4 * q + 2] * f,
+                          acc[i][j][4 * q + 3] * f);
         }
-    }
+  };
+  if constexpr (EPI <= EPI_DZ) {
+    float* scale = (float*)(smem + STAGE_ROWS * PITCH * 4);     // MULTI: dloss / tau of the tile's tokens
+    const int have = g.nv - m0 < M_T ? g.nv - m0 : M_T;        // ids of the tile that exist
     const float c2 = g.inv_tau * LOG2E;
-    int tok[TJ], want[TJ];                                     // token, and its target less this lane's first row
+    int want[TJ];                                              // the token's target less this lane's first id
+    float lse2[TJ], cz[TJ];                                    // lse / log 2, dloss / tau
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
-      const int col = n0 + wn * 32 * TJ + 32 * j + lr;
-      tok[j] = col < n ? g.row_of[col] : -1;
-      want[j] = -1;
-      if (!MULTI && tok[j] >= 0) {
-        const int64_t local = g.targets[tok[j]] - (g.v0 + m0 + row0);
-        if (local >= 0 && local < 32 * TI) want[j] = (int)local - 4 * lg;
-        if (local >= have - row0) want[j] = -1;
+      const bool there = n0 + wn * 32 * TJ + 32 * j + lr < n;  // past the last row: exp(-inf) 0 = 0
+      const int64_t local = MULTI ? -1 : target[j] - (g.v0 + m0 + row0);
+      want[j] = there && local >= 0 && local < 32 * TI && local < have - row0 ? (int)local - 4 * lg : -1;
+      if (EPI == EPI_DZ) {
+        const bool bad = MULTI ? state[j] == ROW_BAD : target[j] >= g.vocab;
+        lse2[j] = there ? lse[j] * LOG2E : __builtin_inff();
+        cz[j] = !there ? 0.0f : bad ? __builtin_nanf("") : dloss[j] * g.inv_tau;
       }
     }
-    if constexpr (EPI == EPI_STATS) {
+    // z of id i, r; where the tile runs past the last id, -inf there (two
+    // instances: a choice made on the accumulators themselves would move all
+    // of them to vector registers)
+    auto finish = [&](auto full_c) {
+      constexpr bool FULL = decltype(full_c)::value;
+      auto z = [&](int i, int j, int r) {
+        return FULL || row0 + 32 * i + 8 * (r >> 2) + 4 * lg + (r & 3) < have ? acc[i][j][r] : none;
+      };
 #pragma unroll
       for (int j = 0; j < TJ; ++j) {
-        float mx = none;
+        if constexpr (EPI == EPI_STATS) {
+          float mx = none;
 #pragma unroll
-        for (int i = 0; i < TI; ++i)
+          for (int i = 0; i < TI; ++i)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) mx = fmaxf(mx, acc[i][j][r]);
-        mx *= c2;                                              // everything in units of log 2 from here
-        const float safe = mx == none ? 0.0f : mx;             // nothing but -inf: the sum stays 0
-        float sum = 0.0f;
+            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, z(i, j, r));
+          mx *= c2;                                            // everything in units of log 2 from here
+          const float safe = mx == none ? 0.0f : mx;           // nothing but -inf: the sum stays 0
+          float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < TI; ++i)
+          for (int i = 0; i < TI; ++i) {
+            // sixteen independent exponentials, then a tree: one running sum
+            // would wait out the instruction's latency 16 TI times
+            float e[16];
 #pragma unroll
-          for (int r = 0; r < 16; ++r) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], c2, -safe));
-        const float mo = __shfl_xor(mx, 32, 64), so = __shfl_xor(sum, 32, 64);
-        const float m1 = fmaxf(mx, mo), safe1 = m1 == none ? 0.0f : m1;
-        sum = sum * __builtin_amdgcn_exp2f(mx - safe1) + so * __builtin_amdgcn_exp2f(mo - safe1);
-        if (lg == 0)
-          g.stats[(int64_t)(tm * 2 + wm) * g.rows + n0 + wn * 32 * TJ + 32 * j + lr] = make_float2(m1, sum);
+            for (int r = 0; r < 16; ++r) e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(z(i, j, r), c2, -safe));
+#pragma unroll
+            for (int o = 8; o >= 1; o >>= 1)
+#pragma unroll
+              for (int r = 0; r < o; ++r) e[r] += e[r + o];
+            sum += e[0];
+          }
+          const float mo = __shfl_xor(mx, 32, 64), so = __shfl_xor(sum, 32, 64);
+          const float m1 = fmaxf(mx, mo), safe1 = m1 == none ? 0.0f : m1;
+          sum = sum * __builtin_amdgcn_exp2f(mx - safe1) + so * __builtin_amdgcn_exp2f(mo - safe1);
+          if (lg == 0)
+            g.stats[(int64_t)(tm * 2 + wm) * g.rows + n0 + wn * 32 * TJ + 32 * j + lr] = make_float2(m1, sum);
+        } else {
+#pragma unroll
+          for (int i = 0; i < TI; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              acc[i][j][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(z(i, j, r), c2, -lse2[j])) * cz[j];
+        }
         if (!MULTI && __any(want[j] >= 0)) {
-          float z = 0.0f;
+          float at = 0.0f;
           bool mine = false;
 #pragma unroll
           for (int i = 0; i < TI; ++i)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
               const bool hit = want[j] == 32 * i + 8 * (r >> 2) + (r & 3);
-              z = hit ? acc[i][j][r] : z;
+              if (EPI == EPI_DZ) acc[i][j][r] -= hit ? cz[j] : 0.0f;
+              else at = hit ? acc[i][j][r] : at;
               mine |= hit;
             }
-          if (mine) g.zsel[tok[j]] = z * g.inv_tau;
+          if (EPI == EPI_STATS && mine) g.zsel[tok[j]] = at * g.inv_tau;
         }
+        if (!MULTI && EPI == EPI_DZ) stage_bf16(j);
       }
-    }
-    float cz[TJ];
-    if constexpr (EPI == EPI_DZ) {
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        float lse2 = __builtin_inff();                         // rows past the last: exp(-inf) 0 = 0
-        cz[j] = 0.0f;
-        if (tok[j] >= 0) {
-          lse2 = g.lse[tok[j]] * LOG2E;
-          const bool bad = MULTI ? g.state[tok[j]] == ROW_BAD : g.targets[tok[j]] >= g.vocab;
-          cz[j] = bad ? __builtin_nanf("") : g.dloss[tok[j]] * g.inv_tau;
-        }
-#pragma unroll
-        for (int i = 0; i < TI; ++i)
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            acc[i][j][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], c2, -lse2)) * cz[j];
-        if (!MULTI && __any(want[j] >= 0)) {
-#pragma unroll
-          for (int i = 0; i < TI; ++i)
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-              acc[i][j][r] -= want[j] == 32 * i + 8 * (r >> 2) + (r & 3) ? cz[j] : 0.0f;
-        }
-      }
-    }
+    };
+    if (have == M_T) finish(std::integral_constant<bool, true>{});
+    else finish(std::integral_constant<bool, false>{});
     if constexpr (!MULTI && EPI == EPI_DZ) {
-#pragma unroll
-      for (int j = 0; j < TJ; ++j)
-#pragma unroll
-        for (int i = 0; i < TI; ++i)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *(uint2*)(smem + (wn * 32 * TJ + 32 * j + lr) * PITCHB + (row0 + 32 * i + 8 * q + 4 * lg) * 2) =
-                make_uint2(pk_bf16(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
-                           pk_bf16(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]));
       __syncthreads();
       constexpr int LPR = M_T / 8;                             // lanes a row, 8 values each
 #pragma unroll 4
@@ -453,25 +509,14 @@ __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(H
             *(const uint4*)(smem + s * PITCHB + (t % LPR) * 16);
     }
     if constexpr (MULTI) {
-      // fp32, 128 tokens a pass: staged row s is token 32 TJ (s / 64) + 64 p + s % 64
+      // fp32, 128 tokens a pass
       if (EPI == EPI_DZ && wm == 0 && lg == 0) {
 #pragma unroll
         for (int j = 0; j < TJ; ++j) scale[wn * 32 * TJ + 32 * j + lr] = cz[j];
       }
 #pragma unroll
       for (int p = 0; p < N_T / STAGE_ROWS; ++p) {
-#pragma unroll
-        for (int jj = 0; jj < 2; ++jj)
-#pragma unroll
-          for (int i = 0; i < TI; ++i)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int j = 2 * p + jj;
-              const float f = EPI == EPI_STATS ? g.inv_tau : 1.0f;
-              *(float4*)(stage + (wn * 64 + 32 * jj + lr) * PITCH + row0 + 32 * i + 8 * q + 4 * lg) =
-                  make_float4(acc[i][j][4 * q] * f, acc[i][j][4 * q + 1] * f, acc[i][j][4 * q + 2] * f,
-                              acc[i][j][4 * q + 3] * f);
-            }
+        stage_f32(p, EPI == EPI_STATS ? g.inv_tau : 1.0f);
         __syncthreads();
         // the slots: thread (s, part) looks for those of its token in its half of the ids
         constexpr int PW = M_T / 2;
@@ -513,47 +558,44 @@ __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(H
       }
     }
   } else {
-    // fp32, 128 rows a pass: staged row s is row 32 TI (s / 64) + 64 p + s % 64 of the tile
-    constexpr int PITCH = N_T + STAGE_PAD / 4;
-    constexpr int LPR = N_T / 8, RPI = 256 / LPR;
-    float* stage = (float*)smem;
-    const int col = n0 + (t % LPR) * 8;
+    constexpr int LPR = M_T / 8, RPI = 256 / LPR;              // lanes a row, 8 values each; rows a round
+    const int col = m0 + (t % LPR) * 8;
+    if (EPI == EPI_DW && splits == 1 && g.out_bf16) {
 #pragma unroll
-    for (int p = 0; p < M_T / STAGE_ROWS; ++p) {
+      for (int j = 0; j < TJ; ++j) stage_bf16(j);
+      __syncthreads();
+#pragma unroll 4
+      for (int s = t / LPR; s < N_T; s += RPI)
+        if (n0 + s < N && col < M)
+          *(uint4*)((uint16_t*)g.dw + (int64_t)(n0 + s) * g.hidden + col) =
+              *(const uint4*)(smem + s * PITCHB + (t % LPR) * 16);
+      return;
+    }
+    // dx partials: the splits' live rows, in whole tiles, one after the other; dW itself, or its partials
+    float* out = EPI == EPI_DW && splits == 1
+                     ? (float*)g.dw
+                     : g.part + (int64_t)split * (EPI == EPI_DX ? tiles_n * N_T : g.dz_ld) * g.hidden;
 #pragma unroll
-      for (int ii = 0; ii < 2; ++ii)
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-#pragma unroll
-          for (int j = 0; j < TJ; ++j)
-            stage[(wm * 64 + 32 * ii + 8 * (r >> 2) + 4 * lg + (r & 3)) * PITCH + wn * 32 * TJ + 32 * j + lr] =
-                acc[2 * p + ii][j][r];
+    for (int p = 0; p < N_T / STAGE_ROWS; ++p) {
+      stage_f32(p, 1.0f);
       __syncthreads();
 #pragma unroll 4
       for (int s = t / LPR; s < STAGE_ROWS; s += RPI) {
         const float* q = stage + s * PITCH + (t % LPR) * 8;
         float4 lo = *(const float4*)q, hi = *(const float4*)(q + 4);
-        const int row = m0 + 32 * TI * (s / 64) + 64 * p + s % 64;
-        if (row < M && col < N) {
-          // dx partials: the splits' live rows, in whole tiles, one after the other; dW itself, or its partials
-          const int64_t at = (int64_t)split * (EPI == EPI_DX ? tiles_m * M_T : g.dz_ld) * g.hidden +
-                             (int64_t)row * g.hidden + col;
-          if (EPI == EPI_DW && splits == 1 && g.out_bf16) {
-            *(uint4*)((uint16_t*)g.dw + at) =
-                make_uint4(pk_bf16(lo.x, lo.y), pk_bf16(lo.z, lo.w), pk_bf16(hi.x, hi.y), pk_bf16(hi.z, hi.w));
-          } else {
-            float4* o = (float4*)((EPI == EPI_DW && splits == 1 ? (float*)g.dw : g.part) + at);
-            if (EPI == EPI_DX && g.add) {
-              const float4 u = o[0], v = o[1];
-              lo = make_float4(lo.x + u.x, lo.y + u.y, lo.z + u.z, lo.w + u.w);
-              hi = make_float4(hi.x + v.x, hi.y + v.y, hi.z + v.z, hi.w + v.w);
-            }
-            o[0] = lo;
-            o[1] = hi;
+        const int row = n0 + 32 * TJ * (s / 64) + 64 * p + s % 64;
+        if (row < N && col < M) {
+          float4* o = (float4*)(out + (int64_t)row * g.hidden + col);
+          if (EPI == EPI_DX && g.add) {
+            const float4 u = o[0], v = o[1];
+            lo = make_float4(lo.x + u.x, lo.y + u.y, lo.z + u.z, lo.w + u.w);
+            hi = make_float4(hi.x + v.x, hi.y + v.y, hi.z + v.z, hi.w + v.w);
           }
+          o[0] = lo;
+          o[1] = hi;
         }
       }
-      if (p + 1 < M_T / STAGE_ROWS) __syncthreads();
+      if (p + 1 < N_T / STAGE_ROWS) __syncthreads();
     }
   }
 }
@@ -561,7 +603,7 @@ __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(H
 typedef void (*head_fn)(HeadArgs);
 template <int TI, int TJ, int EPI, bool MULTI>
 static head_fn head_product() {
-  return head_gemm_kernel<TI, TJ, EPI == EPI_DW ? MNMAJ : KMAJ, EPI >= EPI_DX ? MNMAJ : KMAJ, EPI, MULTI>;
+  return head_gemm_kernel<TI, TJ, EPI >= EPI_DX ? MNMAJ : KMAJ, EPI == EPI_DW ? MNMAJ : KMAJ, EPI, MULTI>;
 }
 
 // ---------------------------------------------------------------------------
