@@ -340,47 +340,70 @@ def quantize_pass(recipe, pass_, x, w, dy, states=None, outs=None, stream=None):
 # the ends of a step: the norm ahead of a linear layer, the losses of the head
 # ---------------------------------------------------------------------------
 FMT_OF = {torch.bfloat16: PBS_FMT_BF16, torch.float32: PBS_FMT_F32}
+BF16_F32 = (torch.bfloat16, torch.float32)
+F32 = (torch.float32,)
+I64 = (torch.int64,)
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
-
-
-def _matrix(name, t, shape=None):
+def _matrix(name, t, device, shape=None):
     """Checks a [rows, cols] operand of bf16 or fp32 whose rows are contiguous; returns (format, row stride)."""
-    _need(t.dim() == 2 and (shape is None or t.shape == shape),
-          f"{name}: want shape {tuple(shape) if shape else '[rows, cols]'}, got {tuple(t.shape)}")
-    _need(t.dtype in FMT_OF, f"{name}: want bf16 or fp32, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name}: want shape {tuple(shape) if shape else '[rows, cols]'}, got {tuple(t.shape)}")
+    fmt = FMT_OF.get(t.dtype)
+    if fmt is None:
+        raise ValueError(f"{name}: want bf16 or fp32, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, want {device}")
     rows, cols = t.shape
-    _need(cols <= 1 or t.stride(1) == 1, f"{name}: the last axis must be contiguous")
-    ld = t.stride(0) if rows > 1 else max(cols, 1)
-    _need(ld >= cols, f"{name}: rows overlap (row stride {ld}, {cols} columns)")
-    return FMT_OF[t.dtype], ld
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    if rows <= 1:
+        ld = max(cols, 1)
+    elif ld < cols:
+        raise ValueError(f"{name}: rows overlap (row stride {ld}, {cols} columns)")
+    return fmt, ld
 
 
 def _vector(name, t, n, dtypes, device):
-    """Checks an optional contiguous vector of n values; returns it."""
-    if t is not None:
-        _need(t.shape == (n,) and t.is_contiguous(), f"{name}: want {n} contiguous values, got shape {tuple(t.shape)}")
-        _need(t.dtype in dtypes, f"{name}: got {t.dtype}, want {' or '.join(str(d) for d in dtypes)}")
-        _need(t.device == device, f"{name}: on {t.device}, want {device}")
-    return t
+    """Checks a contiguous vector of n values; returns its address (None: none)."""
+    if t is None:
+        return None
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name}: want {n} contiguous values, got shape {tuple(t.shape)}, strides {t.stride()}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: got {t.dtype}, want {' or '.join(str(d) for d in dtypes)}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, want {device}")
+    return t.data_ptr()
+
+
+def _given(**tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{name} is missing")
 
 
 _HERE = contextlib.nullcontext()
 
 
-def _on(t, stream):
-    """The context that runs a call on t's device and on `stream` (None: that
+def _on(device, stream):
+    """The context that runs a call on `device` and on `stream` (None: the
     device's current stream), so that what the call allocates belongs there."""
-    _need(t.is_cuda, "tensors must be on the GPU")
+    if device.type != "cuda":
+        raise ValueError("tensors must be on the GPU")
     if stream is None:
-        return _HERE if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+        return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=t.device)
-    _need(stream.device == t.device, f"stream of {stream.device} for tensors on {t.device}")
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    if stream.device != device:
+        raise ValueError(f"stream of {stream.device} for tensors on {device}")
     return torch.cuda.stream(stream)
+
+
+def _current(device):
+    """The address of the device's current stream, without building a Stream."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def layernorm(x, gamma=None, beta=None, eps=1e-5, out_dtype=None, y=None, amax=None, stream=None):
@@ -393,26 +416,31 @@ def layernorm(x, gamma=None, beta=None, eps=1e-5, out_dtype=None, y=None, amax=N
     element) receives max |y| as stored: ``quantize(..., known_amax=amax)``
     then needs no pass of its own.
     """
-    x_fmt, ldx = _matrix("x", x)
+    dev = x.device
+    x_fmt, ldx = _matrix("x", x, dev)
     R, C = x.shape
-    _need(C >= 1, "x: no columns")
-    both = tuple(FMT_OF)
-    _vector("gamma", gamma, C, both, x.device)
-    _vector("beta", beta, C, both, x.device)
-    _need(gamma is None or beta is None or gamma.dtype == beta.dtype, "gamma and beta must have the same type")
-    w = gamma if gamma is not None else beta
-    _vector("amax", amax, 1, (torch.float32,), x.device)
-    _need(y is None or out_dtype in (None, y.dtype), "out_dtype is not y's")
-    with _on(x, stream):
+    if C < 1:
+        raise ValueError("x: no columns")
+    g, b = _vector("gamma", gamma, C, BF16_F32, dev), _vector("beta", beta, C, BF16_F32, dev)
+    if g is not None and b is not None and gamma.dtype != beta.dtype:
+        raise ValueError("gamma and beta must have the same type")
+    w = gamma if g is not None else beta
+    a = _vector("amax", amax, 1, F32, dev)
+    if y is None:
+        if out_dtype is not None and out_dtype not in FMT_OF:
+            raise ValueError(f"out_dtype: want bf16 or fp32, got {out_dtype}")
+    else:
+        if out_dtype not in (None, y.dtype):
+            raise ValueError("out_dtype is not y's")
+        y_fmt, ldy = _matrix("y", y, dev, x.shape)
+    with _on(dev, stream):
         if y is None:
-            _need(out_dtype is None or out_dtype in FMT_OF, f"out_dtype: want bf16 or fp32, got {out_dtype}")
-            y = torch.empty((R, C), dtype=out_dtype or x.dtype, device=x.device)
-        _need(y.device == x.device, f"y: on {y.device}, want {x.device}")
-        y_fmt, ldy = _matrix("y", y, x.shape)
-        mean = torch.empty(R, dtype=torch.float32, device=x.device)
-        rstd = torch.empty(R, dtype=torch.float32, device=x.device)
-        pbs_layernorm(x, x_fmt, R, C, ldx, gamma, beta, PBS_FMT_F32 if w is None else FMT_OF[w.dtype], eps, y, y_fmt,
-                      ldy, mean, rstd, amax)
+            y = torch.empty((R, C), dtype=out_dtype or x.dtype, device=dev)
+            y_fmt, ldy = FMT_OF[y.dtype], C
+        mean = torch.empty(R, dtype=torch.float32, device=dev)
+        rstd = torch.empty(R, dtype=torch.float32, device=dev)
+        pbs_layernorm(x.data_ptr(), x_fmt, R, C, ldx, g, b, PBS_FMT_F32 if w is None else FMT_OF[w.dtype], eps,
+                      y.data_ptr(), y_fmt, ldy, mean.data_ptr(), rstd.data_ptr(), a, _current(dev))
     return y, mean, rstd
 
 
@@ -421,64 +449,84 @@ def layernorm_grad(dy, x, gamma, mean, rstd, dx=None, stream=None):
     dbeta [C] in fp32) from dy [R, C] (bf16 or fp32), the forward's x, gamma
     (None: 1) and the statistics it returned.  ``dx`` may be given, x or dy
     itself among the choices."""
-    x_fmt, ldx = _matrix("x", x)
+    dev = x.device
+    x_fmt, ldx = _matrix("x", x, dev)
     R, C = x.shape
-    _need(C >= 1, "x: no columns")
-    y_fmt, lddy = _matrix("dy", dy, x.shape)
-    _need(dy.device == x.device, f"dy: on {dy.device}, want {x.device}")
-    _vector("gamma", gamma, C, tuple(FMT_OF), x.device)
-    _need(mean is not None and rstd is not None, "mean and rstd are the forward's")
-    _vector("mean", mean, R, (torch.float32,), x.device)
-    _vector("rstd", rstd, R, (torch.float32,), x.device)
-    with _on(x, stream):
+    if C < 1:
+        raise ValueError("x: no columns")
+    y_fmt, lddy = _matrix("dy", dy, dev, x.shape)
+    g = _vector("gamma", gamma, C, BF16_F32, dev)
+    _given(mean=mean, rstd=rstd)
+    m, r = _vector("mean", mean, R, F32, dev), _vector("rstd", rstd, R, F32, dev)
+    lddx = C
+    if dx is not None:
+        d_fmt, lddx = _matrix("dx", dx, dev, x.shape)
+        if d_fmt != x_fmt:
+            raise ValueError(f"dx: want x's type, got {dx.dtype}")
+    with _on(dev, stream):
         if dx is None:
-            dx = torch.empty((R, C), dtype=x.dtype, device=x.device)
-        _need(dx.dtype == x.dtype and dx.device == x.device, "dx: want x's type and device")
-        lddx = _matrix("dx", dx, x.shape)[1]
-        dgamma = torch.empty(C, dtype=torch.float32, device=x.device)
-        dbeta = torch.empty(C, dtype=torch.float32, device=x.device)
+            dx = torch.empty((R, C), dtype=x.dtype, device=dev)
+        dgamma = torch.empty(C, dtype=torch.float32, device=dev)
+        dbeta = torch.empty(C, dtype=torch.float32, device=dev)
         n = pbs_layernorm_grad_bytes(R, C)
-        ws = torch.empty(n, dtype=torch.uint8, device=x.device)
-        pbs_layernorm_grad(dy, y_fmt, lddy, x, x_fmt, ldx, R, C, gamma,
-                           PBS_FMT_F32 if gamma is None else FMT_OF[gamma.dtype], mean, rstd, dx, lddx, dgamma, dbeta,
-                           ws, n)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        pbs_layernorm_grad(dy.data_ptr(), y_fmt, lddy, x.data_ptr(), x_fmt, ldx, R, C, g,
+                           PBS_FMT_F32 if g is None else FMT_OF[gamma.dtype], m, r, dx.data_ptr(), lddx,
+                           dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), n, _current(dev))
     return dx, dgamma, dbeta
 
 
 def _head(x, w):
     """Checks the head's operands; returns (tokens, vocab, hidden)."""
     for name, t in (("x", x), ("w", w)):
-        _need(t.dim() == 2 and t.dtype == torch.bfloat16 and t.is_contiguous(),
-              f"{name}: want a contiguous bf16 matrix, got {t.dtype} {tuple(t.shape)}")
-    _need(w.device == x.device, f"w: on {w.device}, want {x.device}")
-    _need(w.shape[1] == x.shape[1], f"w {tuple(w.shape)} does not fit x {tuple(x.shape)}")
-    return x.shape[0], w.shape[0], x.shape[1]
+        if t.dim() != 2 or t.dtype != torch.bfloat16 or not t.is_contiguous():
+            raise ValueError(f"{name}: want a contiguous bf16 matrix, got {t.dtype} {tuple(t.shape)}, strides "
+                             f"{t.stride()}")
+    T, H = x.shape
+    V = w.shape[0]
+    if w.shape[1] != H or V < 1:
+        raise ValueError(f"w {tuple(w.shape)} does not fit x {tuple(x.shape)}")
+    if w.device != x.device:
+        raise ValueError(f"w: on {w.device}, want {x.device}")
+    return T, V, H
 
 
 def _teacher(top_ids, top_logits, T, device):
-    _need(top_ids.dim() == 2 and top_ids.shape[0] == T and top_ids.shape[1] >= 1 and top_ids.is_contiguous() and
-          top_ids.dtype == torch.int64, f"top_ids: want contiguous int64 [{T}, top], got {top_ids.dtype} "
-          f"{tuple(top_ids.shape)}")
-    _need(top_logits.shape == top_ids.shape and top_logits.is_contiguous() and top_logits.dtype in FMT_OF,
-          f"top_logits: want contiguous bf16 or fp32 {tuple(top_ids.shape)}, got {top_logits.dtype} "
-          f"{tuple(top_logits.shape)}")
-    _need(top_ids.device == device and top_logits.device == device, f"the teacher's tensors must be on {device}")
+    if (top_ids.dim() != 2 or top_ids.shape[0] != T or top_ids.shape[1] < 1 or not top_ids.is_contiguous() or
+            top_ids.dtype != torch.int64):
+        raise ValueError(f"top_ids: want contiguous int64 [{T}, top], got {top_ids.dtype} {tuple(top_ids.shape)}")
+    if top_logits.shape != top_ids.shape or not top_logits.is_contiguous() or top_logits.dtype not in FMT_OF:
+        raise ValueError(f"top_logits: want contiguous bf16 or fp32 {tuple(top_ids.shape)}, got {top_logits.dtype} "
+                         f"{tuple(top_logits.shape)}")
+    if top_ids.device != device or top_logits.device != device:
+        raise ValueError(f"the teacher's tensors must be on {device}")
     return top_ids.shape[1]
 
 
-def _loss_outputs(T, V, H, top, x):
-    n = pbs_linear_loss_bytes(T, V, H, top)[0]
-    return (torch.empty(T, dtype=torch.float32, device=x.device), torch.empty(T, dtype=torch.float32, device=x.device),
-            torch.empty(n, dtype=torch.uint8, device=x.device), n)
+def _loss(dev, stream, T, V, H, top, call):
+    """Allocates a loss's outputs and workspace and makes the call."""
+    with _on(dev, stream):
+        n = pbs_linear_loss_bytes(T, V, H, top)[0]
+        loss = torch.empty(T, dtype=torch.float32, device=dev)
+        lse = torch.empty(T, dtype=torch.float32, device=dev)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        call(loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), n, _current(dev))
+    return loss, lse
 
 
-def _grad_outputs(T, V, H, top, piece, x, need_dx, need_dw, dw_dtype):
-    _need(need_dx or need_dw, "neither dx nor dw is wanted")
-    _need(dw_dtype in FMT_OF, f"dw_dtype: want bf16 or fp32, got {dw_dtype}")
-    n = pbs_linear_loss_bytes(T, V, H, top, piece)[1]
-    return (torch.empty((T, H), dtype=torch.bfloat16, device=x.device) if need_dx else None,
-            torch.empty((V, H), dtype=dw_dtype, device=x.device) if need_dw else None,
-            torch.empty(n, dtype=torch.uint8, device=x.device), n)
+def _loss_grad(dev, stream, T, V, H, top, piece, need_dx, need_dw, dw_dtype, call):
+    """The same for a gradient."""
+    if not (need_dx or need_dw):
+        raise ValueError("neither dx nor dw is wanted")
+    if dw_dtype not in FMT_OF:
+        raise ValueError(f"dw_dtype: want bf16 or fp32, got {dw_dtype}")
+    with _on(dev, stream):
+        n = pbs_linear_loss_bytes(T, V, H, top, piece)[1]
+        dx = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if need_dx else None
+        dw = torch.empty((V, H), dtype=dw_dtype, device=dev) if need_dw else None
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        call(piece, dx, dw, FMT_OF[dw_dtype], ws.data_ptr(), n, _current(dev))
+    return dx, dw
 
 
 def linear_xent(x, w, targets, stream=None):
@@ -488,12 +536,10 @@ def linear_xent(x, w, targets, stream=None):
     lse = log sum exp of a token's logits is what ``linear_xent_grad`` takes.
     """
     T, V, H = _head(x, w)
-    _need(targets is not None, "targets are missing")
-    _vector("targets", targets, T, (torch.int64,), x.device)
-    with _on(x, stream):
-        loss, lse, ws, n = _loss_outputs(T, V, H, 0, x)
-        pbs_linear_xent(x, w, T, V, H, targets, loss, lse, ws, n)
-    return loss, lse
+    _given(targets=targets)
+    t = _vector("targets", targets, T, I64, x.device)
+    return _loss(x.device, stream, T, V, H, 0,
+                 lambda *a: pbs_linear_xent(x.data_ptr(), w.data_ptr(), T, V, H, t, *a))
 
 
 def linear_xent_grad(dloss, x, w, targets, lse, piece=0, need_dx=True, need_dw=True, dw_dtype=torch.bfloat16,
@@ -502,14 +548,11 @@ def linear_xent_grad(dloss, x, w, targets, lse, piece=0, need_dx=True, need_dw=T
     [V, H] in ``dw_dtype``), None for one that is not needed.  The workspace
     holds the logits' gradient for ``piece`` ids at a time (0: about 1 GiB)."""
     T, V, H = _head(x, w)
-    _need(dloss is not None and targets is not None and lse is not None, "dloss, targets or lse is missing")
-    _vector("targets", targets, T, (torch.int64,), x.device)
-    _vector("dloss", dloss, T, (torch.float32,), x.device)
-    _vector("lse", lse, T, (torch.float32,), x.device)
-    with _on(x, stream):
-        dx, dw, ws, n = _grad_outputs(T, V, H, 0, piece, x, need_dx, need_dw, dw_dtype)
-        pbs_linear_xent_grad(dloss, x, w, T, V, H, targets, lse, piece, dx, dw, FMT_OF[dw_dtype], ws, n)
-    return dx, dw
+    _given(dloss=dloss, targets=targets, lse=lse)
+    t = _vector("targets", targets, T, I64, x.device)
+    d, s = _vector("dloss", dloss, T, F32, x.device), _vector("lse", lse, T, F32, x.device)
+    return _loss_grad(x.device, stream, T, V, H, 0, piece, need_dx, need_dw, dw_dtype,
+                      lambda *a: pbs_linear_xent_grad(d, x.data_ptr(), w.data_ptr(), T, V, H, t, s, *a))
 
 
 def linear_distill(x, w, top_ids, top_logits, temperature=1.0, stream=None):
@@ -520,11 +563,9 @@ def linear_distill(x, w, top_ids, top_logits, temperature=1.0, stream=None):
     token without used slots; no factor temperature^2 is applied."""
     T, V, H = _head(x, w)
     top = _teacher(top_ids, top_logits, T, x.device)
-    with _on(x, stream):
-        loss, lse, ws, n = _loss_outputs(T, V, H, top, x)
-        pbs_linear_distill(x, w, T, V, H, top_ids, top_logits, FMT_OF[top_logits.dtype], top, temperature, loss, lse,
-                           ws, n)
-    return loss, lse
+    return _loss(x.device, stream, T, V, H, top,
+                 lambda *a: pbs_linear_distill(x.data_ptr(), w.data_ptr(), T, V, H, top_ids.data_ptr(),
+                                               top_logits.data_ptr(), FMT_OF[top_logits.dtype], top, temperature, *a))
 
 
 def linear_distill_grad(dloss, x, w, top_ids, top_logits, temperature, lse, piece=0, need_dx=True, need_dw=True,
@@ -533,11 +574,9 @@ def linear_distill_grad(dloss, x, w, top_ids, top_logits, temperature, lse, piec
     ``linear_xent_grad`` returns them."""
     T, V, H = _head(x, w)
     top = _teacher(top_ids, top_logits, T, x.device)
-    _need(dloss is not None and lse is not None, "dloss or lse is missing")
-    _vector("dloss", dloss, T, (torch.float32,), x.device)
-    _vector("lse", lse, T, (torch.float32,), x.device)
-    with _on(x, stream):
-        dx, dw, ws, n = _grad_outputs(T, V, H, top, piece, x, need_dx, need_dw, dw_dtype)
-        pbs_linear_distill_grad(dloss, x, w, T, V, H, top_ids, top_logits, FMT_OF[top_logits.dtype], top, temperature,
-                                lse, piece, dx, dw, FMT_OF[dw_dtype], ws, n)
-    return dx, dw
+    _given(dloss=dloss, lse=lse)
+    d, s = _vector("dloss", dloss, T, F32, x.device), _vector("lse", lse, T, F32, x.device)
+    return _loss_grad(x.device, stream, T, V, H, top, piece, need_dx, need_dw, dw_dtype,
+                      lambda *a: pbs_linear_distill_grad(d, x.data_ptr(), w.data_ptr(), T, V, H, top_ids.data_ptr(),
+                                                         top_logits.data_ptr(), FMT_OF[top_logits.dtype], top,
+                                                         temperature, s, *a))
