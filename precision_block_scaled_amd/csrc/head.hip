@@ -50,8 +50,10 @@ struct HeadArgs {
   const float* lse;        // per token
   const float* dloss;      // per token
   uint16_t* dz;            // [rows][dz_ld]
-  float* part;             // partial products of dx, or of dW
+  float* dx_part;          // partial products of dx
+  float* dw_part;          // partial products of dW
   void* dw;                // this piece of dW
+  int dx_blocks;           // workgroups of dx ahead of dW's
   int tokens, rows, hidden, slots;   // rows: tokens, rounded up to whole tiles
   int v0, nv;              // this piece: first id, ids in it
   int dz_ld;
@@ -217,8 +219,7 @@ constexpr float LN2 = 0.69314718055994530942f;
 // unit's time there and hold up the wave.
 // ---------------------------------------------------------------------------
 template <int TI, int TJ, int LDA, int LDB, int EPI, bool MULTI>
-__global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(HeadArgs g) {
-  __shared__ __align__(16) uint8_t smem[head_smem<TI, TJ>()];
+__device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8_t* smem) {
   constexpr int M_T = 64 * TI, N_T = 64 * TJ;
 
   const int t = threadIdx.x, lane = t & 63;
@@ -236,9 +237,9 @@ __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(H
   const int nk = EPI <= EPI_DZ ? g.hidden / 64 : ((EPI == EPI_DX ? g.nv : n) + 63) / 64;
   const int tiles_m = (M + M_T - 1) / M_T, tiles_n = (N + N_T - 1) / N_T;
   const int tiles = tiles_m * tiles_n * splits;
-  if ((int)blockIdx.x >= tiles) return;
+  if (block >= tiles) return;
   int tm, tn;
-  tile_of(blockIdx.x, tiles_m, tiles_n * splits, tm, tn);
+  tile_of(block, tiles_m, tiles_n * splits, tm, tn);
   const int split = tn / tiles_n;
   tn -= split * tiles_n;
   const int m0 = tm * M_T, n0 = tn * N_T;
@@ -518,29 +519,37 @@ __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(H
       for (int p = 0; p < N_T / STAGE_ROWS; ++p) {
         stage_f32(p, EPI == EPI_STATS ? g.inv_tau : 1.0f);
         __syncthreads();
-        // the slots: thread (s, part) looks for those of its token in its half of the ids
-        constexpr int PW = M_T / 2;
+        // The slots of staged token s.  For the loss its two threads share
+        // the slots; for dz, where slots of one id add up in one place, they
+        // share the ids, and every place has one writer.
+        constexpr int PW = EPI == EPI_STATS ? M_T : M_T / 2;
         const int s = t % STAGE_ROWS, part = t / STAGE_ROWS;
         const int at_tile = 32 * TJ * (s / 64) + 64 * p + s % 64;
         if (n0 + at_tile < n) {
           const int token = g.row_of[n0 + at_tile];
-          float* mine = stage + s * PITCH + part * PW;
-          const int first = g.v0 + m0 + part * PW;
-          const int some = have - part * PW < PW ? have - part * PW : PW;
+          const int c0 = EPI == EPI_STATS ? 0 : part * PW;
+          float* mine = stage + s * PITCH + c0;
+          const int first = g.v0 + m0 + c0;
+          const int some = have - c0 < PW ? have - c0 : PW;    // ids in reach; none if negative
           const int64_t at = (int64_t)token * g.slots;
           const int4* ids = (const int4*)(g.ids + at);
-          auto slot = [&](int id, int64_t k) {
-            const int c = id - first;
-            if (id < 0 || c < 0 || c >= some) return;
-            if (EPI == EPI_STATS) g.zsel[k] = mine[c];
-            else mine[c] -= g.p[k] * scale[at_tile];
-          };
-          for (int q = 0; q < g.slots / 4; ++q) {
-            const int4 id4 = ids[q];
-            slot(id4.x, at + 4 * q);
-            slot(id4.y, at + 4 * q + 1);
-            slot(id4.z, at + 4 * q + 2);
-            slot(id4.w, at + 4 * q + 3);
+          const int q1 = g.slots / 4;
+          for (int q = EPI == EPI_STATS ? 4 * part : 0; q < q1; q += EPI == EPI_STATS ? 8 : 4) {
+            int4 id4[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) id4[u] = q + u < q1 ? ids[q + u] : make_int4(-1, -1, -1, -1);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int id = k == 0 ? id4[u].x : k == 1 ? id4[u].y : k == 2 ? id4[u].z : id4[u].w;
+                const int c = id - first;
+                if (id < 0 || c < 0 || c >= some) continue;
+                const int64_t slot = at + 4 * (q + u) + k;
+                if (EPI == EPI_STATS) g.zsel[slot] = mine[c];
+                else mine[c] -= g.p[slot] * scale[at_tile];
+              }
+            }
           }
         }
         __syncthreads();
@@ -574,7 +583,8 @@ __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(H
     // dx partials: the splits' live rows, in whole tiles, one after the other; dW itself, or its partials
     float* out = EPI == EPI_DW && splits == 1
                      ? (float*)g.dw
-                     : g.part + (int64_t)split * (EPI == EPI_DX ? tiles_n * N_T : g.dz_ld) * g.hidden;
+                     : (EPI == EPI_DX ? g.dx_part + (int64_t)split * tiles_n * N_T * g.hidden
+                                        : g.dw_part + (int64_t)split * g.dz_ld * g.hidden);
 #pragma unroll
     for (int p = 0; p < N_T / STAGE_ROWS; ++p) {
       stage_f32(p, 1.0f);
@@ -600,10 +610,21 @@ __global__ __launch_bounds__(256, TI * TJ >= 16 ? 1 : 2) void head_gemm_kernel(H
   }
 }
 
-typedef void (*head_fn)(HeadArgs);
-template <int TI, int TJ, int EPI, bool MULTI>
-static head_fn head_product() {
-  return head_gemm_kernel<TI, TJ, EPI >= EPI_DX ? MNMAJ : KMAJ, EPI == EPI_DW ? MNMAJ : KMAJ, EPI, MULTI>;
+// z's statistics or dz, T x T tiles of 64 values.
+template <int T, int EPI, bool MULTI>
+__global__ __launch_bounds__(256, T >= 4 ? 1 : 2) void head_logits_kernel(HeadArgs g) {
+  __shared__ __align__(16) uint8_t smem[head_smem<T, T>()];
+  head_product<T, T, KMAJ, KMAJ, EPI, MULTI>(g, blockIdx.x, smem);
+}
+
+// dx and dW of a piece in one launch: the two need nothing of each other, and
+// the tiles of one fill the compute units that the other's last round leaves
+// idle.  dx's tiles, the longer ones, come first.
+template <int T>
+__global__ __launch_bounds__(256, T >= 4 ? 1 : 2) void head_grads_kernel(HeadArgs g) {
+  __shared__ __align__(16) uint8_t smem[head_smem<T, T>()];
+  if ((int)blockIdx.x < g.dx_blocks) head_product<T, T, MNMAJ, KMAJ, EPI_DX, false>(g, blockIdx.x, smem);
+  else head_product<T, T, MNMAJ, MNMAJ, EPI_DW, false>(g, blockIdx.x - g.dx_blocks, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -706,75 +727,85 @@ struct RowsArgs {
   int* pos_of;             // token -> live row, or -1
   float* loss;             // of the tokens that take no part: 0 (null in the gradient)
   float* lse;
-  int tile_m, dx_tn, dx_nk, dw_tiles, slots;     // the gradient's products, for their splits
+  const uint4* x;
+  uint4* xc;
+  int chunks;              // 16-byte chunks of a row of x
+  int tile, dx_tn, dx_nk, dw_tiles, slots;       // the gradient's products, for their splits
 };
 
-// The live tokens in order, by one workgroup: a wave takes 8 x 64 consecutive
-// tokens a step, ranks them by ballots, and the waves' counts are added up in LDS.
-constexpr int ROWS_THR = 1024, ROWS_PER = 8;
+// The live tokens in order, and their rows of x one after the other (unless
+// every token is live: the products then read x itself).  Every workgroup
+// counts all tokens, 8 x 64 consecutive ones a wave and step by ballots, and
+// so knows how many are live ahead of its own share of the tokens, which it
+// then ranks and copies: one launch instead of a scan and a copy.
+constexpr int ROWS_THR = 1024, ROWS_PER = 8, ROWS_WAVES = ROWS_THR / 64;
 __global__ __launch_bounds__(ROWS_THR) void head_rows_kernel(RowsArgs a) {
-  __shared__ int wave_n[2][ROWS_THR / 64];
+  __shared__ int wave_n[2][ROWS_WAVES][2];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  int base = 0, buf = 0;
+  auto is_live = [&](int64_t t) { return a.targets ? a.targets[t] >= 0 : a.state[t] != ROW_OUT; };
+  // this workgroup's tokens: [lo, hi), whole groups of 64
+  const int64_t groups = ((int64_t)a.tokens + 63) / 64;
+  const int64_t lo = groups * blockIdx.x / gridDim.x * 64;
+  int64_t hi = groups * (blockIdx.x + 1) / gridDim.x * 64;
+  hi = hi < a.tokens ? hi : a.tokens;
+  int n = 0, before = 0, buf = 0;
   for (int64_t t0 = 0; t0 < a.tokens; t0 += ROWS_THR * ROWS_PER, buf ^= 1) {
-    const int64_t first = t0 + w * 64 * ROWS_PER + lane;
+    const int64_t first = t0 + w * 64 * ROWS_PER;
     bool on[ROWS_PER];
 #pragma unroll
     for (int i = 0; i < ROWS_PER; ++i) {
-      const int64_t t = first + 64 * i;
-      on[i] = t < a.tokens && (a.targets ? a.targets[t] >= 0 : a.state[t] != ROW_OUT);
+      const int64_t t = first + 64 * i + lane;
+      on[i] = t < a.tokens && is_live(t);
     }
-    uint64_t mask[ROWS_PER];
-    int mine = 0;
+    int all = 0, ahead = 0;
 #pragma unroll
     for (int i = 0; i < ROWS_PER; ++i) {
-      mask[i] = __ballot(on[i]);
-      mine += __popcll(mask[i]);
+      const int c = __popcll(__ballot(on[i]));
+      all += c;
+      ahead += first + 64 * i < lo ? c : 0;
     }
-    if (lane == 0) wave_n[buf][w] = mine;
+    if (lane == 0) {
+      wave_n[buf][w][0] = all;
+      wave_n[buf][w][1] = ahead;
+    }
     __syncthreads();
-    int at = base;
 #pragma unroll
-    for (int i = 0; i < ROWS_THR / 64; ++i) {
-      const int c = wave_n[buf][i];
-      at += i < w ? c : 0;
-      base += c;
+    for (int i = 0; i < ROWS_WAVES; ++i) {
+      n += wave_n[buf][i][0];
+      before += wave_n[buf][i][1];
     }
-#pragma unroll
-    for (int i = 0; i < ROWS_PER; ++i) {
-      const int64_t t = first + 64 * i;
-      const int pos = at + __popcll(mask[i] & ((1ull << lane) - 1));
-      at += __popcll(mask[i]);
-      if (t >= a.tokens) continue;
-      a.pos_of[t] = on[i] ? pos : -1;
-      if (on[i]) a.row_of[pos] = (int)t;
-      if (!on[i] && a.loss) {
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.live[0] = n;
+    if (!a.loss) {
+      a.live[1] = head_splits((int64_t)((n + a.tile - 1) / a.tile) * a.dx_tn, a.dx_nk, a.slots);
+      a.live[2] = head_splits(a.dw_tiles, (n + 63) / 64, a.slots);
+    }
+  }
+  // groups of 64 of the own tokens, one after the other for every wave, which
+  // copies every 16th row
+  for (int64_t t0 = lo; t0 < hi; t0 += 64) {
+    const int64_t t = t0 + lane;
+    const bool in = t < hi, on = in && is_live(t);
+    const uint64_t mask = __ballot(on);
+    const int pos = before + __popcll(mask & ((1ull << lane) - 1));
+    if (in && w == 0) {
+      a.pos_of[t] = on ? pos : -1;
+      if (on) a.row_of[pos] = (int)t;
+      if (!on && a.loss) {
         a.loss[t] = 0.0f;
         a.lse[t] = 0.0f;
       }
     }
-  }
-  if (threadIdx.x == 0) {
-    a.live[0] = base;
-    if (!a.loss) {
-      a.live[1] = head_splits((int64_t)((base + a.tile_m - 1) / a.tile_m) * a.dx_tn, a.dx_nk, a.slots);
-      a.live[2] = head_splits(a.dw_tiles, (base + 63) / 64, a.slots);
+    if (n < a.tokens) {
+      for (int k = w; k < 64; k += ROWS_WAVES) {
+        if (!((mask >> k) & 1)) continue;
+        const uint4* from = a.x + (t0 + k) * a.chunks;
+        uint4* to = a.xc + (int64_t)(before + __popcll(mask & ((1ull << k) - 1))) * a.chunks;
+        for (int c = lane; c < a.chunks; c += 64) to[c] = from[c];
+      }
     }
-  }
-}
-
-// The live rows of x, one after the other: a wave per row.  Nothing to do when
-// every token is live (the products then read x itself).
-constexpr int GATHER_THR = 512;
-__global__ __launch_bounds__(GATHER_THR) void head_gather_kernel(const uint4* x, uint4* xc, const int* live,
-                                                                 const int* row_of, int tokens, int chunks) {
-  constexpr int PER = GATHER_THR / 64;
-  const int n = *live;
-  if (n == tokens) return;
-  for (int64_t i = (int64_t)blockIdx.x * PER + (threadIdx.x >> 6); i < n; i += (int64_t)gridDim.x * PER) {
-    const uint4* from = x + (int64_t)row_of[i] * chunks;
-    uint4* to = xc + i * chunks;
-    for (int c = threadIdx.x & 63; c < chunks; c += 64) to[c] = from[c];
+    before += __popcll(mask);
   }
 }
 
@@ -913,17 +944,23 @@ constexpr int HEAD_TILE = 256, HEAD_SMALL = 128, HEAD_CUS = 256;
 
 struct HeadPlan {
   int64_t rows, slots, parts, piece;
-  int loss_tile, grad_tile, wg_slots;                    // the gradient's workgroups at a time
+  int loss_tile, dz_tile, grad_tile, wg_slots;                    // the gradient's workgroups at a time
   int64_t dx_grid, dw_grid;                              // most tiles, splits included
-  bool dw_can_split;
+  bool dw_can_split, apart;
   size_t live, row_of, pos_of, state, ids, p, ent, xc;
   size_t zsel, stats, loss_bytes;                        // the loss
   size_t dz, dxp, dwp, grad_bytes;                       // the gradient
 };
 
-// The tile of products whose 256 x 256 tiles are `tiles`: while these leave
-// most compute units idle, four times as many small ones.
-static int head_tile(int64_t tiles) { return tiles < HEAD_CUS ? HEAD_SMALL : HEAD_TILE; }
+// The tile of a product of rows x cols outputs.  A round of 256 x 256 tiles,
+// one a compute unit, takes 1.64 times a round of 128 x 128 ones, two a
+// compute unit (100 and 61 us at 64 K stages; on 4096 x 32768 outputs 0.80
+// against 0.98 ms), so the small tile pays where rounds are few and unfilled.
+static int head_tile(int64_t rows, int64_t cols) {
+  const int64_t big = ceil_div(ceil_div(rows, HEAD_TILE) * ceil_div(cols, HEAD_TILE), HEAD_CUS);
+  const int64_t small = ceil_div(ceil_div(rows, HEAD_SMALL) * ceil_div(cols, HEAD_SMALL), 2 * HEAD_CUS);
+  return big * 164 <= small * 100 ? HEAD_TILE : HEAD_SMALL;
+}
 
 static HeadPlan head_plan(int64_t tokens, int64_t vocab, int64_t hidden, int64_t top, bool xent, int64_t piece) {
   HeadPlan h = {};
@@ -936,7 +973,7 @@ static HeadPlan head_plan(int64_t tokens, int64_t vocab, int64_t hidden, int64_t
   const int64_t tm = ceil_div(tokens, HEAD_TILE), tv = ceil_div(vocab, HEAD_TILE), th = ceil_div(hidden, HEAD_TILE);
   h.rows = tm * HEAD_TILE;
   h.slots = xent ? 1 : ceil_div(top, 4) * 4;
-  h.loss_tile = head_tile(tm * tv);
+  h.loss_tile = head_tile(tokens, vocab);
   h.parts = ceil_div(vocab, h.loss_tile) * 2;
   h.live = take(12);
   h.row_of = take(4 * tokens);
@@ -954,15 +991,22 @@ static HeadPlan head_plan(int64_t tokens, int64_t vocab, int64_t hidden, int64_t
   // default piece: dz of a piece at most 1 GiB, and at least 2048 ids
   if (piece <= 0) piece = std::max<int64_t>(2048, (1ll << 30) / (2 * std::max<int64_t>(h.rows, 1)));
   h.piece = std::min(ceil_div(piece, HEAD_TILE), tv) * HEAD_TILE;
-  h.grad_tile = head_tile(tm * (h.piece / HEAD_TILE));
+  h.dz_tile = head_tile(tokens, std::min(h.piece, vocab));
+  // dx and dW together, dx counted as the splits it may have: small tiles while both leave compute units idle
+  h.grad_tile = (h.piece / HEAD_TILE + tm) * th < HEAD_CUS / 2 ? HEAD_SMALL : HEAD_TILE;
   h.wg_slots = h.grad_tile == HEAD_TILE ? HEAD_CUS : 2 * HEAD_CUS;
   const int64_t hn = ceil_div(hidden, h.grad_tile);
-  h.dx_grid = std::max<int64_t>(ceil_div(tokens, h.grad_tile) * hn, HEAD_SPLIT_TILES);
+  h.dx_grid = ceil_div(std::max<int64_t>(ceil_div(tokens, h.grad_tile) * hn, HEAD_SPLIT_TILES), NXCD) * NXCD;
   h.dw_grid = std::max<int64_t>(h.piece / h.grad_tile * hn, HEAD_SPLIT_TILES);
   h.dz = take(2 * h.rows * h.piece);
   // partial products: the tiles of one product, or of all splits of one that is split
   const int64_t tile_values = (int64_t)h.grad_tile * hidden;
   h.dxp = take(4 * tile_values * std::max(ceil_div(tokens, h.grad_tile), HEAD_SPLIT_TILES / hn));
+  // Two full rounds of dx tiles need nothing to fill up with, and the two
+  // products then run apart, each with its own operands in the caches (8192 x
+  // 131072 x 4096: 19.26 ms apart, 19.58 together; 512 x 32000 x 2048: 239 us
+  // apart, 221 together).
+  h.apart = ceil_div(tokens, h.grad_tile) * hn >= 2 * h.wg_slots;
   // as head_splits decides for any number of live rows
   h.dw_can_split = h.piece / h.grad_tile * hn * 2 <= HEAD_SPLIT_TILES && ceil_div(tokens, 64) / 2 >= HEAD_LEAST_STAGES;
   h.dwp = take(h.dw_can_split ? 4 * tile_values * (HEAD_SPLIT_TILES / hn) : 0);
@@ -1062,12 +1106,11 @@ static HeadArgs head_rows(const HeadCall& c, const HeadPlan& h, hipStream_t stre
   r.targets = c.targets; r.state = (const int*)(ws + h.state); r.tokens = (int)c.tokens;
   r.live = (int*)(ws + h.live); r.row_of = (int*)(ws + h.row_of); r.pos_of = (int*)(ws + h.pos_of);
   r.loss = c.loss; r.lse = c.loss ? c.lse : nullptr;
-  r.tile_m = h.grad_tile; r.dx_tn = (int)ceil_div(c.hidden, h.grad_tile); r.dx_nk = (int)(h.piece / 64);
+  r.x = (const uint4*)c.x; r.xc = (uint4*)(ws + h.xc); r.chunks = (int)(c.hidden / 8);
+  r.tile = h.grad_tile; r.dx_tn = (int)ceil_div(c.hidden, h.grad_tile); r.dx_nk = (int)(h.piece / 64);
   r.dw_tiles = (int)(h.piece / h.grad_tile) * r.dx_tn; r.slots = h.wg_slots;
-  hipLaunchKernelGGL(head_rows_kernel, dim3(1), dim3(ROWS_THR), 0, stream, r);
-  hipLaunchKernelGGL(head_gather_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(c.tokens, GATHER_THR / 64), 512)),
-                     dim3(GATHER_THR), 0, stream, (const uint4*)c.x, (uint4*)(ws + h.xc), r.live, r.row_of,
-                     (int)c.tokens, (int)(c.hidden / 8));
+  hipLaunchKernelGGL(head_rows_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(c.tokens, 64), HEAD_CUS)),
+                     dim3(ROWS_THR), 0, stream, r);
   HeadArgs g = {};
   g.x = (const uint8_t*)c.x; g.xc = ws + h.xc; g.w = (const uint8_t*)c.w; g.targets = c.targets;
   g.live = r.live; g.row_of = r.row_of; g.state = r.state; g.ids = (const int*)(ws + h.ids);
@@ -1077,12 +1120,22 @@ static HeadArgs head_rows(const HeadCall& c, const HeadPlan& h, hipStream_t stre
 }
 
 template <int EPI>
-static void head_launch(int tile, int64_t grid, const HeadArgs& g, hipStream_t stream) {
-  constexpr bool SLOTS = EPI <= EPI_DZ;             // the products of dz know no slots
-  const bool multi = SLOTS && !g.targets;
-  head_fn fn = tile == HEAD_TILE ? head_product<4, 4, EPI, false>() : head_product<2, 2, EPI, false>();
-  if (multi) fn = tile == HEAD_TILE ? head_product<4, 4, EPI, SLOTS>() : head_product<2, 2, EPI, SLOTS>();
-  hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(256), 0, stream, g);
+static void head_logits(int tile, const HeadArgs& g, hipStream_t stream) {
+  const unsigned grid = (unsigned)(ceil_div(g.tokens, tile) * ceil_div(g.nv, tile));
+  if (tile == HEAD_TILE) {
+    if (g.targets) hipLaunchKernelGGL((head_logits_kernel<4, EPI, false>), dim3(grid), dim3(256), 0, stream, g);
+    else hipLaunchKernelGGL((head_logits_kernel<4, EPI, true>), dim3(grid), dim3(256), 0, stream, g);
+  } else {
+    if (g.targets) hipLaunchKernelGGL((head_logits_kernel<2, EPI, false>), dim3(grid), dim3(256), 0, stream, g);
+    else hipLaunchKernelGGL((head_logits_kernel<2, EPI, true>), dim3(grid), dim3(256), 0, stream, g);
+  }
+}
+
+static void head_grads(int tile, int64_t dx_blocks, int64_t dw_blocks, HeadArgs g, hipStream_t stream) {
+  g.dx_blocks = (int)dx_blocks;
+  const unsigned grid = (unsigned)(dx_blocks + dw_blocks);
+  if (tile == HEAD_TILE) hipLaunchKernelGGL(head_grads_kernel<4>, dim3(grid), dim3(256), 0, stream, g);
+  else hipLaunchKernelGGL(head_grads_kernel<2>, dim3(grid), dim3(256), 0, stream, g);
 }
 
 static pbs_status head_loss(const HeadCall& c, hipStream_t stream) {
@@ -1092,10 +1145,9 @@ static pbs_status head_loss(const HeadCall& c, hipStream_t stream) {
   uint8_t* ws = (uint8_t*)c.ws;
   HeadArgs g = head_rows(c, h, stream);
   g.zsel = (float*)(ws + h.zsel); g.stats = (float2*)(ws + h.stats);
-  const int64_t grid = ceil_div(c.tokens, h.loss_tile) * ceil_div(c.vocab, h.loss_tile);
-  log_dispatch("%s tokens=%lld vocab=%lld hidden=%lld top=%lld tile=%d tiles=%lld", c.what, (long long)c.tokens,
-               (long long)c.vocab, (long long)c.hidden, (long long)c.top, h.loss_tile, (long long)grid);
-  head_launch<EPI_STATS>(h.loss_tile, grid, g, stream);
+  log_dispatch("%s tokens=%lld vocab=%lld hidden=%lld top=%lld tile=%d", c.what, (long long)c.tokens,
+               (long long)c.vocab, (long long)c.hidden, (long long)c.top, h.loss_tile);
+  head_logits<EPI_STATS>(h.loss_tile, g, stream);
   JoinArgs j = {};
   j.live = g.live; j.row_of = g.row_of; j.targets = g.targets; j.state = g.state; j.ids = g.ids; j.p = g.p;
   j.ent = (const float*)(ws + h.ent); j.zsel = g.zsel; j.stats = g.stats;
@@ -1118,28 +1170,27 @@ static pbs_status head_grad(const HeadCall& c, hipStream_t stream) {
   uint8_t* ws = (uint8_t*)c.ws;
   HeadArgs g = head_rows(c, h, stream);
   g.lse = c.lse; g.dloss = c.dloss; g.dz = (uint16_t*)(ws + h.dz); g.dz_ld = (int)h.piece; g.out_bf16 = dwb == 2;
-  log_dispatch("%s tokens=%lld vocab=%lld hidden=%lld top=%lld piece=%lld tile=%d", c.what, (long long)c.tokens,
-               (long long)c.vocab, (long long)c.hidden, (long long)c.top, (long long)h.piece, h.grad_tile);
+  g.dx_part = (float*)(ws + h.dxp); g.dw_part = (float*)(ws + h.dwp);
+  log_dispatch("%s tokens=%lld vocab=%lld hidden=%lld top=%lld piece=%lld tiles=%d,%d", c.what, (long long)c.tokens,
+               (long long)c.vocab, (long long)c.hidden, (long long)c.top, (long long)h.piece, h.dz_tile, h.grad_tile);
   for (int64_t v0 = 0; v0 < c.vocab; v0 += h.piece) {
     const int64_t nv = std::min(h.piece, c.vocab - v0);
     g.v0 = (int)v0;
     g.nv = (int)nv;
     g.w = (const uint8_t*)c.w + v0 * c.hidden * 2;
-    head_launch<EPI_DZ>(h.grad_tile, ceil_div(c.tokens, h.grad_tile) * ceil_div(nv, h.grad_tile), g, stream);
-    if (c.dx) {
-      g.part = (float*)(ws + h.dxp);
-      g.add = v0 > 0;
-      head_launch<EPI_DX>(h.grad_tile, h.dx_grid, g, stream);
+    g.add = v0 > 0;
+    g.dw = c.dw ? (uint8_t*)c.dw + v0 * c.hidden * dwb : nullptr;
+    head_logits<EPI_DZ>(h.dz_tile, g, stream);
+    if (h.apart && c.dx && c.dw) {
+      head_grads(h.grad_tile, h.dx_grid, 0, g, stream);
+      head_grads(h.grad_tile, 0, h.dw_grid, g, stream);
+    } else {
+      head_grads(h.grad_tile, c.dx ? h.dx_grid : 0, c.dw ? h.dw_grid : 0, g, stream);
     }
-    if (c.dw) {
-      g.part = (float*)(ws + h.dwp);
-      g.dw = (uint8_t*)c.dw + v0 * c.hidden * dwb;
-      head_launch<EPI_DW>(h.grad_tile, h.dw_grid, g, stream);
-      if (h.dw_can_split)
-        hipLaunchKernelGGL(head_dw_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(nv * c.hidden / 8, 256), 2048)),
-                           dim3(256), 0, stream, g.part, g.live, h.piece * c.hidden, nv * c.hidden / 8, g.dw,
-                           g.out_bf16);
-    }
+    if (c.dw && h.dw_can_split)
+      hipLaunchKernelGGL(head_dw_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(nv * c.hidden / 8, 256), 2048)),
+                         dim3(256), 0, stream, g.dw_part, g.live, h.piece * c.hidden, nv * c.hidden / 8, g.dw,
+                         g.out_bf16);
   }
   if (c.dx)
     hipLaunchKernelGGL(head_dx_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(c.tokens * c.hidden / 8, 256), 2048)),
