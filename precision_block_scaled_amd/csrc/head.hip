@@ -49,7 +49,7 @@ struct HeadArgs {
   float2* stats;           // [parts][rows]: maximum of a part of a row over log 2, sum of exponentials above it
   const float* lse;        // per token
   const float* dloss;      // per token
-  uint16_t* dz;            // [rows][dz_ld]
+  uint16_t* dz;            // [rows][dz_ld]; PAIR: [rows][2][dz_ld], dz rounded and what that left out
   float* dx_part;          // partial products of dx
   float* dw_part;          // partial products of dW
   void* dw;                // this piece of dW
@@ -107,8 +107,9 @@ struct KLoad {
       off[i] = (uint32_t)(t < last ? t : last) * (uint32_t)ld + (uint32_t)(((lane & 7) ^ swz_key(t)) << 4);
     }
   }
-  __device__ __forceinline__ void load(int kt, uint8_t* tile, int w, int i) const {
-    buffer_to_lds(b, tile + (w * 2 * T + i) * 1024, off[i], (uint32_t)(kt * ROWB));
+  // K stage kt, `along` bytes further in every row
+  __device__ __forceinline__ void load(int kt, int64_t along, uint8_t* tile, int w, int i) const {
+    buffer_to_lds(b, tile + (w * 2 * T + i) * 1024, off[i], (uint32_t)(kt * ROWB + along));
   }
 };
 
@@ -141,10 +142,10 @@ struct MnLoad {
       off[i] = (uint32_t)row * (uint32_t)ld + (uint32_t)(lc << 4);
     }
   }
-  __device__ __forceinline__ void load(int kt, uint8_t* tile, int w, int i) const {
+  __device__ __forceinline__ void load(int kt, int64_t along, uint8_t* tile, int w, int i) const {
     const int left = krows - 64 * kt;
     const uint32_t top = (uint32_t)((left < 64 ? left : 64) - 1) * (uint32_t)ld + c[i & 1];
-    buffer_to_lds(buffer_rows(base + (int64_t)kt * 64 * ld, (uint32_t)(64 * ld)), tile + (w * 2 * T + i) * 1024,
+    buffer_to_lds(buffer_rows(base + (int64_t)kt * 64 * ld + along, (uint32_t)(64 * ld)), tile + (w * 2 * T + i) * 1024,
                   off[i] < top ? off[i] : top, 0);
   }
 };
@@ -218,7 +219,7 @@ constexpr float LN2 = 0.69314718055994530942f;
 // over the whole stage: issued over phase C alone, they fill the address
 // unit's time there and hold up the wave.
 // ---------------------------------------------------------------------------
-template <int TI, int TJ, int LDA, int LDB, int EPI, bool MULTI>
+template <int TI, int TJ, int LDA, int LDB, int EPI, bool MULTI, bool PAIR>
 __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8_t* smem) {
   constexpr int M_T = 64 * TI, N_T = 64 * TJ;
 
@@ -227,14 +228,17 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
   const int wm = w >> 1, wn = w & 1;
   const int n = g.live[0], splits = EPI <= EPI_DZ ? 1 : g.live[EPI == EPI_DX ? 1 : 2];
   const uint8_t* xs = n == g.tokens ? g.x : g.xc;
-  const int64_t ldx = (int64_t)g.hidden * 2, ldz = (int64_t)g.dz_ld * 2;
+  const int64_t ldx = (int64_t)g.hidden * 2, ldz = (int64_t)g.dz_ld * (PAIR ? 4 : 2);
   // every product is formed transposed: M is the result's contiguous axis (ids
   // of z and dz, hidden of dx and dW), N its rows.  A lane then holds 16 TI
   // values of each of TJ rows, four consecutive ones at a time: a token's
   // maximum, sum and gradient need one other lane, and stores are wide.
   const int M = EPI <= EPI_DZ ? g.nv : g.hidden;
   const int N = EPI == EPI_DW ? g.nv : n;
-  const int nk = EPI <= EPI_DZ ? g.hidden / 64 : ((EPI == EPI_DX ? g.nv : n) + 63) / 64;
+  // PAIR: a stage of dz's rounded part and one of the rest, with the same
+  // stage of the other operand, by turns
+  constexpr int TURNS = PAIR && EPI >= EPI_DX ? 2 : 1;
+  const int nk = EPI <= EPI_DZ ? g.hidden / 64 : ((EPI == EPI_DX ? g.nv : n) + 63) / 64 * TURNS;
   const int tiles_m = (M + M_T - 1) / M_T, tiles_n = (N + N_T - 1) / N_T;
   const int tiles = tiles_m * tiles_n * splits;
   if (block >= tiles) return;
@@ -266,7 +270,7 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
     lb.init((const uint8_t*)g.dz, ldz, n0, n, w);
   } else {
     la.init(xs, ldx, m0, g.hidden, n, w);
-    lb.init((const uint8_t*)g.dz, ldz, n0, g.dz_ld, 64 * nk, w);
+    lb.init((const uint8_t*)g.dz, ldz, n0, g.dz_ld, 64 * nk / TURNS, w);
   }
 
   const int lr = lane & 31, lg = lane >> 5;
@@ -289,6 +293,10 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
   Half<TI> a0, a1;
   Half<TJ> b0, b1;
 
+  auto load_a = [&](int kt, int v) { la.load(kt / TURNS, 0, tileA(kt), w, v); };
+  auto load_b = [&](int kt, int v) {
+    lb.load(kt / TURNS, TURNS == 2 ? (int64_t)(kt & 1) * g.dz_ld * 2 : 0, tileB(kt), w, v);
+  };
   auto mfma = [&](const Half<TI>& a, const Half<TJ>& b, int m) {
     const int s = m / (TI * TJ), i = (m / TJ) % TI, j = m % TJ;
     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a.x[i][s]),
@@ -325,14 +333,14 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
 
   if (k1 > k0) {
 #pragma unroll
-    for (int v = 0; v < NA; ++v) la.load(k0, tileA(k0), w, v);
+    for (int v = 0; v < NA; ++v) load_a(k0, v);
 #pragma unroll
-    for (int v = 0; v < NB; ++v) lb.load(k0, tileB(k0), w, v);
+    for (int v = 0; v < NB; ++v) load_b(k0, v);
     if (k1 > k0 + 1) {
 #pragma unroll
-      for (int v = 0; v < NA; ++v) la.load(k0 + 1, tileA(k0 + 1), w, v);
+      for (int v = 0; v < NA; ++v) load_a(k0 + 1, v);
 #pragma unroll
-      for (int v = 0; v < NB; ++v) lb.load(k0 + 1, tileB(k0 + 1), w, v);
+      for (int v = 0; v < NB; ++v) load_b(k0 + 1, v);
       stage_barrier<NA + NB>();
     } else {
       stage_barrier<0>();
@@ -360,7 +368,7 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
         }
         if (ISSUE) {
 #pragma unroll
-          for (int v = part_lo(NB, NMFMA, m); v < part_hi(NB, NMFMA, m); ++v) lb.load(kt + 2, tileB(kt + 2), w, v);
+          for (int v = part_lo(NB, NMFMA, m); v < part_hi(NB, NMFMA, m); ++v) load_b(kt + 2, v);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -377,7 +385,7 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
         }
         if (ISSUE) {
 #pragma unroll
-          for (int v = part_lo(NA, NMFMA, m); v < part_hi(NA, NMFMA, m); ++v) la.load(kt + 2, tileA(kt + 2), w, v);
+          for (int v = part_lo(NA, NMFMA, m); v < part_hi(NA, NMFMA, m); ++v) load_a(kt + 2, v);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -496,18 +504,35 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
             }
           if (EPI == EPI_STATS && mine) g.zsel[tok[j]] = at * g.inv_tau;
         }
-        if (!MULTI && EPI == EPI_DZ) stage_bf16(j);
+        if (!MULTI && !PAIR && EPI == EPI_DZ) stage_bf16(j);
       }
     };
     if (have == M_T) finish(std::integral_constant<bool, true>{});
     else finish(std::integral_constant<bool, false>{});
+    constexpr int LPR = M_T / 8;                               // lanes a row, 8 values each
+    constexpr int PARTS = PAIR ? 2 : 1;
     if constexpr (!MULTI && EPI == EPI_DZ) {
-      __syncthreads();
-      constexpr int LPR = M_T / 8;                             // lanes a row, 8 values each
+#pragma unroll
+      for (int h = 0; h < PARTS; ++h) {
+        if (PAIR) {
+          if (h) __syncthreads();
+#pragma unroll
+          for (int j = 0; j < TJ; ++j) {
+            if (h) {
+#pragma unroll
+              for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][j][r] -= (float)(__bf16)acc[i][j][r];
+            }
+            stage_bf16(j);
+          }
+        }
+        __syncthreads();
 #pragma unroll 4
-      for (int s = t / LPR; s < N_T; s += 256 / LPR)
-        *(uint4*)(g.dz + (int64_t)(n0 + s) * g.dz_ld + m0 + (t % LPR) * 8) =
-            *(const uint4*)(smem + s * PITCHB + (t % LPR) * 16);
+        for (int s = t / LPR; s < N_T; s += 256 / LPR)
+          *(uint4*)(g.dz + ((int64_t)(n0 + s) * PARTS + h) * g.dz_ld + m0 + (t % LPR) * 8) =
+              *(const uint4*)(smem + s * PITCHB + (t % LPR) * 16);
+      }
     }
     if constexpr (MULTI) {
       // fp32, 128 tokens a pass
@@ -554,13 +579,22 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
         }
         __syncthreads();
         if (EPI == EPI_DZ) {
-          constexpr int LPR = M_T / 8;
 #pragma unroll 4
           for (int s2 = t / LPR; s2 < STAGE_ROWS; s2 += 256 / LPR) {
             const float* q = stage + s2 * PITCH + (t % LPR) * 8;
-            const float4 lo = *(const float4*)q, hi = *(const float4*)(q + 4);
-            *(uint4*)(g.dz + (int64_t)(n0 + 32 * TJ * (s2 / 64) + 64 * p + s2 % 64) * g.dz_ld + m0 + (t % LPR) * 8) =
-                make_uint4(pk_bf16(lo.x, lo.y), pk_bf16(lo.z, lo.w), pk_bf16(hi.x, hi.y), pk_bf16(hi.z, hi.w));
+            float4 lo = *(const float4*)q, hi = *(const float4*)(q + 4);
+            uint16_t* to = g.dz + (int64_t)(n0 + 32 * TJ * (s2 / 64) + 64 * p + s2 % 64) * PARTS * g.dz_ld + m0 +
+                           (t % LPR) * 8;
+#pragma unroll
+            for (int h = 0; h < PARTS; ++h) {
+              *(uint4*)(to + h * g.dz_ld) =
+                  make_uint4(pk_bf16(lo.x, lo.y), pk_bf16(lo.z, lo.w), pk_bf16(hi.x, hi.y), pk_bf16(hi.z, hi.w));
+              if (h + 1 < PARTS) {
+                auto rest = [](float& v) { v -= (float)(__bf16)v; };
+                rest(lo.x); rest(lo.y); rest(lo.z); rest(lo.w);
+                rest(hi.x); rest(hi.y); rest(hi.z); rest(hi.w);
+              }
+            }
           }
           if (p + 1 < N_T / STAGE_ROWS) __syncthreads();
         }
@@ -611,20 +645,20 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
 }
 
 // z's statistics or dz, T x T tiles of 64 values.
-template <int T, int EPI, bool MULTI>
+template <int T, int EPI, bool MULTI, bool PAIR>
 __global__ __launch_bounds__(256, T >= 4 ? 1 : 2) void head_logits_kernel(HeadArgs g) {
   __shared__ __align__(16) uint8_t smem[head_smem<T, T>()];
-  head_product<T, T, KMAJ, KMAJ, EPI, MULTI>(g, blockIdx.x, smem);
+  head_product<T, T, KMAJ, KMAJ, EPI, MULTI, PAIR>(g, blockIdx.x, smem);
 }
 
 // dx and dW of a piece in one launch: the two need nothing of each other, and
 // the tiles of one fill the compute units that the other's last round leaves
 // idle.  dx's tiles, the longer ones, come first.
-template <int T>
+template <int T, bool PAIR>
 __global__ __launch_bounds__(256, T >= 4 ? 1 : 2) void head_grads_kernel(HeadArgs g) {
   __shared__ __align__(16) uint8_t smem[head_smem<T, T>()];
-  if ((int)blockIdx.x < g.dx_blocks) head_product<T, T, MNMAJ, KMAJ, EPI_DX, false>(g, blockIdx.x, smem);
-  else head_product<T, T, MNMAJ, MNMAJ, EPI_DW, false>(g, blockIdx.x - g.dx_blocks, smem);
+  if ((int)blockIdx.x < g.dx_blocks) head_product<T, T, MNMAJ, KMAJ, EPI_DX, false, PAIR>(g, blockIdx.x, smem);
+  else head_product<T, T, MNMAJ, MNMAJ, EPI_DW, false, PAIR>(g, blockIdx.x - g.dx_blocks, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -730,7 +764,7 @@ struct RowsArgs {
   const uint4* x;
   uint4* xc;
   int chunks;              // 16-byte chunks of a row of x
-  int tile, dx_tn, dx_nk, dw_tiles, slots;       // the gradient's products, for their splits
+  int tile, dx_tn, dx_nk, dw_tiles, turns, slots;  // the gradient's products, for their splits
 };
 
 // The live tokens in order, and their rows of x one after the other (unless
@@ -779,7 +813,7 @@ __global__ __launch_bounds__(ROWS_THR) void head_rows_kernel(RowsArgs a) {
     a.live[0] = n;
     if (!a.loss) {
       a.live[1] = head_splits((int64_t)((n + a.tile - 1) / a.tile) * a.dx_tn, a.dx_nk, a.slots);
-      a.live[2] = head_splits(a.dw_tiles, (n + 63) / 64, a.slots);
+      a.live[2] = head_splits(a.dw_tiles, (n + 63) / 64 * a.turns, a.slots);
     }
   }
   // groups of 64 of the own tokens, one after the other for every wave, which
@@ -942,11 +976,20 @@ __global__ void head_zero_kernel(uint4* p, int64_t n16) {
 // Tiles: 256 x 256, one workgroup per compute unit, or 128 x 128, two.
 constexpr int HEAD_TILE = 256, HEAD_SMALL = 128, HEAD_CUS = 256;
 
+// dz goes into the products as bf16, each value off by up to 2^-8 of itself.
+// In sums over many tokens and ids these errors average to less than the
+// result's own rounding.  With few tokens they do not: a row of dx, and the
+// rows of dW it decides, hang on the one or few values of dz at its targets.
+// Up to this many tokens dz is kept as two bf16 terms, the rounded value and
+// what the rounding left (2^-16 together), and both are multiplied: these
+// calls are bound by reading w, not by the matrix cores.
+constexpr int HEAD_PAIR_TOKENS = 128;
+
 struct HeadPlan {
   int64_t rows, slots, parts, piece;
   int loss_tile, dz_tile, grad_tile, wg_slots;                    // the gradient's workgroups at a time
   int64_t dx_grid, dw_grid;                              // most tiles, splits included
-  bool dw_can_split, apart;
+  bool pair, dw_can_split, apart;
   size_t live, row_of, pos_of, state, ids, p, ent, xc;
   size_t zsel, stats, loss_bytes;                        // the loss
   size_t dz, dxp, dwp, grad_bytes;                       // the gradient
@@ -991,14 +1034,15 @@ static HeadPlan head_plan(int64_t tokens, int64_t vocab, int64_t hidden, int64_t
   // default piece: dz of a piece at most 1 GiB, and at least 2048 ids
   if (piece <= 0) piece = std::max<int64_t>(2048, (1ll << 30) / (2 * std::max<int64_t>(h.rows, 1)));
   h.piece = std::min(ceil_div(piece, HEAD_TILE), tv) * HEAD_TILE;
-  h.dz_tile = head_tile(tokens, std::min(h.piece, vocab));
+  h.pair = tokens <= HEAD_PAIR_TOKENS;
+  h.dz_tile = h.pair ? HEAD_SMALL : head_tile(tokens, std::min(h.piece, vocab));
   // dx and dW together, dx counted as the splits it may have: small tiles while both leave compute units idle
-  h.grad_tile = (h.piece / HEAD_TILE + tm) * th < HEAD_CUS / 2 ? HEAD_SMALL : HEAD_TILE;
+  h.grad_tile = h.pair || (h.piece / HEAD_TILE + tm) * th < HEAD_CUS / 2 ? HEAD_SMALL : HEAD_TILE;
   h.wg_slots = h.grad_tile == HEAD_TILE ? HEAD_CUS : 2 * HEAD_CUS;
   const int64_t hn = ceil_div(hidden, h.grad_tile);
   h.dx_grid = ceil_div(std::max<int64_t>(ceil_div(tokens, h.grad_tile) * hn, HEAD_SPLIT_TILES), NXCD) * NXCD;
   h.dw_grid = std::max<int64_t>(h.piece / h.grad_tile * hn, HEAD_SPLIT_TILES);
-  h.dz = take(2 * h.rows * h.piece);
+  h.dz = take((h.pair ? 4 : 2) * h.rows * h.piece);
   // partial products: the tiles of one product, or of all splits of one that is split
   const int64_t tile_values = (int64_t)h.grad_tile * hidden;
   h.dxp = take(4 * tile_values * std::max(ceil_div(tokens, h.grad_tile), HEAD_SPLIT_TILES / hn));
@@ -1008,7 +1052,7 @@ static HeadPlan head_plan(int64_t tokens, int64_t vocab, int64_t hidden, int64_t
   // apart, 221 together).
   h.apart = ceil_div(tokens, h.grad_tile) * hn >= 2 * h.wg_slots;
   // as head_splits decides for any number of live rows
-  h.dw_can_split = h.piece / h.grad_tile * hn * 2 <= HEAD_SPLIT_TILES && ceil_div(tokens, 64) / 2 >= HEAD_LEAST_STAGES;
+  h.dw_can_split = h.piece / h.grad_tile * hn * 2 <= HEAD_SPLIT_TILES && ceil_div(tokens, 64) * (h.pair ? 2 : 1) / 2 >= HEAD_LEAST_STAGES;
   h.dwp = take(h.dw_can_split ? 4 * tile_values * (HEAD_SPLIT_TILES / hn) : 0);
   h.grad_bytes = at;
   return h;
@@ -1107,7 +1151,8 @@ static HeadArgs head_rows(const HeadCall& c, const HeadPlan& h, hipStream_t stre
   r.live = (int*)(ws + h.live); r.row_of = (int*)(ws + h.row_of); r.pos_of = (int*)(ws + h.pos_of);
   r.loss = c.loss; r.lse = c.loss ? c.lse : nullptr;
   r.x = (const uint4*)c.x; r.xc = (uint4*)(ws + h.xc); r.chunks = (int)(c.hidden / 8);
-  r.tile = h.grad_tile; r.dx_tn = (int)ceil_div(c.hidden, h.grad_tile); r.dx_nk = (int)(h.piece / 64);
+  r.tile = h.grad_tile; r.dx_tn = (int)ceil_div(c.hidden, h.grad_tile); r.turns = h.pair ? 2 : 1;
+  r.dx_nk = (int)(h.piece / 64) * r.turns;
   r.dw_tiles = (int)(h.piece / h.grad_tile) * r.dx_tn; r.slots = h.wg_slots;
   hipLaunchKernelGGL(head_rows_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(c.tokens, 64), HEAD_CUS)),
                      dim3(ROWS_THR), 0, stream, r);
@@ -1119,23 +1164,19 @@ static HeadArgs head_rows(const HeadCall& c, const HeadPlan& h, hipStream_t stre
   return g;
 }
 
-template <int EPI>
-static void head_logits(int tile, const HeadArgs& g, hipStream_t stream) {
-  const unsigned grid = (unsigned)(ceil_div(g.tokens, tile) * ceil_div(g.nv, tile));
-  if (tile == HEAD_TILE) {
-    if (g.targets) hipLaunchKernelGGL((head_logits_kernel<4, EPI, false>), dim3(grid), dim3(256), 0, stream, g);
-    else hipLaunchKernelGGL((head_logits_kernel<4, EPI, true>), dim3(grid), dim3(256), 0, stream, g);
-  } else {
-    if (g.targets) hipLaunchKernelGGL((head_logits_kernel<2, EPI, false>), dim3(grid), dim3(256), 0, stream, g);
-    else hipLaunchKernelGGL((head_logits_kernel<2, EPI, true>), dim3(grid), dim3(256), 0, stream, g);
-  }
+template <int T, int EPI, bool PAIR>
+static void head_logits(const HeadArgs& g, hipStream_t stream) {
+  const dim3 grid((unsigned)(ceil_div(g.tokens, 64 * T) * ceil_div(g.nv, 64 * T)));
+  if (g.targets) hipLaunchKernelGGL((head_logits_kernel<T, EPI, false, PAIR>), grid, dim3(256), 0, stream, g);
+  else hipLaunchKernelGGL((head_logits_kernel<T, EPI, true, PAIR>), grid, dim3(256), 0, stream, g);
 }
 
-static void head_grads(int tile, int64_t dx_blocks, int64_t dw_blocks, HeadArgs g, hipStream_t stream) {
+static void head_grads(const HeadPlan& h, int64_t dx_blocks, int64_t dw_blocks, HeadArgs g, hipStream_t stream) {
   g.dx_blocks = (int)dx_blocks;
-  const unsigned grid = (unsigned)(dx_blocks + dw_blocks);
-  if (tile == HEAD_TILE) hipLaunchKernelGGL(head_grads_kernel<4>, dim3(grid), dim3(256), 0, stream, g);
-  else hipLaunchKernelGGL(head_grads_kernel<2>, dim3(grid), dim3(256), 0, stream, g);
+  const dim3 grid((unsigned)(dx_blocks + dw_blocks));
+  if (h.pair) hipLaunchKernelGGL((head_grads_kernel<2, true>), grid, dim3(256), 0, stream, g);
+  else if (h.grad_tile == HEAD_SMALL) hipLaunchKernelGGL((head_grads_kernel<2, false>), grid, dim3(256), 0, stream, g);
+  else hipLaunchKernelGGL((head_grads_kernel<4, false>), grid, dim3(256), 0, stream, g);
 }
 
 static pbs_status head_loss(const HeadCall& c, hipStream_t stream) {
@@ -1147,7 +1188,8 @@ static pbs_status head_loss(const HeadCall& c, hipStream_t stream) {
   g.zsel = (float*)(ws + h.zsel); g.stats = (float2*)(ws + h.stats);
   log_dispatch("%s tokens=%lld vocab=%lld hidden=%lld top=%lld tile=%d", c.what, (long long)c.tokens,
                (long long)c.vocab, (long long)c.hidden, (long long)c.top, h.loss_tile);
-  head_logits<EPI_STATS>(h.loss_tile, g, stream);
+  if (h.loss_tile == HEAD_TILE) head_logits<4, EPI_STATS, false>(g, stream);
+  else head_logits<2, EPI_STATS, false>(g, stream);
   JoinArgs j = {};
   j.live = g.live; j.row_of = g.row_of; j.targets = g.targets; j.state = g.state; j.ids = g.ids; j.p = g.p;
   j.ent = (const float*)(ws + h.ent); j.zsel = g.zsel; j.stats = g.stats;
@@ -1180,12 +1222,14 @@ static pbs_status head_grad(const HeadCall& c, hipStream_t stream) {
     g.w = (const uint8_t*)c.w + v0 * c.hidden * 2;
     g.add = v0 > 0;
     g.dw = c.dw ? (uint8_t*)c.dw + v0 * c.hidden * dwb : nullptr;
-    head_logits<EPI_DZ>(h.dz_tile, g, stream);
+    if (h.pair) head_logits<2, EPI_DZ, true>(g, stream);
+    else if (h.dz_tile == HEAD_SMALL) head_logits<2, EPI_DZ, false>(g, stream);
+    else head_logits<4, EPI_DZ, false>(g, stream);
     if (h.apart && c.dx && c.dw) {
-      head_grads(h.grad_tile, h.dx_grid, 0, g, stream);
-      head_grads(h.grad_tile, 0, h.dw_grid, g, stream);
+      head_grads(h, h.dx_grid, 0, g, stream);
+      head_grads(h, 0, h.dw_grid, g, stream);
     } else {
-      head_grads(h.grad_tile, c.dx ? h.dx_grid : 0, c.dw ? h.dw_grid : 0, g, stream);
+      head_grads(h, c.dx ? h.dx_grid : 0, c.dw ? h.dw_grid : 0, g, stream);
     }
     if (c.dw && h.dw_can_split)
       hipLaunchKernelGGL(head_dw_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(nv * c.hidden / 8, 256), 2048)),

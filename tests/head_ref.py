@@ -3,7 +3,8 @@ calls' arithmetic may add (first order, worst case).
 
 U = 2^-24: one fp32 rounding.  The matrix instruction's sums run through at
 most ``hidden`` (``vocab``, tokens) fp32 additions.  Half a step of bf16 is
-2^-8 of the value.  TINY = 2^-126, the smallest normal number of fp32 and of
+2^-8 of the value; up to PAIR_TOKENS tokens dz is a sum of two bf16 terms,
+2^-16 of the value.  TINY = 2^-126, the smallest normal number of fp32 and of
 bf16: the exponential instruction and the matrix instruction may take anything
 below it for 0, so a q or a dz smaller than that is off by up to TINY (a logit
 100 below the maximum gives q = 4e-44; times x = 1000 summed into dw, the
@@ -13,6 +14,7 @@ import torch
 
 U = 2.0 ** -24
 TINY = 2.0 ** -126
+PAIR_TOKENS = 128
 BF16 = torch.finfo(torch.bfloat16).eps / 2
 
 
@@ -71,7 +73,7 @@ def head_ref(x, w, slots, tau=1.0, dloss=None):
     # q carries the logit's and lse's errors, the argument's roundings and the function's
     e_q = q * (e_z + 2 * e_lse[:, None] + (4 * (z - lse[:, None]).abs() + 6) * U)
     e_dz = c.abs() * (e_q + e_hit + 4 * U * (q + (k + 1) * hit))
-    e_dz = e_dz + BF16 * (dz.abs() + e_dz) + TINY * (1 + c.abs())
+    e_dz = e_dz + (BF16 ** 2 if T <= PAIR_TOKENS else BF16) * (dz.abs() + e_dz) + TINY * (1 + c.abs())
     dx = dz @ w
     e_dx = e_dz @ w.abs() + (V + 40) * U * (dz.abs() @ w.abs())
     out["dx"] = (dx, e_dx + BF16 * (dx.abs() + e_dx) + TINY)

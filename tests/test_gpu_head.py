@@ -14,7 +14,7 @@ BF, F32 = torch.bfloat16, torch.float32
 # vocabulary; a small vocabulary against many tokens), one to several stages of K; the last three fill the GPU with
 # 256 x 256 tiles, the others take 128 x 128
 SHAPES = [(1, 1, 64), (1, 257, 64), (2, 256, 128), (37, 300, 64), (63, 1000, 192), (64, 64, 64), (65, 129, 128),
-          (128, 128, 256), (255, 1000, 192), (256, 512, 64), (257, 513, 128), (300, 2003, 320), (513, 131, 64),
+          (128, 128, 256), (129, 500, 64), (255, 1000, 192), (256, 512, 64), (257, 513, 128), (300, 2003, 320), (513, 131, 64),
           (70, 9001, 512), (2100, 300, 64), (1500, 17, 128),
           (300, 33001, 192), (1100, 14001, 64), (4100, 4100, 128)]
 
