@@ -737,19 +737,24 @@ __global__ __launch_bounds__(256) void head_teacher_kernel(TeacherArgs a) {
 // Splits of a product's K loop over nk stages when its tiles alone leave
 // workgroup slots idle: the number that minimises rounds of tiles times
 // (stages + a tile's fixed cost) plus the partial products' traffic, all in
-// stages.  Never more than 2 x 256 tiles' worth of partial products.
+// stages.  Never more than 2 x 256 tiles' worth of partial products.  Lanes 0
+// to 15 of a wave weigh 1 to 16 splits each; every lane gets the answer.
 constexpr int HEAD_FIXED = 6, HEAD_LEAST_STAGES = 8, HEAD_MOST_SPLITS = 16, HEAD_SPLIT_TILES = 512;
-__host__ __device__ inline int head_splits(int64_t tiles, int64_t nk, int slots) {
-  int best = 1;
-  int64_t cost = 0;
-  for (int s = 1; s <= HEAD_MOST_SPLITS && (s == 1 || (nk / s >= HEAD_LEAST_STAGES && tiles * s <= HEAD_SPLIT_TILES)); ++s) {
-    const int64_t c = (tiles * s + slots - 1) / slots * ((nk + s - 1) / s + HEAD_FIXED) + (s > 1 ? tiles * s / 23 : 0);
-    if (s == 1 || c < cost) {
-      best = s;
-      cost = c;
-    }
+__device__ __forceinline__ int head_splits(int tiles, int nk, int slots) {
+  const int s = (threadIdx.x & (HEAD_MOST_SPLITS - 1)) + 1;
+  const bool may = s == 1 || (nk / s >= HEAD_LEAST_STAGES && tiles <= HEAD_SPLIT_TILES / s);
+  const uint32_t rounds = (uint32_t)((tiles - 1) / slots + 1);
+  uint32_t cost = s == 1 ? rounds * (uint32_t)(nk + HEAD_FIXED)
+                         : (uint32_t)((tiles * s + slots - 1) / slots * ((nk + s - 1) / s + HEAD_FIXED) + tiles * s / 23);
+  // one split of a product that may not be split costs what it costs: no comparison, no overflow to fear
+  cost = may ? (cost > 0x07FFFFFFu ? 0x07FFFFFFu : cost) : 0x07FFFFFFu;
+  uint32_t key = cost * 16 + (uint32_t)(s - 1) ;
+#pragma unroll
+  for (int o = HEAD_MOST_SPLITS / 2; o >= 1; o >>= 1) {
+    const uint32_t u = (uint32_t)__shfl_xor((int)key, o, 64);
+    key = key < u ? key : u;
   }
-  return best;
+  return (int)(key & 15u) + 1;
 }
 
 struct RowsArgs {
@@ -809,11 +814,16 @@ __global__ __launch_bounds__(ROWS_THR) void head_rows_kernel(RowsArgs a) {
       before += wave_n[buf][i][1];
     }
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    a.live[0] = n;
+  if (blockIdx.x == 0 && w == 0) {
+    int dx = 1, dw = 1;
     if (!a.loss) {
-      a.live[1] = head_splits((int64_t)((n + a.tile - 1) / a.tile) * a.dx_tn, a.dx_nk, a.slots);
-      a.live[2] = head_splits(a.dw_tiles, (n + 63) / 64 * a.turns, a.slots);
+      dx = head_splits((n + a.tile - 1) / a.tile * a.dx_tn, a.dx_nk, a.slots);
+      dw = head_splits(a.dw_tiles, (n + 63) / 64 * a.turns, a.slots);
+    }
+    if (lane == 0) {
+      a.live[0] = n;
+      a.live[1] = dx;
+      a.live[2] = dw;
     }
   }
   // groups of 64 of the own tokens, one after the other for every wave, which
@@ -889,10 +899,13 @@ __global__ __launch_bounds__(JOIN_ROWS * JOIN_Q) void head_join_kernel(JoinArgs 
   sm[q][r] = u;
   __syncthreads();
   // every thread of the row joins the 32 sums, in the same order
-  u = sm[0][r];
-#pragma unroll 4
-  for (int i = 1; i < JOIN_Q; ++i) add(sm[i][r]);
-  const float lse = (u.x + __builtin_amdgcn_logf(u.y)) * LN2;
+  float mx = none, sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < JOIN_Q; ++i) mx = fmaxf(mx, sm[i][r].x);
+  const float safe = mx == none ? 0.0f : mx;
+#pragma unroll
+  for (int i = 0; i < JOIN_Q; ++i) sum = __builtin_fmaf(sm[i][r].y, __builtin_amdgcn_exp2f(sm[i][r].x - safe), sum);
+  const float lse = (mx + __builtin_amdgcn_logf(sum)) * LN2;
   const int tok = ok ? a.row_of[row] : 0;
   if (a.targets) {
     if (q == 0 && ok) {
