@@ -456,7 +456,7 @@ __global__ __launch_bounds__(norm_threads(TPR)) void layernorm_grad_kernel(NormA
     nr = a.rstd[q];
   };
   // 1024 threads have 128 registers each: the next row's values would spill
-  // (8192 x 16384, fp32 in and bf16 dy: 483 us with them, 293 without, unpacking again for dx)
+  // (8192 x 16384, fp32 in and bf16 dy: 483 us with them, 260 without, unpacking again for dx)
   constexpr bool AHEAD = TPR < 1024;
   if (AHEAD && row < a.rows) fetch(row);
 #pragma unroll
@@ -576,7 +576,11 @@ __global__ void norm_fill_kernel(uint32_t* p, int64_t n) {
 // 50.2 / 50.6 / 51.8 us on 15872 x 4096 bf16.  The gradient, which keeps two
 // sums a column in registers, takes a row of 4096 by 512 threads (74.6 us on
 // the same rows; 78.7 with 256 threads of two chunks each), the forward pass,
-// which has one more barrier a row, by 256 (50 us; 51 to 62 with 512).
+// which has one more barrier a row, by 256 (50 us; 51 to 62 with 512).  Widths
+// just past 4096 would leave the second chunk of 512 threads empty: three
+// chunks of 256 threads take 33.9 us on 8192 x 5120 bf16 against 39.8, and
+// 34 against 62 at 4099; at 6144 they lose, 56.8 against 53.6.  Three chunks of
+// 512 threads from 8193 on: 32 us on 4096 x 10240 against 41 with two of 1024.
 struct NormShape {
   int tpr, nch, cap;
 };
@@ -587,7 +591,9 @@ static NormShape norm_shape(int64_t cols, bool grad) {
   if (cols <= 2048) return {256, 1, 768};
   if (cols <= 4096 && !grad) return {256, 2, 768};
   if (cols <= 4096) return {512, 1, 256};
+  if (cols <= 5632 && !grad) return {256, 3, 768};
   if (cols <= 8192) return {512, 2, 256};
+  if (cols <= 12288) return {512, 3, 256};
   if (cols <= 16384) return {1024, 2, grad ? 256 : 512};
   return {0, 0, grad ? 512 : 2048};
 }
@@ -650,6 +656,7 @@ static bool norm_misaligned(const void* p, int bytes) { return ((uintptr_t)p & (
     else if (f.tpr == 64) PBS_NORM_RAGGED(kernel, grid, 256, a, 64, 2);                              \
     else if (f.tpr == 256 && f.nch == 1) PBS_NORM_RAGGED(kernel, grid, 256, a, 256, 1);              \
     else if (f.tpr == T4096 && f.nch == N4096) PBS_NORM_RAGGED(kernel, grid, T4096, a, T4096, N4096); \
+    else if (f.tpr == 512 && f.nch == 3) PBS_NORM_RAGGED(kernel, grid, 512, a, 512, 3);              \
     else if (f.tpr == 512) PBS_NORM_RAGGED(kernel, grid, 512, a, 512, 2);                            \
     else PBS_NORM_RAGGED(kernel, grid, 1024, a, 1024, 2);                                            \
   } while (0)
@@ -677,7 +684,8 @@ pbs_status pbs_layernorm(const void* x, pbs_format x_fmt, int64_t rows, int64_t 
     const unsigned grid = (unsigned)norm_grid(f, rows);
     log_dispatch("layernorm rows=%lld cols=%lld threads/row=%d chunks=%d grid=%u", (long long)rows, (long long)cols,
                  f.tpr, f.nch, grid);
-    if (f.tpr) PBS_NORM_SHAPED(layernorm_kernel, f, dim3(grid), a, 256, 2);
+    if (f.tpr == 256 && f.nch == 3) PBS_NORM_RAGGED(layernorm_kernel, dim3(grid), 256, a, 256, 3);
+    else if (f.tpr) PBS_NORM_SHAPED(layernorm_kernel, f, dim3(grid), a, 256, 2);
     else PBS_NORM_LAUNCH(layernorm_wide_kernel, dim3(grid), WIDE_THR, a);
   }
   return check_launch("pbs_layernorm");

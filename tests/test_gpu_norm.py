@@ -9,10 +9,11 @@ from tests.norm_ref import assert_within, norm_grad_ref, norm_ref
 pytestmark = pytest.mark.gpu
 
 BF, F32 = torch.bfloat16, torch.float32
-# widths around every split of a row over threads: one to 16 values a thread group, 128, 512, 2048, 4096, 8192,
-# 16384 and beyond
+# widths around every split of a row over threads: one to 16 values a thread group, 128, 512, 1024, 2048, 4096, 5632,
+# 8192, 12288, 16384 and beyond
 SHAPES = [(1, 1), (1, 7), (3, 8), (5, 9), (70, 64), (2, 127), (17, 128), (65, 129), (33, 512), (9, 513), (7, 1000),
-          (5, 2048), (3, 2049), (515, 4096), (2, 4097), (3, 8192), (2, 8200), (2, 16384), (2, 16391), (1, 40000),
+          (5, 2048), (3, 2049), (515, 4096), (2, 4097), (3, 5003), (2, 5632), (2, 5640),
+          (3, 8192), (2, 8200), (3, 10007), (2, 12288), (2, 12290), (2, 16384), (2, 16391), (1, 40000),
           (5000, 24), (2500, 770)]
 TYPES = [(BF, BF, BF), (F32, BF, F32), (F32, F32, F32), (BF, F32, BF)]
 
