@@ -11,12 +11,12 @@ pytestmark = pytest.mark.gpu
 
 BF, F32 = torch.bfloat16, torch.float32
 # one token, one id, tile edges on either side, products whose K loop is split (few tokens against a long
-# vocabulary; a small vocabulary against many tokens), one to several stages of K; the last three fill the GPU with
-# 256 x 256 tiles, the others take 128 x 128
+# vocabulary; a small vocabulary against many tokens), one to several stages of K; the last two take 256 x 256 tiles
+# for the logits, the last for the gradients' products too, the others 128 x 128
 SHAPES = [(1, 1, 64), (1, 257, 64), (2, 256, 128), (37, 300, 64), (63, 1000, 192), (64, 64, 64), (65, 129, 128),
-          (128, 128, 256), (129, 500, 64), (255, 1000, 192), (256, 512, 64), (257, 513, 128), (300, 2003, 320), (513, 131, 64),
-          (70, 9001, 512), (2100, 300, 64), (1500, 17, 128),
-          (300, 33001, 192), (1100, 14001, 64), (4100, 4100, 128)]
+          (128, 128, 256), (129, 500, 64), (255, 1000, 192), (256, 512, 64), (257, 513, 128),
+          (300, 2003, 320), (513, 131, 64), (70, 9001, 512), (2100, 300, 64), (1500, 17, 128),
+          (300, 33001, 192), (4100, 4100, 128), (2000, 8100, 64), (2000, 8100, 832)]
 
 
 def make(T, V, H, seed=0, masked=0.0):
@@ -294,10 +294,11 @@ def gpu_ref(x, w, targets, dloss):
     return loss, lse, (dx, dz, 2 ** -8 * (dz.abs_() @ w.double().abs())), dw
 
 
-@pytest.mark.parametrize("T,V,H,piece", [(3, (1 << 21) + 70, 1024, 0), (8450, 262400, 64, 262400)],
-                         ids=["weight", "piece"])
-def test_beyond_four_gib(T, V, H, piece):
-    """A head of more than 4 GiB; a piece whose dz takes more than 4 GiB."""
+@pytest.mark.parametrize("T,V,H,piece", [(3, (1 << 21) + 70, 1024, 0), (8450, 262400, 64, 262400),
+                                         (4200, 16500, 832, 8192)],
+                         ids=["weight beyond 4 GiB", "piece beyond 4 GiB", "large tiles, three pieces"])
+def test_large(T, V, H, piece):
+    """A head of more than 4 GiB; a piece whose dz takes more than 4 GiB; pieces of 256 x 256 tiles."""
     g = torch.Generator(device="cuda").manual_seed(3)
     w = (torch.randn(V, H, device="cuda", generator=g) * 0.05).to(BF)
     x = torch.randn(T, H, device="cuda", generator=g).to(BF)

@@ -96,11 +96,13 @@ def test_pipeline_refuses():
                 lambda: PL.linear_xent(x.float(), w, t), lambda: PL.linear_xent(x, w.half(), t),
                 lambda: PL.linear_xent(x, w[:, :32], t), lambda: PL.linear_xent(x[:, ::2], w[:, ::2], t),
                 lambda: PL.linear_xent(x, w, t[:3]), lambda: PL.linear_xent(x, w, t.int()),
-                lambda: PL.linear_xent(x, w, None), lambda: PL.linear_xent(x, w, torch.zeros(8, dtype=torch.int64)[::2]),
-                lambda: PL.linear_xent_grad(f[0].expand(4), x, w, t, f), lambda: PL.linear_xent_grad(f.double(), x, w, t, f),
+                lambda: PL.linear_xent(x, w, None), lambda: PL.linear_xent(x, w, t.repeat(2)[::2]),
+                lambda: PL.linear_xent_grad(f[0].expand(4), x, w, t, f),
+                lambda: PL.linear_xent_grad(f.double(), x, w, t, f),
                 lambda: PL.linear_xent_grad(f, x, w, t, f[:2]), lambda: PL.linear_xent_grad(f, x, w, t, None),
                 lambda: PL.linear_distill(x, w, ids[:, 0], logits), lambda: PL.linear_distill(x, w, ids.int(), logits),
-                lambda: PL.linear_distill(x, w, ids, logits[:, :2]), lambda: PL.linear_distill(x, w, ids, logits.half()),
+                lambda: PL.linear_distill(x, w, ids, logits[:, :2]),
+                lambda: PL.linear_distill(x, w, ids, logits.half()),
                 lambda: PL.linear_distill(x, w, ids[:, :0], logits[:, :0]),
                 lambda: PL.linear_distill_grad(f, x, w, ids[:3], logits[:3], 1.0, f)):
         with pytest.raises(ValueError):
@@ -122,5 +124,6 @@ def test_reference_gradients_against_differences():
                 for h in (1e-5, -1e-5):
                     moved = t.clone()
                     moved[at] += h
-                    ends.append((head_ref(moved if t is x else x, moved if t is w else w, slots, tau)["loss"][0] * c).sum())
+                    args = (moved if t is x else x, moved if t is w else w)
+                    ends.append((head_ref(*args, slots, tau)["loss"][0] * c).sum())
                 assert abs((ends[0] - ends[1]) / 2e-5 - ref[name][0][at]) < 1e-8
