@@ -484,9 +484,11 @@ __global__ __launch_bounds__(norm_threads(TPR)) void layernorm_grad_kernel(NormA
     for (int j = 0; j < NCH; ++j)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        // (a chunk that is not there was loaded as zeros)
+        // (a chunk that is not there was loaded as zeros; its n is 0 too, as
+        // mu r may overflow where the row's own n do not)
         const bool mine = !RAGGED || at[j].mine(k, a.cols);
-        const float d = mine ? dy[j].get(k) : 0.0f, n = (x[j].get(k) - mu) * r;
+        const float d = mine ? dy[j].get(k) : 0.0f;
+        const float n = RAGGED ? (mine ? (x[j].get(k) - mu) * r : 0.0f) : (x[j].get(k) - (at[j].any ? mu : 0.0f)) * r;
         const float u = d * gam[j][k];
         sg[j][k] = __builtin_fmaf(d, n, sg[j][k]);
         sb[j][k] += d;

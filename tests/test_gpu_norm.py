@@ -138,6 +138,16 @@ def test_common_offset_and_constant_rows(cols):
     check_grad(dy, x, gamma, mean, rstd, *got, "offset")
 
 
+@pytest.mark.parametrize("cols", [5, 64, 256, 768, 2304, 8256, 17000])
+def test_mean_times_rstd_past_the_range(cols):
+    """Constant rows of 2^83 with eps = 1e-30: n is 0 although mean * rstd overflows, and dx = rstd (u - mean(u))."""
+    x = torch.full((3, cols), 2.0 ** 83)
+    _, gamma, beta, dy = make(3, cols, F32, F32, F32, seed=cols)
+    mean, rstd = torch.full((3,), 2.0 ** 83), torch.full((3,), 1e15)
+    got = PL.layernorm_grad(dy.cuda(), x.cuda(), gamma.cuda(), mean.cuda(), rstd.cuda())
+    check_grad(dy, x, gamma, mean, rstd, *got, "overflow")
+
+
 @pytest.mark.parametrize("cols", [48, 4096, 17000])
 def test_nan_and_infinite_rows_stay_alone(cols):
     x, gamma, beta, _ = make(9, cols, BF, BF, BF, seed=1)
