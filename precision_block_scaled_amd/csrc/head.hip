@@ -1048,7 +1048,7 @@ static HeadPlan head_plan(int64_t tokens, int64_t vocab, int64_t hidden, int64_t
     at += (bytes + 255) / 256 * 256;
     return here;
   };
-  const int64_t tm = ceil_div(tokens, HEAD_TILE), tv = ceil_div(vocab, HEAD_TILE), th = ceil_div(hidden, HEAD_TILE);
+  const int64_t tm = ceil_div(tokens, HEAD_TILE), th = ceil_div(hidden, HEAD_TILE);
   h.rows = tm * HEAD_TILE;
   h.slots = xent ? 1 : ceil_div(top, 4) * 4;
   h.loss_tile = head_tile(tokens, vocab);
@@ -1068,7 +1068,7 @@ static HeadPlan head_plan(int64_t tokens, int64_t vocab, int64_t hidden, int64_t
   at = shared;
   // default piece: dz of a piece at most 1 GiB, and at least 2048 ids
   if (piece <= 0) piece = std::max<int64_t>(2048, (1ll << 30) / (2 * std::max<int64_t>(h.rows, 1)));
-  h.piece = std::min(ceil_div(piece, HEAD_TILE), tv) * HEAD_TILE;
+  h.piece = ceil_div(std::min(piece, vocab), HEAD_TILE) * HEAD_TILE;
   h.pair = tokens <= HEAD_PAIR_TOKENS;
   h.dz_tile = h.pair ? HEAD_SMALL : head_tile(tokens, std::min(h.piece, vocab));
   // dx and dW together, dx counted as the splits it may have: small tiles while both leave compute units idle

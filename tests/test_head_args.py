@@ -83,6 +83,8 @@ def test_workspace_bytes():
     # a piece of 4096 ids at a time: its dz, dx sums, a gathered x and what splits may take
     small = P.pbs_linear_loss_bytes(8192, 131072, 4096, 0, 4096)[1]
     assert small < grad and small < 8192 * 4096 * (2 + 2 + 4 * 4)
+    # a piece of more than the vocabulary is the vocabulary, whatever the number
+    assert P.pbs_linear_loss_bytes(300, 5000, 64, 0, (1 << 63) - 1) == P.pbs_linear_loss_bytes(300, 5000, 64, 0, 5000)
     # one byte short is refused
     a = args(dict(n=P.pbs_linear_loss_bytes(8, 100, 64)[0] - 1))
     refused(1, P.pbs_linear_xent, *(a[k] for k in "x w tokens vocab hidden targets loss lse ws n".split()), 0)
