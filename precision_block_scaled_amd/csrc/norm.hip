@@ -635,6 +635,12 @@ static pbs_status norm_check(const char* what, pbs_format x_fmt, pbs_format y_fm
   return PBS_OK;
 }
 
+// Whether an output may stand where it does: in an input's place only with the input's type and rows.
+static bool norm_in_place(const void* out, pbs_format out_fmt, int64_t ldo, const void* in, pbs_format in_fmt,
+                          int64_t ldi, int64_t rows) {
+  return out != in || (out_fmt == in_fmt && (rows <= 1 || ldo == ldi));
+}
+
 static bool norm_misaligned(const void* p, int bytes) { return ((uintptr_t)p & (bytes - 1)) != 0; }
 
 // One launch of kernel<TX, TY ...> for the call's formats.
@@ -682,6 +688,8 @@ pbs_status pbs_layernorm(const void* x, pbs_format x_fmt, int64_t rows, int64_t 
   PBS_REQUIRE(!norm_misaligned(gamma, wb) && !norm_misaligned(beta, wb) && !norm_misaligned(mean, 4) &&
                   !norm_misaligned(rstd, 4) && !norm_misaligned(amax_out, 4),
               PBS_ERR_INVALID_ARG, "pbs_layernorm: a vector is not aligned to its elements");
+  PBS_REQUIRE(rows == 0 || norm_in_place(y, y_fmt, ldy, x, x_fmt, ldx, rows), PBS_ERR_INVALID_ARG,
+              "pbs_layernorm: y is x with another type or row stride");
   if (amax_out) hipLaunchKernelGGL(norm_fill_kernel, dim3(1), dim3(64), 0, stream, (uint32_t*)amax_out, (int64_t)1);
   if (rows > 0) {
     NormArgs a = {};
@@ -721,6 +729,9 @@ pbs_status pbs_layernorm_grad(const void* dy, pbs_format y_fmt, int64_t lddy, co
                   !norm_misaligned(dx, x_fmt == PBS_FMT_BF16 ? 2 : 4) && !norm_misaligned(mean, 4) &&
                   !norm_misaligned(rstd, 4) && !norm_misaligned(dgamma, 4) && !norm_misaligned(dbeta, 4),
               PBS_ERR_INVALID_ARG, "pbs_layernorm_grad: a tensor is not aligned to its elements");
+  PBS_REQUIRE(rows == 0 || !dx || (norm_in_place(dx, x_fmt, lddx, x, x_fmt, ldx, rows) &&
+                                   norm_in_place(dx, x_fmt, lddx, dy, y_fmt, lddy, rows)),
+              PBS_ERR_INVALID_ARG, "pbs_layernorm_grad: dx is x or dy with another type or row stride");
   if (rows == 0) {
     if (dgamma) hipLaunchKernelGGL(norm_fill_kernel, dim3(64), dim3(256), 0, stream, (uint32_t*)dgamma, cols);
     if (dbeta) hipLaunchKernelGGL(norm_fill_kernel, dim3(64), dim3(256), 0, stream, (uint32_t*)dbeta, cols);

@@ -338,6 +338,11 @@ def quantize_pass(recipe, pass_, x, w, dy, states=None, outs=None, stream=None):
 
 # ---------------------------------------------------------------------------
 # the ends of a step: the norm ahead of a linear layer, the losses of the head
+#
+# Outputs and workspaces are allocated on the call's device and stream.  A call
+# on another stream than the current one (``stream``) is ordered against the
+# other streams' work, and its tensors are kept until it is done, by the
+# caller, as for torch's own operators under ``torch.cuda.stream``.
 # ---------------------------------------------------------------------------
 FMT_OF = {torch.bfloat16: PBS_FMT_BF16, torch.float32: PBS_FMT_F32}
 BF16_F32 = (torch.bfloat16, torch.float32)
@@ -411,8 +416,8 @@ def layernorm(x, gamma=None, beta=None, eps=1e-5, out_dtype=None, y=None, amax=N
     mean [R], rstd [R]), the statistics in fp32 for ``layernorm_grad``.
 
     ``gamma`` / ``beta`` [C]: both bf16 or both fp32 (None: 1 / 0).  ``y`` may
-    be given ([R, C], bf16 or fp32; ``x`` itself for in place), else it is
-    allocated in ``out_dtype`` (None: x's).  ``amax`` (a device fp32 of one
+    be given ([R, C], bf16 or fp32; ``x`` itself for in place, else apart from
+    it), else it is allocated in ``out_dtype`` (None: x's).  ``amax`` (a device fp32 of one
     element) receives max |y| as stored: ``quantize(..., known_amax=amax)``
     then needs no pass of its own.
     """
@@ -447,8 +452,8 @@ def layernorm(x, gamma=None, beta=None, eps=1e-5, out_dtype=None, y=None, amax=N
 def layernorm_grad(dy, x, gamma, mean, rstd, dx=None, stream=None):
     """Gradients of ``layernorm``: returns (dx [R, C] in x's type, dgamma [C],
     dbeta [C] in fp32) from dy [R, C] (bf16 or fp32), the forward's x, gamma
-    (None: 1) and the statistics it returned.  ``dx`` may be given, x or dy
-    itself among the choices."""
+    (None: 1) and the statistics it returned.  ``dx`` may be given: x or dy
+    itself, or apart from them."""
     dev = x.device
     x_fmt, ldx = _matrix("x", x, dev)
     R, C = x.shape

@@ -38,6 +38,8 @@ def grad(dy=FAKE, y_fmt=BF, lddy=64, x=FAKE, x_fmt=BF, ldx=64, rows=4, cols=64, 
     (1, dict(x=None)), (1, dict(y=None)), (1, dict(x=FAKE + 1)), (1, dict(x=FAKE + 2, x_fmt=F32)),
     (1, dict(y=FAKE + 2, y_fmt=F32)), (1, dict(gamma=FAKE + 1)), (1, dict(beta=FAKE + 2, w_fmt=F32)),
     (1, dict(mean=FAKE + 2)), (1, dict(rstd=FAKE + 1)), (1, dict(amax=FAKE + 2)),
+    # y on x's memory in another type or with other rows: not in place
+    (1, dict(y=FAKE, y_fmt=F32)), (1, dict(y=FAKE, ldy=65)),
     (1, dict(eps=-1.0)), (1, dict(eps=float("nan"))), (1, dict(eps=float("inf")))])
 def test_layernorm_refuses(status, change):
     _expect(status, P.pbs_layernorm, *forward(**change))
@@ -49,7 +51,9 @@ def test_layernorm_refuses(status, change):
     (2, dict(rows=-1)), (2, dict(cols=0)), (2, dict(lddy=63)), (2, dict(ldx=1)), (2, dict(lddx=63)),
     (1, dict(dy=None)), (1, dict(x=None)), (1, dict(mean=None)), (1, dict(rstd=None)),
     (1, dict(dy=FAKE + 1)), (1, dict(dx=FAKE + 1)), (1, dict(dgamma=FAKE + 2)), (1, dict(dbeta=FAKE + 2)),
-    (1, dict(ws=None)), (1, dict(ws=FAKE + 8)), (1, dict(n=0)), (1, dict(n=2 * 64 * 4 - 1))])
+    (1, dict(ws=None)), (1, dict(ws=FAKE + 8)), (1, dict(n=0)), (1, dict(n=2 * 64 * 4 - 1)),
+    # dx on x's or dy's memory in another type or with other rows
+    (1, dict(x=FAKE, lddx=65)), (1, dict(dy=FAKE, y_fmt=F32, x=2 * FAKE)), (1, dict(dy=FAKE, lddx=65, x=2 * FAKE))])
 def test_layernorm_grad_refuses(status, change):
     _expect(status, P.pbs_layernorm_grad, *grad(**change))
 
