@@ -317,7 +317,16 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
   int tok[TJ], state[TJ];
   int64_t target[TJ];
   float lse[TJ], dloss[TJ];
+  // MULTI: the staged tokens whose slots the thread looks through, one a pass
+  constexpr int PASSES = N_T / STAGE_ROWS;
+  const int srow = t % STAGE_ROWS, half = t / STAGE_ROWS;
+  auto staged = [&](int p) { return 32 * TJ * (srow / 64) + 64 * p + srow % 64; };
+  int slot_tok[PASSES];
   auto token_rows = [&]() {
+    if constexpr (MULTI) {
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) slot_tok[p] = g.row_of[n0 + staged(p) < n ? n0 + staged(p) : n - 1];
+    }
     if constexpr (EPI <= EPI_DZ) {
 #pragma unroll
       for (int j = 0; j < TJ; ++j) {
@@ -425,7 +434,7 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
   };
   // rows 32 TJ wn + 64 p .. of the wave's columns, to staged rows 64 wn ..: a
   // pass p stages row s of the tile's row 32 TJ (s / 64) + 64 p + s % 64
-  auto stage_f32 = [&](int p, float f) {
+  auto stage_f32 = [&](int p) {
 #pragma unroll
     for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
@@ -434,13 +443,33 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
         for (int q = 0; q < 4; ++q) {
           const int j = 2 * p + jj;
           *(float4*)(stage + (wn * 64 + 32 * jj + lr) * PITCH + row0 + 32 * i + 8 * q + 4 * lg) =
-              make_float4(acc[i][j][4 * q] * f, acc[i][j][4 * q + 1] * f, acc[i][j][4 * q + 2] * f,
-                          acc[i][j][4 * q + 3] * f);
+              make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
         }
   };
   if constexpr (EPI <= EPI_DZ) {
     float* scale = (float*)(smem + STAGE_ROWS * PITCH * 4);     // MULTI: dloss / tau of the tile's tokens
     const int have = g.nv - m0 < M_T ? g.nv - m0 : M_T;        // ids of the tile that exist
+    // MULTI: a token's slots lie in groups of four; its two threads take the
+    // even and the odd ones.  The first AHEAD of each are loaded ahead of the
+    // statistics, or of the pass before (read where they are used, they and
+    // the row's token cost 5 us a tile in latency).
+    constexpr int AHEAD = 8, HELD = EPI == EPI_STATS ? PASSES : 1;
+    const int groups = g.slots / 4;
+    int4 sid[HELD][AHEAD];
+    float4 sp[AHEAD];
+    auto load_slots = [&](int p) {
+      const int64_t at = (int64_t)slot_tok[p] * groups;
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        const int q = half + 2 * k;                            // past the last group: that one, for nothing
+        sid[HELD == 1 ? 0 : p][k] = ((const int4*)g.ids)[at + (q < groups ? q : groups - 1)];
+        if (EPI == EPI_DZ) sp[k] = ((const float4*)g.p)[at + (q < groups ? q : groups - 1)];
+      }
+    };
+    if constexpr (MULTI) {
+#pragma unroll
+      for (int p = 0; p < HELD; ++p) load_slots(p);
+    }
     const float c2 = g.inv_tau * LOG2E;
     int want[TJ];                                              // the token's target less this lane's first id
     float lse2[TJ], cz[TJ];                                    // lse / log 2, dloss / tau
@@ -455,76 +484,97 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
         cz[j] = !there ? 0.0f : bad ? __builtin_nanf("") : dloss[j] * g.inv_tau;
       }
     }
-    // z of id i, r; where the tile runs past the last id, -inf there (two
-    // instances: a choice made on the accumulators themselves would move all
-    // of them to vector registers)
-    auto finish = [&](auto full_c) {
+    // Token j: its statistics or its dz, staged.  FULL: no id of the tile is
+    // past the last one (-inf in its place).  The accumulators are read here
+    // and not earlier: hoisted ahead of the choice between the two instances
+    // they filled the vector registers and spilled (loss 0.5 to 1.5% slower).
+    auto column = [&](auto full_c, int j) {
       constexpr bool FULL = decltype(full_c)::value;
-      auto z = [&](int i, int j, int r) {
-        return FULL || row0 + 32 * i + 8 * (r >> 2) + 4 * lg + (r & 3) < have ? acc[i][j][r] : none;
+      float v[TI][16];
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          v[i][r] = acc[i][j][r];
+          if (TI == 4) asm volatile("" : "+v"(v[i][r]));
+        }
+      auto z = [&](int i, int r) {
+        return FULL || row0 + 32 * i + 8 * (r >> 2) + 4 * lg + (r & 3) < have ? v[i][r] : none;
       };
+      if constexpr (EPI == EPI_STATS) {
+        float mx = none;
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        // the token's accumulators stay where they are until here: read for
-        // both instances ahead of the choice between them, they filled the
-        // vector registers and spilled (loss 0.5 to 1.5% slower)
-        if constexpr (TI == 4 && !MULTI) {
+        for (int i = 0; i < TI; ++i)
 #pragma unroll
-          for (int i = 0; i < TI; ++i) asm volatile("" : "+a"(acc[i][j]));
+          for (int r = 0; r < 16; ++r) mx = fmaxf(mx, z(i, r));
+        mx *= c2;                                            // everything in units of log 2 from here
+        const float safe = mx == none ? 0.0f : mx;           // nothing but -inf: the sum stays 0
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < TI; ++i) {
+          // sixteen independent exponentials, then a tree: one running sum
+          // would wait out the instruction's latency 16 TI times
+          float e[16];
+#pragma unroll
+          for (int r = 0; r < 16; ++r) e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(z(i, r), c2, -safe));
+#pragma unroll
+          for (int o = 8; o >= 1; o >>= 1)
+#pragma unroll
+            for (int r = 0; r < o; ++r) e[r] += e[r + o];
+          sum += e[0];
         }
-        if constexpr (EPI == EPI_STATS) {
-          float mx = none;
+        const float mo = __shfl_xor(mx, 32, 64), so = __shfl_xor(sum, 32, 64);
+        const float m1 = fmaxf(mx, mo), safe1 = m1 == none ? 0.0f : m1;
+        sum = sum * __builtin_amdgcn_exp2f(mx - safe1) + so * __builtin_amdgcn_exp2f(mo - safe1);
+        if (lg == 0)
+          g.stats[(int64_t)(tm * 2 + wm) * g.rows + n0 + wn * 32 * TJ + 32 * j + lr] = make_float2(m1, sum);
+      } else {
 #pragma unroll
-          for (int i = 0; i < TI; ++i)
+        for (int i = 0; i < TI; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, z(i, j, r));
-          mx *= c2;                                            // everything in units of log 2 from here
-          const float safe = mx == none ? 0.0f : mx;           // nothing but -inf: the sum stays 0
-          float sum = 0.0f;
+          for (int r = 0; r < 16; ++r)
+            v[i][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(z(i, r), c2, -lse2[j])) * cz[j];
+      }
+      if (!MULTI && __any(want[j] >= 0)) {
+        float at = 0.0f;
+        bool mine = false;
 #pragma unroll
-          for (int i = 0; i < TI; ++i) {
-            // sixteen independent exponentials, then a tree: one running sum
-            // would wait out the instruction's latency 16 TI times
-            float e[16];
+        for (int i = 0; i < TI; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(z(i, j, r), c2, -safe));
-#pragma unroll
-            for (int o = 8; o >= 1; o >>= 1)
-#pragma unroll
-              for (int r = 0; r < o; ++r) e[r] += e[r + o];
-            sum += e[0];
+          for (int r = 0; r < 16; ++r) {
+            const bool hit = want[j] == 32 * i + 8 * (r >> 2) + (r & 3);
+            if (EPI == EPI_DZ) v[i][r] -= hit ? cz[j] : 0.0f;
+            else at = hit ? v[i][r] : at;
+            mine |= hit;
           }
-          const float mo = __shfl_xor(mx, 32, 64), so = __shfl_xor(sum, 32, 64);
-          const float m1 = fmaxf(mx, mo), safe1 = m1 == none ? 0.0f : m1;
-          sum = sum * __builtin_amdgcn_exp2f(mx - safe1) + so * __builtin_amdgcn_exp2f(mo - safe1);
-          if (lg == 0)
-            g.stats[(int64_t)(tm * 2 + wm) * g.rows + n0 + wn * 32 * TJ + 32 * j + lr] = make_float2(m1, sum);
-        } else {
+        if (EPI == EPI_STATS && mine) g.zsel[tok[j]] = at * g.inv_tau;
+      }
+      if constexpr (MULTI) {
+        const float f = EPI == EPI_STATS ? g.inv_tau : 1.0f;
 #pragma unroll
-          for (int i = 0; i < TI; ++i)
+        for (int i = 0; i < TI; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-              acc[i][j][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(z(i, j, r), c2, -lse2[j])) * cz[j];
-        }
-        if (!MULTI && __any(want[j] >= 0)) {
-          float at = 0.0f;
-          bool mine = false;
+          for (int q = 0; q < 4; ++q)
+            *(float4*)(stage + (wn * 64 + 32 * (j % 2) + lr) * PITCH + row0 + 32 * i + 8 * q + 4 * lg) =
+                make_float4(v[i][4 * q] * f, v[i][4 * q + 1] * f, v[i][4 * q + 2] * f, v[i][4 * q + 3] * f);
+      } else if constexpr (EPI == EPI_DZ) {
 #pragma unroll
-          for (int i = 0; i < TI; ++i)
+        for (int i = 0; i < TI; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              const bool hit = want[j] == 32 * i + 8 * (r >> 2) + (r & 3);
-              if (EPI == EPI_DZ) acc[i][j][r] -= hit ? cz[j] : 0.0f;
-              else at = hit ? acc[i][j][r] : at;
-              mine |= hit;
-            }
-          if (EPI == EPI_STATS && mine) g.zsel[tok[j]] = at * g.inv_tau;
-        }
-        if (!MULTI && !PAIR && EPI == EPI_DZ) stage_bf16(j);
+          for (int r = 0; r < 16; ++r) acc[i][j][r] = v[i][r];
+        if (!PAIR) stage_bf16(j);
       }
     };
-    if (have == M_T) finish(std::integral_constant<bool, true>{});
-    else finish(std::integral_constant<bool, false>{});
+    auto columns = [&](int j0, int j1) {
+      if (have == M_T) {
+#pragma unroll
+        for (int j = j0; j < j1; ++j) column(std::integral_constant<bool, true>{}, j);
+      } else {
+#pragma unroll
+        for (int j = j0; j < j1; ++j) column(std::integral_constant<bool, false>{}, j);
+      }
+    };
+    if (!MULTI) columns(0, TJ);
     constexpr int LPR = M_T / 8;                               // lanes a row, 8 values each
     constexpr int PARTS = PAIR ? 2 : 1;
     if constexpr (!MULTI && EPI == EPI_DZ) {
@@ -557,43 +607,41 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
         for (int j = 0; j < TJ; ++j) scale[wn * 32 * TJ + 32 * j + lr] = cz[j];
       }
 #pragma unroll
-      for (int p = 0; p < N_T / STAGE_ROWS; ++p) {
-        stage_f32(p, EPI == EPI_STATS ? g.inv_tau : 1.0f);
-        __syncthreads();
-        // The slots of staged token s.  For the loss its two threads share
-        // the slots; for dz, where slots of one id add up in one place, they
-        // share the ids, and every place has one writer.
-        constexpr int PW = EPI == EPI_STATS ? M_T : M_T / 2;
-        const int s = t % STAGE_ROWS, part = t / STAGE_ROWS;
-        const int at_tile = 32 * TJ * (s / 64) + 64 * p + s % 64;
-        if (n0 + at_tile < n) {
-          const int token = g.row_of[n0 + at_tile];
-          const int c0 = EPI == EPI_STATS ? 0 : part * PW;
-          float* mine = stage + s * PITCH + c0;
-          const int first = g.v0 + m0 + c0;
-          const int some = have - c0 < PW ? have - c0 : PW;    // ids in reach; none if negative
-          const int64_t at = (int64_t)token * g.slots;
-          const int4* ids = (const int4*)(g.ids + at);
-          const int q1 = g.slots / 4;
-          for (int q = EPI == EPI_STATS ? 4 * part : 0; q < q1; q += EPI == EPI_STATS ? 8 : 4) {
-            int4 id4[4];
+      for (int p = 0; p < PASSES; ++p) {
+        columns(2 * p, 2 * p + 2);
+        stage_barrier<63>();
+        const int some = n0 + staged(p) < n ? have : 0;        // ids in reach
+        float* mine = stage + srow * PITCH;
+        const int first = g.v0 + m0;
+        const int64_t at = (int64_t)slot_tok[p] * g.slots;
+        // (an unused slot's id is -1, which is in no tile)
+        auto group = [&](int q, const int4& id4, const float4& p4) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) id4[u] = q + u < q1 ? ids[q + u] : make_int4(-1, -1, -1, -1);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int id = k == 0 ? id4[u].x : k == 1 ? id4[u].y : k == 2 ? id4[u].z : id4[u].w;
-                const int c = id - first;
-                if (id < 0 || c < 0 || c >= some) continue;
-                const int64_t slot = at + 4 * (q + u) + k;
-                if (EPI == EPI_STATS) g.zsel[slot] = mine[c];
-                else mine[c] -= g.p[slot] * scale[at_tile];
-              }
-            }
+          for (int k = 0; k < 4; ++k) {
+            const int c = (k == 0 ? id4.x : k == 1 ? id4.y : k == 2 ? id4.z : id4.w) - first;
+            if ((uint32_t)c >= (uint32_t)some) continue;
+            if (EPI == EPI_STATS) g.zsel[at + 4 * q + k] = mine[c];
+            else mine[c] -= (k == 0 ? p4.x : k == 1 ? p4.y : k == 2 ? p4.z : p4.w) * scale[staged(p)];
           }
+        };
+        auto look = [&]() {
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k)
+            if (half + 2 * k < groups) group(half + 2 * k, sid[HELD == 1 ? 0 : p][k], sp[k]);
+          for (int q = half + 2 * AHEAD; q < groups; q += 2)
+            group(q, ((const int4*)g.ids)[at / 4 + q],
+                  EPI == EPI_DZ ? ((const float4*)g.p)[at / 4 + q] : make_float4(0, 0, 0, 0));
+        };
+        if (EPI == EPI_STATS) {
+          look();
+        } else {
+          // slots of one id add up in one place: one thread of the two after the other
+          if (half == 0) look();
+          stage_barrier<63>();
+          if (half == 1) look();
+          if (p + 1 < PASSES) load_slots(p + 1);
         }
-        __syncthreads();
+        stage_barrier<63>();
         if (EPI == EPI_DZ) {
 #pragma unroll 4
           for (int s2 = t / LPR; s2 < STAGE_ROWS; s2 += 256 / LPR) {
@@ -612,7 +660,7 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
               }
             }
           }
-          if (p + 1 < N_T / STAGE_ROWS) __syncthreads();
+          if (p + 1 < PASSES) stage_barrier<63>();
         }
       }
     }
@@ -637,7 +685,7 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
                                         : g.dw_part + (int64_t)split * g.dz_ld * g.hidden);
 #pragma unroll
     for (int p = 0; p < N_T / STAGE_ROWS; ++p) {
-      stage_f32(p, 1.0f);
+      stage_f32(p);
       __syncthreads();
 #pragma unroll 4
       for (int s = t / LPR; s < STAGE_ROWS; s += RPI) {
