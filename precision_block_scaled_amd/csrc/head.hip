@@ -670,7 +670,7 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
     if (EPI == EPI_DW && splits == 1 && g.out_bf16) {
 #pragma unroll
       for (int j = 0; j < TJ; ++j) stage_bf16(j);
-      __syncthreads();
+      stage_barrier<63>();
 #pragma unroll 4
       for (int s = t / LPR; s < N_T; s += RPI)
         if (n0 + s < N && col < M)
@@ -686,7 +686,7 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
 #pragma unroll
     for (int p = 0; p < N_T / STAGE_ROWS; ++p) {
       stage_f32(p);
-      __syncthreads();
+      stage_barrier<63>();
 #pragma unroll 4
       for (int s = t / LPR; s < STAGE_ROWS; s += RPI) {
         const float* q = stage + s * PITCH + (t % LPR) * 8;
@@ -703,7 +703,7 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
           o[1] = hi;
         }
       }
-      if (p + 1 < N_T / STAGE_ROWS) __syncthreads();
+      if (p + 1 < N_T / STAGE_ROWS) stage_barrier<63>();
     }
   }
 }
