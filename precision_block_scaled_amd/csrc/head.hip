@@ -25,12 +25,13 @@
 // LDS-DMA, v_mfma_f32_32x32x16_bf16.
 //
 // What bounds them: the matrix cores and the power they draw.  On 8192 x
-// 131072 x 4096 the loss runs at 1390 TFLOP/s (6.3 ms) and the gradient at 1360
-// (19.4 ms) with the matrix cores busy 79% of the time at 1.68 GHz; a large
-// library product reaches 1490 on the same operands.  A K stage of a 256 x 256
-// tile takes 1.43 us, a tile's fixed cost (first loads 2.5 us, epilogue 4 to 6)
-// 9% of it at hidden = 4096 and 16% at 2048.  The loss without its epilogue
-// would be 3% faster.
+// 131072 x 4096 the loss runs at 1430 TFLOP/s (6.1 ms) and the gradient at 1395
+// (18.9 ms) with the matrix cores busy 82% of the time (dz 78%) at 1.67 GHz; a
+// large library product reaches 1490 on the same operands.  A K stage of a
+// 256 x 256 tile takes 1.43 us, a tile's fixed cost (first loads 2.5 us,
+// epilogue 4 to 5) 8% of it at hidden = 4096 and 15% at 2048.  Workgroups that
+// stay and issue the next tile's loads ahead of the loss's epilogue changed
+// nothing (within 1%, with no spills): the time saved comes back as clock.
 #include "device.hpp"
 #include "gemm_common.hpp"
 #include "host.hpp"
@@ -452,7 +453,7 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
     // MULTI: a token's slots lie in groups of four; its two threads take the
     // even and the odd ones.  The first AHEAD of each are loaded ahead of the
     // statistics, or of the pass before (read where they are used, they and
-    // the row's token cost 5 us a tile in latency).
+    // the row's token cost 4 us a tile in latency).
     constexpr int AHEAD = 8, HELD = EPI == EPI_STATS ? PASSES : 1;
     const int groups = g.slots / 4;
     int4 sid[HELD][AHEAD];
