@@ -28,10 +28,11 @@
 // 131072 x 4096 the loss runs at 1430 TFLOP/s (6.1 ms) and the gradient at 1395
 // (18.9 ms) with the matrix cores busy 82% of the time (dz 78%) at 1.67 GHz; a
 // large library product reaches 1490 on the same operands.  A K stage of a
-// 256 x 256 tile takes 1.43 us, a tile's fixed cost (first loads 2.5 us,
-// epilogue 4 to 5) 8% of it at hidden = 4096 and 15% at 2048.  Workgroups that
-// stay and issue the next tile's loads ahead of the loss's epilogue changed
-// nothing (within 1%, with no spills): the time saved comes back as clock.
+// 256 x 256 tile takes 2220 cycles, 2048 of them matrix instructions, or 1.32
+// to 1.4 us; a tile's fixed cost (first loads 2.3 us, the loss's epilogue 4) is
+// 7% at hidden = 4096 and 13% at 2048.  Workgroups that stay and issue the next
+// tile's loads ahead of the loss's epilogue, all at once or spread over it,
+// took 1 to 2% fewer cycles a tile and no less time (within 1%).
 #include "device.hpp"
 #include "gemm_common.hpp"
 #include "host.hpp"

@@ -170,6 +170,18 @@ def test_slots_that_are_empty_repeated_lowest_or_infinite():
         check(distill(x, w, ids, logits, tau, dloss), want)
 
 
+@pytest.mark.parametrize("T,V,H", [(40, 300, 64), (2000, 8100, 64)])
+def test_many_slots_of_one_id(T, V, H):
+    """Seventy slots over four ids each: their probabilities add up, in the same order every time."""
+    x, w, targets, dloss = make(T, V, H, seed=12, masked=0.1)
+    ids, logits = teacher(T, V, 70, targets, seed=3)
+    ids = torch.where(ids < 0, ids, ids % 4 * (V // 4) + 5)
+    want = head_ref(x.double(), w.double(), slots_of(None, ids, logits, 1.5), 1.5, dloss.double())
+    got = distill(x, w, ids, logits, 1.5, dloss)
+    check(got, want)
+    assert same(got, distill(x, w, ids, logits, 1.5, dloss))
+
+
 def test_one_slot_is_cross_entropy():
     x, w, targets, dloss = make(90, 700, 128, seed=7, masked=0.2)
     a = xent(x, w, targets, dloss)
