@@ -416,9 +416,8 @@ pbs_status pbs_layernorm_grad(const void* dy, pbs_format y_fmt, int64_t lddy, co
  *  dx or dw may be NULL (not computed; not both).  z is formed again, and dz
  *  held in the workspace, for `piece` ids of the vocabulary at a time (rounded
  *  up to a multiple of 256; 0: the library's choice, about 1 GiB of dz).  dz
- *  is rounded to bf16 for the two products (for up to 128 tokens, where such
- *  roundings hardly average out, to a sum of two bf16 terms); all sums are
- *  fp32.
+ *  is rounded to bf16 for the two products (for up to 128 tokens, where that
+ *  costs little more, to a sum of two bf16 terms); all sums are fp32.
  *
  *  workspace: the bytes that pbs_linear_loss_bytes gives for the same tokens,
  *    vocab, hidden, top (0 for cross entropy) and piece, 256-byte aligned.

@@ -1069,12 +1069,15 @@ __global__ void head_zero_kernel(uint4* p, int64_t n16) {
 constexpr int HEAD_TILE = 256, HEAD_SMALL = 128, HEAD_CUS = 256;
 
 // dz goes into the products as bf16, each value off by up to 2^-8 of itself.
-// In sums over many tokens and ids these errors average to less than the
-// result's own rounding.  With few tokens they do not: a row of dx, and the
-// rows of dW it decides, hang on the one or few values of dz at its targets.
-// Up to this many tokens dz is kept as two bf16 terms, the rounded value and
-// what the rounding left (2^-16 together), and both are multiplied: these
-// calls are bound by reading w, not by the matrix cores.
+// A row of dx, and the rows of dW that it decides, hang on the one or few
+// values of dz at its targets, so this does not average out: it is as large as
+// the results' own rounding to bf16 (errors against 64 bits, in 2-norms: 0.0024
+// of dx and dW, 0.0017 of that by their store).  Up to this many tokens dz is
+// kept as two bf16 terms, the rounded value and what the rounding left (2^-16
+// together), and both are multiplied (0.0017): these calls are bound by
+// reading w, not by the matrix cores (gradient 8 x 100000 x 4096 612 -> 694 us,
+// 128 x 50000 x 2048 179 -> 210; with more tokens it would be half as much
+// again).
 constexpr int HEAD_PAIR_TOKENS = 128;
 
 struct HeadPlan {
