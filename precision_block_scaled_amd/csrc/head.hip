@@ -815,8 +815,14 @@ __global__ __launch_bounds__(256) void head_teacher_kernel(TeacherArgs a) {
 // (stages + a tile's fixed cost) plus the partial products' traffic, all in
 // stages.  Never more than 2 x 256 tiles' worth of partial products.  Lanes 0
 // to 15 of a wave weigh 1 to 16 splits each; every lane gets the answer.
+// `beside`: stages that each slot has to do for the other product of the
+// launch.  Its tiles come after these and fill what they leave idle, so the
+// fewest splits do whose tiles end before both products would if spread evenly
+// (gradient, against as many splits as fill the card: 1433 x 49999 x 2048 806
+// -> 770 us, 512 x 32000 x 2048 213 -> 197, 8 x 100000 x 4096 675 -> 614; with
+// 3/4 of that time as the limit 781, 205 and 624).
 constexpr int HEAD_FIXED = 6, HEAD_LEAST_STAGES = 8, HEAD_MOST_SPLITS = 16, HEAD_SPLIT_TILES = 512;
-__device__ __forceinline__ int head_splits(int tiles, int nk, int slots) {
+__device__ __forceinline__ int head_splits(int tiles, int nk, int slots, int beside) {
   const int s = (threadIdx.x & (HEAD_MOST_SPLITS - 1)) + 1;
   const bool may = s == 1 || (nk / s >= HEAD_LEAST_STAGES && tiles <= HEAD_SPLIT_TILES / s);
   const uint32_t rounds = (uint32_t)((tiles - 1) / slots + 1);
@@ -831,7 +837,11 @@ __device__ __forceinline__ int head_splits(int tiles, int nk, int slots) {
     const uint32_t u = (uint32_t)__shfl_xor((int)key, o, 64);
     key = key < u ? key : u;
   }
-  return (int)(key & 15u) + 1;
+  const int best = (int)(key & 15u) + 1;
+  const int all = beside + (int)((int64_t)tiles * (nk + HEAD_FIXED) / slots);
+  const uint64_t fit = __ballot(beside > 0 && may && (nk + s - 1) / s + HEAD_FIXED <= all);
+  const int few = fit ? __ffsll((unsigned long long)fit) : best;
+  return few < best ? few : best;
 }
 
 struct RowsArgs {
@@ -847,6 +857,7 @@ struct RowsArgs {
   uint4* xc;
   int chunks;              // 16-byte chunks of a row of x
   int tile, dx_tn, dx_nk, dw_tiles, turns, slots;  // the gradient's products, for their splits
+  int together;            // dx and dW share their launches
 };
 
 // The live tokens in order, and their rows of x one after the other (unless
@@ -892,8 +903,10 @@ __global__ __launch_bounds__(ROWS_THR) void head_rows_kernel(RowsArgs a) {
   if (blockIdx.x == 0 && w == 0) {
     int dx = 1, dw = 1;
     if (!a.loss) {
-      dx = head_splits((n + a.tile - 1) / a.tile * a.dx_tn, a.dx_nk, a.slots);
-      dw = head_splits(a.dw_tiles, (n + 63) / 64 * a.turns, a.slots);
+      const int dw_nk = (n + 63) / 64 * a.turns;
+      const int beside = a.together ? (int)((int64_t)a.dw_tiles * (dw_nk + HEAD_FIXED) / a.slots) : 0;
+      dx = head_splits((n + a.tile - 1) / a.tile * a.dx_tn, a.dx_nk, a.slots, beside);
+      dw = head_splits(a.dw_tiles, dw_nk, a.slots, 0);
     }
     if (lane == 0) {
       a.live[0] = n;
@@ -1250,6 +1263,7 @@ static HeadArgs head_rows(const HeadCall& c, const HeadPlan& h, hipStream_t stre
   r.tile = h.grad_tile; r.dx_tn = (int)ceil_div(c.hidden, h.grad_tile); r.turns = h.pair ? 2 : 1;
   r.dx_nk = (int)(h.piece / 64) * r.turns;
   r.dw_tiles = (int)(h.piece / h.grad_tile) * r.dx_tn; r.slots = h.wg_slots;
+  r.together = c.dx && c.dw && !h.apart;
   hipLaunchKernelGGL(head_rows_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(c.tokens, 16), HEAD_CUS)),
                      dim3(ROWS_THR), 0, stream, r);
   HeadArgs g = {};
