@@ -177,7 +177,7 @@ __global__ __launch_bounds__(WIDE_THR) void layernorm_dw_wide_kernel(NormArgs a)
 // Rows held in registers: a row is read once.
 //
 // TPR threads share a row (16 or 64: part of a wave or one wave, no barrier;
-// 256 and more: a workgroup), each with NCH chunks of 8 consecutive values, so
+// 192 and more: a workgroup), each with NCH chunks of 8 consecutive values, so
 // a lane's loads and stores are 16 bytes (32 in fp32) at any element address.
 // Workgroups stay and walk over the rows, the next row's loads in flight while
 // a row is reduced; the weights stay in registers.
@@ -372,7 +372,7 @@ struct Chunks {
   __device__ __forceinline__ Chunk<RAGGED> operator[](int j) const { return Chunk<RAGGED>((sub + j * TPR) * 8, cols); }
 };
 
-constexpr int norm_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
+constexpr int norm_threads(int tpr) { return tpr <= 64 ? 256 : tpr; }
 
 template <typename TX, typename TY, int TPR, int NCH, bool RAGGED>
 __global__ __launch_bounds__(norm_threads(TPR)) void layernorm_kernel(NormArgs a) {
@@ -576,45 +576,80 @@ __global__ void norm_fill_kernel(uint32_t* p, int64_t n) {
 }
 
 // Threads a row and chunks of 8 values a thread; 0: the row is too wide for
-// registers.  Workgroups are few enough that their start (weights, the first
-// row's latency) is paid over several rows, and many enough to fill memory's
-// queues: 256-thread workgroups at 512 / 768 / 1024 / 2048 of them took 49.6 /
-// 50.2 / 50.6 / 51.8 us on 15872 x 4096 bf16.  The gradient, which keeps two
-// sums a column in registers, takes a row of 4096 by 512 threads (74.6 us on
-// the same rows; 78.7 with 256 threads of two chunks each), the forward pass,
-// which has one more barrier a row, by 256 (50 us; 51 to 62 with 512).  Widths
-// just past 4096 would leave the second chunk of 512 threads empty: three
-// chunks of 256 threads take 33.9 us on 8192 x 5120 bf16 against 39.8, and
-// 34 against 62 at 4099; at 6144 they lose, 56.8 against 53.6.  Three chunks of
-// 512 threads from 8193 on: 32 us on 4096 x 10240 against 41 with two of 1024.
-// The gradient of widths up to 2048 takes 512 workgroups, each of which leaves
-// a strip of sums to be joined: 21.6 us on 4099 x 1537 fp32, 39.3 on 16384 x
-// 2048 bf16 (768: 22.6 and 40.2; 384: 22.3 and 44.1).
+// registers.  The widest row of a shape is 8 tpr nch; a shape is taken where
+// the row fills most of it, as threads without a chunk cost bandwidth, more of
+// it the shorter the row is in bytes.  65536 rows of bf16, forward / gradient,
+// in us, against the next shape: 16 threads x 2 chunks at 136 and 256 columns
+// 13 / 24 and 15 / 28 (64 x 1: 23 / 33 and 24 / 34), 16 x 3 at 320 18 (24), 64 x
+// 3 at 1032 and 1280 56 / 84 and 62 / 99 (256 x 1: 92 / 130 and 96 / 131), 192 x
+// 2 on 50000 x 2560 105 / 142 (256 x 2: 111, 512 x 1: 203).  In fp32 the forward
+// pass gains by these up to 1280 columns only (65536 x 1536 166 us by 64 x 3,
+// 156 by 256 x 1; 50000 x 2560 208 and 195).  The gradient, which keeps two
+// sums a column in registers, takes a row of 4096 by 512 threads (15872 rows:
+// 74.6 us; 78.7 with 256 threads of two chunks each), the forward pass, which
+// has one more barrier a row, by 256 (50 us; 51 to 62 with 512).  Widths just
+// past 4096 would leave the second chunk of 512 threads empty: three chunks of
+// 256 threads take 33.9 us on 8192 x 5120 bf16 against 39.8, and 34 against 62
+// at 4099; at 6144 they lose, 56.8 against 53.6.  Three chunks of 512 threads
+// from 8193 on: 32 us on 4096 x 10240 against 41 with two of 1024.
+//
+// Workgroups (cap) are few enough that their start (weights, the first row's
+// latency) is paid over several rows, and many enough to fill memory's queues.
+// Forward: 768 (15872 x 4096 bf16 45.4 us, at 512 48.7; 65536 x 768 fp32 to bf16
+// 53 us, at 256 69); from fp32 to fp32, past the 256 MiB of the last-level cache,
+// rows of about 4 MiB in flight (65536 x 2048 at 512 182 us, at 768 217; 32768 x
+// 4096 at 256 184, at 768 196; but 4096 x 3579 26 and 22.5).
+// Gradient: each leaves a strip of sums to be joined, as many for every type:
+// 512 of 256 threads (4099 x 1537 fp32 21.6 us, at 768 22.6), 256 of 512.
 struct NormShape {
   int tpr, nch, cap;
 };
-static NormShape norm_shape(int64_t cols, bool grad) {
+static int norm_rows_per_group(int tpr) { return tpr > 0 && tpr <= 64 ? 256 / tpr : 1; }
+
+static NormShape norm_shape_forward(int64_t rows, int64_t cols, bool x_bf16, bool y_bf16) {
+  if (cols > 16384) return {0, 0, 2048};
+  if (cols > 12288) return {1024, 2, 512};
+  if (cols > 8192) return {512, 3, 256};
+  if (cols > 5632) return {512, 2, 256};
+  NormShape f = cols <= 128                      ? NormShape{16, 1, 768}
+                : cols <= 256                    ? NormShape{16, 2, 1024}
+                : cols <= 384                    ? NormShape{16, 3, 1024}
+                : cols <= 512                    ? NormShape{64, 1, 768}
+                : cols <= 1024                   ? NormShape{64, 2, 768}
+                : cols <= (x_bf16 ? 1536 : 1280) ? NormShape{64, 3, 512}
+                : cols <= 2048                   ? NormShape{256, 1, 768}
+                : cols <= 2816 && x_bf16         ? NormShape{192, 2, 768}
+                : cols <= 4096                   ? NormShape{256, 2, 768}
+                                                 : NormShape{256, 3, 768};
+  if (!x_bf16 && !y_bf16 && rows > (256ll << 20) / (cols * 4)) {
+    const int64_t each = cols * 4 * norm_rows_per_group(f.tpr) * 256;
+    f.cap = 256 * (int)std::min<int64_t>(4, std::max<int64_t>(1, ((4 << 20) + each / 2) / each));
+  }
+  return f;
+}
+
+static NormShape norm_shape_grad(int64_t cols) {
   if (cols <= 128) return {16, 1, 768};
-  if (cols <= 512) return {64, 1, grad ? 512 : 768};
-  if (cols <= 1024) return {64, 2, grad ? 512 : 768};
-  if (cols <= 2048) return {256, 1, grad ? 512 : 768};
-  if (cols <= 4096 && !grad) return {256, 2, 768};
+  if (cols <= 256) return {16, 2, 512};
+  if (cols <= 512) return {64, 1, 512};
+  if (cols <= 1024) return {64, 2, 512};
+  if (cols <= 1280) return {64, 3, 512};
+  if (cols <= 2048) return {256, 1, 512};
+  if (cols <= 2816) return {192, 2, 512};
   if (cols <= 4096) return {512, 1, 256};
-  if (cols <= 5632 && !grad) return {256, 3, 768};
   if (cols <= 8192) return {512, 2, 256};
   if (cols <= 12288) return {512, 3, 256};
-  if (cols <= 16384) return {1024, 2, grad ? 256 : 512};
-  return {0, 0, grad ? 512 : 2048};
+  if (cols <= 16384) return {1024, 2, 256};
+  return {0, 0, 512};
 }
 
 static int norm_grid(const NormShape& f, int64_t rows) {
-  const int64_t groups = ceil_div(std::max<int64_t>(rows, 1), f.tpr && f.tpr < 256 ? 256 / f.tpr : 1);
-  return (int)std::min<int64_t>(groups, f.cap);
+  return (int)std::min<int64_t>(ceil_div(std::max<int64_t>(rows, 1), norm_rows_per_group(f.tpr)), f.cap);
 }
 
 // Strips of rows that leave partial column sums, one for each workgroup of the
 // gradient's pass.
-static int norm_strips(int64_t rows, int64_t cols) { return norm_grid(norm_shape(cols, true), rows); }
+static int norm_strips(int64_t rows, int64_t cols) { return norm_grid(norm_shape_grad(cols), rows); }
 
 }  // namespace pbs
 
@@ -666,16 +701,21 @@ static bool norm_misaligned(const void* p, int bytes) { return ((uintptr_t)p & (
     if (a.cols % 8) PBS_NORM_LAUNCH(kernel, grid, thr, a, PBS_NORM_COMMA T, N, true);                \
     else PBS_NORM_LAUNCH(kernel, grid, thr, a, PBS_NORM_COMMA T, N, false);                          \
   } while (0)
-#define PBS_NORM_SHAPED(kernel, f, grid, a, T4096, N4096)                                           \
-  do {                                                                                              \
-    if (f.tpr == 16) PBS_NORM_RAGGED(kernel, grid, 256, a, 16, 1);                                   \
-    else if (f.tpr == 64 && f.nch == 1) PBS_NORM_RAGGED(kernel, grid, 256, a, 64, 1);                \
-    else if (f.tpr == 64) PBS_NORM_RAGGED(kernel, grid, 256, a, 64, 2);                              \
-    else if (f.tpr == 256 && f.nch == 1) PBS_NORM_RAGGED(kernel, grid, 256, a, 256, 1);              \
-    else if (f.tpr == T4096 && f.nch == N4096) PBS_NORM_RAGGED(kernel, grid, T4096, a, T4096, N4096); \
-    else if (f.tpr == 512 && f.nch == 3) PBS_NORM_RAGGED(kernel, grid, 512, a, 512, 3);              \
-    else if (f.tpr == 512) PBS_NORM_RAGGED(kernel, grid, 512, a, 512, 2);                            \
-    else PBS_NORM_RAGGED(kernel, grid, 1024, a, 1024, 2);                                            \
+#define PBS_NORM_CASE(kernel, f, grid, a, T, N) \
+  if (f.tpr == T && f.nch == N) PBS_NORM_RAGGED(kernel, grid, norm_threads(T), a, T, N)
+// the shapes that both passes use
+#define PBS_NORM_SHAPED(kernel, f, grid, a)             \
+  do {                                                  \
+    PBS_NORM_CASE(kernel, f, grid, a, 16, 1);           \
+    else PBS_NORM_CASE(kernel, f, grid, a, 16, 2);      \
+    else PBS_NORM_CASE(kernel, f, grid, a, 64, 1);      \
+    else PBS_NORM_CASE(kernel, f, grid, a, 64, 2);      \
+    else PBS_NORM_CASE(kernel, f, grid, a, 64, 3);      \
+    else PBS_NORM_CASE(kernel, f, grid, a, 192, 2);     \
+    else PBS_NORM_CASE(kernel, f, grid, a, 256, 1);     \
+    else PBS_NORM_CASE(kernel, f, grid, a, 512, 2);     \
+    else PBS_NORM_CASE(kernel, f, grid, a, 512, 3);     \
+    else PBS_NORM_RAGGED(kernel, grid, 1024, a, 1024, 2); \
   } while (0)
 
 extern "C" {
@@ -699,13 +739,15 @@ pbs_status pbs_layernorm(const void* x, pbs_format x_fmt, int64_t rows, int64_t 
     a.x = x; a.gamma = gamma; a.beta = beta; a.w_bf16 = wb == 2;
     a.rows = rows; a.cols = (int)cols; a.ldx = ldx; a.ldy = ldy; a.eps = eps;
     a.y = y; a.mean = mean; a.rstd = rstd; a.amax = (uint32_t*)amax_out;
-    const NormShape f = norm_shape(cols, false);
+    const NormShape f = norm_shape_forward(rows, cols, x_fmt == PBS_FMT_BF16, y_fmt == PBS_FMT_BF16);
     const unsigned grid = (unsigned)norm_grid(f, rows);
     log_dispatch("layernorm rows=%lld cols=%lld threads/row=%d chunks=%d grid=%u", (long long)rows, (long long)cols,
                  f.tpr, f.nch, grid);
-    if (f.tpr == 256 && f.nch == 3) PBS_NORM_RAGGED(layernorm_kernel, dim3(grid), 256, a, 256, 3);
-    else if (f.tpr) PBS_NORM_SHAPED(layernorm_kernel, f, dim3(grid), a, 256, 2);
-    else PBS_NORM_LAUNCH(layernorm_wide_kernel, dim3(grid), WIDE_THR, a);
+    if (!f.tpr) PBS_NORM_LAUNCH(layernorm_wide_kernel, dim3(grid), WIDE_THR, a);
+    else PBS_NORM_CASE(layernorm_kernel, f, dim3(grid), a, 16, 3);
+    else PBS_NORM_CASE(layernorm_kernel, f, dim3(grid), a, 256, 2);
+    else PBS_NORM_CASE(layernorm_kernel, f, dim3(grid), a, 256, 3);
+    else PBS_NORM_SHAPED(layernorm_kernel, f, dim3(grid), a);
   }
   return check_launch("pbs_layernorm");
 }
@@ -753,13 +795,13 @@ pbs_status pbs_layernorm_grad(const void* dy, pbs_format y_fmt, int64_t lddy, co
   a.x = x; a.dy = dy; a.gamma = gamma; a.w_bf16 = w_fmt == PBS_FMT_BF16;
   a.rows = rows; a.cols = (int)cols; a.ldx = ldx; a.ldy = lddy; a.lddx = lddx;
   a.mean = (float*)mean; a.rstd = (float*)rstd; a.dx = dx; a.part = (float*)workspace;
-  const NormShape f = norm_shape(cols, true);
+  const NormShape f = norm_shape_grad(cols);
   log_dispatch("layernorm_grad rows=%lld cols=%lld threads/row=%d chunks=%d strips=%d", (long long)rows,
                (long long)cols, f.tpr, f.nch, a.strips);
   if (!sums) a.part = nullptr;
-  if (f.tpr) {
-    PBS_NORM_SHAPED(layernorm_grad_kernel, f, dim3(a.strips), a, 512, 1);
-  } else if (sums) {
+  PBS_NORM_CASE(layernorm_grad_kernel, f, dim3(a.strips), a, 512, 1);
+  else if (f.tpr) PBS_NORM_SHAPED(layernorm_grad_kernel, f, dim3(a.strips), a);
+  else if (sums) {
     PBS_NORM_LAUNCH(layernorm_dw_wide_kernel, dim3((unsigned)ceil_div(cols, WIDE_THR), a.strips), WIDE_THR, a);
   }
   if (sums)

@@ -9,12 +9,13 @@ from tests.norm_ref import assert_within, norm_grad_ref, norm_ref
 pytestmark = pytest.mark.gpu
 
 BF, F32 = torch.bfloat16, torch.float32
-# widths around every split of a row over threads: one to 16 values a thread group, 128, 512, 1024, 2048, 4096, 5632,
-# 8192, 12288, 16384 and beyond
+# widths around every split of a row over threads: one to 16 values a thread group, 128, 256, 384, 512, 1024, 1536, 2048,
+# 2816, 4096, 5632, 8192, 12288, 16384 and beyond
 SHAPES = [(1, 1), (1, 7), (3, 8), (5, 9), (70, 64), (2, 127), (17, 128), (65, 129), (33, 512), (9, 513), (7, 1000),
           (5, 2048), (3, 2049), (515, 4096), (2, 4097), (3, 5003), (2, 5632), (2, 5640),
           (3, 8192), (2, 8200), (3, 10007), (2, 12288), (2, 12290), (2, 16384), (2, 16391), (1, 40000),
-          (5000, 24), (2500, 770)]
+          (5000, 24), (2500, 770), (70, 136), (5000, 256), (33, 257), (4100, 384), (9, 385), (66, 1032), (2100, 1536),
+          (5, 1537), (3, 2056), (600, 2816), (4, 2817)]
 TYPES = [(BF, BF, BF), (F32, BF, F32), (F32, F32, F32), (BF, F32, BF)]
 
 
@@ -61,6 +62,15 @@ def test_forward_and_gradient(rows, cols, types):
     again = PL.layernorm_grad(dyg, xg, gg, mean, rstd)
     for a, b in zip(again, (dx, dgamma, dbeta)):
         assert torch.equal(a, b)
+
+
+def test_many_rows():
+    """Many rows a strip, and a last row that is not the last strip's."""
+    x, gamma, beta, dy = make(33001, 1601, BF, BF, BF, seed=5)
+    y, mean, rstd = PL.layernorm(x.cuda(), gamma.cuda(), beta.cuda(), 1e-5)
+    check_forward(x, gamma, beta, y, mean, rstd, 1e-5, "rows")
+    got = PL.layernorm_grad(dy.cuda(), x.cuda(), gamma.cuda(), mean, rstd)
+    check_grad(dy, x, gamma, mean, rstd, *got, "rows")
 
 
 def test_no_weights_and_single_outputs():
