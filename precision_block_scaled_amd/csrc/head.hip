@@ -61,7 +61,8 @@ struct HeadArgs {
   const float* lse;        // per token
   const float* dloss;      // per token
   uint16_t* dz;            // [rows][dz_ld]; PAIR: [rows][2][dz_ld], dz rounded and what that left out
-  float* dx_part;          // partial products of dx
+  uint16_t* dx;            // dx itself, where one product gives all of it; else null and
+  float* dx_part;          //   partial products of dx
   float* dw_part;          // partial products of dW
   void* dw;                // this piece of dW
   int dx_blocks;           // workgroups of dx ahead of dW's
@@ -669,14 +670,15 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
   } else {
     constexpr int LPR = M_T / 8, RPI = 256 / LPR;              // lanes a row, 8 values each; rows a round
     const int col = m0 + (t % LPR) * 8;
-    if (EPI == EPI_DW && splits == 1 && g.out_bf16) {
+    if (EPI == EPI_DX ? g.dx != nullptr : splits == 1 && g.out_bf16) {
+      uint16_t* out = EPI == EPI_DX ? g.dx : (uint16_t*)g.dw;
 #pragma unroll
       for (int j = 0; j < TJ; ++j) stage_bf16(j);
       stage_barrier<63>();
 #pragma unroll 4
       for (int s = t / LPR; s < N_T; s += RPI)
         if (n0 + s < N && col < M)
-          *(uint4*)((uint16_t*)g.dw + (int64_t)(n0 + s) * g.hidden + col) =
+          *(uint4*)(out + (int64_t)(EPI == EPI_DX ? g.row_of[n0 + s] : n0 + s) * g.hidden + col) =
               *(const uint4*)(smem + s * PITCHB + (t % LPR) * 16);
       return;
     }
@@ -858,6 +860,8 @@ struct RowsArgs {
   int chunks;              // 16-byte chunks of a row of x
   int tile, dx_tn, dx_nk, dw_tiles, turns, slots;  // the gradient's products, for their splits
   int together;            // dx and dW share their launches
+  int dx_whole;            // dx is not split
+  uint4* zero_dx;          // the rows of dx that nothing else writes, those of the tokens left out (or null)
 };
 
 // The live tokens in order, and their rows of x one after the other (unless
@@ -905,7 +909,7 @@ __global__ __launch_bounds__(ROWS_THR) void head_rows_kernel(RowsArgs a) {
     if (!a.loss) {
       const int dw_nk = (n + 63) / 64 * a.turns;
       const int beside = a.together ? (int)((int64_t)a.dw_tiles * (dw_nk + HEAD_FIXED) / a.slots) : 0;
-      dx = head_splits((n + a.tile - 1) / a.tile * a.dx_tn, a.dx_nk, a.slots, beside);
+      if (!a.dx_whole) dx = head_splits((n + a.tile - 1) / a.tile * a.dx_tn, a.dx_nk, a.slots, beside);
       dw = head_splits(a.dw_tiles, dw_nk, a.slots, 0);
     }
     if (lane == 0) {
@@ -933,8 +937,11 @@ __global__ __launch_bounds__(ROWS_THR) void head_rows_kernel(RowsArgs a) {
       const int items = (int)(hi - t0 < 64 ? hi - t0 : 64) * segs;
       for (int i = w; i < items; i += ROWS_WAVES) {
         const int k = i / segs, c = (i - k * segs) * 64 + lane;
-        if (!((mask >> k) & 1) || c >= a.chunks) continue;
-        a.xc[(int64_t)(before + __popcll(mask & ((1ull << k) - 1))) * a.chunks + c] = a.x[(t0 + k) * a.chunks + c];
+        if (c >= a.chunks) continue;
+        if ((mask >> k) & 1)
+          a.xc[(int64_t)(before + __popcll(mask & ((1ull << k) - 1))) * a.chunks + c] = a.x[(t0 + k) * a.chunks + c];
+        else if (a.zero_dx)
+          a.zero_dx[(t0 + k) * a.chunks + c] = make_uint4(0, 0, 0, 0);
       }
     }
     before += __popcll(mask);
@@ -1097,7 +1104,7 @@ struct HeadPlan {
   int64_t rows, slots, parts, piece;
   int loss_tile, dz_tile, grad_tile, wg_slots;                    // the gradient's workgroups at a time
   int64_t dx_grid, dw_grid;                              // most tiles, splits included
-  bool pair, dw_can_split, apart;
+  bool pair, dw_can_split, apart, dx_whole;
   size_t live, row_of, pos_of, state, ids, p, ent, xc;
   size_t zsel, stats, loss_bytes;                        // the loss
   size_t dz, dxp, dwp, grad_bytes;                       // the gradient
@@ -1151,9 +1158,18 @@ static HeadPlan head_plan(int64_t tokens, int64_t vocab, int64_t hidden, int64_t
   h.dx_grid = ceil_div(std::max<int64_t>(ceil_div(tokens, h.grad_tile) * hn, HEAD_SPLIT_TILES), NXCD) * NXCD;
   h.dw_grid = std::max<int64_t>(h.piece / h.grad_tile * hn, HEAD_SPLIT_TILES);
   h.dz = take((h.pair ? 4 : 2) * h.rows * h.piece);
+  // A vocabulary of one piece whose product for dx is too short to be split, or
+  // short (a tile of 64 stages takes 90 us) and with tiles enough: its result is
+  // dx, stored as such.  Otherwise dx goes through fp32 partial products and
+  // head_dx_kernel (gradient 15872 x 69 x 4096: 142 us, 261 through them; 15872 x
+  // 1000 x 4096: 373 and 488).
+  const int64_t dx_nk = h.piece / 64 * (h.pair ? 2 : 1);
+  h.dx_whole = vocab <= h.piece &&
+               (dx_nk < 2 * HEAD_LEAST_STAGES ||
+                (dx_nk <= 64 && ceil_div(tokens, h.grad_tile) * hn * 2 > HEAD_SPLIT_TILES));
   // partial products: the tiles of one product, or of all splits of one that is split
   const int64_t tile_values = (int64_t)h.grad_tile * hidden;
-  h.dxp = take(4 * tile_values * std::max(ceil_div(tokens, h.grad_tile), HEAD_SPLIT_TILES / hn));
+  h.dxp = take(h.dx_whole ? 0 : 4 * tile_values * std::max(ceil_div(tokens, h.grad_tile), HEAD_SPLIT_TILES / hn));
   // Two full rounds of dx tiles need nothing to fill up with, and the two
   // products then run apart, each with its own operands in the caches (8192 x
   // 131072 x 4096: 19.26 ms apart, 19.58 together; 512 x 32000 x 2048: 239 us
@@ -1264,6 +1280,8 @@ static HeadArgs head_rows(const HeadCall& c, const HeadPlan& h, hipStream_t stre
   r.dx_nk = (int)(h.piece / 64) * r.turns;
   r.dw_tiles = (int)(h.piece / h.grad_tile) * r.dx_tn; r.slots = h.wg_slots;
   r.together = c.dx && c.dw && !h.apart;
+  r.dx_whole = h.dx_whole;
+  r.zero_dx = h.dx_whole ? (uint4*)c.dx : nullptr;
   hipLaunchKernelGGL(head_rows_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(c.tokens, 16), HEAD_CUS)),
                      dim3(ROWS_THR), 0, stream, r);
   HeadArgs g = {};
@@ -1323,6 +1341,7 @@ static pbs_status head_grad(const HeadCall& c, hipStream_t stream) {
   uint8_t* ws = (uint8_t*)c.ws;
   HeadArgs g = head_rows(c, h, stream);
   g.lse = c.lse; g.dloss = c.dloss; g.dz = (uint16_t*)(ws + h.dz); g.dz_ld = (int)h.piece; g.out_bf16 = dwb == 2;
+  g.dx = h.dx_whole ? (uint16_t*)c.dx : nullptr;
   g.dx_part = (float*)(ws + h.dxp); g.dw_part = (float*)(ws + h.dwp);
   log_dispatch("%s tokens=%lld vocab=%lld hidden=%lld top=%lld piece=%lld tiles=%d,%d", c.what, (long long)c.tokens,
                (long long)c.vocab, (long long)c.hidden, (long long)c.top, (long long)h.piece, h.dz_tile, h.grad_tile);
@@ -1347,7 +1366,7 @@ static pbs_status head_grad(const HeadCall& c, hipStream_t stream) {
                          dim3(256), 0, stream, g.dw_part, g.live, h.piece * c.hidden, nv * c.hidden / 8, g.dw,
                          g.out_bf16);
   }
-  if (c.dx)
+  if (c.dx && !h.dx_whole)
     hipLaunchKernelGGL(head_dx_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(c.tokens * c.hidden / 8, 256), 2048)),
                        dim3(256), 0, stream, (const float*)(ws + h.dxp), g.live, h.grad_tile, g.hidden,
                        (const int*)(ws + h.pos_of), c.tokens * c.hidden / 8, (int)(c.hidden / 8), (uint16_t*)c.dx);

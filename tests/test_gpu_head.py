@@ -76,6 +76,19 @@ def test_cross_entropy(T, V, H, masked):
     assert same(got, xent(x, w, targets, dloss))
 
 
+@pytest.mark.parametrize("T,V,H", [(33000, 69, 1024), (8300, 1100, 2048)])
+def test_small_vocabulary(T, V, H):
+    """Many tokens against few ids: dx is stored by its product, zeros for the tokens left out."""
+    x, w, targets, dloss = make(T, V, H, seed=14, masked=0.3)
+    want = head_ref(x.double(), w.double(), slots_of(targets), 1.0, dloss.double())
+    got = xent(x, w, targets, dloss)
+    check(got, want)
+    assert not got["dx"][(targets < 0).cuda()].any()
+    assert same(got, xent(x, w, targets, dloss))
+    alone, _ = PL.linear_xent_grad(dloss.cuda(), x.cuda(), w.cuda(), targets.cuda(), got["lse"], need_dw=False)
+    assert torch.equal(alone, got["dx"])
+
+
 @pytest.mark.parametrize("k,tau,dtype", [(1, 1.0, F32), (5, 2.0, BF), (32, 0.7, F32), (130, 3.0, F32)])
 @pytest.mark.parametrize("T,V,H", SHAPES)
 def test_distillation(T, V, H, k, tau, dtype):
