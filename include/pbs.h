@@ -415,7 +415,8 @@ pbs_status pbs_layernorm_grad(const void* dy, pbs_format y_fmt, int64_t lddy, co
  *   dw = dz^T x   bf16 or fp32 (dw_fmt) [vocab, hidden]
  *  dx or dw may be NULL (not computed; not both).  z is formed again, and dz
  *  held in the workspace, for `piece` ids of the vocabulary at a time (rounded
- *  up to a multiple of 256; 0: the library's choice, about 1 GiB of dz).  dz
+ *  up to a multiple of 256; 0: the library's choice, up to 1 GiB of dz, or 2048
+ *  ids where those take more, beyond 2^18 tokens).  dz
  *  is rounded to bf16 for the two products (for up to 128 tokens, where that
  *  costs little more, to a sum of two bf16 terms); all sums are fp32.
  *

@@ -1129,9 +1129,12 @@ static HeadPlan head_plan(int64_t tokens, int64_t vocab, int64_t hidden, int64_t
     return here;
   };
   const int64_t tm = ceil_div(tokens, HEAD_TILE), th = ceil_div(hidden, HEAD_TILE);
-  h.rows = tm * HEAD_TILE;
+  h.pair = tokens <= HEAD_PAIR_TOKENS;
+  // rows of dz and of the statistics, in whole tiles: those few tokens only meet small ones
+  const int64_t row_tile = h.pair ? HEAD_SMALL : HEAD_TILE;
+  h.rows = ceil_div(tokens, row_tile) * row_tile;
   h.slots = xent ? 1 : ceil_div(top, 4) * 4;
-  h.loss_tile = head_tile(tokens, vocab);
+  h.loss_tile = h.pair ? HEAD_SMALL : head_tile(tokens, vocab);
   h.parts = ceil_div(vocab, h.loss_tile) * 2;
   h.live = take(12);
   h.row_of = take(4 * tokens);
@@ -1146,10 +1149,11 @@ static HeadPlan head_plan(int64_t tokens, int64_t vocab, int64_t hidden, int64_t
   h.stats = take(8 * h.parts * h.rows);
   h.loss_bytes = at;
   at = shared;
-  // default piece: dz of a piece at most 1 GiB, and at least 2048 ids
-  if (piece <= 0) piece = std::max<int64_t>(2048, (1ll << 30) / (2 * std::max<int64_t>(h.rows, 1)));
+  // default piece: dz of a piece (both its terms) at most 1 GiB, or 2048 ids where these take more
+  const int64_t dz_row = h.pair ? 4 : 2;
+  if (piece <= 0)
+    piece = std::max<int64_t>(2048, (1ll << 30) / (dz_row * std::max<int64_t>(h.rows, 1)) / HEAD_TILE * HEAD_TILE);
   h.piece = ceil_div(std::min(piece, vocab), HEAD_TILE) * HEAD_TILE;
-  h.pair = tokens <= HEAD_PAIR_TOKENS;
   h.dz_tile = h.pair ? HEAD_SMALL : head_tile(tokens, std::min(h.piece, vocab));
   // dx and dW together, dx counted as the splits it may have: small tiles while both leave compute units idle
   h.grad_tile = h.pair || (h.piece / HEAD_TILE + tm) * th < HEAD_CUS / 2 ? HEAD_SMALL : HEAD_TILE;
@@ -1157,7 +1161,7 @@ static HeadPlan head_plan(int64_t tokens, int64_t vocab, int64_t hidden, int64_t
   const int64_t hn = ceil_div(hidden, h.grad_tile);
   h.dx_grid = ceil_div(std::max<int64_t>(ceil_div(tokens, h.grad_tile) * hn, HEAD_SPLIT_TILES), NXCD) * NXCD;
   h.dw_grid = std::max<int64_t>(h.piece / h.grad_tile * hn, HEAD_SPLIT_TILES);
-  h.dz = take((h.pair ? 4 : 2) * h.rows * h.piece);
+  h.dz = take(dz_row * h.rows * h.piece);
   // A vocabulary of one piece whose product for dx is too short to be split, or
   // short (a tile of 64 stages takes 90 us) and with tiles enough: its result is
   // dx, stored as such.  Otherwise dx goes through fp32 partial products and

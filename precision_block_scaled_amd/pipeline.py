@@ -551,7 +551,8 @@ def linear_xent_grad(dloss, x, w, targets, lse, piece=0, need_dx=True, need_dw=T
                      stream=None):
     """Gradients of sum(dloss * loss) of ``linear_xent``: (dx [T, H] bf16, dw
     [V, H] in ``dw_dtype``), None for one that is not needed.  The workspace
-    holds the logits' gradient for ``piece`` ids at a time (0: about 1 GiB)."""
+    holds the logits' gradient for ``piece`` ids at a time (0: up to 1 GiB of
+    it, or 2048 ids where those take more)."""
     T, V, H = _head(x, w)
     _given(dloss=dloss, targets=targets, lse=lse)
     t = _vector("targets", targets, T, I64, x.device)

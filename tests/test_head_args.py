@@ -129,3 +129,16 @@ def test_reference_gradients_against_differences():
                     args = (moved if t is x else x, moved if t is w else w)
                     ends.append((head_ref(*args, slots, tau)["loss"][0] * c).sum())
                 assert abs((ends[0] - ends[1]) / 2e-5 - ref[name][0][at]) < 1e-8
+
+
+@needs_lib
+def test_default_piece_is_a_gib_of_dz():
+    """Without a piece the workspace is at most 1 GiB of dz (one or two terms, rows in whole tiles) and what the rest
+    takes: x and dx of the tokens in 2 and 4 bytes, 64 MiB of splits and lists.  More than 2^18 tokens take 2048 ids all
+    the same."""
+    for tokens, vocab in ((1, 1 << 21), (1, 1 << 22), (17, 1 << 22), (100, 1 << 21), (128, 1 << 22), (129, 1 << 22),
+                          (1000, 1 << 20), (20000, 1 << 18), (200000, 1 << 14), (1 << 18, 1 << 14)):
+        most = (1 << 30) + (64 << 20) + (2 + 4) * tokens * 64
+        assert P.pbs_linear_loss_bytes(tokens, vocab, 64)[1] <= most, (tokens, vocab)
+    dz = 2 * (1 << 20) * 2048
+    assert dz <= P.pbs_linear_loss_bytes(1 << 20, 5000, 64)[1] < dz + (1 << 30)
