@@ -1171,9 +1171,14 @@ static HeadPlan head_plan(int64_t tokens, int64_t vocab, int64_t hidden, int64_t
   h.dx_whole = vocab <= h.piece &&
                (dx_nk < 2 * HEAD_LEAST_STAGES ||
                 (dx_nk <= 64 && ceil_div(tokens, h.grad_tile) * hn * 2 > HEAD_SPLIT_TILES));
-  // partial products: the tiles of one product, or of all splits of one that is split
+  // partial products: the tiles of one product, or of all splits of one that
+  // is split (fewer live rows may be split more often, but not into more tiles
+  // than HEAD_SPLIT_TILES nor more often than HEAD_MOST_SPLITS)
   const int64_t tile_values = (int64_t)h.grad_tile * hidden;
-  h.dxp = take(h.dx_whole ? 0 : 4 * tile_values * std::max(ceil_div(tokens, h.grad_tile), HEAD_SPLIT_TILES / hn));
+  auto partial = [&](int64_t tile_rows) {
+    return 4 * tile_values * std::max(tile_rows, std::min<int64_t>(HEAD_SPLIT_TILES / hn, HEAD_MOST_SPLITS * tile_rows));
+  };
+  h.dxp = take(h.dx_whole ? 0 : partial(ceil_div(tokens, h.grad_tile)));
   // Two full rounds of dx tiles need nothing to fill up with, and the two
   // products then run apart, each with its own operands in the caches (8192 x
   // 131072 x 4096: 19.26 ms apart, 19.58 together; 512 x 32000 x 2048: 239 us
@@ -1182,7 +1187,7 @@ static HeadPlan head_plan(int64_t tokens, int64_t vocab, int64_t hidden, int64_t
   // as head_splits decides for any number of live rows
   h.dw_can_split = h.piece / h.grad_tile * hn * 2 <= HEAD_SPLIT_TILES &&
                    ceil_div(tokens, 64) * (h.pair ? 2 : 1) / 2 >= HEAD_LEAST_STAGES;
-  h.dwp = take(h.dw_can_split ? 4 * tile_values * (HEAD_SPLIT_TILES / hn) : 0);
+  h.dwp = take(h.dw_can_split ? partial(h.piece / h.grad_tile) : 0);
   h.grad_bytes = at;
   return h;
 }

@@ -363,3 +363,27 @@ def test_norm_head_loss_and_back():
     assert abs((loss.double().cpu() * dloss).sum() - want) < 2 ** -8 * want
     for name, got, ref in zip(("dx", "dw", "dgamma", "dbeta"), (dx, dw, dgamma, dbeta), grads):
         assert (got.double().cpu() - ref).norm() <= 4 * 2 ** -8 * ref.norm(), name
+
+
+@pytest.mark.parametrize("T,V,H,top", [(1, 300, 64, 0), (37, 2003, 256, 7), (70, 9001, 512, 0), (129, 500, 64, 5),
+                                       (300, 33001, 192, 0), (2100, 300, 64, 0), (4100, 1000, 128, 9)])
+@pytest.mark.parametrize("masked", [0.0, 0.7])
+def test_workspace_is_not_overrun(T, V, H, top, masked):
+    """Exactly the bytes that pbs_linear_loss_bytes gives, what lies behind them untouched: partial products of dx and
+    dW in as many splits as the live rows allow."""
+    x, w, targets, dloss = make(T, V, H, seed=21, masked=masked)
+    ids, logits = (t.cuda() for t in teacher(T, V, top or 1, targets))
+    x, w, targets, dloss = (t.cuda() for t in (x, w, targets, dloss))
+    a, b = P.pbs_linear_loss_bytes(T, V, H, top)
+    lse = (PL.linear_distill(x, w, ids, logits, 2.0) if top else PL.linear_xent(x, w, targets))[1]
+    ws = torch.full((b + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    if top:
+        P.pbs_linear_distill_grad(dloss, x, w, T, V, H, ids, logits, P.PBS_FMT_F32, top, 2.0, lse, 0, dx, dw,
+                                  P.PBS_FMT_BF16, ws, b)
+        want = PL.linear_distill_grad(dloss, x, w, ids, logits, 2.0, lse)
+    else:
+        P.pbs_linear_xent_grad(dloss, x, w, T, V, H, targets, lse, 0, dx, dw, P.PBS_FMT_BF16, ws, b)
+        want = PL.linear_xent_grad(dloss, x, w, targets, lse)
+    assert (ws[b:] == 0x5A).all()
+    assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])

@@ -142,3 +142,14 @@ def test_default_piece_is_a_gib_of_dz():
         assert P.pbs_linear_loss_bytes(tokens, vocab, 64)[1] <= most, (tokens, vocab)
     dz = 2 * (1 << 20) * 2048
     assert dz <= P.pbs_linear_loss_bytes(1 << 20, 5000, 64)[1] < dz + (1 << 30)
+
+
+@needs_lib
+def test_workspace_of_small_gradients():
+    """Partial products take 16 splits of the tiles that a call has (128 x 128, whole rows of dx and dW) and no more."""
+    for tokens, vocab, hidden, top in ((37, 2003, 256, 7), (1, 300, 64, 0), (100, 5000, 4096, 0), (700, 131, 64, 0)):
+        rows, ids = (-(-n // 256) * 256 for n in (tokens, vocab))
+        most = 16 * 4 * hidden * (rows + ids)                    # splits of dx and dW
+        most += 4 * rows * ids + 2 * tokens * hidden             # dz, x of the live tokens
+        most += tokens * (20 + 8 * (top + 3)) + 16 * 256         # lists, slots, alignment
+        assert P.pbs_linear_loss_bytes(tokens, vocab, hidden, top)[1] <= most, (tokens, vocab, hidden)
