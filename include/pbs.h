@@ -373,8 +373,8 @@ pbs_status pbs_layernorm(const void* x, pbs_format x_fmt, int64_t rows, int64_t 
  *  mean, rstd: what pbs_layernorm returned.
  *  dx, dgamma, dbeta: any of them may be NULL (not computed).  dgamma and
  *    dbeta are fp32 [cols]; their sums over the rows are split and joined in
- *    an order that depends on rows and cols alone, so identical inputs give
- *    identical bytes.  dx may be x or dy itself (same format and stride).
+ *    an order that depends on rows, cols and formats alone, so identical
+ *    inputs give identical bytes.  dx may be x or dy itself (same format and stride).
  *  workspace: pbs_layernorm_grad_bytes(rows, cols) bytes, 16-byte aligned,
  *    for dgamma / dbeta (unused, may be NULL, if both are); its contents are
  *    of no use afterwards.  Calls that may run at the same time need one each.

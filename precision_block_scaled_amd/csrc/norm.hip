@@ -14,6 +14,7 @@
 #include "host.hpp"
 
 #include <algorithm>
+#include <cstdlib>
 
 namespace pbs {
 
@@ -580,11 +581,19 @@ __global__ void norm_fill_kernel(uint32_t* p, int64_t n) {
 // the row fills most of it, as threads without a chunk cost bandwidth, more of
 // it the shorter the row is in bytes.  65536 rows of bf16, forward / gradient,
 // in us, against the next shape: 16 threads x 2 chunks at 136 and 256 columns
-// 13 / 24 and 15 / 28 (64 x 1: 23 / 33 and 24 / 34), 16 x 3 at 320 18 (24), 64 x
-// 3 at 1032 and 1280 56 / 84 and 62 / 99 (256 x 1: 92 / 130 and 96 / 131), 192 x
-// 2 on 50000 x 2560 105 / 142 (256 x 2: 111, 512 x 1: 203).  In fp32 the forward
-// pass gains by these up to 1280 columns only (65536 x 1536 166 us by 64 x 3,
-// 156 by 256 x 1; 50000 x 2560 208 and 195).  The gradient, which keeps two
+// 13 / 26 and 14 / 29 (64 x 1: 23 / 33 and 24 / 34), 16 x 3 at 320 17 (24), 64 x
+// 3 at 1032 and 1280 59 / 84 and 62 / 99 (256 x 1: 93 / 130 and 97 / 132), 192 x
+// 2 on 52428 x 2560 110 / 148 (256 x 2: 116, 512 x 1: 211).
+//
+// The wider the values, the sooner the next shape is the better one, as its
+// empty threads cost less and its fuller ones take longer.  Forward, 65536 x
+// 1536: bf16 79 by 64 x 3 and 98 by 256 x 1, bf16 to fp32 130 and 116, fp32 166
+// and 156.  Gradient: fp32 with bf16 dy, 65536 x 1100 149 by 64 x 3 and 152 by
+// 256 x 1, at 1200 159 and 156; 65280 x 2056 266 by 192 x 2 and 279 by 512 x 1, at
+// 2304 262 and 256; fp32 with fp32 dy, 65536 x 1032 166 and 162, at 1200 185 and
+// 174, 52428 x 2560 298 and 275.
+//
+// The gradient, which keeps two
 // sums a column in registers, takes a row of 4096 by 512 threads (15872 rows:
 // 74.6 us; 78.7 with 256 threads of two chunks each), the forward pass, which
 // has one more barrier a row, by 256 (50 us; 51 to 62 with 512).  Widths just
@@ -597,10 +606,12 @@ __global__ void norm_fill_kernel(uint32_t* p, int64_t n) {
 // latency) is paid over several rows, and many enough to fill memory's queues.
 // Forward: 768 (15872 x 4096 bf16 45.4 us, at 512 48.7; 65536 x 768 fp32 to bf16
 // 53 us, at 256 69); from fp32 to fp32, past the 256 MiB of the last-level cache,
-// rows of about 4 MiB in flight (65536 x 2048 at 512 182 us, at 768 217; 32768 x
-// 4096 at 256 184, at 768 196; but 4096 x 3579 26 and 22.5).
-// Gradient: each leaves a strip of sums to be joined, as many for every type:
-// 512 of 256 threads (4099 x 1537 fp32 21.6 us, at 768 22.6), 256 of 512.
+// rows of about 4 MiB in flight (65536 x 2048 at 512 183 us, at 768 218; 32768 x
+// 4096 at 256 184, at 768 196; but 4096 x 3579 26 and 22.5), where a multiple of
+// 256 workgroups of one row each comes within a fifth of that (52428 x 2560 at
+// 512 220, at 256 225, at 768 204).
+// Gradient: each leaves a strip of sums to be joined: 512 of 256 threads (4099 x
+// 1537 fp32 21.6 us, at 768 22.6), 256 of 512.
 struct NormShape {
   int tpr, nch, cap;
 };
@@ -616,26 +627,27 @@ static NormShape norm_shape_forward(int64_t rows, int64_t cols, bool x_bf16, boo
                 : cols <= 384                    ? NormShape{16, 3, 1024}
                 : cols <= 512                    ? NormShape{64, 1, 768}
                 : cols <= 1024                   ? NormShape{64, 2, 768}
-                : cols <= (x_bf16 ? 1536 : 1280) ? NormShape{64, 3, 512}
+                : cols <= (x_bf16 && y_bf16 ? 1536 : 1280) ? NormShape{64, 3, 512}
                 : cols <= 2048                   ? NormShape{256, 1, 768}
                 : cols <= 2816 && x_bf16         ? NormShape{192, 2, 768}
                 : cols <= 4096                   ? NormShape{256, 2, 768}
                                                  : NormShape{256, 3, 768};
   if (!x_bf16 && !y_bf16 && rows > (256ll << 20) / (cols * 4)) {
-    const int64_t each = cols * 4 * norm_rows_per_group(f.tpr) * 256;
-    f.cap = 256 * (int)std::min<int64_t>(4, std::max<int64_t>(1, ((4 << 20) + each / 2) / each));
+    const int64_t want = 4 << 20, each = cols * 4 * norm_rows_per_group(f.tpr) * 256;
+    const int64_t n = std::min<int64_t>(4, std::max<int64_t>(1, (want + each / 2) / each));
+    if (f.tpr <= 64 || 5 * std::abs(n * each - want) <= want) f.cap = 256 * (int)n;
   }
   return f;
 }
 
-static NormShape norm_shape_grad(int64_t cols) {
+static NormShape norm_shape_grad(int64_t cols, bool x_bf16, bool dy_bf16) {
   if (cols <= 128) return {16, 1, 768};
   if (cols <= 256) return {16, 2, 512};
   if (cols <= 512) return {64, 1, 512};
   if (cols <= 1024) return {64, 2, 512};
-  if (cols <= 1280) return {64, 3, 512};
+  if (cols <= (x_bf16 ? 1280 : dy_bf16 ? 1152 : 1024)) return {64, 3, 512};
   if (cols <= 2048) return {256, 1, 512};
-  if (cols <= 2816) return {192, 2, 512};
+  if (cols <= (x_bf16 ? 2816 : dy_bf16 ? 2176 : 2048)) return {192, 2, 512};
   if (cols <= 4096) return {512, 1, 256};
   if (cols <= 8192) return {512, 2, 256};
   if (cols <= 12288) return {512, 3, 256};
@@ -647,9 +659,13 @@ static int norm_grid(const NormShape& f, int64_t rows) {
   return (int)std::min<int64_t>(ceil_div(std::max<int64_t>(rows, 1), norm_rows_per_group(f.tpr)), f.cap);
 }
 
-// Strips of rows that leave partial column sums, one for each workgroup of the
-// gradient's pass.
-static int norm_strips(int64_t rows, int64_t cols) { return norm_grid(norm_shape_grad(cols), rows); }
+// Bytes for the partial column sums of a gradient's strips of rows, one strip
+// for each workgroup of its pass, whatever its formats.
+static size_t norm_grad_bytes(int64_t rows, int64_t cols) {
+  int strips = 0;
+  for (int t = 0; t < 4; ++t) strips = std::max(strips, norm_grid(norm_shape_grad(cols, t & 1, t >> 1), rows));
+  return (size_t)strips * 2 * (size_t)cols * 4;
+}
 
 }  // namespace pbs
 
@@ -757,7 +773,7 @@ pbs_status pbs_layernorm_grad_bytes(int64_t rows, int64_t cols, size_t* bytes) {
   PBS_REQUIRE(rows >= 0 && cols >= 1 && cols <= (1 << 24) && rows <= (1ll << 40), PBS_ERR_SHAPE,
               "pbs_layernorm_grad_bytes: needs rows in [0, 2^40] and cols in [1, 2^24] (got %lld x %lld)",
               (long long)rows, (long long)cols);
-  *bytes = (size_t)norm_strips(rows, cols) * 2 * (size_t)cols * 4;
+  *bytes = norm_grad_bytes(rows, cols);
   return PBS_OK;
 }
 
@@ -783,19 +799,20 @@ pbs_status pbs_layernorm_grad(const void* dy, pbs_format y_fmt, int64_t lddy, co
     return check_launch("pbs_layernorm_grad");
   }
   NormArgs a = {};
-  a.strips = norm_strips(rows, cols);
+  const NormShape f = norm_shape_grad(cols, x_fmt == PBS_FMT_BF16, y_fmt == PBS_FMT_BF16);
+  a.strips = norm_grid(f, rows);
   const bool sums = dgamma || dbeta;
   if (sums) {
     PBS_REQUIRE(workspace && ((uintptr_t)workspace & 15) == 0, PBS_ERR_INVALID_ARG,
                 "pbs_layernorm_grad: the workspace is null or not 16-byte aligned");
-    PBS_REQUIRE(workspace_bytes >= (size_t)a.strips * 2 * (size_t)cols * 4, PBS_ERR_INVALID_ARG,
+    const size_t need = norm_grad_bytes(rows, cols);
+    PBS_REQUIRE(workspace_bytes >= need, PBS_ERR_INVALID_ARG,
                 "pbs_layernorm_grad: the workspace holds %zu bytes, pbs_layernorm_grad_bytes asks for %zu",
-                workspace_bytes, (size_t)a.strips * 2 * (size_t)cols * 4);
+                workspace_bytes, need);
   }
   a.x = x; a.dy = dy; a.gamma = gamma; a.w_bf16 = w_fmt == PBS_FMT_BF16;
   a.rows = rows; a.cols = (int)cols; a.ldx = ldx; a.ldy = lddy; a.lddx = lddx;
   a.mean = (float*)mean; a.rstd = (float*)rstd; a.dx = dx; a.part = (float*)workspace;
-  const NormShape f = norm_shape_grad(cols);
   log_dispatch("layernorm_grad rows=%lld cols=%lld threads/row=%d chunks=%d strips=%d", (long long)rows,
                (long long)cols, f.tpr, f.nch, a.strips);
   if (!sums) a.part = nullptr;
