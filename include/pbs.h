@@ -417,8 +417,12 @@ pbs_status pbs_layernorm_grad(const void* dy, pbs_format y_fmt, int64_t lddy, co
  *  held in the workspace, for `piece` ids of the vocabulary at a time (rounded
  *  up to a multiple of 256; 0: the library's choice, up to 1 GiB of dz, or 2048
  *  ids where those take more, beyond 2^18 tokens).  dz
- *  is rounded to bf16 for the two products (for up to 128 tokens, where that
- *  costs little more, to a sum of two bf16 terms); all sums are fp32.
+ *  is rounded to bf16 for the two products, but for a token's large values,
+ *  those at its target or at the ids with p > 1/5 of its teacher: what their
+ *  rounding leaves out is added in fp32, to dx always, to dw where an id is one
+ *  of these for up to 8 tokens (with more their roundings average out).  For up
+ *  to 128 tokens all of dz is a sum of two bf16 terms, which costs little more
+ *  there.  All sums are fp32.
  *
  *  workspace: the bytes that pbs_linear_loss_bytes gives for the same tokens,
  *    vocab, hidden, top (0 for cross entropy) and piece, 256-byte aligned.

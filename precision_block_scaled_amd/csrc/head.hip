@@ -15,7 +15,8 @@
 // the slots' own logits; a second kernel joins them.  The
 // gradient forms z again for a piece of the vocabulary at a time, turns it
 // into dz (bf16, in the workspace) in the product's epilogue and multiplies
-// that by W and, transposed, by x.  Tokens that take no part are left out:
+// that by W and, transposed, by x; what the rounding to bf16 leaves out of a
+// token's few large values is added in fp32.  Tokens that take no part are left out:
 // the others' rows are gathered first, so a masked token costs nothing and
 // whatever its row of x holds reaches no sum.
 //
@@ -46,6 +47,43 @@ enum { KMAJ = 0, MNMAJ = 1 };                    // how an operand is stored
 enum { EPI_STATS = 0, EPI_DZ = 1, EPI_DX = 2, EPI_DW = 3 };
 enum { ROW_OUT = 0, ROW_LIVE = 1, ROW_BAD = 2 }; // a token: no part, part, an id past the vocabulary
 
+// dz goes into the products as bf16, each value off by up to 2^-8 of itself.
+// Of a token's values one or a few stand out, those at the ids its teacher
+// thinks likely: a row of dx, and the rows of dW that these ids have, hang on
+// them alone, so their roundings do not average out and come to as much as the
+// results' own rounding to bf16 (errors against 64 bits, in 2-norms, of dx and
+// dW alike: 0.0023 to 0.0024, where their store alone is 0.0017).  What the
+// rounding left out there is kept in fp32 and added to the products' sums ahead
+// of their own rounding: rest * W's row to dx, rest * x's row to dW (0.0017 in
+// cross entropy, 0.0018 in distillation).  These are the heavy slots: cross
+// entropy's one, and distillation's with p > 1/5 (four at most; with those
+// above 1/16 the error would be 0.0017 too, but they are three times as many).
+// It costs 1 to 7% of a gradient, the more the shorter it is: 8192 x 131072 x
+// 4096 18.77 -> 18.93 ms, 2048 x 32768 x 4096 1258 -> 1290 us, 512 x 32000 x 2048
+// 195 -> 208, 129 x 5000 x 1024 36 -> 37.5; two terms for all of dz would cost
+// half as much again.
+// A row of dW whose id is heavy for many tokens averages their roundings after
+// all: it is left as it is where they are more than MOST_SHARED.
+constexpr int MOST_HEAVY = 4, MOST_SHARED = 8;
+constexpr float HEAVY_P = 0.2f;
+// The row of side of an id whose list begins at head, -1: none.
+__device__ __forceinline__ int side_row(int head, int id, int by_id) { return head < 0 || !by_id ? head : id; }
+// What rounding v to bf16 leaves out (nothing where that overflows).
+__device__ __forceinline__ float bf16_rest(float v) {
+  const float b = (float)(__bf16)v;
+  return __builtin_fabsf(b) < __builtin_inff() ? v - b : 0.0f;
+}
+
+// v += f * (eight bf16 values)
+__device__ __forceinline__ void add_bf16x8(float (&v)[8], float f, const uint4& u) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t b = k == 0 ? u.x : k == 1 ? u.y : k == 2 ? u.z : u.w;
+    v[2 * k] = __builtin_fmaf(f, __uint_as_float(b << 16), v[2 * k]);
+    v[2 * k + 1] = __builtin_fmaf(f, __uint_as_float(b & 0xFFFF0000u), v[2 * k + 1]);
+  }
+}
+
 struct HeadArgs {
   const uint8_t* x;        // [tokens, hidden]
   const uint8_t* xc;       // the live tokens' rows, used when not all are live
@@ -64,9 +102,16 @@ struct HeadArgs {
   uint16_t* dx;            // dx itself, where one product gives all of it; else null and
   float* dx_part;          //   partial products of dx
   float* dw_part;          // partial products of dW
+  const int* heavy;        // [tokens][heavy_n]: ids of the token's heavy slots, -1: none (null: dz is a pair)
+  float* rest;             // [tokens][heavy_n]: what dz's rounding left out there
+  int* head;               // [vocab]: one of the places of heavy that hold the id, -1: none (null: dW stays as it is)
+  int* next;               // for every place another one with its id, -1: none (lists, in no order)
+  float* side;             // rows of a bf16 dW before their rounding, those of the ids that a place holds
+  int side_by_id;          // ... an id's row at the id, else at its head
   void* dw;                // this piece of dW
   int dx_blocks;           // workgroups of dx ahead of dW's
   int tokens, rows, hidden, slots;   // rows: tokens, rounded up to whole tiles
+  int heavy_n;             // 1 in cross entropy, MOST_HEAVY in distillation
   int v0, nv;              // this piece: first id, ids in it
   int dz_ld;
   int vocab;
@@ -320,13 +365,25 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
   int tok[TJ], state[TJ];
   int64_t target[TJ];
   float lse[TJ], dloss[TJ];
-  // MULTI: the staged tokens whose slots the thread looks through, one a pass
+  // A bf16 dW: the rows of side that the lane's ids' rows go to, -1: none
+  // (loaded ahead of the first stage: the barrier in the last one would wait
+  // for them, 0.5 us a tile)
+  int own[TJ];
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) {
+    own[j] = -1;
+    if constexpr (EPI == EPI_DW && !PAIR) {
+      const int id = n0 + wn * 32 * TJ + 32 * j + lr;
+      if (g.head && g.out_bf16 && id < N) own[j] = side_row(g.head[g.v0 + id], g.v0 + id, g.side_by_id);
+    }
+  }
+  // The staged tokens, one a pass, whose slots (MULTI) the thread looks through or whose heavy slots it fetches
   constexpr int PASSES = N_T / STAGE_ROWS;
   const int srow = t % STAGE_ROWS, half = t / STAGE_ROWS;
   auto staged = [&](int p) { return 32 * TJ * (srow / 64) + 64 * p + srow % 64; };
   int slot_tok[PASSES];
   auto token_rows = [&]() {
-    if constexpr (MULTI) {
+    if (MULTI || (EPI == EPI_DX && !PAIR && g.dx)) {
 #pragma unroll
       for (int p = 0; p < PASSES; ++p) slot_tok[p] = g.row_of[n0 + staged(p) < n ? n0 + staged(p) : n - 1];
     }
@@ -460,6 +517,7 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
     const int groups = g.slots / 4;
     int4 sid[HELD][AHEAD];
     float4 sp[AHEAD];
+    int4 heavy4;
     auto load_slots = [&](int p) {
       const int64_t at = (int64_t)slot_tok[p] * groups;
 #pragma unroll
@@ -468,6 +526,7 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
         sid[HELD == 1 ? 0 : p][k] = ((const int4*)g.ids)[at + (q < groups ? q : groups - 1)];
         if (EPI == EPI_DZ) sp[k] = ((const float4*)g.p)[at + (q < groups ? q : groups - 1)];
       }
+      if (EPI == EPI_DZ && !PAIR) heavy4 = ((const int4*)g.heavy)[slot_tok[p]];
     };
     if constexpr (MULTI) {
 #pragma unroll
@@ -485,6 +544,17 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
         const bool bad = MULTI ? state[j] == ROW_BAD : target[j] >= g.vocab;
         lse2[j] = there ? lse[j] * LOG2E : __builtin_inff();
         cz[j] = !there ? 0.0f : bad ? __builtin_nanf("") : dloss[j] * g.inv_tau;
+      }
+    }
+    // Each token's heavy place goes to the head of its id's list; what stood there comes next.
+    int behind[TJ];
+    bool here[TJ];
+    if constexpr (!MULTI && EPI == EPI_DZ && !PAIR) {
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        const int64_t local = target[j] - (g.v0 + m0);
+        here[j] = g.head && wm == 0 && lg == 0 && n0 + wn * 32 * TJ + 32 * j + lr < n && local >= 0 && local < have;
+        if (here[j]) behind[j] = atomicExch(g.head + target[j], tok[j]);
       }
     }
     // Token j: its statistics or its dz, staged.  FULL: no id of the tile is
@@ -547,10 +617,11 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
           for (int r = 0; r < 16; ++r) {
             const bool hit = want[j] == 32 * i + 8 * (r >> 2) + (r & 3);
             if (EPI == EPI_DZ) v[i][r] -= hit ? cz[j] : 0.0f;
-            else at = hit ? v[i][r] : at;
+            at = hit ? v[i][r] : at;
             mine |= hit;
           }
         if (EPI == EPI_STATS && mine) g.zsel[tok[j]] = at * g.inv_tau;
+        if (EPI == EPI_DZ && !PAIR && mine) g.rest[tok[j]] = bf16_rest(at);
       }
       if constexpr (MULTI) {
         const float f = EPI == EPI_STATS ? g.inv_tau : 1.0f;
@@ -581,6 +652,11 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
     constexpr int LPR = M_T / 8;                               // lanes a row, 8 values each
     constexpr int PARTS = PAIR ? 2 : 1;
     if constexpr (!MULTI && EPI == EPI_DZ) {
+      if constexpr (!PAIR) {
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+          if (here[j]) g.next[tok[j]] = behind[j];
+      }
 #pragma unroll
       for (int h = 0; h < PARTS; ++h) {
         if (PAIR) {
@@ -611,11 +687,19 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
       }
 #pragma unroll
       for (int p = 0; p < PASSES; ++p) {
+        const int some = n0 + staged(p) < n ? have : 0;        // ids in reach
+        const int first = g.v0 + m0;
+        int after[MOST_HEAVY];
+        auto heavy_id = [&](int e) { return e == 0 ? heavy4.x : e == 1 ? heavy4.y : e == 2 ? heavy4.z : heavy4.w; };
+        if constexpr (EPI == EPI_DZ && !PAIR) {
+#pragma unroll
+          for (int e = 0; e < MOST_HEAVY; ++e)
+            if (g.head && half == 0 && (uint32_t)(heavy_id(e) - first) < (uint32_t)some)
+              after[e] = atomicExch(g.head + heavy_id(e), slot_tok[p] * MOST_HEAVY + e);
+        }
         columns(2 * p, 2 * p + 2);
         stage_barrier<63>();
-        const int some = n0 + staged(p) < n ? have : 0;        // ids in reach
         float* mine = stage + srow * PITCH;
-        const int first = g.v0 + m0;
         const int64_t at = (int64_t)slot_tok[p] * g.slots;
         // (an unused slot's id is -1, which is in no tile)
         auto group = [&](int q, const int4& id4, const float4& p4) {
@@ -642,9 +726,20 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
           if (half == 0) look();
           stage_barrier<63>();
           if (half == 1) look();
-          if (p + 1 < PASSES) load_slots(p + 1);
         }
         stage_barrier<63>();
+        if constexpr (EPI == EPI_DZ && !PAIR) {
+          if (half == 0) {
+#pragma unroll
+            for (int e = 0; e < MOST_HEAVY; ++e) {
+              const int c = heavy_id(e) - first, place = slot_tok[p] * MOST_HEAVY + e;
+              if ((uint32_t)c >= (uint32_t)some) continue;
+              g.rest[place] = bf16_rest(mine[c]);
+              if (g.head) g.next[place] = after[e];
+            }
+          }
+        }
+        if (EPI == EPI_DZ && p + 1 < PASSES) load_slots(p + 1);
         if (EPI == EPI_DZ) {
 #pragma unroll 4
           for (int s2 = t / LPR; s2 < STAGE_ROWS; s2 += 256 / LPR) {
@@ -670,8 +765,24 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
   } else {
     constexpr int LPR = M_T / 8, RPI = 256 / LPR;              // lanes a row, 8 values each; rows a round
     const int col = m0 + (t % LPR) * 8;
-    if (EPI == EPI_DX ? g.dx != nullptr : splits == 1 && g.out_bf16) {
+    if (EPI == EPI_DX ? PAIR && g.dx : splits == 1 && g.out_bf16) {
       uint16_t* out = EPI == EPI_DX ? g.dx : (uint16_t*)g.dw;
+      if constexpr (EPI == EPI_DW && !PAIR) {
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) {
+          if (own[j] >= 0) {
+            float* to = g.side + (int64_t)own[j] * g.hidden + m0 + row0 + 4 * lg;
+#pragma unroll
+            for (int i = 0; i < TI; ++i) {
+              if (m0 + row0 + 32 * i >= M) break;              // (hidden is a multiple of 64)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                *(float4*)(to + 32 * i + 8 * q) =
+                    make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+            }
+          }
+        }
+      }
 #pragma unroll
       for (int j = 0; j < TJ; ++j) stage_bf16(j);
       stage_barrier<63>();
@@ -682,13 +793,62 @@ __device__ __forceinline__ void head_product(const HeadArgs& g, int block, uint8
               *(const uint4*)(smem + s * PITCHB + (t % LPR) * 16);
       return;
     }
-    // dx partials: the splits' live rows, in whole tiles, one after the other; dW itself, or its partials
+    // dx partials: the splits' live rows, in whole tiles, one after the other, or dx itself with its heavy slots' part
+    // (W is one piece then); dW itself, or its partials
     float* out = EPI == EPI_DW && splits == 1
                      ? (float*)g.dw
                      : (EPI == EPI_DX ? g.dx_part + (int64_t)split * tiles_n * N_T * g.hidden
                                         : g.dw_part + (int64_t)split * g.dz_ld * g.hidden);
 #pragma unroll
     for (int p = 0; p < N_T / STAGE_ROWS; ++p) {
+      if (EPI == EPI_DX && !PAIR && g.dx) {
+        // dx itself: the rows' tokens and heavy slots go to LDS, and the rows of W for eight results are fetched at once
+        // (each where it is used, gradient 15872 x 69 x 4096 took 212 us)
+        struct Row {
+          int tok, id[MOST_HEAVY];
+          float rest[MOST_HEAVY];
+        };
+        static_assert(STAGE_ROWS * (PITCH * 4 + (int)sizeof(Row)) <= head_smem<TI, TJ>(), "no room for the rows");
+        Row* rows = (Row*)(smem + STAGE_ROWS * PITCH * 4);
+        if (half == 0) {
+          Row r;
+          r.tok = n0 + staged(p) < n ? slot_tok[p] : -1;
+#pragma unroll
+          for (int e = 0; e < MOST_HEAVY; ++e) {
+            const int64_t at = (int64_t)slot_tok[p] * g.heavy_n + e;
+            r.id[e] = e < g.heavy_n ? g.heavy[at] : -1;
+            r.rest[e] = r.id[e] >= 0 ? g.rest[at] : 0.0f;
+          }
+          rows[srow] = r;
+        }
+        stage_f32(p);
+        stage_barrier<0>();
+        constexpr int AT_ONCE = 8;
+        for (int s0 = t / LPR; s0 < STAGE_ROWS; s0 += AT_ONCE * RPI) {
+          uint4 u[AT_ONCE];
+#pragma unroll
+          for (int k = 0; k < AT_ONCE; ++k) {      // (no heavy slot: some row, times 0)
+            const int id = rows[s0 + k * RPI].id[0];
+            u[k] = *(const uint4*)(g.w + (id > 0 ? id : 0) * ldx + (col < M ? col : 0) * 2);
+          }
+#pragma unroll
+          for (int k = 0; k < AT_ONCE; ++k) {
+            const Row* r = rows + s0 + k * RPI;
+            if (r->tok < 0 || col >= M) continue;
+            const float* q = stage + (s0 + k * RPI) * PITCH + (t % LPR) * 8;
+            float v[8];
+            *(float4*)v = *(const float4*)q;
+            *(float4*)(v + 4) = *(const float4*)(q + 4);
+            add_bf16x8(v, r->rest[0], u[k]);
+            for (int e = 1; e < MOST_HEAVY && r->id[e] >= 0; ++e)   // (they stand first)
+              add_bf16x8(v, r->rest[e], *(const uint4*)(g.w + r->id[e] * ldx + col * 2));
+            *(uint4*)(g.dx + (int64_t)r->tok * g.hidden + col) =
+                make_uint4(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]), pk_bf16(v[6], v[7]));
+          }
+        }
+        if (p + 1 < N_T / STAGE_ROWS) stage_barrier<63>();
+        continue;
+      }
       stage_f32(p);
       stage_barrier<63>();
 #pragma unroll 4
@@ -741,6 +901,7 @@ struct TeacherArgs {
   int* ids32;
   float* p;
   float* ent;              // sum p log p
+  int4* heavy;             // per token: its heavy slots' ids, each once, -1: none (null: not wanted)
 };
 
 __device__ __forceinline__ float wave_max_f(float v) {
@@ -797,16 +958,24 @@ __global__ __launch_bounds__(256) void head_teacher_kernel(TeacherArgs a) {
   sum = wave_sum_f(sum);
   const float ls = logf(sum);
   float ent = 0.0f;
+  int4 heavy = make_int4(-1, -1, -1, -1);
   for (int s = lane; s < a.slots; s += 64) {
     const Slot u = s < 64 ? first : read(s);
     const float e = (u.v - safe) * a.inv_tau;
     const float p = live ? expf(e) / sum : 0.0f;
     if (!(p == 0.0f)) ent += p * (e - ls);
+    const int id = u.id >= 0 && u.id < a.vocab ? (int)u.id : -1;
     a.p[out + s] = p;
-    a.ids32[out + s] = u.id >= 0 && u.id < a.vocab ? (int)u.id : -1;
+    a.ids32[out + s] = id;
+    // (slots are a multiple of 4: lane 0 is here whenever one is)
+    for (uint64_t m = __ballot(p > HEAVY_P && id >= 0); m; m &= m - 1) {
+      const int h = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)m) - 1);
+      if (h != heavy.x && h != heavy.y && h != heavy.z && h != heavy.w) heavy = make_int4(h, heavy.x, heavy.y, heavy.z);
+    }
   }
   ent = wave_sum_f(ent);
   if (lane == 0) {
+    if (a.heavy) a.heavy[tok] = heavy;
     a.ent[tok] = ent;
     a.state[tok] = bad ? ROW_BAD : live ? ROW_LIVE : ROW_OUT;
   }
@@ -862,6 +1031,9 @@ struct RowsArgs {
   int together;            // dx and dW share their launches
   int dx_whole;            // dx is not split
   uint4* zero_dx;          // the rows of dx that nothing else writes, those of the tokens left out (or null)
+  int* heavy;              // out, cross entropy: the token's target, -1 where it has none (or null)
+  int* head;               // out: -1 for every id (or null)
+  int vocab;
 };
 
 // The live tokens in order, and their rows of x one after the other (unless
@@ -874,6 +1046,9 @@ constexpr int ROWS_THR = 1024, ROWS_PER = 8, ROWS_WAVES = ROWS_THR / 64;
 __global__ __launch_bounds__(ROWS_THR) void head_rows_kernel(RowsArgs a) {
   __shared__ int wave_n[2][ROWS_WAVES][2];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  if (a.head)
+    for (int64_t i = (int64_t)blockIdx.x * ROWS_THR + threadIdx.x; i < a.vocab; i += (int64_t)gridDim.x * ROWS_THR)
+      a.head[i] = -1;
   auto is_live = [&](int64_t t) { return a.targets ? a.targets[t] >= 0 : a.state[t] != ROW_OUT; };
   // this workgroup's tokens: [lo, hi)
   const int64_t lo = (int64_t)a.tokens * blockIdx.x / gridDim.x;
@@ -928,6 +1103,7 @@ __global__ __launch_bounds__(ROWS_THR) void head_rows_kernel(RowsArgs a) {
     if (in && w == 0) {
       a.pos_of[t] = on ? pos : -1;
       if (on) a.row_of[pos] = (int)t;
+      if (a.heavy) a.heavy[t] = on && a.targets[t] < a.vocab ? (int)a.targets[t] : -1;
       if (!on && a.loss) {
         a.loss[t] = 0.0f;
         a.lse[t] = 0.0f;
@@ -1029,34 +1205,10 @@ __global__ __launch_bounds__(JOIN_ROWS * JOIN_Q) void head_join_kernel(JoinArgs 
   a.loss[tok] = a.state[tok] == ROW_BAD ? __builtin_nanf("") : loss + a.ent[tok];
 }
 
-// dx [tokens, hidden] bf16 from the partial products of the live rows; zeros
-// for the tokens that take no part.  8 values a thread.
-__global__ __launch_bounds__(256) void head_dx_kernel(const float* part, const int* live, int tile_m, int hidden,
-                                                      const int* pos_of, int64_t chunks8, int per_row,
-                                                      uint16_t* dx) {
-  const int splits = live[1];
-  const int64_t split_stride = (int64_t)((live[0] + tile_m - 1) / tile_m) * tile_m * hidden;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < chunks8; i += (int64_t)gridDim.x * 256) {
-    const int64_t tok = i / per_row;
-    const int c = (int)(i - tok * per_row);
-    const int pos = pos_of[tok];
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (pos >= 0) {
-      const float* q = part + ((int64_t)pos * per_row + c) * 8;
-      for (int s = 0; s < splits; ++s, q += split_stride) {
-        const float4 lo = *(const float4*)q, hi = *(const float4*)(q + 4);
-        v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
-        v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
-      }
-    }
-    *(uint4*)(dx + i * 8) =
-        make_uint4(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]), pk_bf16(v[6], v[7]));
-  }
-}
-
 // dW of a piece from its splits' partial products.
 __global__ __launch_bounds__(256) void head_dw_kernel(const float* part, const int* live, int64_t split_stride,
-                                                      int64_t chunks8, void* dw, int bf16) {
+                                                      int64_t chunks8, void* dw, int bf16, const int* head, float* side,
+                                                      int side_by_id, int v0, int per_row) {
   const int splits = live[2];
   if (splits == 1) return;                     // the product stored dW itself
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < chunks8; i += (int64_t)gridDim.x * 256) {
@@ -1067,6 +1219,13 @@ __global__ __launch_bounds__(256) void head_dw_kernel(const float* part, const i
       v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
       v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
     }
+    const int64_t row = i / per_row;
+    const int own = bf16 && head ? side_row(head[v0 + row], v0 + (int)row, side_by_id) : -1;
+    if (own >= 0) {
+      float4* o = (float4*)side + ((int64_t)own * per_row + (i - row * per_row)) * 2;
+      o[0] = make_float4(v[0], v[1], v[2], v[3]);
+      o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
     if (bf16) {
       *(uint4*)((uint16_t*)dw + i * 8) =
           make_uint4(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]), pk_bf16(v[6], v[7]));
@@ -1075,6 +1234,99 @@ __global__ __launch_bounds__(256) void head_dw_kernel(const float* part, const i
       ((float4*)dw)[2 * i + 1] = make_float4(v[4], v[5], v[6], v[7]);
     }
   }
+}
+
+struct FinishArgs {
+  const int* live;
+  const int* pos_of;
+  const float* dx_part;    // partial products of dx
+  const int* heavy;
+  const float* rest;
+  const int* head;
+  const int* next;
+  const float* side;
+  const uint4* x;
+  const uint4* w;
+  uint16_t* dx;
+  void* dw;
+  int64_t chunks8;         // 8-value chunks of dx
+  int dx_blocks;           // workgroups of dx ahead of dW's
+  int tile, hidden, per_row, heavy_n;   // per_row: 8-value chunks of a row
+  int dw_bf16, side_by_id;
+};
+
+// dx [tokens, hidden] bf16 from the partial products of the live rows and their
+// heavy slots; zeros for the tokens that take no part.  8 values a thread.
+__device__ __forceinline__ void finish_dx(const FinishArgs& a) {
+  const int splits = a.live[1];
+  const int64_t split_stride = (int64_t)((a.live[0] + a.tile - 1) / a.tile) * a.tile * a.hidden;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.chunks8; i += (int64_t)a.dx_blocks * 256) {
+    const int64_t tok = i / a.per_row;
+    const int c = (int)(i - tok * a.per_row);
+    const int pos = a.pos_of[tok];
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (pos >= 0) {
+      const float* q = a.dx_part + ((int64_t)pos * a.per_row + c) * 8;
+      for (int s = 0; s < splits; ++s, q += split_stride) {
+        const float4 lo = *(const float4*)q, hi = *(const float4*)(q + 4);
+        v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+        v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+      }
+      for (int64_t e = tok * a.heavy_n; e < (tok + 1) * a.heavy_n; ++e) {
+        const int id = a.heavy[e];
+        if (id >= 0) add_bf16x8(v, a.rest[e], a.w[(int64_t)id * a.per_row + c]);
+      }
+    }
+    *(uint4*)(a.dx + i * 8) =
+        make_uint4(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]), pk_bf16(v[6], v[7]));
+  }
+}
+
+// The heavy slots' part of dW, 8 columns a thread: the token whose place is the
+// head of an id's list adds rest * x's row of each of its places, in the order of
+// the tokens, to the id's row.
+__device__ __forceinline__ void finish_dw(const FinishArgs& a, int block) {
+  const int64_t i = (int64_t)block * 256 + threadIdx.x;
+  if (i >= a.chunks8) return;
+  const int tok = (int)(i / a.per_row), c = (int)(i - (int64_t)tok * a.per_row);
+  for (int place = tok * a.heavy_n; place < (tok + 1) * a.heavy_n; ++place) {
+    const int64_t id = a.heavy[place];
+    if (id < 0) break;                             // (a token's heavy slots stand first)
+    if (a.head[id] != place) continue;
+    const float4* from = a.dw_bf16 ? (const float4*)a.side + ((a.side_by_id ? id : place) * a.per_row + c) * 2
+                                   : (const float4*)a.dw + (id * a.per_row + c) * 2;
+    const float4 lo = from[0], hi = from[1];
+    float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    int places[MOST_SHARED], more = place;
+#pragma unroll
+    for (int k = 0; k < MOST_SHARED; ++k) {
+      places[k] = more;
+      if (more >= 0) more = a.next[more];
+    }
+    if (more >= 0) continue;
+    for (int last = -1;;) {
+      int low = 0x7FFFFFFF;                        // the lowest place above the last one
+#pragma unroll
+      for (int k = 0; k < MOST_SHARED; ++k)
+        if (places[k] > last && places[k] < low) low = places[k];
+      if (low == 0x7FFFFFFF) break;
+      add_bf16x8(v, a.rest[low], a.x[(int64_t)(low / a.heavy_n) * a.per_row + c]);
+      last = low;
+    }
+    if (a.dw_bf16) {
+      ((uint4*)a.dw)[id * a.per_row + c] =
+          make_uint4(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]), pk_bf16(v[6], v[7]));
+    } else {
+      float4* to = (float4*)a.dw + (id * a.per_row + c) * 2;
+      to[0] = make_float4(v[0], v[1], v[2], v[3]);
+      to[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void head_finish_kernel(FinishArgs a) {
+  if ((int)blockIdx.x < a.dx_blocks) finish_dx(a);
+  else finish_dw(a, (int)blockIdx.x - a.dx_blocks);
 }
 
 __global__ void head_zero_kernel(uint4* p, int64_t n16) {
@@ -1088,26 +1340,22 @@ __global__ void head_zero_kernel(uint4* p, int64_t n16) {
 // Tiles: 256 x 256, one workgroup per compute unit, or 128 x 128, two.
 constexpr int HEAD_TILE = 256, HEAD_SMALL = 128, HEAD_CUS = 256;
 
-// dz goes into the products as bf16, each value off by up to 2^-8 of itself.
-// A row of dx, and the rows of dW that it decides, hang on the one or few
-// values of dz at its targets, so this does not average out: it is as large as
-// the results' own rounding to bf16 (errors against 64 bits, in 2-norms: 0.0024
-// of dx and dW, 0.0017 of that by their store).  Up to this many tokens dz is
-// kept as two bf16 terms, the rounded value and what the rounding left (2^-16
-// together), and both are multiplied (0.0017): these calls are bound by
-// reading w, not by the matrix cores (gradient 8 x 100000 x 4096 612 -> 694 us,
-// 128 x 50000 x 2048 179 -> 210; with more tokens it would be half as much
-// again).
+// Up to this many tokens dz is kept as two bf16 terms, the rounded value and
+// what the rounding left (2^-16 together), and both are multiplied, in place of
+// the heavy slots' rests: these calls are bound by reading w, not by the matrix
+// cores (gradient 8 x 100000 x 4096 612 -> 694 us, 128 x 50000 x 2048 179 -> 210;
+// with more tokens it would be half as much again).
 constexpr int HEAD_PAIR_TOKENS = 128;
 
 struct HeadPlan {
   int64_t rows, slots, parts, piece;
   int loss_tile, dz_tile, grad_tile, wg_slots;                    // the gradient's workgroups at a time
   int64_t dx_grid, dw_grid;                              // most tiles, splits included
-  bool pair, dw_can_split, apart, dx_whole;
+  bool pair, dw_can_split, apart, dx_whole, heavy_dw, side_by_id;
+  int heavy_n;                                           // 0: a pair has none
   size_t live, row_of, pos_of, state, ids, p, ent, xc;
   size_t zsel, stats, loss_bytes;                        // the loss
-  size_t dz, dxp, dwp, grad_bytes;                       // the gradient
+  size_t dz, dxp, dwp, heavy, rest, head, next, side, grad_bytes;   // the gradient
 };
 
 // The tile of a product of rows x cols outputs.  A round of 256 x 256 tiles,
@@ -1165,8 +1413,8 @@ static HeadPlan head_plan(int64_t tokens, int64_t vocab, int64_t hidden, int64_t
   // A vocabulary of one piece whose product for dx is too short to be split, or
   // short (a tile of 64 stages takes 90 us) and with tiles enough: its result is
   // dx, stored as such.  Otherwise dx goes through fp32 partial products and
-  // head_dx_kernel (gradient 15872 x 69 x 4096: 142 us, 261 through them; 15872 x
-  // 1000 x 4096: 373 and 488).
+  // head_finish_kernel (gradient 15872 x 69 x 4096: 157 us, 264 through them;
+  // 15872 x 1000 x 4096: 404 us and 489).
   const int64_t dx_nk = h.piece / 64 * (h.pair ? 2 : 1);
   h.dx_whole = vocab <= h.piece &&
                (dx_nk < 2 * HEAD_LEAST_STAGES ||
@@ -1188,6 +1436,15 @@ static HeadPlan head_plan(int64_t tokens, int64_t vocab, int64_t hidden, int64_t
   h.dw_can_split = h.piece / h.grad_tile * hn * 2 <= HEAD_SPLIT_TILES &&
                    ceil_div(tokens, 64) * (h.pair ? 2 : 1) / 2 >= HEAD_LEAST_STAGES;
   h.dwp = take(h.dw_can_split ? partial(h.piece / h.grad_tile) : 0);
+  h.heavy_n = h.pair ? 0 : xent ? 1 : MOST_HEAVY;
+  // (with more tokens than that hardly an id is heavy for so few)
+  h.heavy_dw = !h.pair && tokens <= MOST_SHARED * vocab;
+  h.heavy = take(4 * tokens * h.heavy_n);
+  h.rest = take(4 * tokens * h.heavy_n);
+  h.head = take(h.heavy_dw ? 4 * vocab : 0);
+  h.next = take(h.heavy_dw ? 4 * tokens * h.heavy_n : 0);
+  h.side_by_id = vocab < tokens * h.heavy_n;
+  h.side = take(h.heavy_dw ? 4 * std::min(vocab, tokens * h.heavy_n) * hidden : 0);
   h.grad_bytes = at;
   return h;
 }
@@ -1278,6 +1535,7 @@ static HeadArgs head_rows(const HeadCall& c, const HeadPlan& h, hipStream_t stre
     a.inv_tau = 1.0f / c.tau;
     a.state = (int*)(ws + h.state); a.ids32 = (int*)(ws + h.ids); a.p = (float*)(ws + h.p);
     a.ent = (float*)(ws + h.ent);
+    a.heavy = c.loss || h.pair ? nullptr : (int4*)(ws + h.heavy);
     hipLaunchKernelGGL(head_teacher_kernel, dim3((unsigned)ceil_div(c.tokens, 4)), dim3(256), 0, stream, a);
   }
   RowsArgs r = {};
@@ -1291,6 +1549,11 @@ static HeadArgs head_rows(const HeadCall& c, const HeadPlan& h, hipStream_t stre
   r.together = c.dx && c.dw && !h.apart;
   r.dx_whole = h.dx_whole;
   r.zero_dx = h.dx_whole ? (uint4*)c.dx : nullptr;
+  r.vocab = (int)c.vocab;
+  if (!c.loss) {
+    r.heavy = c.xent && !h.pair ? (int*)(ws + h.heavy) : nullptr;
+    r.head = h.heavy_dw && c.dw ? (int*)(ws + h.head) : nullptr;
+  }
   hipLaunchKernelGGL(head_rows_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(c.tokens, 16), HEAD_CUS)),
                      dim3(ROWS_THR), 0, stream, r);
   HeadArgs g = {};
@@ -1352,6 +1615,10 @@ static pbs_status head_grad(const HeadCall& c, hipStream_t stream) {
   g.lse = c.lse; g.dloss = c.dloss; g.dz = (uint16_t*)(ws + h.dz); g.dz_ld = (int)h.piece; g.out_bf16 = dwb == 2;
   g.dx = h.dx_whole ? (uint16_t*)c.dx : nullptr;
   g.dx_part = (float*)(ws + h.dxp); g.dw_part = (float*)(ws + h.dwp);
+  g.heavy = h.pair ? nullptr : (const int*)(ws + h.heavy); g.heavy_n = h.heavy_n; g.rest = (float*)(ws + h.rest);
+  g.head = h.heavy_dw && c.dw ? (int*)(ws + h.head) : nullptr; g.next = (int*)(ws + h.next);
+  g.side = (float*)(ws + h.side); g.side_by_id = h.side_by_id;
+  const int per_row = (int)(c.hidden / 8);
   log_dispatch("%s tokens=%lld vocab=%lld hidden=%lld top=%lld piece=%lld tiles=%d,%d", c.what, (long long)c.tokens,
                (long long)c.vocab, (long long)c.hidden, (long long)c.top, (long long)h.piece, h.dz_tile, h.grad_tile);
   for (int64_t v0 = 0; v0 < c.vocab; v0 += h.piece) {
@@ -1373,12 +1640,16 @@ static pbs_status head_grad(const HeadCall& c, hipStream_t stream) {
     if (c.dw && h.dw_can_split)
       hipLaunchKernelGGL(head_dw_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(nv * c.hidden / 8, 256), 2048)),
                          dim3(256), 0, stream, g.dw_part, g.live, h.piece * c.hidden, nv * c.hidden / 8, g.dw,
-                         g.out_bf16);
+                         g.out_bf16, g.head, g.side, g.side_by_id, g.v0, per_row);
   }
-  if (c.dx && !h.dx_whole)
-    hipLaunchKernelGGL(head_dx_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(c.tokens * c.hidden / 8, 256), 2048)),
-                       dim3(256), 0, stream, (const float*)(ws + h.dxp), g.live, h.grad_tile, g.hidden,
-                       (const int*)(ws + h.pos_of), c.tokens * c.hidden / 8, (int)(c.hidden / 8), (uint16_t*)c.dx);
+  FinishArgs a = {};
+  a.live = g.live; a.pos_of = (const int*)(ws + h.pos_of); a.dx_part = g.dx_part; a.heavy = g.heavy; a.rest = g.rest;
+  a.head = g.head; a.next = g.next; a.side = g.side; a.x = (const uint4*)c.x; a.w = (const uint4*)c.w;
+  a.dx = (uint16_t*)c.dx; a.dw = c.dw; a.chunks8 = c.tokens * per_row; a.tile = h.grad_tile; a.hidden = g.hidden;
+  a.per_row = per_row; a.heavy_n = h.heavy_n; a.dw_bf16 = g.out_bf16; a.side_by_id = h.side_by_id;
+  if (c.dx && !h.dx_whole) a.dx_blocks = (int)std::min<int64_t>(ceil_div(a.chunks8, 256), 2048);
+  const int64_t blocks = a.dx_blocks + (g.head ? ceil_div(a.chunks8, 256) : 0);
+  if (blocks > 0) hipLaunchKernelGGL(head_finish_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a);
   return check_launch(c.what);
 }
 

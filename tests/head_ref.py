@@ -34,11 +34,12 @@ def slots_of(targets=None, top_ids=None, top_logits=None, tau=1.0):
     return torch.where(p > 0, top_ids, -1), p, live, ent
 
 
-def head_ref(x, w, slots, tau=1.0, dloss=None):
+def head_ref(x, w, slots, tau=1.0, dloss=None, kept=(None, None)):
     """x [T, H], w [V, H] float64 (rows of x that take no part may hold anything).
 
     Returns a dict of (value, bound) for loss, lse and, with dloss, dx (bf16
-    store) and dw (before its own store's rounding).
+    store) and dw (before its own store's rounding).  kept: masks [T, V] of the
+    values of dz that reach dx, and dw, with what their rounding left out.
     """
     ids, p, live, ent = slots
     T, H = x.shape
@@ -73,12 +74,17 @@ def head_ref(x, w, slots, tau=1.0, dloss=None):
     # q carries the logit's and lse's errors, the argument's roundings and the function's
     e_q = q * (e_z + 2 * e_lse[:, None] + (4 * (z - lse[:, None]).abs() + 6) * U)
     e_dz = c.abs() * (e_q + e_hit + 4 * U * (q + (k + 1) * hit))
-    e_dz = e_dz + (BF16 ** 2 if T <= PAIR_TOKENS else BF16) * (dz.abs() + e_dz) + TINY * (1 + c.abs())
+    e_32 = e_dz
+
+    def rounded(mask):
+        step = BF16 ** 2 if T <= PAIR_TOKENS else BF16 if mask is None else torch.where(mask, BF16 ** 2, BF16)
+        return e_32 + step * (dz.abs() + e_32) + TINY * (1 + c.abs())
+
     dx = dz @ w
-    e_dx = e_dz @ w.abs() + (V + 40) * U * (dz.abs() @ w.abs())
+    e_dx = rounded(kept[0]) @ w.abs() + (V + 40) * U * (dz.abs() @ w.abs())
     out["dx"] = (dx, e_dx + BF16 * (dx.abs() + e_dx) + TINY)
     dw = dz.t() @ x
-    out["dw"] = (dw, e_dz.t() @ x.abs() + (T + 40) * U * (dz.abs().t() @ x.abs()) + TINY)
+    out["dw"] = (dw, rounded(kept[1]).t() @ x.abs() + (T + 40) * U * (dz.abs().t() @ x.abs()) + TINY)
     return out
 
 
