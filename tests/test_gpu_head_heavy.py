@@ -135,3 +135,24 @@ def test_infinite_weight_of_a_token():
     lse = PL.linear_xent(x, w, targets)[1]
     dx, dw = PL.linear_xent_grad(dloss, x, w, targets, lse, dw_dtype=F32)
     assert not dw[targets[7], 0].isnan() and dw[targets[7], 0] < -3e38
+
+
+@pytest.mark.parametrize("T,V,H", [(1000, 5003, 64), (3000, 33001, 192)])
+def test_most_tokens_on_one_id(T, V, H):
+    """Most targets are one id and a few others, in the lanes of many waves: their lists hold them all once, whatever
+    the order, and the ids of a few tokens beside them get theirs."""
+    x, w, targets, dloss = make(T, V, H, seed=5, crowd=(T // 2, T // 4, 8, 7, 2))
+    slots = [t.cuda() for t in slots_of(targets.cpu())]
+    want = head_ref(x.double(), w.double(), slots, 1.0, dloss.double(), kept(slots[0], slots[1], T, V))
+    lse = PL.linear_xent(x, w, targets)[1]
+    got = PL.linear_xent_grad(dloss, x, w, targets, lse, dw_dtype=F32)
+    check(dict(zip(("dx", "dw"), got)), want, F32)
+    ids = torch.stack([targets, (targets + 16) % V, targets, (targets + 32) % V], 1).contiguous()
+    logits = torch.log(torch.tensor([0.26, 0.3, 0.14, 0.3], device="cuda")).expand(T, 4).contiguous()
+    slots = [t.cuda() for t in slots_of(None, ids.cpu(), logits.cpu(), 1.0)]
+    want = head_ref(x.double(), w.double(), slots, 1.0, dloss.double(), kept(slots[0], slots[1], T, V))
+    lse = PL.linear_distill(x, w, ids, logits, 1.0)[1]
+    got = PL.linear_distill_grad(dloss, x, w, ids, logits, 1.0, lse, dw_dtype=F32)
+    check(dict(zip(("dx", "dw"), got)), want, F32)
+    for _ in range(5):
+        assert same(PL.linear_distill_grad(dloss, x, w, ids, logits, 1.0, lse, dw_dtype=F32), got)
