@@ -48,7 +48,8 @@
 extern "C" {
 #endif
 
-#define PBS_VERSION 4   /* 3: pbs_rht_cast, pbs_debug_sr_encode; 4: four SR words per Philox call */
+#define PBS_VERSION 4   /* 3: pbs_rht_cast, pbs_debug_sr_encode; 4: four SR words per Philox call.  The layer norm's and
+                           the linear head's entry points came with no change to these and without a new number */
 
 typedef enum {
   PBS_OK = 0,

@@ -26,9 +26,9 @@
 // LDS-DMA, v_mfma_f32_32x32x16_bf16.
 //
 // What bounds them: the matrix cores and the power they draw.  On 8192 x
-// 131072 x 4096 the loss runs at 1430 TFLOP/s (6.1 ms) and the gradient at 1395
-// (18.9 ms) with the matrix cores busy 82% of the time (dz 78%) at 1.67 GHz; a
-// large library product reaches 1490 on the same operands.  A K stage of a
+// 131072 x 4096 the loss runs at 1430 TFLOP/s (6.1 ms) and the gradient at 1390
+// (19.0 ms) with the matrix cores busy 80% of the time (dz 76%) at 1.6 to 1.67
+// GHz; a large library product reaches 1490 on the same operands.  A K stage of a
 // 256 x 256 tile takes 2220 cycles, 2048 of them matrix instructions, or 1.32
 // to 1.4 us; a tile's fixed cost (first loads 2.3 us, the loss's epilogue 4) is
 // 7% at hidden = 4096 and 13% at 2048.  Workgroups that stay and issue the next

@@ -106,7 +106,9 @@ __device__ __forceinline__ void block_amax(uint32_t m, uint32_t* out, uint32_t* 
   }
 }
 
-// Rows of any width: a workgroup reads its row three times.
+// Rows of any width: a workgroup reads its row three times, the gradient reads x
+// and dy once more for the columns' sums (8192 x 16392 bf16 347 us forward, 520
+// backward, where 16384 columns take 98 and 161).
 template <typename TX, typename TY>
 __global__ __launch_bounds__(WIDE_THR) void layernorm_wide_kernel(NormArgs a) {
   __shared__ float part[3][WIDE_THR / 64];
@@ -461,7 +463,12 @@ __global__ __launch_bounds__(norm_threads(TPR)) void layernorm_grad_kernel(NormA
     nr = a.rstd[q];
   };
   // 1024 threads have 128 registers each: the next row's values would spill
-  // (8192 x 16384, fp32 in and bf16 dy: 483 us with them, 260 without, unpacking again for dx)
+  // (8192 x 16384, fp32 in and bf16 dy: 483 us with them, 257 without, unpacking
+  // again for dx; 3 registers still spill there).  Beyond 8192 columns of fp32 a
+  // width that is no multiple of 8, whose window costs registers, spills all the
+  // same, 50 of them with 512 x 3 and 143 with 1024 x 2: 15872 x 8201 fp32 403 us
+  // (3.9 TB/s) against 290 at 8200, 8192 x 16383 481 us (3.4 TB/s) against 307 at
+  // 16384.
   constexpr bool AHEAD = TPR < 1024;
   if (AHEAD && row < a.rows) fetch(row);
 #pragma unroll
