@@ -1318,9 +1318,7 @@ __device__ __forceinline__ void finish_dx(const FinishArgs& a) {
 // The heavy slots' part of dW, 8 columns a thread: the token whose place is the
 // head of an id's list adds rest * x's row of each of its places, in the order of
 // the tokens, to the id's row.
-__device__ __forceinline__ void finish_dw(const FinishArgs& a, int block) {
-  const int64_t i = (int64_t)block * 256 + threadIdx.x;
-  if (i >= a.chunks8) return;
+__device__ __forceinline__ void finish_dw(const FinishArgs& a, int64_t i) {
   const int tok = (int)(i / a.per_row), c = (int)(i - (int64_t)tok * a.per_row);
   for (int place = tok * a.heavy_n; place < (tok + 1) * a.heavy_n; ++place) {
     const int64_t id = a.heavy[place];
@@ -1358,8 +1356,13 @@ __device__ __forceinline__ void finish_dw(const FinishArgs& a, int block) {
 }
 
 __global__ __launch_bounds__(256) void head_finish_kernel(FinishArgs a) {
-  if ((int)blockIdx.x < a.dx_blocks) finish_dx(a);
-  else finish_dw(a, (int)blockIdx.x - a.dx_blocks);
+  if ((int)blockIdx.x < a.dx_blocks) {
+    finish_dx(a);
+  } else {
+    for (int64_t i = (int64_t)(blockIdx.x - a.dx_blocks) * 256 + threadIdx.x; i < a.chunks8;
+         i += (int64_t)(gridDim.x - a.dx_blocks) * 256)
+      finish_dw(a, i);
+  }
 }
 
 __global__ void head_zero_kernel(uint4* p, int64_t n16) {
@@ -1681,7 +1684,7 @@ static pbs_status head_grad(const HeadCall& c, hipStream_t stream) {
   a.dx = (uint16_t*)c.dx; a.dw = c.dw; a.chunks8 = c.tokens * per_row; a.tile = h.grad_tile; a.hidden = g.hidden;
   a.per_row = per_row; a.heavy_n = h.heavy_n; a.dw_bf16 = g.out_bf16; a.side_by_id = h.side_by_id;
   if (c.dx && !h.dx_whole) a.dx_blocks = (int)std::min<int64_t>(ceil_div(a.chunks8, 256), 2048);
-  const int64_t blocks = a.dx_blocks + (g.head ? ceil_div(a.chunks8, 256) : 0);
+  const int64_t blocks = a.dx_blocks + (g.head ? std::min<int64_t>(ceil_div(a.chunks8, 256), 1 << 20) : 0);
   if (blocks > 0) hipLaunchKernelGGL(head_finish_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a);
   return check_launch(c.what);
 }
