@@ -49,7 +49,8 @@ extern "C" {
 #endif
 
 #define PBS_VERSION 4   /* 3: pbs_rht_cast, pbs_debug_sr_encode; 4: four SR words per Philox call.  The layer norm's and
-                           the linear head's entry points came with no change to these and without a new number */
+                           the linear head's entry points came with no change to these and without a new number, so did
+                           those of the queries' and keys' norm and rotation */
 
 typedef enum {
   PBS_OK = 0,
@@ -451,6 +452,67 @@ pbs_status pbs_linear_distill_grad(const float* dloss, const void* x, const void
                                    int64_t hidden, const int64_t* top_ids, const void* top_logits, pbs_format top_fmt,
                                    int64_t top, float temperature, const float* lse, int64_t piece, void* dx, void* dw,
                                    pbs_format dw_fmt, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------
+ * pbs_qk_norm_rope: norm of each head's queries and keys and their rotation by
+ * position, in one pass, between the QKV projection and attention.  For a row
+ * x [head_dim] of a head of the token at position p:
+ *   r = 1 / sqrt(mean(x^2) + eps),  u = x r w
+ *   y = u with pair i of its first rot_dim values turned by the angle p freqs[i]:
+ *   (u_i cos - u_i' sin, u_i' cos + u_i sin)
+ *  Pairs: i and i + rot_dim / 2, or with interleaved 2 i and 2 i + 1.
+ *  q, q_out [batch, seq, heads, head_dim], k, k_out the same with kv_heads;
+ *    x_fmt and y_fmt bf16 or fp32.  Each has its strides [host] of batch, seq
+ *    and head in elements (three int64; the last axis is contiguous), so parts
+ *    of a packed projection and [batch, heads, seq, head_dim] tensors are taken
+ *    as they lie.  An output's rows do not overlap; q_out may be q itself (and
+ *    k_out k) with its type and strides, otherwise outputs do not overlap inputs.
+ *    heads or kv_heads 0: that tensor is left out (pointers may be NULL).
+ *  q_weight, k_weight [head_dim]: w, bf16 or fp32 (w_fmt); NULL is 1.
+ *  norm 0: r is 1 (rotation alone; eps unused).
+ *  positions: int64, batch rows pos_batch_stride apart (0: one row for all);
+ *    any value.  NULL: the place in the sequence, 0 to seq - 1.
+ *  freqs: fp64 [rot_dim / 2]; may be NULL if rot_dim is 0.
+ *  The angle is formed and reduced in fp64; all else is fp32, with one
+ *  rounding at the store.
+ *  Shapes (else PBS_ERR_SHAPE): head_dim 1 to 512, rot_dim even and at most
+ *    head_dim, at most 2^30 tokens, 65536 heads.  Alignment: an element.
+ *
+ * pbs_qk_norm_rope_grad: from dq, dk (y_fmt), and q, k as the forward had them
+ * (x_fmt), with g = dy turned back, v = g w, n = x r:
+ *   dx = r (v - n mean(v n)),   dw = sum over tokens and heads of g n
+ *  dq_out, dk_out: dx in x_fmt.  dv, dv_out (both or neither; kv_heads heads):
+ *    dv is copied to dv_out in x_fmt, so that the three outputs may be the parts
+ *    of one packed gradient of the projection's output.  An output may be the
+ *    q / k or dq / dk / dv of its own part with the same type and strides.
+ *  dq_weight, dk_weight: fp32 [head_dim], overwritten (zeros if there are no
+ *    rows); either may be NULL.  Sums are split and joined in an order that
+ *    depends on the shapes alone, so identical inputs give identical bytes.
+ *  amax_out: 1 float, max |value| of all that is stored to dq_out, dk_out and
+ *    dv_out, overwritten: what pbs_amax would return on the packed gradient, for
+ *    pbs_scale_from_amax.  NULL: not wanted.
+ *  workspace: pbs_qk_norm_rope_grad_bytes(batch, seq, head_dim) bytes, 16-byte
+ *    aligned, for the weights' gradients (unused, may be NULL, if both are).
+ *    Its contents are of no use afterwards; calls that may run at the same time
+ *    need one each.
+ * ------------------------------------------------------------------- */
+pbs_status pbs_qk_norm_rope(const void* q, const int64_t* q_strides, int64_t heads, const void* k,
+                            const int64_t* k_strides, int64_t kv_heads, pbs_format x_fmt, int64_t batch, int64_t seq,
+                            int64_t head_dim, const void* q_weight, const void* k_weight, pbs_format w_fmt, int norm,
+                            float eps, const int64_t* positions, int64_t pos_batch_stride, const double* freqs,
+                            int64_t rot_dim, int interleaved, void* q_out, const int64_t* q_out_strides, void* k_out,
+                            const int64_t* k_out_strides, pbs_format y_fmt, hipStream_t stream);
+pbs_status pbs_qk_norm_rope_grad_bytes(int64_t batch, int64_t seq, int64_t head_dim, size_t* bytes /* [host] */);
+pbs_status pbs_qk_norm_rope_grad(const void* dq, const int64_t* dq_strides, const void* dk, const int64_t* dk_strides,
+                                 const void* dv, const int64_t* dv_strides, pbs_format y_fmt, const void* q,
+                                 const int64_t* q_strides, int64_t heads, const void* k, const int64_t* k_strides,
+                                 int64_t kv_heads, pbs_format x_fmt, int64_t batch, int64_t seq, int64_t head_dim,
+                                 const void* q_weight, const void* k_weight, pbs_format w_fmt, int norm, float eps,
+                                 const int64_t* positions, int64_t pos_batch_stride, const double* freqs,
+                                 int64_t rot_dim, int interleaved, void* dq_out, const int64_t* dq_out_strides,
+                                 void* dk_out, const int64_t* dk_out_strides, void* dv_out,
+                                 const int64_t* dv_out_strides, float* dq_weight, float* dk_weight, float* amax_out,
+                                 void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------------------
  * pbs_quantized_bytes [host]: bytes of the codes and of the block scales

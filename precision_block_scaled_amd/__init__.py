@@ -27,6 +27,7 @@ __all__ = [
     "pbs_rht_cast", "pbs_gemm", "pbs_gemm_amax", "pbs_quantized_bytes", "pbs_debug_sr_encode",
     "pbs_layernorm", "pbs_layernorm_grad_bytes", "pbs_layernorm_grad", "pbs_linear_loss_bytes",
     "pbs_linear_xent", "pbs_linear_xent_grad", "pbs_linear_distill", "pbs_linear_distill_grad",
+    "pbs_qk_norm_rope", "pbs_qk_norm_rope_grad_bytes", "pbs_qk_norm_rope_grad",
     "pbs_last_error", "pbs_version",
 ]
 
@@ -43,6 +44,7 @@ lib_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpbs.so")
 
 _c = ctypes
 _vp, _i64, _i32, _u64, _f32 = _c.c_void_p, _c.c_int64, _c.c_int, _c.c_uint64, _c.c_float
+_i64p = _c.POINTER(_c.c_int64)
 
 # name -> (restype, argtypes); mirrors include/pbs.h
 SIGNATURES = {
@@ -74,6 +76,12 @@ SIGNATURES = {
                                   _c.c_size_t, _vp]),
     "pbs_linear_distill_grad": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _f32, _vp, _i64, _vp,
                                        _vp, _i32, _vp, _c.c_size_t, _vp]),
+    "pbs_qk_norm_rope": (_i32, [_vp, _i64p, _i64, _vp, _i64p, _i64, _i32, _i64, _i64, _i64, _vp, _vp, _i32, _i32, _f32,
+                                _vp, _i64, _vp, _i64, _i32, _vp, _i64p, _vp, _i64p, _i32, _vp]),
+    "pbs_qk_norm_rope_grad_bytes": (_i32, [_i64, _i64, _i64, _c.POINTER(_c.c_size_t)]),
+    "pbs_qk_norm_rope_grad": (_i32, [_vp, _i64p, _vp, _i64p, _vp, _i64p, _i32, _vp, _i64p, _i64, _vp, _i64p, _i64, _i32,
+                                     _i64, _i64, _i64, _vp, _vp, _i32, _i32, _f32, _vp, _i64, _vp, _i64, _i32, _vp,
+                                     _i64p, _vp, _i64p, _vp, _i64p, _vp, _vp, _vp, _vp, _c.c_size_t, _vp]),
     "pbs_quantized_bytes": (_i32, [_i32, _i64, _i64, _i32, _c.POINTER(_c.c_size_t),
                                    _c.POINTER(_c.c_size_t)]),
     "pbs_last_error": (_c.c_char_p, []),
@@ -117,6 +125,11 @@ def _ptr(x):
     if isinstance(x, int):
         return x
     return x.data_ptr()
+
+
+def _strides(x):
+    """Three int64 (batch, seq, head) as the C side takes them."""
+    return None if x is None else (_i64 * 3)(*x)
 
 
 def _stream(s):
@@ -243,6 +256,36 @@ def pbs_linear_distill_grad(dloss, x, w, tokens, vocab, hidden, top_ids, top_log
     _check(lib().pbs_linear_distill_grad(_ptr(dloss), _ptr(x), _ptr(w), tokens, vocab, hidden, _ptr(top_ids),
                                          _ptr(top_logits), top_fmt, top, temperature, _ptr(lse), piece, _ptr(dx),
                                          _ptr(dw), dw_fmt, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def pbs_qk_norm_rope(q, q_strides, heads, k, k_strides, kv_heads, x_fmt, batch, seq, head_dim, q_weight, k_weight, w_fmt,
+                     norm, eps, positions, pos_batch_stride, freqs, rot_dim, interleaved, q_out, q_out_strides, k_out,
+                     k_out_strides, y_fmt, stream=None):
+    _check(lib().pbs_qk_norm_rope(_ptr(q), _strides(q_strides), heads, _ptr(k), _strides(k_strides), kv_heads, x_fmt,
+                                  batch, seq, head_dim, _ptr(q_weight), _ptr(k_weight), w_fmt, int(norm), eps,
+                                  _ptr(positions), pos_batch_stride, _ptr(freqs), rot_dim, int(interleaved), _ptr(q_out),
+                                  _strides(q_out_strides), _ptr(k_out), _strides(k_out_strides), y_fmt,
+                                  _stream(stream)))
+
+
+def pbs_qk_norm_rope_grad_bytes(batch, seq, head_dim):
+    n = _c.c_size_t(0)
+    _check(lib().pbs_qk_norm_rope_grad_bytes(batch, seq, head_dim, _c.byref(n)))
+    return n.value
+
+
+def pbs_qk_norm_rope_grad(dq, dq_strides, dk, dk_strides, dv, dv_strides, y_fmt, q, q_strides, heads, k, k_strides,
+                          kv_heads, x_fmt, batch, seq, head_dim, q_weight, k_weight, w_fmt, norm, eps, positions,
+                          pos_batch_stride, freqs, rot_dim, interleaved, dq_out, dq_out_strides, dk_out, dk_out_strides,
+                          dv_out, dv_out_strides, dq_weight, dk_weight, amax_out, workspace, workspace_bytes,
+                          stream=None):
+    _check(lib().pbs_qk_norm_rope_grad(
+        _ptr(dq), _strides(dq_strides), _ptr(dk), _strides(dk_strides), _ptr(dv), _strides(dv_strides), y_fmt, _ptr(q),
+        _strides(q_strides), heads, _ptr(k), _strides(k_strides), kv_heads, x_fmt, batch, seq, head_dim, _ptr(q_weight),
+        _ptr(k_weight), w_fmt, int(norm), eps, _ptr(positions), pos_batch_stride, _ptr(freqs), rot_dim, int(interleaved),
+        _ptr(dq_out), _strides(dq_out_strides), _ptr(dk_out), _strides(dk_out_strides), _ptr(dv_out),
+        _strides(dv_out_strides), _ptr(dq_weight), _ptr(dk_weight), _ptr(amax_out), _ptr(workspace), workspace_bytes,
+        _stream(stream)))
 
 
 def pbs_quantized_bytes(recipe, rows, cols, weight_2d):

@@ -37,7 +37,8 @@ from . import (PBS_COL, PBS_DGRAD, PBS_FLAG_RHT16, PBS_FLAG_SR, PBS_FMT_BF16, PB
                pbs_delayed_init, pbs_delayed_scale, pbs_delayed_scale_inv, pbs_delayed_state_bytes,
                pbs_delayed_update, pbs_gemm, pbs_gemm_amax, pbs_layernorm, pbs_layernorm_grad,
                pbs_layernorm_grad_bytes, pbs_linear_distill, pbs_linear_distill_grad, pbs_linear_loss_bytes,
-               pbs_linear_xent, pbs_linear_xent_grad, pbs_scale_from_amax)
+               pbs_linear_xent, pbs_linear_xent_grad, pbs_qk_norm_rope, pbs_qk_norm_rope_grad,
+               pbs_qk_norm_rope_grad_bytes, pbs_scale_from_amax)
 
 RECIPES = {
     "bf16": PBS_RECIPE_BF16,
@@ -586,3 +587,159 @@ def linear_distill_grad(dloss, x, w, top_ids, top_logits, temperature, lse, piec
                       lambda *a: pbs_linear_distill_grad(d, x.data_ptr(), w.data_ptr(), T, V, H, top_ids.data_ptr(),
                                                          top_logits.data_ptr(), FMT_OF[top_logits.dtype], top,
                                                          temperature, s, *a))
+
+
+# ---------------------------------------------------------------------------
+# the QKV projection's output: norm and rotation of the queries and keys
+# ---------------------------------------------------------------------------
+F64 = (torch.float64,)
+
+
+def rope_frequencies(rot_dim, base=10000.0, device="cuda"):
+    """base^(-2 i / rot_dim) for the pairs i of a rotation, fp64 [rot_dim / 2]:
+    the angle a pair turns by from one position to the next."""
+    if rot_dim < 0 or rot_dim % 2:
+        raise ValueError(f"rot_dim: want an even number, got {rot_dim}")
+    return torch.tensor([float(base) ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)], dtype=torch.float64,
+                        device=device)
+
+
+def _heads4(name, t, device, shape=None, dtype=None):
+    """Checks a [batch, seq, heads, head_dim] tensor whose last axis is contiguous; returns its strides."""
+    if t.dim() != 4 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name}: want shape {tuple(shape) if shape else '[batch, seq, heads, head_dim]'}, got "
+                         f"{tuple(t.shape)}")
+    if t.dtype not in FMT_OF or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name}: want {dtype or 'bf16 or fp32'}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, want {device}")
+    s = t.stride()
+    if t.shape[3] > 1 and s[3] != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    return s[:3]
+
+
+def _qk_common(q, k, q_weight, k_weight, positions, freqs, norm, eps):
+    """Checks what the pass and its gradient share; returns (device, x format,
+    (batch, seq, head_dim), the strides of q and k, heads, kv_heads, the call's
+    arguments from the weights to interleaved, less that)."""
+    if q is None:
+        raise ValueError("q is missing")
+    dev = q.device
+    sq = _heads4("q", q, dev)
+    B, S, H, D = q.shape
+    sk, kv = None, 0
+    if k is not None:
+        kv = k.shape[2] if k.dim() == 4 else 0
+        sk = _heads4("k", k, dev, torch.Size((B, S, kv, D)), q.dtype)
+    elif k_weight is not None:
+        raise ValueError("k_weight without k")
+    w = q_weight if q_weight is not None else k_weight
+    qw, kw = _vector("q_weight", q_weight, D, BF16_F32, dev), _vector("k_weight", k_weight, D, BF16_F32, dev)
+    if qw is not None and kw is not None and q_weight.dtype != k_weight.dtype:
+        raise ValueError("q_weight and k_weight must have the same type")
+    p, psb = None, 0
+    if positions is not None:
+        if positions.dtype != torch.int64 or positions.shape not in ((S,), (B, S)):
+            raise ValueError(f"positions: want int64 [{S}] or [{B}, {S}], got {positions.dtype} {tuple(positions.shape)}")
+        if positions.device != dev:
+            raise ValueError(f"positions: on {positions.device}, want {dev}")
+        if S > 1 and positions.stride(-1) != 1:
+            raise ValueError("positions: the last axis must be contiguous")
+        if positions.dim() == 2 and B > 1:
+            psb = positions.stride(0)
+            if psb != 0 and psb < S:
+                raise ValueError("positions: rows overlap")
+        p = positions.data_ptr()
+    rot, f = 0, None
+    if freqs is not None:
+        rot = 2 * freqs.shape[0] if freqs.dim() == 1 else -1
+        if rot < 0 or rot > D:
+            raise ValueError(f"freqs: want at most {D // 2} values, got shape {tuple(freqs.shape)}")
+        f = _vector("freqs", freqs, rot // 2, F64, dev)
+    args = (qw, kw, PBS_FMT_F32 if w is None else FMT_OF[w.dtype], int(norm), float(eps), p, psb, f, rot)
+    return dev, FMT_OF[q.dtype], (B, S, D), sq, sk, H, kv, args
+
+
+def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, positions=None, freqs=None, interleaved=False, eps=1e-6,
+                 norm=True, q_out=None, k_out=None, out_dtype=None, stream=None):
+    """RMS norm of each head of ``q`` [B, S, H, D] and ``k`` [B, S, Hk, D] (bf16
+    or fp32; None: queries alone) and their rotation by position, in one pass.
+    Returns (q_out, k_out).
+
+    Any strides with a contiguous last axis: views of a packed projection, or
+    ``t.transpose(1, 2)`` of [B, H, S, D], for the outputs too (``q_out``,
+    ``k_out``: also q and k themselves), which are else allocated contiguous in
+    ``out_dtype`` (None: q's).  ``q_weight`` / ``k_weight`` [D]: both bf16 or both
+    fp32 (None: 1).  ``positions``: int64 [S] or [B, S] (None: 0 to S - 1).
+    ``freqs``: fp64 [rot / 2] (``rope_frequencies``), the pairs' angle a position
+    (None: no rotation); the first ``rot`` values of a head are turned, in pairs
+    (i, i + rot / 2), or (2 i, 2 i + 1) if ``interleaved``.  ``norm=False``:
+    rotation alone.
+    """
+    dev, x_fmt, (B, S, D), sq, sk, H, kv, args = _qk_common(q, k, q_weight, k_weight, positions, freqs, norm, eps)
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    given = q_out if q_out is not None else k_out
+    if out_dtype is None:
+        out_dtype = given.dtype if given is not None else q.dtype
+    if out_dtype not in FMT_OF:
+        raise ValueError(f"out_dtype: want bf16 or fp32, got {out_dtype}")
+    oq = None if q_out is None else _heads4("q_out", q_out, dev, q.shape, out_dtype)
+    ok = None if k_out is None else _heads4("k_out", k_out, dev, k.shape, out_dtype)
+    with _on(dev, stream):
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=out_dtype, device=dev)
+            oq = q_out.stride()[:3]
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=out_dtype, device=dev)
+            ok = k_out.stride()[:3]
+        pbs_qk_norm_rope(q, sq, H, k, sk, kv, x_fmt, B, S, D, *args, interleaved, q_out, oq, k_out, ok,
+                         FMT_OF[out_dtype], _current(dev))
+    return q_out, k_out
+
+
+def qk_norm_rope_grad(dq, dk, q, k=None, q_weight=None, k_weight=None, positions=None, freqs=None, interleaved=False,
+                      eps=1e-6, norm=True, dv=None, dq_out=None, dk_out=None, dv_out=None, amax=None, stream=None):
+    """Gradients of ``qk_norm_rope``: returns (dq_out, dk_out in q's type,
+    dq_weight [D], dk_weight [D] in fp32; None for k's without k) from ``dq``, ``dk``
+    (the outputs' gradients, both bf16 or both fp32) and the forward's arguments.
+
+    ``dq_out``, ``dk_out`` may be given (any strides; q / dq, k / dk themselves
+    with the same type).  ``dv`` [B, S, Hk, D] (dq's type) is copied to ``dv_out``
+    (q's type): with the three outputs as the parts of one packed tensor, that is
+    the gradient of the projection's output, and ``amax`` (a device fp32 of one
+    element) receives its max |value| as stored, for ``quantize(...,
+    known_amax=amax)``.
+    """
+    dev, x_fmt, (B, S, D), sq, sk, H, kv, args = _qk_common(q, k, q_weight, k_weight, positions, freqs, norm, eps)
+    if dq is None or (dk is None) != (k is None):
+        raise ValueError("dq or dk is missing, or dk given without k")
+    if k is None and dk_out is not None:
+        raise ValueError("dk_out without k")
+    if (dv is None) != (dv_out is None):
+        raise ValueError("dv and dv_out go together")
+    sdq = _heads4("dq", dq, dev, q.shape)
+    sdk = None if k is None else _heads4("dk", dk, dev, k.shape, dq.dtype)
+    sdv = odv = None
+    if dv is not None:
+        if k is None:
+            raise ValueError("dv without k")
+        sdv, odv = _heads4("dv", dv, dev, k.shape, dq.dtype), _heads4("dv_out", dv_out, dev, k.shape, q.dtype)
+    oq = None if dq_out is None else _heads4("dq_out", dq_out, dev, q.shape, q.dtype)
+    ok = None if dk_out is None else _heads4("dk_out", dk_out, dev, k.shape, q.dtype)
+    a = _vector("amax", amax, 1, F32, dev)
+    with _on(dev, stream):
+        if dq_out is None:
+            dq_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            oq = dq_out.stride()[:3]
+        if k is not None and dk_out is None:
+            dk_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
+            ok = dk_out.stride()[:3]
+        dqw = torch.empty(D, dtype=torch.float32, device=dev)
+        dkw = None if k is None else torch.empty(D, dtype=torch.float32, device=dev)
+        n = pbs_qk_norm_rope_grad_bytes(B, S, D)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        pbs_qk_norm_rope_grad(dq, sdq, dk, sdk, dv, sdv, FMT_OF[dq.dtype], q, sq, H, k, sk, kv, x_fmt, B, S, D, *args,
+                              interleaved, dq_out, oq, dk_out, ok, dv_out, odv, dqw, dkw, a, ws, n, _current(dev))
+    return dq_out, dk_out, dqw, dkw
