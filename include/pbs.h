@@ -492,9 +492,9 @@ pbs_status pbs_linear_distill_grad(const float* dloss, const void* x, const void
  *    dv_out, overwritten: what pbs_amax would return on the packed gradient, for
  *    pbs_scale_from_amax.  NULL: not wanted.
  *  workspace: pbs_qk_norm_rope_grad_bytes(batch, seq, head_dim) bytes, 16-byte
- *    aligned, for the weights' gradients (unused, may be NULL, if both are).
- *    Its contents are of no use afterwards; calls that may run at the same time
- *    need one each.
+ *    aligned, for the weights' gradients and the maximum (unused, may be NULL,
+ *    if none of them is wanted).  Its contents are of no use afterwards; calls
+ *    that may run at the same time need one each.
  * ------------------------------------------------------------------- */
 pbs_status pbs_qk_norm_rope(const void* q, const int64_t* q_strides, int64_t heads, const void* k,
                             const int64_t* k_strides, int64_t kv_heads, pbs_format x_fmt, int64_t batch, int64_t seq,

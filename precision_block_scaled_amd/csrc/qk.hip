@@ -14,6 +14,11 @@
 // and its strips are joined in their order, so identical inputs give identical
 // bytes.
 //
+// Bound by memory: on 15872 tokens of 32 + 32 heads of 128 in bf16 the forward
+// pass takes 101 us (5.15 TB/s of the 520 MB it must read and write, a large
+// copy's rate) and the gradient, with 32 heads of values, 211 us (4.95 TB/s of
+// 1040 MB).  Few tokens are bound by latency: 16 of 32 + 8 heads 7 us.
+//
 // A row is spread over G lanes; a lane holds units of two chunks of CH values,
 // the two that the rotation takes together, so it turns its values by itself.
 // A wave takes one token and several of its heads, of which all need the same
@@ -51,28 +56,8 @@ struct QkArgs {
   int seq, dim, rot, interleaved, norm, w_bf16;
   int heads_each;          // heads of a block
   float eps;
-  uint32_t* amax;          // gradient: may be null
-  float* dw;               // gradient: [strips of all parts][dim]; may be null
-};
-
-template <typename T>
-struct QkIo;
-template <>
-struct QkIo<bf16_t> {
-  static __device__ __forceinline__ float get(const bf16_t* p) { return bf16_to_float(*p); }
-  static __device__ __forceinline__ uint32_t put(bf16_t* p, float v) {
-    const uint32_t b = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v);
-    *p = (bf16_t)b;
-    return (b & 0x7FFFu) << 16;
-  }
-};
-template <>
-struct QkIo<float> {
-  static __device__ __forceinline__ float get(const float* p) { return *p; }
-  static __device__ __forceinline__ uint32_t put(float* p, float v) {
-    *p = v;
-    return __float_as_uint(v) & 0x7FFFFFFFu;
-  }
+  uint32_t* most;          // gradient: a workgroup's max |value| as stored; may be null
+  float* dw;               // gradient: [workgroups of q and k][dim]; may be null
 };
 
 __device__ __forceinline__ uint32_t qk_pk(float lo, float hi) {
@@ -82,57 +67,75 @@ __device__ __forceinline__ uint32_t qk_pk(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, b2));
 }
 
-// CH consecutive values; CH 4 and 8 take aligned addresses (8 or 16 bytes).
+// CH consecutive values as they lie in memory; CH 4 and 8 take aligned
+// addresses (8 or 16 bytes).
 template <typename T, int CH>
-__device__ __forceinline__ void qk_load(const T* p, float* v) {
-  if constexpr (CH == 1) {
-    v[0] = QkIo<T>::get(p);
-  } else if constexpr (sizeof(T) == 4) {
+struct QkRaw {
+  static constexpr int WORDS = CH * (int)sizeof(T) / 4;
+  uint32_t w[WORDS ? WORDS : 1];
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int k = 0; k < CH / 4; ++k) {
-      const float4 f = ((const float4*)p)[k];
-      v[4 * k] = f.x; v[4 * k + 1] = f.y; v[4 * k + 2] = f.z; v[4 * k + 3] = f.w;
-    }
-  } else {
-    uint32_t w[CH / 2];
-    if constexpr (CH == 8) {
-      const uint4 u = *(const uint4*)p;
-      w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-    } else {
+    for (int k = 0; k < (WORDS ? WORDS : 1); ++k) w[k] = 0u;
+  }
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (CH == 1) {
+      if constexpr (sizeof(T) == 4) w[0] = *(const uint32_t*)p;
+      else w[0] = *(const uint16_t*)p;
+    } else if constexpr (WORDS == 2) {
       const uint2 u = *(const uint2*)p;
       w[0] = u.x; w[1] = u.y;
-    }
+    } else {
 #pragma unroll
-    for (int k = 0; k < CH / 2; ++k) {
-      v[2 * k] = __uint_as_float(w[k] << 16);
-      v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+      for (int k = 0; k < WORDS / 4; ++k) {
+        const uint4 u = ((const uint4*)p)[k];
+        w[4 * k] = u.x; w[4 * k + 1] = u.y; w[4 * k + 2] = u.z; w[4 * k + 3] = u.w;
+      }
     }
   }
-}
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else return __uint_as_float(CH > 1 && (i & 1) ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+  }
+};
 
-// Stores CH values and returns the largest magnitude as stored, as fp32 bits.
+// CH values rounded to T, as they go to memory, and their largest magnitude as
+// stored, as fp32 bits.  (Rounded ahead of the condition that the store hangs
+// on: a branch around both made the compiler keep the values in scratch.)
 template <typename T, int CH>
-__device__ __forceinline__ uint32_t qk_store(T* p, const float* v) {
-  uint32_t m = 0;
-  if constexpr (CH == 1) {
-    m = QkIo<T>::put(p, v[0]);
-  } else if constexpr (sizeof(T) == 4) {
+struct QkOut {
+  static constexpr int WORDS = QkRaw<T, CH>::WORDS ? QkRaw<T, CH>::WORDS : 1;
+  uint32_t w[WORDS], most;
+  __device__ __forceinline__ QkOut(const float (&v)[2 * CH], int first) {
+    most = 0;
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int k = 0; k < CH / 4; ++k) ((float4*)p)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+      for (int k = 0; k < CH; ++k) {
+        w[k] = __float_as_uint(v[first + k]);
+        most = max(most, w[k] & 0x7FFFFFFFu);
+      }
+    } else if constexpr (CH == 1) {
+      w[0] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[first]);
+      most = (w[0] & 0x7FFFu) << 16;
+    } else {
 #pragma unroll
-    for (int k = 0; k < CH; ++k) m = max(m, __float_as_uint(v[k]) & 0x7FFFFFFFu);
-  } else {
-    uint32_t w[CH / 2];
-#pragma unroll
-    for (int k = 0; k < CH / 2; ++k) {
-      w[k] = qk_pk(v[2 * k], v[2 * k + 1]);
-      m = max(m, max((w[k] & 0x7FFFu) << 16, w[k] & 0x7FFF0000u));
+      for (int k = 0; k < CH / 2; ++k) {
+        w[k] = qk_pk(v[first + 2 * k], v[first + 2 * k + 1]);
+        most = max(most, max((w[k] & 0x7FFFu) << 16, w[k] & 0x7FFF0000u));
+      }
     }
-    if constexpr (CH == 8) *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
-    else *(uint2*)p = make_uint2(w[0], w[1]);
   }
-  return m;
-}
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (CH == 1) {
+      if constexpr (sizeof(T) == 4) *(uint32_t*)p = w[0];
+      else *(uint16_t*)p = (uint16_t)w[0];
+    } else if constexpr (WORDS == 2) {
+      *(uint2*)p = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < WORDS / 4; ++k) ((uint4*)p)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    }
+  }
+};
 
 // Sum over the G lanes of a group, to each of them.
 template <int G>
@@ -170,25 +173,18 @@ __device__ __forceinline__ QkUnit qk_unit(int u, int dim, int rot, int interleav
   return q;
 }
 
-// Turns a unit's values by +- its angles.
-template <int CH>
-__device__ __forceinline__ void qk_turn(float (&v)[2 * CH], const float2 (&cs)[CH], int interleaved, float sign) {
-  if constexpr (CH > 1) {
-    if (interleaved) {
-#pragma unroll
-      for (int k = 0; k < CH; ++k) {
-        const float p = v[2 * k], q = v[2 * k + 1], c = cs[k].x, s = sign * cs[k].y;
-        v[2 * k] = p * c - q * s;
-        v[2 * k + 1] = q * c + p * s;
-      }
-      return;
-    }
-  }
+// Turns a unit's values by +- its angles.  INTER: pairs are neighbours (a
+// kernel of its own: a branch here made the compiler choose between addresses
+// and keep the values in scratch); single values lie as pairs either way.
+template <int CH, bool INTER>
+__device__ __forceinline__ void qk_turn(float (&v)[2 * CH], const float2 (&cs)[CH], float sign) {
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
-    const float p = v[k], q = v[CH + k], c = cs[k].x, s = sign * cs[k].y;
-    v[k] = p * c - q * s;
-    v[CH + k] = q * c + p * s;
+    float& u = v[INTER ? 2 * k : k];
+    float& w = v[INTER ? 2 * k + 1 : CH + k];
+    const float p = u, q = w, c = cs[k].x, s = sign * cs[k].y;
+    u = p * c - q * s;
+    w = q * c + p * s;
   }
 }
 
@@ -209,7 +205,7 @@ __device__ __forceinline__ void qk_angles(const QkArgs& a, int64_t pos, float2* 
 
 // One token's heads h0 .. h1 of a part.  UN rounds of 64 / G heads are loaded
 // before the first is used.
-template <typename TX, typename TY, int CH, int G, int NU, int UN, bool GRAD>
+template <typename TX, typename TY, int CH, bool INTER, int G, int NU, int UN, bool GRAD>
 struct QkRows {
   static constexpr int PER = 64 / G;
   QkUnit u[NU];
@@ -232,13 +228,13 @@ struct QkRows {
   }
 
   template <typename T>
-  __device__ __forceinline__ void load(const T* row, bool there, float (&v)[NU][2 * CH]) const {
+  __device__ __forceinline__ void load(const T* row, bool there, QkRaw<T, CH> (&v)[NU][2]) const {
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
-#pragma unroll
-      for (int i = 0; i < 2 * CH; ++i) v[k][i] = 0.0f;
-      if (there && u[k].has_a) qk_load<T, CH>(row + u[k].a, v[k]);
-      if (there && u[k].has_b) qk_load<T, CH>(row + u[k].b, v[k] + CH);
+      v[k][0].zero();
+      v[k][1].zero();
+      if (there && u[k].has_a) v[k][0].load(row + u[k].a);
+      if (there && u[k].has_b) v[k][1].load(row + u[k].b);
     }
   }
   template <typename T>
@@ -246,56 +242,79 @@ struct QkRows {
     uint32_t m = 0;
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
-      if (there && u[k].has_a) m = max(m, qk_store<T, CH>(row + u[k].a, v[k]));
-      if (there && u[k].has_b) m = max(m, qk_store<T, CH>(row + u[k].b, v[k] + CH));
+      const QkOut<T, CH> a(v[k], 0), b(v[k], CH);
+      if (there && u[k].has_a) {
+        a.store(row + u[k].a);
+        m = max(m, a.most);
+      }
+      if (there && u[k].has_b) {
+        b.store(row + u[k].b);
+        m = max(m, b.most);
+      }
     }
     return m;
   }
 
   __device__ __forceinline__ uint32_t run(const QkArgs& a, const QkPart& p, int64_t token, int h0, int h1, float2* lds) {
     const int b = (int)(token / a.seq), s = (int)(token - (int64_t)b * a.seq);
-    if (a.rot) qk_angles(a, a.pos ? a.pos[b * a.pos_sb + s] : s, lds);
-    float2 cs[NU][CH];
-#pragma unroll
-    for (int k = 0; k < NU; ++k)
-#pragma unroll
-      for (int i = 0; i < CH; ++i) cs[k][i] = u[k].pair >= 0 ? lds[u[k].pair + i] : make_float2(1.0f, 0.0f);
+    const int64_t pos = a.rot && a.pos ? a.pos[b * a.pos_sb + s] : s;
     const TX* x = (const TX*)p.x.p + b * p.x.sb + s * p.x.ss;
     const TY* dy = GRAD ? (const TY*)p.dy.p + b * p.dy.sb + s * p.dy.ss : nullptr;
     const int64_t o = b * p.out.sb + s * p.out.ss;
     const float inv = 1.0f / (float)a.dim;
     uint32_t mx = 0;
-    for (int h = h0 + (threadIdx.x & 63) / G; h - (threadIdx.x & 63) / G < h1; h += PER * UN) {
-      float v[UN][NU][2 * CH], g[GRAD ? UN : 1][NU][2 * CH];
+    const int g0 = (threadIdx.x & 63) / G;
+    QkRaw<TX, CH> rx[UN][NU][2];
+    QkRaw<TY, CH> ry[GRAD ? UN : 1][NU][2];
+    auto fetch = [&](int h) {
 #pragma unroll
       for (int n = 0; n < UN; ++n) {
-        load(x + (h + n * PER) * p.x.sh, h + n * PER < h1, v[n]);
-        if constexpr (GRAD) load(dy + (h + n * PER) * p.dy.sh, h + n * PER < h1, g[n]);
+        load(x + (h + n * PER) * p.x.sh, h + n * PER < h1, rx[n]);
+        if constexpr (GRAD) load(dy + (h + n * PER) * p.dy.sh, h + n * PER < h1, ry[n]);
       }
+    };
+    // the first rows are on their way while the angles are formed
+    fetch(h0 + g0);
+    if (a.rot) qk_angles(a, pos, lds);
+    float2 cs[NU][CH];
+#pragma unroll
+    for (int k = 0; k < NU; ++k)
+#pragma unroll
+      for (int i = 0; i < CH; ++i) cs[k][i] = u[k].pair >= 0 ? lds[u[k].pair + i] : make_float2(1.0f, 0.0f);
+    for (int h = h0 + g0; h - g0 < h1; h += PER * UN) {
+      if (h - g0 > h0) fetch(h);
 #pragma unroll
       for (int n = 0; n < UN; ++n) {
         const bool there = h + n * PER < h1;
+        float v[NU][2 * CH], g[NU][2 * CH];
+#pragma unroll
+        for (int k = 0; k < NU; ++k)
+#pragma unroll
+          for (int i = 0; i < 2 * CH; ++i) {
+            v[k][i] = rx[n][k][i / CH].get(i % CH);
+            if constexpr (GRAD) g[k][i] = ry[n][k][i / CH].get(i % CH);
+          }
         float sum = 0.0f;
 #pragma unroll
         for (int k = 0; k < NU; ++k)
 #pragma unroll
-          for (int i = 0; i < 2 * CH; ++i) sum = __builtin_fmaf(v[n][k][i], v[n][k][i], sum);
+          for (int i = 0; i < 2 * CH; ++i) sum = __builtin_fmaf(v[k][i], v[k][i], sum);
         if constexpr (!GRAD) {
           const float r = a.norm ? 1.0f / sqrtf(group_sum<G>(sum) * inv + a.eps) : 1.0f;
 #pragma unroll
           for (int k = 0; k < NU; ++k) {
 #pragma unroll
-            for (int i = 0; i < 2 * CH; ++i) v[n][k][i] = v[n][k][i] * r * w[k][i];
-            if (u[k].pair >= 0) qk_turn<CH>(v[n][k], cs[k], a.interleaved, 1.0f);
+            for (int i = 0; i < 2 * CH; ++i) v[k][i] = v[k][i] * r * w[k][i];
+            if (u[k].pair >= 0) qk_turn<CH, INTER>(v[k], cs[k], 1.0f);
           }
-          store((TY*)p.out.p + o + (h + n * PER) * p.out.sh, there, v[n]);
+          store((TY*)p.out.p + o + (h + n * PER) * p.out.sh, there, v);
         } else {
           float dot = 0.0f;
 #pragma unroll
           for (int k = 0; k < NU; ++k) {
-            if (u[k].pair >= 0) qk_turn<CH>(g[n][k], cs[k], a.interleaved, -1.0f);
+            if (u[k].pair >= 0) qk_turn<CH, INTER>(g[k], cs[k], -1.0f);
 #pragma unroll
-            for (int i = 0; i < 2 * CH; ++i) dot = __builtin_fmaf(g[n][k][i] * w[k][i], v[n][k][i], dot);
+            for (int i = 0; i < 2 * CH; ++i) dot = __builtin_fmaf(g[k][i] * w[k][i], v[k][i], dot);
           }
           const float r = a.norm ? 1.0f / sqrtf(group_sum<G>(sum) * inv + a.eps) : 1.0f;
           const float mean = a.norm ? group_sum<G>(dot) * inv * r : 0.0f;       // mean(v n)
@@ -303,11 +322,11 @@ struct QkRows {
           for (int k = 0; k < NU; ++k)
 #pragma unroll
             for (int i = 0; i < 2 * CH; ++i) {
-              const float nrm = v[n][k][i] * r;
-              dw[k][i] = __builtin_fmaf(g[n][k][i], nrm, dw[k][i]);
-              v[n][k][i] = r * (g[n][k][i] * w[k][i] - nrm * mean);
+              const float nrm = v[k][i] * r;
+              dw[k][i] = __builtin_fmaf(g[k][i], nrm, dw[k][i]);
+              v[k][i] = r * (g[k][i] * w[k][i] - nrm * mean);
             }
-          mx = max(mx, store((TX*)p.out.p + o + (h + n * PER) * p.out.sh, there, v[n]));
+          mx = max(mx, store((TX*)p.out.p + o + (h + n * PER) * p.out.sh, there, v));
         }
       }
     }
@@ -315,7 +334,7 @@ struct QkRows {
   }
 };
 
-template <typename TX, typename TY, int CH, int G, int NU>
+template <typename TX, typename TY, int CH, bool INTER, int G, int NU>
 __global__ __launch_bounds__(QK_THR) void qk_norm_rope_kernel(QkArgs a) {
   __shared__ float2 cs[QK_WAVES][QK_MOST_DIM / 2];
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -327,13 +346,13 @@ __global__ __launch_bounds__(QK_THR) void qk_norm_rope_kernel(QkArgs a) {
   if (which) item -= queries;
   const int64_t token = item / p.blocks;
   const int h0 = (int)(item - token * p.blocks) * a.heads_each;
-  QkRows<TX, TY, CH, G, NU, CH == 8 ? 4 : 2, false> rows;
+  QkRows<TX, TY, CH, INTER, G, NU, CH == 8 ? 4 : 2, false> rows;
   rows.init(a, p);
   rows.run(a, p, token, h0, min(h0 + a.heads_each, p.heads), cs[w]);
 }
 
 // A workgroup takes every strips-th group of QK_WAVES tokens of one part.
-template <typename TX, typename TY, int CH, int G, int NU>
+template <typename TX, typename TY, int CH, bool INTER, int G, int NU>
 __global__ __launch_bounds__(QK_THR) void qk_norm_rope_grad_kernel(QkArgs a) {
   __shared__ float2 cs[QK_WAVES][QK_MOST_DIM / 2];
   __shared__ float sums[QK_WAVES][QK_MOST_DIM];
@@ -345,20 +364,40 @@ __global__ __launch_bounds__(QK_THR) void qk_norm_rope_grad_kernel(QkArgs a) {
   const int strip = block - p.first;
   uint32_t mx = 0;
   if (which == 2) {
-    const int n = a.dim / CH;
+    // chunk lane + 64 j of a token's values; eight loads ahead of their stores
+    constexpr int AHEAD = 8;
+    const int n = a.dim / CH, all = n * p.heads, dh = 64 / n, dc = 64 - dh * n;
     for (int64_t t = (int64_t)strip * QK_WAVES + w; t < a.tokens; t += (int64_t)p.strips * QK_WAVES) {
       const int b = (int)(t / a.seq), s = (int)(t - (int64_t)b * a.seq);
       const TY* from = (const TY*)p.dy.p + b * p.dy.sb + s * p.dy.ss;
       TX* to = (TX*)p.out.p + b * p.out.sb + s * p.out.ss;
-      for (int i = lane; i < n * p.heads; i += 64) {
-        const int h = i / n, c = (i - h * n) * CH;
-        float v[CH];
-        qk_load<TY, CH>(from + h * p.dy.sh + c, v);
-        mx = max(mx, qk_store<TX, CH>(to + h * p.out.sh + c, v));
+      int h = lane / n, c = lane - h * n;
+      for (int i = lane; i < all; i += 64 * AHEAD) {
+        QkRaw<TY, CH> r[AHEAD];
+        int64_t at[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+          if (i + 64 * j < all) r[j].load(from + h * p.dy.sh + c * CH);
+          at[j] = h * p.out.sh + c * CH;
+          c += dc;
+          h += dh + (c >= n ? 1 : 0);
+          c -= c >= n ? n : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+          float v[2 * CH];
+#pragma unroll
+          for (int k = 0; k < CH; ++k) v[k] = r[j].get(k);
+          const QkOut<TX, CH> o(v, 0);
+          if (i + 64 * j < all) {
+            o.store(to + at[j]);
+            mx = max(mx, o.most);
+          }
+        }
       }
     }
   } else {
-    QkRows<TX, TY, CH, G, NU, 2, true> rows;
+    QkRows<TX, TY, CH, INTER, G, NU, 2, true> rows;
     rows.init(a, p);
     for (int64_t t = (int64_t)strip * QK_WAVES + w; t < a.tokens; t += (int64_t)p.strips * QK_WAVES)
       mx = max(mx, rows.run(a, p, t, 0, p.heads, cs[w]));
@@ -383,7 +422,7 @@ __global__ __launch_bounds__(QK_THR) void qk_norm_rope_grad_kernel(QkArgs a) {
       }
     }
   }
-  if (a.amax) {
+  if (a.most) {
     __shared__ uint32_t most[QK_WAVES];
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, o, 64));
@@ -392,7 +431,7 @@ __global__ __launch_bounds__(QK_THR) void qk_norm_rope_grad_kernel(QkArgs a) {
     if (threadIdx.x == 0) {
 #pragma unroll
       for (int q = 1; q < QK_WAVES; ++q) mx = max(mx, most[q]);
-      if (mx > __builtin_nontemporal_load(a.amax)) atomicMax(a.amax, mx);
+      a.most[block] = mx;
     }
   }
 }
@@ -401,17 +440,38 @@ __global__ void qk_fill_kernel(uint32_t* p, int n) {
   for (int i = threadIdx.x; i < n; i += blockDim.x) p[i] = 0u;
 }
 
-// dw = the sum of its strips, a column's by 16 threads, each every 16th strip.
-constexpr int QK_JOIN_COLS = 16, QK_JOIN_ROWS = 16;
-__global__ __launch_bounds__(QK_JOIN_COLS * QK_JOIN_ROWS) void qk_join_kernel(QkArgs a, float* dqw, float* dkw) {
+// dw = the sum of its strips, a column's by 64 threads, each every 64th strip
+// (16 threads of it took 8 us for 512 strips, these 4); and the maximum over the
+// workgroups, by a workgroup of its own.
+constexpr int QK_JOIN_COLS = 16, QK_JOIN_ROWS = 64, QK_JOIN_THR = QK_JOIN_COLS * QK_JOIN_ROWS;
+__global__ __launch_bounds__(QK_JOIN_THR) void qk_join_kernel(QkArgs a, float* dqw, float* dkw, uint32_t* amax, int all) {
   __shared__ float part[QK_JOIN_ROWS][QK_JOIN_COLS];
+  if (blockIdx.y == 2) {
+    if (!amax || blockIdx.x) return;
+    uint32_t m = 0;
+    for (int i = threadIdx.x; i < all; i += QK_JOIN_THR) m = max(m, a.most[i]);
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+    uint32_t* most = (uint32_t*)part;
+    if (threadIdx.x % 64 == 0) most[threadIdx.x / 64] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+      for (int i = 1; i < QK_JOIN_THR / 64; ++i) m = max(m, most[i]);
+      *amax = m;
+    }
+    return;
+  }
   const QkPart& p = a.part[blockIdx.y];
   float* out = blockIdx.y ? dkw : dqw;
   if (!out) return;
   const int c = blockIdx.x * QK_JOIN_COLS + threadIdx.x % QK_JOIN_COLS, r = threadIdx.x / QK_JOIN_COLS;
   float s = 0.0f;
-  if (c < a.dim)
-    for (int i = r; i < p.strips; i += QK_JOIN_ROWS) s += a.dw[(int64_t)(p.first + i) * a.dim + c];
+  if (c < a.dim) {
+    const float* from = a.dw + (int64_t)p.first * a.dim + c;
+#pragma unroll 4
+    for (int i = r; i < p.strips; i += QK_JOIN_ROWS) s += from[(int64_t)i * a.dim];
+  }
   part[r][threadIdx.x % QK_JOIN_COLS] = s;
   __syncthreads();
   if (r == 0 && c < a.dim) {
@@ -424,15 +484,21 @@ __global__ __launch_bounds__(QK_JOIN_COLS * QK_JOIN_ROWS) void qk_join_kernel(Qk
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
-// Workgroups of a gradient: what fills the card four times over, shared out
-// by the parts' heads.
-constexpr int QK_STRIPS = 1024;
-static int qk_strips(int64_t tokens, int64_t heads, int64_t all) {
+// Workgroups of a gradient: what the card holds at a time (three a compute
+// unit), shared out by the parts' cost a token (a fixed part, the angles and the
+// first loads' latency, and the rounds of heads).  15872 tokens of 32 + 32 + 32
+// heads take 211 us, 8191 of 32 + 8 + 8 70 us; with 1024 workgroups 14 and 18%
+// longer, with 2048 10 and 16%, four rounds of heads ahead instead of two 28 and
+// 50% (registers).
+constexpr int QK_STRIPS = 768;
+static int qk_strips(int64_t tokens, int64_t cost, int64_t all) {
   const int64_t most = ceil_div(tokens, QK_WAVES);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(most, QK_STRIPS * heads / std::max<int64_t>(all, 1)));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(most, QK_STRIPS * cost / std::max<int64_t>(all, 1)));
 }
+// Sums of the weights' gradients, dim a workgroup of q and k, and every workgroup's maximum.
+static int64_t qk_most_strips(int64_t tokens) { return std::max<int64_t>(1, std::min<int64_t>(ceil_div(tokens, QK_WAVES), QK_STRIPS)); }
 static size_t qk_grad_bytes(int64_t tokens, int64_t dim) {
-  return (size_t)(2 * std::max<int64_t>(1, std::min<int64_t>(ceil_div(tokens, QK_WAVES), QK_STRIPS))) * (size_t)dim * 4;
+  return (size_t)qk_most_strips(tokens) * (2 * (size_t)dim + 3) * 4;
 }
 
 // The widest chunks that the call's sizes, strides and addresses allow.
@@ -450,7 +516,7 @@ static bool qk_fits(const QkTensor& t, int bytes, int ch) {
                   t.sh * bytes % align == 0);
 }
 static int qk_chunk(const QkCall& c, const QkArgs& a, bool grad) {
-  for (int ch = 8; ch > 1; ch -= 4) {
+  for (int ch = grad ? 4 : 8; ch > 1; ch -= 4) {
     bool ok = c.dim % ch == 0 && c.rot / 2 % ch == 0;
     for (int i = 0; i < 3; ++i) {
       const QkPart& p = a.part[i];
@@ -462,26 +528,37 @@ static int qk_chunk(const QkCall& c, const QkArgs& a, bool grad) {
   return 1;
 }
 
-#define PBS_QK_TYPED(kernel, grid, CH, G, NU)                                                                      \
+#define PBS_QK_TYPED(kernel, grid, ...)                                                                            \
   do {                                                                                                             \
-    if (c.x_bf16 && c.y_bf16) hipLaunchKernelGGL((kernel<bf16_t, bf16_t, CH, G, NU>), grid, dim3(QK_THR), 0, stream, a);  \
-    else if (c.x_bf16) hipLaunchKernelGGL((kernel<bf16_t, float, CH, G, NU>), grid, dim3(QK_THR), 0, stream, a);   \
-    else if (c.y_bf16) hipLaunchKernelGGL((kernel<float, bf16_t, CH, G, NU>), grid, dim3(QK_THR), 0, stream, a);   \
-    else hipLaunchKernelGGL((kernel<float, float, CH, G, NU>), grid, dim3(QK_THR), 0, stream, a);                  \
+    if (c.x_bf16 && c.y_bf16) hipLaunchKernelGGL((kernel<bf16_t, bf16_t, __VA_ARGS__>), grid, dim3(QK_THR), 0, stream, a);  \
+    else if (c.x_bf16) hipLaunchKernelGGL((kernel<bf16_t, float, __VA_ARGS__>), grid, dim3(QK_THR), 0, stream, a); \
+    else if (c.y_bf16) hipLaunchKernelGGL((kernel<float, bf16_t, __VA_ARGS__>), grid, dim3(QK_THR), 0, stream, a); \
+    else hipLaunchKernelGGL((kernel<float, float, __VA_ARGS__>), grid, dim3(QK_THR), 0, stream, a);                \
   } while (0)
-// lanes a row: units of 16 values (chunks of 8), 8 (of 4) or 2 (single values)
-#define PBS_QK_LAUNCH(kernel, grid, ch)                              \
+// Lanes a row: units of 16 values (chunks of 8, the forward pass), 8 (of 4) or 2 (single values).
+#define PBS_QK_EIGHT(kernel, grid, INTER)                            \
   do {                                                               \
-    if (ch == 8 && c.dim <= 64) PBS_QK_TYPED(kernel, grid, 8, 4, 1);      \
-    else if (ch == 8 && c.dim <= 128) PBS_QK_TYPED(kernel, grid, 8, 8, 1);     \
-    else if (ch == 8 && c.dim <= 256) PBS_QK_TYPED(kernel, grid, 8, 16, 1);    \
-    else if (ch == 8) PBS_QK_TYPED(kernel, grid, 8, 32, 1);          \
-    else if (ch == 4 && c.dim <= 128) PBS_QK_TYPED(kernel, grid, 4, 16, 1);    \
-    else if (ch == 4) PBS_QK_TYPED(kernel, grid, 4, 64, 1);          \
-    else PBS_QK_TYPED(kernel, grid, 1, 64, 4);                       \
+    if (c.dim <= 64) PBS_QK_TYPED(kernel, grid, 8, INTER, 4, 1);     \
+    else if (c.dim <= 128) PBS_QK_TYPED(kernel, grid, 8, INTER, 8, 1);   \
+    else if (c.dim <= 256) PBS_QK_TYPED(kernel, grid, 8, INTER, 16, 1);  \
+    else PBS_QK_TYPED(kernel, grid, 8, INTER, 32, 1);                \
+  } while (0)
+#define PBS_QK_FOUR(kernel, grid, INTER)                             \
+  do {                                                               \
+    if (c.dim <= 64) PBS_QK_TYPED(kernel, grid, 4, INTER, 8, 1);     \
+    else if (c.dim <= 128) PBS_QK_TYPED(kernel, grid, 4, INTER, 16, 1);  \
+    else if (c.dim <= 256) PBS_QK_TYPED(kernel, grid, 4, INTER, 32, 1);  \
+    else PBS_QK_TYPED(kernel, grid, 4, INTER, 64, 1);                \
+  } while (0)
+#define PBS_QK_FOUR_OR_ONE(kernel, grid)                             \
+  do {                                                               \
+    if (ch == 1) PBS_QK_TYPED(kernel, grid, 1, false, 64, 4);        \
+    else if (c.interleaved) PBS_QK_FOUR(kernel, grid, true);         \
+    else PBS_QK_FOUR(kernel, grid, false);                           \
   } while (0)
 static int qk_per_wave(int ch, int64_t dim) {
-  return ch == 8 ? (dim <= 64 ? 16 : dim <= 128 ? 8 : dim <= 256 ? 4 : 2) : ch == 4 && dim <= 128 ? 4 : 1;
+  const int lanes = ch == 1 ? 64 : dim <= 64 ? 8 : dim <= 128 ? 16 : dim <= 256 ? 32 : 64;
+  return 64 / (ch == 8 ? lanes / 2 : lanes);
 }
 
 static pbs_status qk_check_tensor(const QkCall& c, const char* name, const QkTensor& t, bool bf16) {
@@ -601,7 +678,9 @@ pbs_status pbs_qk_norm_rope(const void* q, const int64_t* q_strides, int64_t hea
   PBS_REQUIRE(grid < (1ll << 31), PBS_ERR_SHAPE, "pbs_qk_norm_rope: too many tokens and heads for one call");
   log_dispatch("qk_norm_rope tokens=%lld heads=%d+%d dim=%d rot=%d chunk=%d heads/wave=%d", (long long)a.tokens,
                a.part[0].heads, a.part[1].heads, a.dim, a.rot, ch, a.heads_each);
-  PBS_QK_LAUNCH(qk_norm_rope_kernel, dim3((unsigned)grid), ch);
+  if (ch != 8) PBS_QK_FOUR_OR_ONE(qk_norm_rope_kernel, dim3((unsigned)grid));
+  else if (c.interleaved) PBS_QK_EIGHT(qk_norm_rope_kernel, dim3((unsigned)grid), true);
+  else PBS_QK_EIGHT(qk_norm_rope_kernel, dim3((unsigned)grid), false);
   return check_launch("pbs_qk_norm_rope");
 }
 
@@ -663,7 +742,7 @@ pbs_status pbs_qk_norm_rope_grad(const void* dq, const int64_t* dq_strides, cons
   }
   const int all = a.part[0].heads + a.part[1].heads + a.part[2].heads;
   const bool sums = all && (dq_weight || dk_weight);
-  if (sums) {
+  if (sums || (all && amax_out)) {
     PBS_REQUIRE(workspace && ((uintptr_t)workspace & 15) == 0, PBS_ERR_INVALID_ARG,
                 "pbs_qk_norm_rope_grad: the workspace is null or not 16-byte aligned");
     const size_t need = qk_grad_bytes(a.tokens, head_dim);
@@ -671,7 +750,7 @@ pbs_status pbs_qk_norm_rope_grad(const void* dq, const int64_t* dq_strides, cons
                 "pbs_qk_norm_rope_grad: the workspace holds %zu bytes, pbs_qk_norm_rope_grad_bytes asks for %zu",
                 workspace_bytes, need);
   }
-  if (amax_out) hipLaunchKernelGGL(qk_fill_kernel, dim3(1), dim3(64), 0, stream, (uint32_t*)amax_out, 1);
+  if (amax_out && all == 0) hipLaunchKernelGGL(qk_fill_kernel, dim3(1), dim3(64), 0, stream, (uint32_t*)amax_out, 1);
   // a part that has no rows leaves its weight's gradient zero
   for (int i = 0; i < 2; ++i)
     if (a.part[i].heads == 0 && (i ? dk_weight : dq_weight))
@@ -680,23 +759,24 @@ pbs_status pbs_qk_norm_rope_grad(const void* dq, const int64_t* dq_strides, cons
   a.pos = positions; a.pos_sb = pos_batch_stride; a.freqs = freqs;
   a.seq = (int)seq; a.dim = (int)head_dim; a.rot = (int)rot_dim;
   a.interleaved = c.interleaved; a.norm = c.norm; a.eps = eps; a.w_bf16 = c.w_bf16;
-  a.amax = (uint32_t*)amax_out;
-  a.dw = sums ? (float*)workspace : nullptr;
+  a.most = amax_out ? (uint32_t*)workspace : nullptr;
+  a.dw = sums ? (float*)workspace + 3 * qk_most_strips(a.tokens) : nullptr;
+  const int ch = qk_chunk(c, a, true), per = qk_per_wave(ch, head_dim);
+  auto cost = [&](int i) { return a.part[i].heads ? 6 + (i < 2 ? 6 : 2) * ceil_div(a.part[i].heads, 2 * per) : 0; };
   int grid = 0;
   for (int i = 0; i < 3; ++i) {
     QkPart& p = a.part[i];
     p.first = grid;
-    p.strips = p.heads ? qk_strips(a.tokens, p.heads, all) : 0;
+    p.strips = p.heads ? qk_strips(a.tokens, cost(i), cost(0) + cost(1) + cost(2)) : 0;
     grid += p.strips;
   }
-  const int ch = qk_chunk(c, a, true);
   log_dispatch("qk_norm_rope_grad tokens=%lld heads=%d+%d+%d dim=%d rot=%d chunk=%d strips=%d+%d+%d", (long long)a.tokens,
                a.part[0].heads, a.part[1].heads, a.part[2].heads, a.dim, a.rot, ch, a.part[0].strips, a.part[1].strips,
                a.part[2].strips);
-  PBS_QK_LAUNCH(qk_norm_rope_grad_kernel, dim3((unsigned)grid), ch);
-  if (sums)
-    hipLaunchKernelGGL(qk_join_kernel, dim3((unsigned)ceil_div(head_dim, QK_JOIN_COLS), 2), dim3(QK_JOIN_COLS * QK_JOIN_ROWS),
-                       0, stream, a, a.part[0].heads ? dq_weight : nullptr, a.part[1].heads ? dk_weight : nullptr);
+  PBS_QK_FOUR_OR_ONE(qk_norm_rope_grad_kernel, dim3((unsigned)grid));
+  if (sums || amax_out)
+    hipLaunchKernelGGL(qk_join_kernel, dim3((unsigned)ceil_div(head_dim, QK_JOIN_COLS), 3), dim3(QK_JOIN_THR), 0, stream, a,
+                       a.part[0].heads ? dq_weight : nullptr, a.part[1].heads ? dk_weight : nullptr, (uint32_t*)amax_out, grid);
   return check_launch("pbs_qk_norm_rope_grad");
 }
 

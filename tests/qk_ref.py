@@ -98,10 +98,12 @@ def grad_ref(dy, x, w, positions, freqs, interleaved, eps, norm, out_dtype, stri
         dx = r * (v - n * mean)
         e = r * (e_v + n.abs() * e_mean + (2 * rel + 4 * U) * (v.abs() + (n * mean).abs()))
     t = g * n
-    chain = -(-(B * S) // (4 * strips)) * H + 6 + 4 + strips // 16 + 17
+    chain = -(-(B * S) // (4 * strips)) * H + 6 + 4 + 768 // 64 + 64
     e_dw = (e_g * n.abs() + (rel + 2 * U) * t.abs() + chain * U * t.abs()).sum((0, 1, 2))
     return dx, e + half_step(out_dtype) * (dx.abs() + e) + 1e-40, t.sum((0, 1, 2)), e_dw + 1e-40
 
 
 def strips_of(tokens, heads, all_heads):
-    return max(1, min(-(-tokens // 4), 1024 * heads // all_heads))
+    """At most as many workgroups as share the sums of a tensor of `heads` among `all_heads` heads: a part's share
+    of 768 goes by its rounds of heads and a constant, so it is no less than half of its share of the heads."""
+    return max(1, min(-(-tokens // 4), 384 * heads // all_heads - 1))

@@ -66,8 +66,8 @@ def test_gradient_refusals(change, status, text):
 
 
 def test_workspace_bytes():
-    assert P.pbs_qk_norm_rope_grad_bytes(0, 5, 128) == 2 * 128 * 4
-    assert P.pbs_qk_norm_rope_grad_bytes(31, 512, 128) == 2 * 1024 * 128 * 4
+    assert P.pbs_qk_norm_rope_grad_bytes(0, 5, 128) == (2 * 128 + 3) * 4
+    assert P.pbs_qk_norm_rope_grad_bytes(31, 512, 128) == 768 * (2 * 128 + 3) * 4
     for bad in ((-1, 1, 128), (1, 1, 0), (1, 1, 513), (1 << 24, 1 << 24, 64)):
         with pytest.raises(P.PBSError):
             P.pbs_qk_norm_rope_grad_bytes(*bad)
