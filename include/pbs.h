@@ -50,7 +50,7 @@ extern "C" {
 
 #define PBS_VERSION 4   /* 3: pbs_rht_cast, pbs_debug_sr_encode; 4: four SR words per Philox call.  The layer norm's and
                            the linear head's entry points came with no change to these and without a new number, so did
-                           those of the queries' and keys' norm and rotation */
+                           those of the queries' and keys' norm and rotation and of Muon's update */
 
 typedef enum {
   PBS_OK = 0,
@@ -513,6 +513,55 @@ pbs_status pbs_qk_norm_rope_grad(const void* dq, const int64_t* dq_strides, cons
                                  void* dk_out, const int64_t* dk_out_strides, void* dv_out,
                                  const int64_t* dv_out_strides, float* dq_weight, float* dk_weight, float* amax_out,
                                  void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------
+ * Newton-Schulz orthogonalisation and Muon's update of a weight with it: what
+ * a Wgrad product's result goes into.  For each matrix of a batch by itself,
+ * with X taken as [m, n], m = min(rows, cols):
+ *   X = U / (||U||_F + eps)
+ *   A = X X^T,  P = b A + c A^2,  X' = a X + P X     for each step (a, b, c)
+ * coefficients [host]: `steps` (1 to 64) triples a, b, c; (3.4445, -4.7750,
+ * 2.0315) five times are the Muon optimiser's.  They may not let singular values
+ * that start within [0, 1], or P's, grow past 4096 (PBS_ERR_INVALID_ARG).
+ *
+ * pbs_orthogonalize: U = x (bf16 or fp32), y = the last X in bf16.
+ * pbs_muon: U = beta M' + (1 - beta) G with nesterov, else M', and
+ *   M' = beta M + (1 - beta) G
+ *   W' = (1 - lr weight_decay) W - lr scale X
+ *  w, momentum: bf16 or fp32 each, updated in place; U and X are formed from M'
+ *    before its rounding.  grad: bf16 or fp32, [rows, cols] as w, or with
+ *    grad_transposed [cols, rows], as pbs_gemm's WGRAD writes it for a weight
+ *    stored [N, K].
+ *  lr_factor: device fp32 of one element that lr is multiplied by (a schedule in
+ *    a captured graph); NULL: 1.  beta in [0, 1]; beta and 1 - beta are rounded
+ *    to fp32 each.
+ *
+ *  Matrices are [rows, cols] with the last axis contiguous, rows ld and matrices
+ *    batch_stride elements apart (any, but written rows do not overlap; any
+ *    alignment of an element).  y may be x itself (bf16, its strides); w,
+ *    momentum and grad lie apart.
+ *  A matrix of zeros gives X = 0; one whose U holds an infinity or a NaN gives NaN
+ *    throughout that matrix, and none elsewhere.
+ *  Accuracy: ||U||_F in 64 bits; products of fp16 operands (11 bits of each
+ *    entry's magnitude, held times a power of two so that none leaves the normal
+ *    range in bulk) with fp32 sums, X carried with 22 bits: X is within about
+ *    0.2% of the result in 64 bits (2-norm).
+ *  Identical inputs give identical bytes.
+ *  workspace: pbs_orthogonalize_bytes(batch, rows, cols) bytes, 256-byte aligned.
+ *    Its contents are of no use afterwards; calls that may run at the same time
+ *    need one each.
+ *  Shapes (else PBS_ERR_SHAPE): batch up to 65535, sides up to 2^20, the shorter
+ *    up to 32768.  An empty batch or matrix enqueues nothing.
+ * ------------------------------------------------------------------- */
+pbs_status pbs_orthogonalize_bytes(int64_t batch, int64_t rows, int64_t cols, size_t* bytes /* [host] */);
+pbs_status pbs_orthogonalize(const void* x, pbs_format x_fmt, int64_t ldx, int64_t x_batch_stride, int64_t batch, int64_t rows,
+                             int64_t cols, const float* coefficients, int steps, float eps, void* y, int64_t ldy,
+                             int64_t y_batch_stride, void* workspace, size_t workspace_bytes, hipStream_t stream);
+pbs_status pbs_muon(void* w, pbs_format w_fmt, int64_t ldw, int64_t w_batch_stride, void* momentum, pbs_format m_fmt, int64_t ldm,
+                    int64_t m_batch_stride, const void* grad, pbs_format g_fmt, int grad_transposed, int64_t ldg,
+                    int64_t g_batch_stride, int64_t batch, int64_t rows, int64_t cols, double beta, int nesterov, float lr,
+                    const float* lr_factor, float weight_decay, float scale, const float* coefficients, int steps, float eps,
+                    void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------------------
  * pbs_quantized_bytes [host]: bytes of the codes and of the block scales

@@ -28,6 +28,7 @@ __all__ = [
     "pbs_layernorm", "pbs_layernorm_grad_bytes", "pbs_layernorm_grad", "pbs_linear_loss_bytes",
     "pbs_linear_xent", "pbs_linear_xent_grad", "pbs_linear_distill", "pbs_linear_distill_grad",
     "pbs_qk_norm_rope", "pbs_qk_norm_rope_grad_bytes", "pbs_qk_norm_rope_grad",
+    "pbs_orthogonalize_bytes", "pbs_orthogonalize", "pbs_muon",
     "pbs_last_error", "pbs_version",
 ]
 
@@ -44,7 +45,7 @@ lib_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpbs.so")
 
 _c = ctypes
 _vp, _i64, _i32, _u64, _f32 = _c.c_void_p, _c.c_int64, _c.c_int, _c.c_uint64, _c.c_float
-_i64p = _c.POINTER(_c.c_int64)
+_i64p, _f32p = _c.POINTER(_c.c_int64), _c.POINTER(_c.c_float)
 
 # name -> (restype, argtypes); mirrors include/pbs.h
 SIGNATURES = {
@@ -82,6 +83,11 @@ SIGNATURES = {
     "pbs_qk_norm_rope_grad": (_i32, [_vp, _i64p, _vp, _i64p, _vp, _i64p, _i32, _vp, _i64p, _i64, _vp, _i64p, _i64, _i32,
                                      _i64, _i64, _i64, _vp, _vp, _i32, _i32, _f32, _vp, _i64, _vp, _i64, _i32, _vp,
                                      _i64p, _vp, _i64p, _vp, _i64p, _vp, _vp, _vp, _vp, _c.c_size_t, _vp]),
+    "pbs_orthogonalize_bytes": (_i32, [_i64, _i64, _i64, _c.POINTER(_c.c_size_t)]),
+    "pbs_orthogonalize": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _i64, _f32p, _i32, _f32, _vp, _i64, _i64, _vp,
+                                 _c.c_size_t, _vp]),
+    "pbs_muon": (_i32, [_vp, _i32, _i64, _i64, _vp, _i32, _i64, _i64, _vp, _i32, _i32, _i64, _i64, _i64, _i64, _i64,
+                        _c.c_double, _i32, _f32, _vp, _f32, _f32, _f32p, _i32, _f32, _vp, _c.c_size_t, _vp]),
     "pbs_quantized_bytes": (_i32, [_i32, _i64, _i64, _i32, _c.POINTER(_c.c_size_t),
                                    _c.POINTER(_c.c_size_t)]),
     "pbs_last_error": (_c.c_char_p, []),
@@ -286,6 +292,37 @@ def pbs_qk_norm_rope_grad(dq, dq_strides, dk, dk_strides, dv, dv_strides, y_fmt,
         _ptr(dq_out), _strides(dq_out_strides), _ptr(dk_out), _strides(dk_out_strides), _ptr(dv_out),
         _strides(dv_out_strides), _ptr(dq_weight), _ptr(dk_weight), _ptr(amax_out), _ptr(workspace), workspace_bytes,
         _stream(stream)))
+
+
+def _triples(coefficients):
+    """Steps' (a, b, c) as the C side takes them, and their number."""
+    flat = [float(v) for step in coefficients for v in step]
+    if len(flat) != 3 * len(coefficients):
+        raise ValueError("coefficients: want (a, b, c) for each step")
+    return (_f32 * max(len(flat), 1))(*flat), len(coefficients)
+
+
+def pbs_orthogonalize_bytes(batch, rows, cols):
+    n = _c.c_size_t(0)
+    _check(lib().pbs_orthogonalize_bytes(batch, rows, cols, _c.byref(n)))
+    return n.value
+
+
+def pbs_orthogonalize(x, x_fmt, ldx, x_batch_stride, batch, rows, cols, coefficients, eps, y, ldy, y_batch_stride, workspace,
+                      workspace_bytes, stream=None):
+    coef, steps = _triples(coefficients)
+    _check(lib().pbs_orthogonalize(_ptr(x), x_fmt, ldx, x_batch_stride, batch, rows, cols, coef, steps, eps, _ptr(y), ldy,
+                                   y_batch_stride, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def pbs_muon(w, w_fmt, ldw, w_batch_stride, momentum, m_fmt, ldm, m_batch_stride, grad, g_fmt, grad_transposed, ldg,
+             g_batch_stride, batch, rows, cols, beta, nesterov, lr, lr_factor, weight_decay, scale, coefficients, eps,
+             workspace, workspace_bytes, stream=None):
+    coef, steps = _triples(coefficients)
+    _check(lib().pbs_muon(_ptr(w), w_fmt, ldw, w_batch_stride, _ptr(momentum), m_fmt, ldm, m_batch_stride, _ptr(grad), g_fmt,
+                          int(grad_transposed), ldg, g_batch_stride, batch, rows, cols, beta, int(nesterov), lr,
+                          _ptr(lr_factor), weight_decay, scale, coef, steps, eps, _ptr(workspace), workspace_bytes,
+                          _stream(stream)))
 
 
 def pbs_quantized_bytes(recipe, rows, cols, weight_2d):

@@ -31,7 +31,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libpbs.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.hip", "amax.hip", "cast.hip", "gemm.hip", "gemm_blk.hip", "norm.hip", "head.hip",
-           "qk.hip"]
+           "qk.hip", "muon.hip"]
 EXTRA_FLAGS = {"gemm_blk.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 ARCH = "gfx950"
 

@@ -1,0 +1,910 @@
+// Orthogonalisation of a matrix by Newton-Schulz products and Muon's update of a
+// weight with it.  With m = min(rows, cols), n the other one, X taken as [m, n]:
+//
+//   M' = beta M + (1 - beta) G,  U = beta M' + (1 - beta) G (Nesterov) or M'
+//   X = U / (||U||_F + eps)
+//   A = X X^T,  P = b A + c A^2,  X' = a X + P X         for each step (a, b, c)
+//   W' = (1 - lr decay) W - lr scale X
+//
+// Number formats.  The products run on fp16 operands and add in fp32.  Every X,
+// A and P is bounded (the singular values of X start within [0, 1] and the
+// steps' polynomials keep them within a bound that the host computes), so one
+// power of two for the whole call puts them into fp16's range, whose three
+// more bits of mantissa than bf16's make the roundings 8 times smaller at the same
+// rate.  What remains of them:
+//  * Small singular directions grow by `a` a step next to large ones that stay
+//    near 1, and with them what X's rounding adds.  X is therefore kept as a pair,
+//    hi + lo 2^-11, of which the sum enters a X and only hi the products: an error
+//    of hi there is multiplied by P, which is small but in the large directions.
+//    A matrix of eight directions 30 times above its noise: error 4% of the
+//    result with hi alone, 0.08% with the pair (bf16 alone: 34%).
+//  * P's diagonal, near b + c, is much larger than the rest of its row and
+//    cancels against a: it is kept apart in fp32 and joins a in a X (a random
+//    matrix 0.17% -> 0.05 to 0.1%).
+// The result is bf16's own rounding (0.17%) or less away from 64 bits.
+//
+// A and P are symmetric: the tiles on and below the diagonal are formed and
+// stored twice, once transposed.
+#include "device.hpp"
+#include "gemm_common.hpp"
+#include "host.hpp"
+#include "mfma_tile.hpp"
+
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+namespace pbs {
+
+typedef _Float16 f16_t;
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+
+constexpr float NS_LO = 2048.0f;           // a pair's lo is held times this
+constexpr int NS_PART = 1024;              // most partial sums of a matrix's norm
+
+// ---------------------------------------------------------------------------
+// Momentum, norm and the first X
+// ---------------------------------------------------------------------------
+struct MuonIn {
+  const void* g;           // gradient, or the matrix to orthogonalise
+  void* m;                 // momentum; may be null: U = G
+  int64_t ldg, sg, ldm, sm;// row and batch strides, elements
+  int rows, cols;          // of the weight
+  int g_bf16, m_bf16, g_transposed, nesterov;
+  float beta, one_less;    // one_less: 1 - beta
+  int mp, np, tall;        // X: [mp][np], the matrix transposed if tall
+  int parts;
+  double* part;            // [batch][parts]
+  float eps, scale;
+  uint8_t *hi, *lo;        // [batch][mp][np] fp16
+};
+
+template <typename T> __device__ __forceinline__ float muon_get(const void* p, int64_t i);
+template <> __device__ __forceinline__ float muon_get<bf16_t>(const void* p, int64_t i) { return bf16_to_float(((const bf16_t*)p)[i]); }
+template <> __device__ __forceinline__ float muon_get<float>(const void* p, int64_t i) { return ((const float*)p)[i]; }
+
+// Four values of a row from column c on; those at or past cols are 0.
+template <typename T>
+__device__ __forceinline__ float4 muon_get4(const T* row, int c, int cols, bool vec) {
+  if (vec && c + 4 <= cols) {
+    if constexpr (sizeof(T) == 4) return *(const float4*)(row + c);
+    else {
+      const uint2 u = *(const uint2*)(row + c);
+      return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                         __uint_as_float(u.y & 0xFFFF0000u));
+    }
+  }
+  float4 v;
+  v.x = c < cols ? muon_get<T>(row, c) : 0.0f;
+  v.y = c + 1 < cols ? muon_get<T>(row, c + 1) : 0.0f;
+  v.z = c + 2 < cols ? muon_get<T>(row, c + 2) : 0.0f;
+  v.w = c + 3 < cols ? muon_get<T>(row, c + 3) : 0.0f;
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ void muon_put4(T* row, int c, int cols, bool vec, float4 v) {
+  if constexpr (sizeof(T) == 4) {
+    if (vec && c + 4 <= cols) { *(float4*)(row + c) = v; return; }
+    if (c < cols) row[c] = v.x;
+    if (c + 1 < cols) row[c + 1] = v.y;
+    if (c + 2 < cols) row[c + 2] = v.z;
+    if (c + 3 < cols) row[c + 3] = v.w;
+  } else {
+    const uint32_t lo = pk_bf16(v.x, v.y), hi = pk_bf16(v.z, v.w);
+    if (vec && c + 4 <= cols) { *(uint2*)(row + c) = make_uint2(lo, hi); return; }
+    if (c < cols) row[c] = (bf16_t)lo;
+    if (c + 1 < cols) row[c + 1] = (bf16_t)(lo >> 16);
+    if (c + 2 < cols) row[c + 2] = (bf16_t)hi;
+    if (c + 3 < cols) row[c + 3] = (bf16_t)(hi >> 16);
+  }
+}
+template <typename T>
+__device__ __forceinline__ bool muon_vec(const void* p, int64_t ld, int64_t batch_stride) {
+  return (((uintptr_t)p & (4 * sizeof(T) - 1)) | (uint64_t)(ld & 3) | (uint64_t)(batch_stride & 3)) == 0;
+}
+
+// A 64 x 64 tile of U: thread t holds four values of the rows t / 16 + 16 k
+// from column 4 (t % 16) on.  m4: M', for the momentum's store.
+constexpr int MT = 64, MPITCH = 65;
+template <typename TG, typename TM>
+struct MuonTile {
+  float4 u[4], m4[4];
+  __device__ __forceinline__ void load(const MuonIn& a, int batch, int r0, int c0, float (*lds)[MPITCH]) {
+    const int t = threadIdx.x, tr = t >> 4, tc = 4 * (t & 15);
+    const TG* g = (const TG*)a.g + batch * a.sg;
+    const bool vg = muon_vec<TG>(a.g, a.ldg, a.sg);
+    float4 gv[4];
+    if (a.g_transposed) {
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = tr + 16 * k;
+        const float4 v = c0 + c < a.cols ? muon_get4<TG>(g + (c0 + c) * a.ldg, r0 + tc, a.rows, vg) : make_float4(0, 0, 0, 0);
+        lds[tc][c] = v.x; lds[tc + 1][c] = v.y; lds[tc + 2][c] = v.z; lds[tc + 3][c] = v.w;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float* p = &lds[tr + 16 * k][tc];
+        gv[k] = make_float4(p[0], p[1], p[2], p[3]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = r0 + tr + 16 * k;
+        gv[k] = r < a.rows ? muon_get4<TG>(g + r * a.ldg, c0 + tc, a.cols, vg) : make_float4(0, 0, 0, 0);
+      }
+    }
+    if (!a.m) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) u[k] = gv[k];
+      return;
+    }
+    const TM* m = (const TM*)a.m + batch * a.sm;
+    const bool vm = muon_vec<TM>(a.m, a.ldm, a.sm);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = r0 + tr + 16 * k;
+      const float4 o = r < a.rows ? muon_get4<TM>(m + r * a.ldm, c0 + tc, a.cols, vm) : make_float4(0, 0, 0, 0);
+      const float4 s = make_float4(a.one_less * gv[k].x, a.one_less * gv[k].y, a.one_less * gv[k].z, a.one_less * gv[k].w);
+      float4 n;
+      n.x = __builtin_fmaf(a.beta, o.x, s.x); n.y = __builtin_fmaf(a.beta, o.y, s.y);
+      n.z = __builtin_fmaf(a.beta, o.z, s.z); n.w = __builtin_fmaf(a.beta, o.w, s.w);
+      m4[k] = n;
+      if (a.nesterov) {
+        n.x = __builtin_fmaf(a.beta, n.x, s.x); n.y = __builtin_fmaf(a.beta, n.y, s.y);
+        n.z = __builtin_fmaf(a.beta, n.z, s.z); n.w = __builtin_fmaf(a.beta, n.w, s.w);
+      }
+      u[k] = n;
+    }
+  }
+};
+
+__device__ __forceinline__ double wave_sum_d(double v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// Partial sums of U's squares in 64 bits (gradients of 1e-25 or 1e25 square past
+// fp32), a fixed set of tiles a workgroup.
+template <typename TG, typename TM>
+__global__ __launch_bounds__(256) void muon_norm_kernel(MuonIn a) {
+  __shared__ float lds[MT][MPITCH];
+  __shared__ double sums[4];
+  const int tc = (a.cols + MT - 1) / MT, tr = (a.rows + MT - 1) / MT;
+  double s = 0.0;
+  for (int64_t i = blockIdx.x; i < (int64_t)tc * tr; i += a.parts) {
+    MuonTile<TG, TM> t;
+    t.load(a, blockIdx.y, (int)(i / tc) * MT, (int)(i % tc) * MT, lds);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const double x = t.u[k].x, y = t.u[k].y, z = t.u[k].z, w = t.u[k].w;
+      s += x * x + y * y + (z * z + w * w);
+    }
+  }
+  s = wave_sum_d(s);
+  if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) a.part[(int64_t)blockIdx.y * a.parts + blockIdx.x] = sums[0] + sums[1] + (sums[2] + sums[3]);
+}
+
+// x as hi + lo 2^-11 in fp16.
+__device__ __forceinline__ void ns_split(float x, f16_t& hi, f16_t& lo) {
+  hi = (f16_t)x;
+  lo = (f16_t)((x - (float)hi) * NS_LO);
+}
+
+// The momentum's store and the first X, zeros past the matrix's end.
+template <typename TG, typename TM>
+__global__ __launch_bounds__(256) void muon_start_kernel(MuonIn a) {
+  __shared__ float lds[MT][MPITCH];
+  __shared__ double sums[4];
+  const int t = threadIdx.x, tr = t >> 4, tc = 4 * (t & 15);
+  const int batch = blockIdx.y;
+  double s = 0.0;
+  for (int i = t; i < a.parts; i += 256) s += a.part[(int64_t)batch * a.parts + i];
+  s = wave_sum_d(s);
+  if ((t & 63) == 0) sums[t >> 6] = s;
+  __syncthreads();
+  const double norm = sqrt(sums[0] + sums[1] + (sums[2] + sums[3])) + (double)a.eps;
+  // a matrix of zeros stays one; one with an infinity or a NaN becomes NaN
+  const double f = norm == 0.0 ? 0.0 : norm < __builtin_inf() ? (double)a.scale / norm : __builtin_nan("");
+  const int wr = a.tall ? a.np : a.mp, wc = a.tall ? a.mp : a.np;           // the weight's padded shape
+  const int tiles_c = wc / MT;
+  const int r0 = (int)(blockIdx.x / tiles_c) * MT, c0 = (int)(blockIdx.x % tiles_c) * MT;
+  if (r0 >= wr) return;
+  MuonTile<TG, TM> u;
+  u.load(a, batch, r0, c0, lds);
+  if (a.m) {
+    TM* m = (TM*)a.m + batch * a.sm;
+    const bool vm = muon_vec<TM>(a.m, a.ldm, a.sm);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = r0 + tr + 16 * k;
+      if (r < a.rows) muon_put4<TM>(m + r * a.ldm, c0 + tc, a.cols, vm, u.m4[k]);
+    }
+  }
+  if (a.tall) {
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float* p = &lds[tr + 16 * k][tc];
+      p[0] = u.u[k].x; p[1] = u.u[k].y; p[2] = u.u[k].z; p[3] = u.u[k].w;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      u.u[k] = make_float4(lds[tc][tr + 16 * k], lds[tc + 1][tr + 16 * k], lds[tc + 2][tr + 16 * k], lds[tc + 3][tr + 16 * k]);
+  }
+  const int x0 = a.tall ? c0 : r0, y0 = a.tall ? r0 : c0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t at = ((int64_t)batch * a.mp + x0 + tr + 16 * k) * a.np + y0 + tc;
+    f16x4 h, l;
+    const float v[4] = {(float)(u.u[k].x * f), (float)(u.u[k].y * f), (float)(u.u[k].z * f), (float)(u.u[k].w * f)};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f16_t hh, ll;
+      ns_split(v[e], hh, ll);
+      h[e] = hh;
+      l[e] = ll;
+    }
+    *(f16x4*)((f16_t*)a.hi + at) = h;
+    *(f16x4*)((f16_t*)a.lo + at) = l;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The products
+// ---------------------------------------------------------------------------
+enum { NS_GRAM = 0, NS_POLY = 1, NS_STEP = 2, NS_LAST = 3 };
+
+struct NsArgs {
+  const uint8_t *hi, *lo;  // X
+  uint8_t *hi2, *lo2;      // the next X
+  uint8_t *gram, *poly;    // A, P: [batch][mp][mp] fp16
+  float* diag;             // [batch][mp]: P's diagonal
+  int mp, np, batch;
+  int tiles_m, tiles_n, per; // tiles of a matrix
+  float a, b, c;
+  float inv;               // 1 / the power of two that X, A and P are held times
+  // the last step: to y, or into the weight
+  void* w;
+  int64_t ldw, sw;
+  int rows, cols;          // of the weight
+  int w_bf16, tall, update;
+  float lr, decay, scale;  // W' = (1 - lr decay) W - lr scale X
+  const float* lr_by;      // may be null: 1
+};
+
+// A tile has 64 T x 64 T outputs; wave (wm, wn) holds its 32 x 32 tiles
+// (2 i + wm, 2 j + wn), i, j < T.
+template <int T> constexpr int ns_pitch() { return 128 * T + 16; }      // staged rows of fp16
+template <int T> constexpr int ns_pitch4() { return 256 * T + 16; }     // and of fp32
+template <int T> constexpr int ns_smem(int mode) {
+  return cmax(5 * tile_bytes<T>(), mode == NS_GRAM   ? 64 * T * ns_pitch<T>()
+                                   : mode == NS_LAST ? 128 * ns_pitch<T>() + 64 * ns_pitch4<T>()
+                                                     : 256 * ns_pitch<T>());
+}
+
+template <int T>
+struct NsHalf {
+  i32x4 x[T][2];
+};
+template <int LD, int T> constexpr int ns_reads() { return LD == KMAJ ? 2 * T : 4 * T; }
+
+// LDS read d of half H of a stage.  K-major: the row's chunk 4 H + 2 part + lg
+// under its swizzle key, which for row 32 (2 i + w) + lr is the lane's XOR
+// 2 (2 i + w).  MN-major: the transposing read of 4 K rows.
+template <int H, int LD, int T>
+__device__ __forceinline__ void ns_read(NsHalf<T>& f, int d, const uint8_t* base, uint32_t lb) {
+  if (LD == KMAJ) {
+    const int tile = d >> 1, part = d & 1;
+    f.x[tile][part] = *(const i32x4*)(base + tile * 8192 + (lb ^ (uint32_t)(((4 * H) ^ ((4 * tile) & 7)) << 4) ^
+                                                            (uint32_t)(part << 5)));
+  } else {
+    const int tile = d >> 2, s = (d >> 1) & 1, q = d & 1;
+    const i16x4 v = read_lds_tr16(base + (16 * (2 * H + s) + 4 * q) * (128 * T) + (lb ^ (uint32_t)(128 * tile)));
+    const int2 w2 = __builtin_bit_cast(int2, v);
+    if (q == 0) {
+      f.x[tile][s].x = w2.x;
+      f.x[tile][s].y = w2.y;
+    } else {
+      f.x[tile][s].z = w2.x;
+      f.x[tile][s].w = w2.y;
+    }
+  }
+}
+
+// Tile `id` of the lower triangle of tiles: rows walked four together, so that
+// neighbours in time share operand rows.
+__device__ __forceinline__ void ns_triangle(int id, int n, int& row, int& col) {
+  int g = (int)((sqrtf(4.0f + 32.0f * (float)id) - 2.0f) * 0.0625f);      // 8 g^2 + 2 g tiles lie ahead of group g
+  while (g > 0 && 8 * g * g + 2 * g > id) --g;
+  while (8 * (g + 1) * (g + 1) + 2 * (g + 1) <= id) ++g;
+  int in = id - 8 * g * g - 2 * g;
+  const int have = n - 4 * g < 4 ? n - 4 * g : 4;
+  if (in < 4 * g * have) {
+    row = 4 * g + in % have;
+    col = in / have;
+    return;
+  }
+  in -= 4 * g * have;
+  int c = 0;
+  while (in >= have - c) in -= have - c++;
+  col = 4 * g + c;
+  row = col + in;
+}
+
+template <int T, int MODE>
+__global__ __launch_bounds__(256, T >= 3 ? 1 : 2) void ns_product_kernel(NsArgs g) {
+  __shared__ __align__(16) uint8_t smem[ns_smem<T>(MODE)];
+  constexpr int LDA = MODE >= NS_STEP ? MNMAJ : KMAJ;
+  constexpr int TILE = 64 * T;
+  const int t = threadIdx.x, lane = t & 63;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = w >> 1, wn = w & 1;
+
+  // XCD b % 8 takes a contiguous range of the matrices' tiles
+  const int total = g.per * g.batch;
+  const int x = (int)blockIdx.x % NXCD, share = total / NXCD, left = total % NXCD;
+  const int id = x * share + (x < left ? x : left) + (int)blockIdx.x / NXCD;
+  const int mat = id / g.per;
+  int tm, tn;
+  if constexpr (MODE >= NS_STEP) {
+    const int in = id - mat * g.per, group = GROUP_M * g.tiles_n, q = in / group;
+    const int gm = g.tiles_m - q * GROUP_M < GROUP_M ? g.tiles_m - q * GROUP_M : GROUP_M, r = in - q * group;
+    tm = q * GROUP_M + r % gm;
+    tn = r / gm;
+  } else {
+    ns_triangle(id - mat * g.per, g.tiles_n, tn, tm);
+  }
+  const int m0 = tm * TILE, n0 = tn * TILE;
+  const int64_t xs = (int64_t)mat * g.mp * g.np, ps = (int64_t)mat * g.mp * g.mp;    // a matrix's X; its A and P
+  // M, the results' contiguous axis, and the contraction's stages
+  const int M = MODE >= NS_STEP ? g.np : g.mp, nk = (MODE == NS_GRAM ? g.np : g.mp) / 64;
+
+  auto tileA = [&](int kt) { return smem + (kt & 1) * tile_bytes<T>(); };
+  auto tileB = [&](int kt) { return smem + 2 * tile_bytes<T>() + kt % 3 * tile_bytes<T>(); };
+
+  f32x16 acc[T][T];
+#pragma unroll
+  for (int i = 0; i < T; ++i)
+#pragma unroll
+    for (int j = 0; j < T; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+  typename std::conditional<LDA == KMAJ, KLoad<T>, MnLoad<T == 3 ? 4 : T>>::type la;
+  KLoad<T> lb;
+  if constexpr (MODE == NS_GRAM) {
+    la.init(g.hi + 2 * xs, (int64_t)g.np * 2, m0, g.mp, w);
+    lb.init(g.hi + 2 * xs, (int64_t)g.np * 2, n0, g.mp, w);
+  } else if constexpr (MODE == NS_POLY) {
+    la.init(g.gram + 2 * ps, (int64_t)g.mp * 2, m0, g.mp, w);
+    lb.init(g.gram + 2 * ps, (int64_t)g.mp * 2, n0, g.mp, w);
+  } else {
+    la.init(g.hi + 2 * xs, (int64_t)g.np * 2, m0, g.np, g.mp, w);
+    lb.init(g.poly + 2 * ps, (int64_t)g.mp * 2, n0, g.mp, w);
+  }
+
+  const int lr = lane & 31, lg = lane >> 5;
+  const int jj = (lr & 15) >> 2;
+  const uint32_t kb = (uint32_t)(lr * 128 + ((lg ^ swz_key(lr)) << 4));
+  const uint32_t fba = LDA == KMAJ ? kb ^ (uint32_t)(wm << 5)
+                                   : (uint32_t)((8 * lg + jj) * (128 * T) + ((64 * jj) ^ (64 * wm)) + 32 * (lr >> 4) +
+                                                16 * ((lr & 3) >> 1) + 8 * (lr & 1));
+  const uint32_t fbb = kb ^ (uint32_t)(wn << 5);
+  const int offA = LDA == KMAJ ? wm * 4096 : 0, offB = wn * 4096;
+
+  constexpr int NMFMA = 2 * T * T, OVER = NMFMA * 3 / 4, NL = 2 * T;
+  constexpr int RA = ns_reads<LDA, T>(), RB = ns_reads<KMAJ, T>();
+  NsHalf<T> a0, a1, b0, b1;
+  auto load_a = [&](int kt, int v) { la.load(kt, 0, tileA(kt), w, v); };
+  auto load_b = [&](int kt, int v) { lb.load(kt, 0, tileB(kt), w, v); };
+  auto mfma = [&](const NsHalf<T>& a, const NsHalf<T>& b, int m) {
+    const int s = m / (T * T), i = (m / T) % T, j = m % T;
+    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a.x[i][s]),
+                                                       __builtin_bit_cast(f16x8, b.x[j][s]), acc[i][j], 0, 0, 0);
+  };
+
+#pragma unroll
+  for (int v = 0; v < NL; ++v) load_a(0, v);
+#pragma unroll
+  for (int v = 0; v < NL; ++v) load_b(0, v);
+  if (nk > 1) {
+#pragma unroll
+    for (int v = 0; v < NL; ++v) load_a(1, v);
+#pragma unroll
+    for (int v = 0; v < NL; ++v) load_b(1, v);
+    stage_barrier<2 * NL>();
+  } else {
+    stage_barrier<0>();
+  }
+#pragma unroll
+  for (int d = 0; d < RA; ++d) ns_read<0, LDA, T>(a0, d, tileA(0) + offA, fba);
+#pragma unroll
+  for (int d = 0; d < RB; ++d) ns_read<0, KMAJ, T>(b0, d, tileB(0) + offB, fbb);
+
+  // A's stages go through two LDS buffers, B's through three, so that the loads
+  // of stage kt + 2 spread over the whole of stage kt; see head.hip's products,
+  // whose schedule this is.
+  auto body = [&](int kt, auto issue_c, auto next_c) {
+    constexpr bool ISSUE = decltype(issue_c)::value;
+    constexpr bool NEXT = decltype(next_c)::value;
+    const uint8_t* curA = tileA(kt) + offA;
+    const uint8_t* curB = tileB(kt) + offB;
+    const uint8_t* nxtA = tileA(kt + 1) + offA;
+    const uint8_t* nxtB = tileB(kt + 1) + offB;
+#pragma unroll
+    for (int m = 0; m < NMFMA; ++m) {
+      mfma(a0, b0, m);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int d = part_lo(RA + RB, OVER, m); d < part_hi(RA + RB, OVER, m); ++d) {
+        if (d < RA) ns_read<1, LDA, T>(a1, d, curA, fba);
+        else ns_read<1, KMAJ, T>(b1, d - RA, curB, fbb);
+      }
+      if (ISSUE) {
+#pragma unroll
+        for (int v = part_lo(NL, NMFMA, m); v < part_hi(NL, NMFMA, m); ++v) load_b(kt + 2, v);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    stage_barrier<ISSUE ? NL : 0>();
+    constexpr int NDS = NEXT ? RA + RB : 0;
+#pragma unroll
+    for (int m = 0; m < NMFMA; ++m) {
+      mfma(a1, b1, m);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int d = part_lo(NDS, OVER, m); d < part_hi(NDS, OVER, m); ++d) {
+        if (d < RA) ns_read<0, LDA, T>(a0, d, nxtA, fba);
+        else ns_read<0, KMAJ, T>(b0, d - RA, nxtB, fbb);
+      }
+      if (ISSUE) {
+#pragma unroll
+        for (int v = part_lo(NL, NMFMA, m); v < part_hi(NL, NMFMA, m); ++v) load_a(kt + 2, v);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  using T_ = std::integral_constant<bool, true>;
+  using F_ = std::integral_constant<bool, false>;
+  for (int kt = 0; kt < nk - 2; ++kt) body(kt, T_{}, T_{});
+  if (nk >= 2) body(nk - 2, F_{}, T_{});
+  body(nk - 1, F_{}, F_{});
+
+  // Every LDS read of the loop finished before its last barrier and no load is
+  // in flight.  acc[i][j][4 q + r] is row n0 + 32 (2 j + wn) + lr, column m0 + 32
+  // (2 i + wm) + 8 q + 4 lg + r.  The results are staged 64 rows at a time (those
+  // of one j) and stored from there in whole rows.
+  constexpr int PITCH = ns_pitch<T>(), PITCH4 = ns_pitch4<T>();
+  constexpr int CHUNKS = 8 * T, PER = 2 * T;                  // 16-byte chunks a row, and a thread in 64 rows
+  const int srow = 32 * wn + lr;                              // the lane's row of a pass
+  auto scol = [&](int i, int q) { return 32 * (2 * i + wm) + 8 * q + 4 * lg; };
+  // 64 staged rows from row r0 of an fp16 matrix with ld columns
+  auto store_rows = [&](const uint8_t* from, uint8_t* to, int r0, int rows, int64_t ld) {
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int at = t + 256 * k, r = at / CHUNKS, c = at % CHUNKS;
+      const uint4 v = *(const uint4*)(from + r * PITCH + 16 * c);
+      if (r0 + r < rows && m0 + 8 * c < M) *(uint4*)(to + 2 * ((int64_t)(r0 + r) * ld + m0 + 8 * c)) = v;
+    }
+  };
+  // and transposed: 8 rows of 16 columns at a time, by the transposing read
+  auto store_transposed = [&](const uint8_t* from, uint8_t* to, int r0) {
+    const int gq = lane >> 4, li = lane & 15;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int block = w + 4 * k, c0 = 16 * (block >> 1), o = 8 * (4 * (block & 1) + gq);
+      const uint8_t* p = from + (o + (li >> 2)) * PITCH + 2 * (c0 + 4 * (li & 3));
+      const int2 lo = __builtin_bit_cast(int2, read_lds_tr16(p));
+      const int2 hi = __builtin_bit_cast(int2, read_lds_tr16(p + 4 * PITCH));
+      if (m0 + c0 + li < g.mp && r0 + o < g.mp)
+        *(int4*)(to + 2 * ((int64_t)(m0 + c0 + li) * g.mp + r0 + o)) = make_int4(lo.x, lo.y, hi.x, hi.y);
+    }
+  };
+
+  if constexpr (MODE == NS_GRAM) {
+#pragma unroll
+    for (int j = 0; j < T; ++j)
+#pragma unroll
+      for (int i = 0; i < T; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          f16x4 v;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] = (f16_t)(acc[i][j][4 * q + r] * g.inv);
+          *(f16x4*)(smem + (64 * j + srow) * PITCH + 2 * scol(i, q)) = v;
+        }
+    __syncthreads();
+    uint8_t* to = g.gram + 2 * ps;
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      store_rows(smem + 64 * j * PITCH, to, n0 + 64 * j, g.mp, g.mp);
+      if (tm != tn) store_transposed(smem + 64 * j * PITCH, to, n0 + 64 * j);
+    }
+  } else {
+    // the sources of 64 rows: A, or X's pair, a pass ahead in registers
+    const uint8_t* src = MODE == NS_POLY ? g.gram + 2 * ps : g.hi + 2 * xs;
+    const uint8_t* src2 = g.lo + 2 * xs;
+    u32x4 v1[PER], v2[MODE >= NS_STEP ? PER : 1];
+    auto fetch = [&](int j) {
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        const int at = t + 256 * k;
+        const int r = n0 + 64 * j + at / CHUNKS, c = m0 + 8 * (at % CHUNKS);
+        const int64_t o = 2 * ((int64_t)(r < g.mp ? r : g.mp - 1) * M + (c < M ? c : M - 8));
+        v1[k] = *(const u32x4*)(src + o);
+        if constexpr (MODE >= NS_STEP) v2[k] = *(const u32x4*)(src2 + o);
+      }
+    };
+    constexpr int AREA = 64 * PITCH;
+    fetch(0);
+    float lr_now = 0.0f;
+    if constexpr (MODE == NS_LAST) lr_now = g.lr_by ? g.lr * *g.lr_by : g.lr;
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      uint8_t* s1 = smem + (MODE == NS_LAST ? 0 : (j & 1) * 2 * AREA);
+      uint8_t* s2 = s1 + AREA;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        const int at = t + 256 * k, o = at / CHUNKS * PITCH + 16 * (at % CHUNKS);
+        *(u32x4*)(s1 + o) = v1[k];
+        if constexpr (MODE >= NS_STEP) *(u32x4*)(s2 + o) = v2[k];
+      }
+      if (j + 1 < T) fetch(j + 1);
+      const int row = n0 + 64 * j + srow;
+      float own = 0.0f;                                       // a + P's diagonal
+      if constexpr (MODE >= NS_STEP) own = g.a + g.diag[(int64_t)mat * g.mp + (row < g.mp ? row : g.mp - 1)];
+      // P's diagonal: where the lane's row meets the tile's columns
+      const int dcol = MODE == NS_POLY && tm == tn ? row - m0 : -64 * T;
+      float dval = 0.0f;
+      bool has = false;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < T; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          f16x4* p1 = (f16x4*)(s1 + srow * PITCH + 2 * scol(i, q));
+          const f16x4 h = *p1;
+          float v[4];
+          if constexpr (MODE == NS_POLY) {
+            const int at = dcol - scol(i, q);
+            f16x4 o;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              v[r] = g.b * (float)h[r] + g.c * (acc[i][j][4 * q + r] * g.inv);
+              dval = at == r ? v[r] : dval;
+              o[r] = (f16_t)(at == r ? 0.0f : v[r]);
+            }
+            has = has || (at >= 0 && at < 4);
+            *p1 = o;
+          } else {
+            f16x4* p2 = (f16x4*)(s2 + srow * PITCH + 2 * scol(i, q));
+            const f16x4 l = *p2;
+            f16x4 oh, ol;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              v[r] = own * ((float)h[r] + (float)l[r] * (1.0f / NS_LO)) + acc[i][j][4 * q + r] * g.inv;
+              f16_t hh, ll;
+              ns_split(v[r], hh, ll);
+              oh[r] = hh;
+              ol[r] = ll;
+            }
+            if constexpr (MODE == NS_STEP) {
+              *p1 = oh;
+              *p2 = ol;
+            } else {
+              *(float4*)(smem + 2 * AREA + srow * PITCH4 + 4 * scol(i, q)) =
+                  make_float4(v[0] * g.inv, v[1] * g.inv, v[2] * g.inv, v[3] * g.inv);
+            }
+          }
+        }
+      if (MODE == NS_POLY && has && row < g.mp) g.diag[(int64_t)mat * g.mp + row] = dval * g.inv;
+      __syncthreads();
+      const int r0 = n0 + 64 * j;
+      if constexpr (MODE == NS_POLY) {
+        store_rows(s1, g.poly + 2 * ps, r0, g.mp, g.mp);
+        if (tm != tn) store_transposed(s1, g.poly + 2 * ps, r0);
+      } else if constexpr (MODE == NS_STEP) {
+        store_rows(s1, g.hi2 + 2 * xs, r0, g.mp, g.np);
+        store_rows(s2, g.lo2 + 2 * xs, r0, g.mp, g.np);
+      } else {
+        // four values of a row of the weight at a time; a tall weight's rows are the staged columns
+        const float* f = (const float*)(smem + 2 * AREA);
+        constexpr int FP = PITCH4 / 4;
+        const float keep = 1.0f - lr_now * g.decay, step = lr_now * g.scale;
+        const bool vec = g.w_bf16 ? muon_vec<bf16_t>(g.w, g.ldw, g.sw) : muon_vec<float>(g.w, g.ldw, g.sw);
+        constexpr int QUADS = 16 * T;                          // of a staged row; 16 of a staged column
+#pragma unroll 2
+        for (int k = 0; k < 64 * QUADS / 256; ++k) {
+          const int at = t + 256 * k;
+          int wr, wc;
+          float4 v;
+          if (g.tall) {
+            const int c = at >> 4, r = 4 * (at & 15);
+            v = make_float4(f[r * FP + c], f[(r + 1) * FP + c], f[(r + 2) * FP + c], f[(r + 3) * FP + c]);
+            wr = m0 + c;
+            wc = r0 + r;
+          } else {
+            const int r = at / QUADS, c = 4 * (at % QUADS);
+            v = *(const float4*)(f + r * FP + c);
+            wr = r0 + r;
+            wc = m0 + c;
+          }
+          if (wr >= g.rows || wc >= g.cols) continue;
+          auto put = [&](auto* base) {
+            auto* p = base + mat * g.sw + wr * g.ldw;
+            typedef typename std::remove_reference<decltype(*p)>::type TW;
+            if (g.update) {
+              const float4 o = muon_get4<TW>(p, wc, g.cols, vec);
+              v = make_float4(keep * o.x - step * v.x, keep * o.y - step * v.y, keep * o.z - step * v.z, keep * o.w - step * v.w);
+            }
+            muon_put4<TW>(p, wc, g.cols, vec, v);
+          };
+          if (g.w_bf16) put((bf16_t*)g.w);
+          else put((float*)g.w);
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+struct NsPlan {
+  int64_t mp, np, x, p;                       // padded sides; bytes of a matrix's X (hi or lo) and of its A or P
+  int parts;
+  size_t hi[2], lo[2], gram, poly, diag, part, bytes;
+};
+
+static NsPlan ns_plan(int64_t batch, int64_t rows, int64_t cols) {
+  NsPlan h = {};
+  const int64_t m = std::min(rows, cols), n = std::max(rows, cols);
+  h.mp = ceil_div(m, 64) * 64;
+  h.np = ceil_div(n, 64) * 64;
+  h.x = h.mp * h.np * 2;
+  h.p = h.mp * h.mp * 2;
+  h.parts = (int)std::min<int64_t>(ceil_div(rows, MT) * ceil_div(cols, MT), NS_PART);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  for (int i = 0; i < 2; ++i) {
+    h.hi[i] = take((size_t)(batch * h.x));
+    h.lo[i] = take((size_t)(batch * h.x));
+  }
+  h.gram = take((size_t)(batch * h.p));
+  h.poly = take((size_t)(batch * h.p));
+  h.diag = take((size_t)(batch * h.mp) * 4);
+  h.part = take((size_t)(batch * h.parts) * 8);
+  h.bytes = at;
+  return h;
+}
+
+constexpr int64_t NS_MOST_SIDE = 1 << 20, NS_MOST_SHORT = 32768, NS_MOST_STEPS = 64, NS_MOST_BATCH = 65535;
+
+static pbs_status ns_check_dims(const char* what, int64_t batch, int64_t rows, int64_t cols) {
+  PBS_REQUIRE(batch >= 0 && batch <= NS_MOST_BATCH && rows >= 0 && cols >= 0 && rows <= NS_MOST_SIDE && cols <= NS_MOST_SIDE &&
+                  std::min(rows, cols) <= NS_MOST_SHORT,
+              PBS_ERR_SHAPE, "%s: needs a batch of at most 65535, sides up to 2^20, the shorter up to 32768 (got %lld x %lld x %lld)",
+              what, (long long)batch, (long long)rows, (long long)cols);
+  PBS_REQUIRE(batch * ceil_div(std::max(rows, cols), 64) * ceil_div(std::min(rows, cols), 64) < (1ll << 31), PBS_ERR_SHAPE,
+              "%s: too many values for one call", what);
+  return PBS_OK;
+}
+
+static pbs_status ns_check_matrix(const char* what, const char* name, const void* p, pbs_format fmt, int64_t batch, int64_t rows,
+                                  int64_t cols, int64_t ld, int64_t stride, bool out) {
+  PBS_REQUIRE(fmt == PBS_FMT_BF16 || fmt == PBS_FMT_F32, PBS_ERR_UNSUPPORTED, "%s: %s must be BF16 or F32", what, name);
+  const int64_t most = 1ll << 40;
+  PBS_REQUIRE(ld >= 0 && stride >= 0 && ld <= most && stride <= most, PBS_ERR_SHAPE, "%s: strides of %s must be in [0, 2^40]", what, name);
+  PBS_REQUIRE(p, PBS_ERR_INVALID_ARG, "%s: %s is null", what, name);
+  PBS_REQUIRE(((uintptr_t)p & (fmt == PBS_FMT_BF16 ? 1 : 3)) == 0, PBS_ERR_INVALID_ARG, "%s: %s is not aligned to its elements", what,
+              name);
+  if (out) {
+    // rows apart, matrices apart, or matrices that lie between each other's rows
+    const int64_t ns = std::min(ld, stride), nl = std::max(ld, stride);
+    const bool both = rows > 1 && batch > 1;
+    const bool apart = both ? ns >= cols && nl >= ns * ((ld <= stride ? rows : batch) - 1) + cols
+                            : (rows <= 1 || ld >= cols) && (batch <= 1 || stride >= cols);
+    PBS_REQUIRE(apart, PBS_ERR_SHAPE, "%s: rows of %s overlap", what, name);
+  }
+  return PBS_OK;
+}
+
+// The power of two that X, A and P are held times: the largest up to 2^14 that
+// keeps all of them below fp16's largest value, 65504, with a third to spare for
+// roundings.  top: the largest singular value ahead of each step, at most 1 at
+// first, then the largest |p(s)| for s up to it (1024 points; between them p
+// differs by less than its largest slope times half the step, which is added).
+static pbs_status ns_scale(const char* what, const float* coef, int steps, float* scale) {
+  double top = 1.0, most = 1.0;
+  for (int k = 0; k < steps; ++k) {
+    const double a = coef[3 * k], b = coef[3 * k + 1], c = coef[3 * k + 2];
+    PBS_REQUIRE(std::isfinite(a) && std::isfinite(b) && std::isfinite(c), PBS_ERR_INVALID_ARG, "%s: coefficients of step %d are not finite",
+                what, k);
+    double next = 0.0, poly = 0.0;
+    const double h = top / 1024, t2 = top * top;
+    for (int i = 0; i <= 1024; ++i) {
+      const double s = h * i, s2 = s * s;
+      next = std::max(next, std::fabs(s * (a + s2 * (b + c * s2))));
+      poly = std::max(poly, std::fabs(s2 * (b + c * s2)));
+    }
+    next += 0.5 * h * (std::fabs(a) + 3 * std::fabs(b) * t2 + 5 * std::fabs(c) * t2 * t2);
+    poly += 0.5 * h * (2 * std::fabs(b) * top + 4 * std::fabs(c) * top * t2);
+    most = std::max({most, t2, poly, next});
+    top = next;
+    PBS_REQUIRE(most < 4096.0, PBS_ERR_INVALID_ARG, "%s: the coefficients let singular values grow past fp16's range (step %d)", what, k);
+  }
+  float s = 16384.0f;
+  while (s * most > 49152.0) s *= 0.5f;
+  *scale = s;
+  return PBS_OK;
+}
+
+// A product's tile: the one whose rounds of tiles take least.  A round of 256 x
+// 256 tiles, one a compute unit, is 1; of 192 x 192 ones, one a compute unit, or
+// of 128 x 128 ones, two a compute unit, about 0.6.
+constexpr int NS_CUS = 256;
+static int ns_tile(int64_t mp, int64_t np, int64_t batch, bool symmetric) {
+  int best = 4;
+  double least = 1e30;
+  for (int t = 4; t >= 2; --t) {
+    if (t == 3 && !symmetric) continue;
+    const int64_t a = ceil_div(mp, 64 * t), b = ceil_div(np, 64 * t);
+    const int64_t tiles = batch * (symmetric ? a * (a + 1) / 2 : a * b), slots = t == 2 ? 2 * NS_CUS : NS_CUS;
+    const double cost = (double)ceil_div(tiles, slots) * (t == 4 ? 1.0 : 0.6);
+    if (cost < least - 1e-9) { least = cost; best = t; }
+  }
+  return best;
+}
+
+template <int MODE>
+static void ns_launch(NsArgs g, hipStream_t stream) {
+  constexpr bool SYM = MODE <= NS_POLY;
+  const int t = ns_tile(g.mp, g.np, g.batch, SYM);
+  g.tiles_n = (int)ceil_div(g.mp, 64 * t);
+  g.tiles_m = SYM ? g.tiles_n : (int)ceil_div(g.np, 64 * t);
+  g.per = SYM ? g.tiles_n * (g.tiles_n + 1) / 2 : g.tiles_m * g.tiles_n;
+  const dim3 grid((unsigned)(g.per * g.batch)), block(256);
+  if (t == 4) hipLaunchKernelGGL((ns_product_kernel<4, MODE>), grid, block, 0, stream, g);
+  else if (t == 2) hipLaunchKernelGGL((ns_product_kernel<2, MODE>), grid, block, 0, stream, g);
+  else if constexpr (SYM) hipLaunchKernelGGL((ns_product_kernel<3, MODE>), grid, block, 0, stream, g);
+}
+
+template <typename TG, typename TM>
+static void muon_begin(const MuonIn& in, int64_t batch, hipStream_t stream) {
+  hipLaunchKernelGGL((muon_norm_kernel<TG, TM>), dim3((unsigned)in.parts, (unsigned)batch), dim3(256), 0, stream, in);
+  hipLaunchKernelGGL((muon_start_kernel<TG, TM>), dim3((unsigned)((in.mp / MT) * (in.np / MT)), (unsigned)batch), dim3(256), 0,
+                     stream, in);
+}
+
+// X from `in`, the steps, and the last of them into g's weight.
+static void ns_run(const NsPlan& h, MuonIn in, NsArgs g, int64_t batch, const float* coef, int steps, float scale, uint8_t* ws,
+                   hipStream_t stream) {
+  in.mp = (int)h.mp; in.np = (int)h.np; in.tall = in.rows > in.cols; in.parts = h.parts;
+  in.part = (double*)(ws + h.part);
+  in.scale = scale;
+  in.hi = ws + h.hi[0]; in.lo = ws + h.lo[0];
+  if (in.g_bf16) {
+    if (in.m_bf16) muon_begin<bf16_t, bf16_t>(in, batch, stream);
+    else muon_begin<bf16_t, float>(in, batch, stream);
+  } else {
+    if (in.m_bf16) muon_begin<float, bf16_t>(in, batch, stream);
+    else muon_begin<float, float>(in, batch, stream);
+  }
+  g.mp = (int)h.mp; g.np = (int)h.np; g.batch = (int)batch;
+  g.gram = ws + h.gram; g.poly = ws + h.poly; g.diag = (float*)(ws + h.diag);
+  g.inv = 1.0f / scale;
+  g.tall = in.tall; g.rows = in.rows; g.cols = in.cols;
+  for (int k = 0; k < steps; ++k) {
+    g.a = coef[3 * k]; g.b = coef[3 * k + 1]; g.c = coef[3 * k + 2];
+    g.hi = ws + h.hi[k & 1]; g.lo = ws + h.lo[k & 1];
+    g.hi2 = ws + h.hi[(k + 1) & 1]; g.lo2 = ws + h.lo[(k + 1) & 1];
+    ns_launch<NS_GRAM>(g, stream);
+    ns_launch<NS_POLY>(g, stream);
+    if (k + 1 < steps) ns_launch<NS_STEP>(g, stream);
+    else ns_launch<NS_LAST>(g, stream);
+  }
+}
+
+static pbs_status ns_check_call(const char* what, const float* coef, int64_t steps, float eps, const void* ws, size_t have, size_t need) {
+  PBS_REQUIRE(coef && steps >= 1 && steps <= NS_MOST_STEPS, PBS_ERR_INVALID_ARG, "%s: needs the coefficients of 1 to %d steps", what,
+              (int)NS_MOST_STEPS);
+  PBS_REQUIRE(eps >= 0.0f && eps <= 3.4e38f, PBS_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", what);
+  PBS_REQUIRE(need == 0 || (ws && ((uintptr_t)ws & 255) == 0), PBS_ERR_INVALID_ARG, "%s: the workspace is null or not 256-byte aligned",
+              what);
+  PBS_REQUIRE(have >= need, PBS_ERR_INVALID_ARG, "%s: the workspace holds %zu bytes, pbs_orthogonalize_bytes asks for %zu", what, have,
+              need);
+  return PBS_OK;
+}
+
+}  // namespace pbs
+
+using namespace pbs;
+
+extern "C" {
+
+pbs_status pbs_orthogonalize_bytes(int64_t batch, int64_t rows, int64_t cols, size_t* bytes) {
+  PBS_REQUIRE(bytes, PBS_ERR_INVALID_ARG, "pbs_orthogonalize_bytes: bytes is null");
+  const pbs_status st = ns_check_dims("pbs_orthogonalize_bytes", batch, rows, cols);
+  if (st != PBS_OK) return st;
+  *bytes = batch && rows && cols ? ns_plan(batch, rows, cols).bytes : 0;
+  return PBS_OK;
+}
+
+pbs_status pbs_orthogonalize(const void* x, pbs_format x_fmt, int64_t ldx, int64_t x_batch_stride, int64_t batch, int64_t rows,
+                             int64_t cols, const float* coefficients, int steps, float eps, void* y, int64_t ldy,
+                             int64_t y_batch_stride, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const char* what = "pbs_orthogonalize";
+  pbs_status st = ns_check_dims(what, batch, rows, cols);
+  if (st != PBS_OK) return st;
+  const bool none = batch == 0 || rows == 0 || cols == 0;
+  const NsPlan h = none ? NsPlan{} : ns_plan(batch, rows, cols);
+  if ((st = ns_check_call(what, coefficients, steps, eps, workspace, workspace_bytes, h.bytes)) != PBS_OK) return st;
+  float scale;
+  if ((st = ns_scale(what, coefficients, steps, &scale)) != PBS_OK) return st;
+  if (none) return PBS_OK;
+  if ((st = ns_check_matrix(what, "x", x, x_fmt, batch, rows, cols, ldx, x_batch_stride, false)) != PBS_OK) return st;
+  if ((st = ns_check_matrix(what, "y", y, PBS_FMT_BF16, batch, rows, cols, ldy, y_batch_stride, true)) != PBS_OK) return st;
+  PBS_REQUIRE(y != workspace && x != workspace, PBS_ERR_INVALID_ARG, "%s: a matrix is on the workspace's memory", what);
+  PBS_REQUIRE(y != x || x_fmt == PBS_FMT_BF16, PBS_ERR_INVALID_ARG, "%s: y is x with another type", what);
+  MuonIn in = {};
+  in.g = x; in.ldg = ldx; in.sg = x_batch_stride; in.g_bf16 = x_fmt == PBS_FMT_BF16;
+  in.rows = (int)rows; in.cols = (int)cols; in.eps = eps;
+  NsArgs g = {};
+  g.w = y; g.ldw = ldy; g.sw = y_batch_stride; g.w_bf16 = 1;
+  log_dispatch("orthogonalize batch=%lld rows=%lld cols=%lld steps=%d tiles=%d,%d scale=%g", (long long)batch, (long long)rows,
+               (long long)cols, steps, 64 * ns_tile(h.mp, h.np, batch, true), 64 * ns_tile(h.mp, h.np, batch, false), scale);
+  ns_run(h, in, g, batch, coefficients, steps, scale, (uint8_t*)workspace, stream);
+  return check_launch(what);
+}
+
+pbs_status pbs_muon(void* w, pbs_format w_fmt, int64_t ldw, int64_t w_batch_stride, void* momentum, pbs_format m_fmt, int64_t ldm,
+                    int64_t m_batch_stride, const void* grad, pbs_format g_fmt, int grad_transposed, int64_t ldg,
+                    int64_t g_batch_stride, int64_t batch, int64_t rows, int64_t cols, double beta, int nesterov, float lr,
+                    const float* lr_factor, float weight_decay, float scale, const float* coefficients, int steps, float eps,
+                    void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const char* what = "pbs_muon";
+  pbs_status st = ns_check_dims(what, batch, rows, cols);
+  if (st != PBS_OK) return st;
+  const bool none = batch == 0 || rows == 0 || cols == 0;
+  const NsPlan h = none ? NsPlan{} : ns_plan(batch, rows, cols);
+  if ((st = ns_check_call(what, coefficients, steps, eps, workspace, workspace_bytes, h.bytes)) != PBS_OK) return st;
+  PBS_REQUIRE(beta >= 0.0 && beta <= 1.0, PBS_ERR_INVALID_ARG, "%s: beta must be in [0, 1]", what);
+  PBS_REQUIRE(std::isfinite(lr) && std::isfinite(weight_decay) && std::isfinite(scale), PBS_ERR_INVALID_ARG,
+              "%s: lr, weight_decay and scale must be finite", what);
+  PBS_REQUIRE(((uintptr_t)lr_factor & 3) == 0, PBS_ERR_INVALID_ARG, "%s: lr_factor is not aligned to its elements", what);
+  float hold;
+  if ((st = ns_scale(what, coefficients, steps, &hold)) != PBS_OK) return st;
+  if (none) return PBS_OK;
+  if ((st = ns_check_matrix(what, "w", w, w_fmt, batch, rows, cols, ldw, w_batch_stride, true)) != PBS_OK) return st;
+  if ((st = ns_check_matrix(what, "momentum", momentum, m_fmt, batch, rows, cols, ldm, m_batch_stride, true)) != PBS_OK) return st;
+  if ((st = ns_check_matrix(what, "grad", grad, g_fmt, batch, grad_transposed ? cols : rows, grad_transposed ? rows : cols, ldg,
+                            g_batch_stride, false)) != PBS_OK)
+    return st;
+  PBS_REQUIRE(w != momentum && w != grad && momentum != grad, PBS_ERR_INVALID_ARG, "%s: w, momentum and grad must lie apart", what);
+  PBS_REQUIRE(w != workspace && momentum != workspace && grad != workspace, PBS_ERR_INVALID_ARG,
+              "%s: a matrix is on the workspace's memory", what);
+  MuonIn in = {};
+  in.g = grad; in.ldg = ldg; in.sg = g_batch_stride; in.g_bf16 = g_fmt == PBS_FMT_BF16; in.g_transposed = grad_transposed != 0;
+  in.m = momentum; in.ldm = ldm; in.sm = m_batch_stride; in.m_bf16 = m_fmt == PBS_FMT_BF16;
+  in.rows = (int)rows; in.cols = (int)cols; in.eps = eps;
+  in.beta = (float)beta; in.one_less = (float)(1.0 - beta); in.nesterov = nesterov != 0;
+  NsArgs g = {};
+  g.w = w; g.ldw = ldw; g.sw = w_batch_stride; g.w_bf16 = w_fmt == PBS_FMT_BF16;
+  g.update = 1; g.lr = lr; g.lr_by = lr_factor; g.decay = weight_decay; g.scale = scale;
+  log_dispatch("muon batch=%lld rows=%lld cols=%lld steps=%d tiles=%d,%d scale=%g", (long long)batch, (long long)rows, (long long)cols,
+               steps, 64 * ns_tile(h.mp, h.np, batch, true), 64 * ns_tile(h.mp, h.np, batch, false), hold);
+  ns_run(h, in, g, batch, coefficients, steps, hold, (uint8_t*)workspace, stream);
+  return check_launch(what);
+}
+
+}  // extern "C"

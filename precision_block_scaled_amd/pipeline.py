@@ -37,7 +37,8 @@ from . import (PBS_COL, PBS_DGRAD, PBS_FLAG_RHT16, PBS_FLAG_SR, PBS_FMT_BF16, PB
                pbs_delayed_init, pbs_delayed_scale, pbs_delayed_scale_inv, pbs_delayed_state_bytes,
                pbs_delayed_update, pbs_gemm, pbs_gemm_amax, pbs_layernorm, pbs_layernorm_grad,
                pbs_layernorm_grad_bytes, pbs_linear_distill, pbs_linear_distill_grad, pbs_linear_loss_bytes,
-               pbs_linear_xent, pbs_linear_xent_grad, pbs_qk_norm_rope, pbs_qk_norm_rope_grad,
+               pbs_linear_xent, pbs_linear_xent_grad, pbs_muon, pbs_orthogonalize,
+               pbs_orthogonalize_bytes, pbs_qk_norm_rope, pbs_qk_norm_rope_grad,
                pbs_qk_norm_rope_grad_bytes, pbs_scale_from_amax)
 
 RECIPES = {
@@ -743,3 +744,89 @@ def qk_norm_rope_grad(dq, dk, q, k=None, q_weight=None, k_weight=None, positions
         pbs_qk_norm_rope_grad(dq, sdq, dk, sdk, dv, sdv, FMT_OF[dq.dtype], q, sq, H, k, sk, kv, x_fmt, B, S, D, *args,
                               interleaved, dq_out, oq, dk_out, ok, dv_out, odv, dqw, dkw, a, ws, n, _current(dev))
     return dq_out, dk_out, dqw, dkw
+
+
+# ---------------------------------------------------------------------------
+# the weights' update
+# ---------------------------------------------------------------------------
+# a, b, c of the Muon optimiser's five quintic steps
+MUON_STEPS = ((3.4445, -4.7750, 2.0315),) * 5
+
+
+def _matrices(name, t, device, shape=None, flip=False):
+    """Checks a [rows, cols] or [batch, rows, cols] tensor of bf16 or fp32 with a contiguous last axis (with
+    ``flip``: or the one before it); returns (format, row stride, batch stride, whether it lies transposed)."""
+    if t.dim() not in (2, 3) or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name}: want shape {tuple(shape) if shape else '[rows, cols] or [batch, rows, cols]'}, got "
+                         f"{tuple(t.shape)}")
+    if t.dtype not in FMT_OF:
+        raise ValueError(f"{name}: want bf16 or fp32, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, want {device}")
+    rows, cols = t.shape[-2:]
+    lr, lc = t.stride()[-2:]
+    turned = flip and cols > 1 and lc != 1
+    if turned:
+        rows, cols, lr, lc = cols, rows, lc, lr
+    if cols > 1 and lc != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    ld = max(cols, 1) if rows <= 1 else lr
+    stride = t.stride(0) if t.dim() == 3 and t.shape[0] > 1 else ld * max(rows, 1)
+    return FMT_OF[t.dtype], ld, stride, turned
+
+
+def orthogonalize(x, y=None, coefficients=MUON_STEPS, eps=1e-7, stream=None):
+    """The nearest matrix with orthonormal rows or columns, approximately: X =
+    x / (||x||_F + eps), then X <- a X + (b A + c A^2) X with A = X X^T (of the
+    shorter side) for each (a, b, c) of ``coefficients``.  ``x`` [R, C] or [B, R,
+    C] (each by itself), bf16 or fp32; returns bf16, ``y`` if given (any rows; x
+    itself if that is bf16)."""
+    dev = x.device
+    x_fmt, ldx, sx, _ = _matrices("x", x, dev)
+    B = x.shape[0] if x.dim() == 3 else 1
+    R, C = x.shape[-2:]
+    if y is not None:
+        if y.dtype != torch.bfloat16:
+            raise ValueError(f"y: want bf16, got {y.dtype}")
+        _, ldy, sy, _ = _matrices("y", y, dev, x.shape)
+        if y.data_ptr() == x.data_ptr() and x.numel() and (y.dtype != x.dtype or (ldy, sy) != (ldx, sx)):
+            raise ValueError("y is on x's memory with another type or other strides")
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+            ldy, sy = max(C, 1), max(R, 1) * max(C, 1)
+        n = pbs_orthogonalize_bytes(B, R, C)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        pbs_orthogonalize(x, x_fmt, ldx, sx, B, R, C, coefficients, eps, y, ldy, sy, ws, n, _current(dev))
+    return y
+
+
+def muon(w, momentum, grad, lr, beta=0.95, nesterov=True, weight_decay=0.0, scale=None, coefficients=MUON_STEPS, eps=1e-7,
+         stream=None):
+    """One step of Muon on ``w`` [R, C] or [B, R, C] (each matrix by itself),
+    in place: momentum <- beta momentum + (1 - beta) grad; U = beta momentum +
+    (1 - beta) grad (``nesterov``) or the momentum; w <- (1 - lr weight_decay) w -
+    lr scale X with X = ``orthogonalize(U)``.  Returns w.
+
+    ``w``, ``momentum`` and ``grad`` are bf16 or fp32 each, rows contiguous;
+    ``grad`` may also lie transposed: what the Wgrad product writes, [in, out],
+    is given as ``dw.t()``.  ``scale`` None: max(1, R / C)^0.5.  ``lr``: a number, or
+    a device fp32 of one element (read when the work runs, so a captured graph
+    follows a schedule)."""
+    dev = w.device
+    w_fmt, ldw, sw, _ = _matrices("w", w, dev)
+    m_fmt, ldm, sm, _ = _matrices("momentum", momentum, dev, w.shape)
+    g_fmt, ldg, sg, turned = _matrices("grad", grad, dev, w.shape, flip=True)
+    B = w.shape[0] if w.dim() == 3 else 1
+    R, C = w.shape[-2:]
+    factor = None
+    if isinstance(lr, torch.Tensor):
+        factor, lr = _vector("lr", lr.reshape(-1), 1, F32, dev), 1.0
+    if scale is None:
+        scale = max(1.0, R / max(C, 1)) ** 0.5
+    with _on(dev, stream):
+        n = pbs_orthogonalize_bytes(B, R, C)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        pbs_muon(w, w_fmt, ldw, sw, momentum, m_fmt, ldm, sm, grad, g_fmt, turned, ldg, sg, B, R, C, beta, nesterov, lr, factor,
+                 weight_decay, scale, coefficients, eps, ws, n, _current(dev))
+    return w
