@@ -36,6 +36,7 @@
 
 namespace pbs {
 
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16_t;
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
@@ -98,6 +99,31 @@ __device__ __forceinline__ void muon_put4(T* row, int c, int cols, bool vec, flo
     if (c + 3 < cols) row[c + 3] = (bf16_t)(hi >> 16);
   }
 }
+// Four aligned values as they lie in memory.
+template <typename T>
+struct MuonQuad {
+  typedef typename std::conditional<sizeof(T) == 4, u32x4, u32x2>::type raw;
+  raw v;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+    if constexpr (sizeof(T) == 4) v = __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+    else v = __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0));
+  }
+  // keep * them - step * x
+  __device__ __forceinline__ float4 moved(float keep, float step, float4 x) const {
+    float o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if constexpr (sizeof(T) == 4) o[i] = __uint_as_float(v[i]);
+      else o[i] = __uint_as_float(i & 1 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16);
+    return make_float4(keep * o[0] - step * x.x, keep * o[1] - step * x.y, keep * o[2] - step * x.z, keep * o[3] - step * x.w);
+  }
+  static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t at, float4 x) {
+    if constexpr (sizeof(T) == 4)
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), r, at, 0, 0);
+    else
+      __builtin_amdgcn_raw_buffer_store_b64(u32x2{pk_bf16(x.x, x.y), pk_bf16(x.z, x.w)}, r, at, 0, 0);
+  }
+};
 template <typename T>
 __device__ __forceinline__ bool muon_vec(const void* p, int64_t ld, int64_t batch_stride) {
   return (((uintptr_t)p & (4 * sizeof(T) - 1)) | (uint64_t)(ld & 3) | (uint64_t)(batch_stride & 3)) == 0;
@@ -282,10 +308,19 @@ struct NsArgs {
 // (2 i + wm, 2 j + wn), i, j < T.
 template <int T> constexpr int ns_pitch() { return 128 * T + 16; }      // staged rows of fp16
 template <int T> constexpr int ns_pitch4() { return 256 * T + 16; }     // and of fp32
+constexpr int NS_TALL_PITCH = 68;                                       // floats: staged columns of 64 rows
 template <int T> constexpr int ns_smem(int mode) {
   return cmax(5 * tile_bytes<T>(), mode == NS_GRAM   ? 64 * T * ns_pitch<T>()
-                                   : mode == NS_LAST ? 128 * ns_pitch<T>() + 64 * ns_pitch4<T>()
+                                   : mode == NS_LAST ? 128 * ns_pitch<T>() + 64 * T * NS_TALL_PITCH * 4
                                                      : 256 * ns_pitch<T>());
+}
+
+// All waves meet with their LDS work done; loads and stores stay in flight
+// (__syncthreads would wait for them).
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
 template <int T>
@@ -337,7 +372,7 @@ __device__ __forceinline__ void ns_triangle(int id, int n, int& row, int& col) {
   row = col + in;
 }
 
-template <int T, int MODE>
+template <int T, int MODE, typename TW>
 __global__ __launch_bounds__(256, T >= 3 ? 1 : 2) void ns_product_kernel(NsArgs g) {
   __shared__ __align__(16) uint8_t smem[ns_smem<T>(MODE)];
   constexpr int LDA = MODE >= NS_STEP ? MNMAJ : KMAJ;
@@ -452,7 +487,9 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : 2) void ns_product_kernel(NsArgs 
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    stage_barrier<ISSUE ? NL : 0>();
+    // (the last stage's loads were waited for in the one before; what is in flight then is the epilogue's)
+    if constexpr (NEXT) stage_barrier<ISSUE ? NL : 0>();
+    else lds_barrier();
     constexpr int NDS = NEXT ? RA + RB : 0;
 #pragma unroll
     for (int m = 0; m < NMFMA; ++m) {
@@ -474,36 +511,71 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : 2) void ns_product_kernel(NsArgs 
   using F_ = std::integral_constant<bool, false>;
   for (int kt = 0; kt < nk - 2; ++kt) body(kt, T_{}, T_{});
   if (nk >= 2) body(nk - 2, F_{}, T_{});
+  // The epilogue's sources of 64 rows, A or X's pair, a pass ahead in
+  // registers: the first behind the last stage's products.
+  constexpr int CHUNKS = 8 * T, PER = 2 * T;                  // 16-byte chunks a row, and a thread in 64 rows
+  const uint8_t* src = MODE == NS_POLY ? g.gram + 2 * ps : g.hi + 2 * xs;
+  const uint8_t* src2 = g.lo + 2 * xs;
+  u32x4 v1[PER], v2[PER];
+  auto fetch = [&](int j) {
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int at = t + 256 * k;
+      const int r = n0 + 64 * j + at / CHUNKS, c = m0 + 8 * (at % CHUNKS);
+      const int64_t o = 2 * ((int64_t)(r < g.mp ? r : g.mp - 1) * M + (c < M ? c : M - 8));
+      v1[k] = *(const u32x4*)(src + o);
+      if constexpr (MODE >= NS_STEP) v2[k] = *(const u32x4*)(src2 + o);
+    }
+  };
+  if constexpr (MODE != NS_GRAM) fetch(0);
+  const int srow = 32 * wn + lr;                              // the lane's row of 64
+  float own[T];                                               // a + P's diagonal there
+  if constexpr (MODE >= NS_STEP) {
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      const int row = n0 + 64 * j + srow;
+      own[j] = g.a + g.diag[(int64_t)mat * g.mp + (row < g.mp ? row : g.mp - 1)];
+    }
+  }
+  __builtin_amdgcn_sched_barrier(0);
   body(nk - 1, F_{}, F_{});
 
-  // Every LDS read of the loop finished before its last barrier and no load is
-  // in flight.  acc[i][j][4 q + r] is row n0 + 32 (2 j + wn) + lr, column m0 + 32
+  // Every LDS read of the loop finished before its last barrier, and no load to
+  // LDS is in flight.  acc[i][j][4 q + r] is row n0 + 32 (2 j + wn) + lr, column m0 + 32
   // (2 i + wm) + 8 q + 4 lg + r.  The results are staged 64 rows at a time (those
   // of one j) and stored from there in whole rows.
   constexpr int PITCH = ns_pitch<T>(), PITCH4 = ns_pitch4<T>();
-  constexpr int CHUNKS = 8 * T, PER = 2 * T;                  // 16-byte chunks a row, and a thread in 64 rows
-  const int srow = 32 * wn + lr;                              // the lane's row of a pass
   auto scol = [&](int i, int q) { return 32 * (2 * i + wm) + 8 * q + 4 * lg; };
-  // 64 staged rows from row r0 of an fp16 matrix with ld columns
-  auto store_rows = [&](const uint8_t* from, uint8_t* to, int r0, int rows, int64_t ld) {
+  // Stores go through buffer resources that begin at the tile's first row and end
+  // with the matrix, and what lies past its columns is sent past that end: the
+  // hardware drops it.  (Behind a condition the compiler no longer knows how many
+  // stores are in flight and waits for all of them ahead of the next pass's
+  // sources.)
+  constexpr uint32_t NOWHERE = 0xFFFFFFF0u;
+  auto rows_of = [](uint8_t* p, int first, int rows, int64_t ld) {
+    return buffer_rows(p + 2 * first * ld, (uint32_t)(2 * (rows - first) * ld < 0xFFFFFFF0ll ? 2 * (rows - first) * ld : 0xFFFFFFF0ll));
+  };
+  // 64 staged rows from the tile's row r0 on, of a matrix with ld columns
+  auto store_rows = [&](const uint8_t* from, const BufferRows& to, int r0, int64_t ld) {
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       const int at = t + 256 * k, r = at / CHUNKS, c = at % CHUNKS;
-      const uint4 v = *(const uint4*)(from + r * PITCH + 16 * c);
-      if (r0 + r < rows && m0 + 8 * c < M) *(uint4*)(to + 2 * ((int64_t)(r0 + r) * ld + m0 + 8 * c)) = v;
+      const u32x4 v = *(const u32x4*)(from + r * PITCH + 16 * c);
+      const uint32_t o = (uint32_t)(r0 + r) * (uint32_t)(2 * ld) + (uint32_t)(2 * (m0 + 8 * c));
+      __builtin_amdgcn_raw_buffer_store_b128(v, to.r, m0 + 8 * c < M ? o : NOWHERE, 0, 0);
     }
   };
   // and transposed: 8 rows of 16 columns at a time, by the transposing read
-  auto store_transposed = [&](const uint8_t* from, uint8_t* to, int r0) {
+  auto store_transposed = [&](const uint8_t* from, const BufferRows& to, int r0) {
     const int gq = lane >> 4, li = lane & 15;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       const int block = w + 4 * k, c0 = 16 * (block >> 1), o = 8 * (4 * (block & 1) + gq);
       const uint8_t* p = from + (o + (li >> 2)) * PITCH + 2 * (c0 + 4 * (li & 3));
-      const int2 lo = __builtin_bit_cast(int2, read_lds_tr16(p));
-      const int2 hi = __builtin_bit_cast(int2, read_lds_tr16(p + 4 * PITCH));
-      if (m0 + c0 + li < g.mp && r0 + o < g.mp)
-        *(int4*)(to + 2 * ((int64_t)(m0 + c0 + li) * g.mp + r0 + o)) = make_int4(lo.x, lo.y, hi.x, hi.y);
+      const u32x2 lo = __builtin_bit_cast(u32x2, read_lds_tr16(p));
+      const u32x2 hi = __builtin_bit_cast(u32x2, read_lds_tr16(p + 4 * PITCH));
+      const uint32_t at = (uint32_t)(c0 + li) * (uint32_t)(2 * g.mp) + (uint32_t)(2 * (n0 + r0 + o));
+      __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo.x, lo.y, hi.x, hi.y}, to.r, n0 + r0 + o < g.mp ? at : NOWHERE, 0, 0);
     }
   };
 
@@ -519,32 +591,55 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : 2) void ns_product_kernel(NsArgs 
           for (int r = 0; r < 4; ++r) v[r] = (f16_t)(acc[i][j][4 * q + r] * g.inv);
           *(f16x4*)(smem + (64 * j + srow) * PITCH + 2 * scol(i, q)) = v;
         }
-    __syncthreads();
-    uint8_t* to = g.gram + 2 * ps;
+    lds_barrier();
+    const BufferRows to = rows_of(g.gram + 2 * ps, n0, g.mp, g.mp), over = rows_of(g.gram + 2 * ps, m0, g.mp, g.mp);
 #pragma unroll
     for (int j = 0; j < T; ++j) {
-      store_rows(smem + 64 * j * PITCH, to, n0 + 64 * j, g.mp, g.mp);
-      if (tm != tn) store_transposed(smem + 64 * j * PITCH, to, n0 + 64 * j);
+      store_rows(smem + 64 * j * PITCH, to, 64 * j, g.mp);
+      if (tm != tn) store_transposed(smem + 64 * j * PITCH, over, 64 * j);
     }
   } else {
-    // the sources of 64 rows: A, or X's pair, a pass ahead in registers
-    const uint8_t* src = MODE == NS_POLY ? g.gram + 2 * ps : g.hi + 2 * xs;
-    const uint8_t* src2 = g.lo + 2 * xs;
-    u32x4 v1[PER], v2[MODE >= NS_STEP ? PER : 1];
-    auto fetch = [&](int j) {
+    constexpr int AREA = 64 * PITCH;
+    const BufferRows to1 = MODE == NS_POLY ? rows_of(g.poly + 2 * ps, n0, g.mp, g.mp) : rows_of(g.hi2 + 2 * xs, n0, g.mp, g.np);
+    const BufferRows to2 = MODE == NS_POLY ? rows_of(g.poly + 2 * ps, m0, g.mp, g.mp) : rows_of(g.lo2 + 2 * xs, n0, g.mp, g.np);
+    // The last step: four values of a row of the weight at a time, QPT a thread
+    // and pass.  A tall weight's rows are the tile's columns, which are then
+    // staged as rows.  Value 4 of step k in pass j lies k * krows rows on from the
+    // thread's first, and j * 64 rows (columns, if tall).
+    constexpr int QUADS = 16 * T, QPT = 64 * QUADS / 256, AHEAD = QPT / 2;
+    const float lr_now = MODE == NS_LAST && g.lr_by ? g.lr * *g.lr_by : g.lr;
+    const float keep = 1.0f - lr_now * g.decay, step = lr_now * g.scale;
+    const int row_step = g.tall ? 1 : PITCH4 / 4, col_step = g.tall ? NS_TALL_PITCH : 1;      // of the staged fp32
+    const int krows = g.tall ? 16 : 256 / QUADS, kstage = g.tall ? 16 * NS_TALL_PITCH : 256 / QUADS * (PITCH4 / 4);
+    const int first = g.tall ? (t >> 4) * NS_TALL_PITCH + 4 * (t & 15) : t / QUADS * (PITCH4 / 4) + 4 * (t % QUADS);
+    const int w0 = g.tall ? m0 : n0, qrow = g.tall ? t >> 4 : t / QUADS, wcol = g.tall ? n0 + 4 * (t & 15) : m0 + 4 * (t % QUADS);
+    // whole quads of rows that one buffer resource reaches
+    const int64_t ldb = g.ldw * (int64_t)sizeof(TW);
+    const bool quads = g.cols % 4 == 0 && muon_vec<TW>(g.w, g.ldw, g.sw) && 256 * ldb < 0x7FFFFFFFll;
+    TW* const weight = (TW*)g.w + mat * g.sw + w0 * g.ldw;                // the tile's first row
+    BufferRows wb;
+    {
+      const int64_t have = ((int64_t)(g.rows - w0 - 1) * g.ldw + g.cols) * (int64_t)sizeof(TW);
+      wb = buffer_rows((const uint8_t*)weight, (uint32_t)(have < 0 ? 0 : have < 0xFFFFFFF0ll ? have : 0xFFFFFFF0ll));
+    }
+    const uint32_t ldb32 = (uint32_t)ldb;
+    auto w_at = [&](int j, int k) {
+      const int c = wcol + (g.tall ? 64 * j : 0), r = qrow + k * krows + (g.tall ? 0 : 64 * j);
+      return c < g.cols && w0 + r < g.rows ? (uint32_t)r * ldb32 + (uint32_t)(c * (int)sizeof(TW)) : NOWHERE;
+    };
+    MuonQuad<TW> old[AHEAD];
+    auto fetch_w = [&](int j, int from) {
 #pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        const int at = t + 256 * k;
-        const int r = n0 + 64 * j + at / CHUNKS, c = m0 + 8 * (at % CHUNKS);
-        const int64_t o = 2 * ((int64_t)(r < g.mp ? r : g.mp - 1) * M + (c < M ? c : M - 8));
-        v1[k] = *(const u32x4*)(src + o);
-        if constexpr (MODE >= NS_STEP) v2[k] = *(const u32x4*)(src2 + o);
+      for (int k = 0; k < AHEAD; ++k) old[k].load(wb.r, w_at(j, from + k));
+    };
+    auto put_w = [&](int j, int from, const float* f) {
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        float4 v = *(const float4*)(f + first + (from + k) * kstage);
+        if (g.update) v = old[k].moved(keep, step, v);
+        MuonQuad<TW>::store(wb.r, w_at(j, from + k), v);
       }
     };
-    constexpr int AREA = 64 * PITCH;
-    fetch(0);
-    float lr_now = 0.0f;
-    if constexpr (MODE == NS_LAST) lr_now = g.lr_by ? g.lr * *g.lr_by : g.lr;
 #pragma unroll
     for (int j = 0; j < T; ++j) {
       uint8_t* s1 = smem + (MODE == NS_LAST ? 0 : (j & 1) * 2 * AREA);
@@ -556,14 +651,13 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : 2) void ns_product_kernel(NsArgs 
         if constexpr (MODE >= NS_STEP) *(u32x4*)(s2 + o) = v2[k];
       }
       if (j + 1 < T) fetch(j + 1);
+      if (MODE == NS_LAST && quads && g.update) fetch_w(j, 0);
       const int row = n0 + 64 * j + srow;
-      float own = 0.0f;                                       // a + P's diagonal
-      if constexpr (MODE >= NS_STEP) own = g.a + g.diag[(int64_t)mat * g.mp + (row < g.mp ? row : g.mp - 1)];
       // P's diagonal: where the lane's row meets the tile's columns
       const int dcol = MODE == NS_POLY && tm == tn ? row - m0 : -64 * T;
       float dval = 0.0f;
       bool has = false;
-      __syncthreads();
+      lds_barrier();
 #pragma unroll
       for (int i = 0; i < T; ++i)
 #pragma unroll
@@ -588,7 +682,7 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : 2) void ns_product_kernel(NsArgs 
             f16x4 oh, ol;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              v[r] = own * ((float)h[r] + (float)l[r] * (1.0f / NS_LO)) + acc[i][j][4 * q + r] * g.inv;
+              v[r] = own[j] * ((float)h[r] + (float)l[r] * (1.0f / NS_LO)) + acc[i][j][4 * q + r] * g.inv;
               f16_t hh, ll;
               ns_split(v[r], hh, ll);
               oh[r] = hh;
@@ -598,55 +692,39 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : 2) void ns_product_kernel(NsArgs 
               *p1 = oh;
               *p2 = ol;
             } else {
-              *(float4*)(smem + 2 * AREA + srow * PITCH4 + 4 * scol(i, q)) =
-                  make_float4(v[0] * g.inv, v[1] * g.inv, v[2] * g.inv, v[3] * g.inv);
+              // (strides, not a branch: ahead of one the accumulators of all passes are read and fill the registers)
+              float* f = (float*)(smem + 2 * AREA) + srow * row_step + scol(i, q) * col_step;
+#pragma unroll
+              for (int r = 0; r < 4; ++r) f[r * col_step] = v[r] * g.inv;
             }
           }
         }
       if (MODE == NS_POLY && has && row < g.mp) g.diag[(int64_t)mat * g.mp + row] = dval * g.inv;
-      __syncthreads();
-      const int r0 = n0 + 64 * j;
+      lds_barrier();
       if constexpr (MODE == NS_POLY) {
-        store_rows(s1, g.poly + 2 * ps, r0, g.mp, g.mp);
-        if (tm != tn) store_transposed(s1, g.poly + 2 * ps, r0);
+        store_rows(s1, to1, 64 * j, g.mp);
+        if (tm != tn) store_transposed(s1, to2, 64 * j);
       } else if constexpr (MODE == NS_STEP) {
-        store_rows(s1, g.hi2 + 2 * xs, r0, g.mp, g.np);
-        store_rows(s2, g.lo2 + 2 * xs, r0, g.mp, g.np);
+        store_rows(s1, to1, 64 * j, g.np);
+        store_rows(s2, to2, 64 * j, g.np);
       } else {
-        // four values of a row of the weight at a time; a tall weight's rows are the staged columns
         const float* f = (const float*)(smem + 2 * AREA);
-        constexpr int FP = PITCH4 / 4;
-        const float keep = 1.0f - lr_now * g.decay, step = lr_now * g.scale;
-        const bool vec = g.w_bf16 ? muon_vec<bf16_t>(g.w, g.ldw, g.sw) : muon_vec<float>(g.w, g.ldw, g.sw);
-        constexpr int QUADS = 16 * T;                          // of a staged row; 16 of a staged column
-#pragma unroll 2
-        for (int k = 0; k < 64 * QUADS / 256; ++k) {
-          const int at = t + 256 * k;
-          int wr, wc;
-          float4 v;
-          if (g.tall) {
-            const int c = at >> 4, r = 4 * (at & 15);
-            v = make_float4(f[r * FP + c], f[(r + 1) * FP + c], f[(r + 2) * FP + c], f[(r + 3) * FP + c]);
-            wr = m0 + c;
-            wc = r0 + r;
-          } else {
-            const int r = at / QUADS, c = 4 * (at % QUADS);
-            v = *(const float4*)(f + r * FP + c);
-            wr = r0 + r;
-            wc = m0 + c;
-          }
-          if (wr >= g.rows || wc >= g.cols) continue;
-          auto put = [&](auto* base) {
-            auto* p = base + mat * g.sw + wr * g.ldw;
-            typedef typename std::remove_reference<decltype(*p)>::type TW;
+        if (quads) {
+          put_w(j, 0, f);
+          if (g.update) fetch_w(j, AHEAD);
+          put_w(j, AHEAD, f);
+        } else {
+          const int r = w0 + qrow + (g.tall ? 0 : 64 * j), c = wcol + (g.tall ? 64 * j : 0);
+          TW* p = weight + (r - w0) * g.ldw;
+#pragma unroll 1
+          for (int k = 0; k < QPT && r + k * krows < g.rows; ++k, p += krows * g.ldw) {
+            float4 v = *(const float4*)(f + first + k * kstage);
             if (g.update) {
-              const float4 o = muon_get4<TW>(p, wc, g.cols, vec);
+              const float4 o = muon_get4<TW>(p, c, g.cols, false);
               v = make_float4(keep * o.x - step * v.x, keep * o.y - step * v.y, keep * o.z - step * v.z, keep * o.w - step * v.w);
             }
-            muon_put4<TW>(p, wc, g.cols, vec, v);
-          };
-          if (g.w_bf16) put((bf16_t*)g.w);
-          else put((float*)g.w);
+            muon_put4<TW>(p, c, g.cols, false, v);
+          }
         }
       }
     }
@@ -766,7 +844,7 @@ static int ns_tile(int64_t mp, int64_t np, int64_t batch, bool symmetric) {
   return best;
 }
 
-template <int MODE>
+template <int MODE, typename TW = float>
 static void ns_launch(NsArgs g, hipStream_t stream) {
   constexpr bool SYM = MODE <= NS_POLY;
   const int t = ns_tile(g.mp, g.np, g.batch, SYM);
@@ -774,9 +852,9 @@ static void ns_launch(NsArgs g, hipStream_t stream) {
   g.tiles_m = SYM ? g.tiles_n : (int)ceil_div(g.np, 64 * t);
   g.per = SYM ? g.tiles_n * (g.tiles_n + 1) / 2 : g.tiles_m * g.tiles_n;
   const dim3 grid((unsigned)(g.per * g.batch)), block(256);
-  if (t == 4) hipLaunchKernelGGL((ns_product_kernel<4, MODE>), grid, block, 0, stream, g);
-  else if (t == 2) hipLaunchKernelGGL((ns_product_kernel<2, MODE>), grid, block, 0, stream, g);
-  else if constexpr (SYM) hipLaunchKernelGGL((ns_product_kernel<3, MODE>), grid, block, 0, stream, g);
+  if (t == 4) hipLaunchKernelGGL((ns_product_kernel<4, MODE, TW>), grid, block, 0, stream, g);
+  else if (t == 2) hipLaunchKernelGGL((ns_product_kernel<2, MODE, TW>), grid, block, 0, stream, g);
+  else if constexpr (SYM) hipLaunchKernelGGL((ns_product_kernel<3, MODE, TW>), grid, block, 0, stream, g);
 }
 
 template <typename TG, typename TM>
@@ -811,7 +889,8 @@ static void ns_run(const NsPlan& h, MuonIn in, NsArgs g, int64_t batch, const fl
     ns_launch<NS_GRAM>(g, stream);
     ns_launch<NS_POLY>(g, stream);
     if (k + 1 < steps) ns_launch<NS_STEP>(g, stream);
-    else ns_launch<NS_LAST>(g, stream);
+    else if (g.w_bf16) ns_launch<NS_LAST, bf16_t>(g, stream);
+    else ns_launch<NS_LAST, float>(g, stream);
   }
 }
 
