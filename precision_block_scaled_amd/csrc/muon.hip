@@ -129,6 +129,10 @@ __device__ __forceinline__ bool muon_vec(const void* p, int64_t ld, int64_t batc
   return (((uintptr_t)p & (4 * sizeof(T) - 1)) | (uint64_t)(ld & 3) | (uint64_t)(batch_stride & 3)) == 0;
 }
 
+// (Each product and sum is rounded by itself, as the formulas stand: a momentum
+// kept in bf16 then comes out as any fp32 evaluation of them has it.  A value
+// rounded the other way, 2^-8 of it, may move the small directions of the next
+// step's X by as much as they are.)
 // A 64 x 64 tile of U: thread t holds four values of the rows t / 16 + 16 k
 // from column 4 (t % 16) on.  m4: M', for the momentum's store.
 constexpr int MT = 64, MPITCH = 65;
@@ -174,12 +178,10 @@ struct MuonTile {
       const float4 o = r < a.rows ? muon_get4<TM>(m + r * a.ldm, c0 + tc, a.cols, vm) : make_float4(0, 0, 0, 0);
       const float4 s = make_float4(a.one_less * gv[k].x, a.one_less * gv[k].y, a.one_less * gv[k].z, a.one_less * gv[k].w);
       float4 n;
-      n.x = __builtin_fmaf(a.beta, o.x, s.x); n.y = __builtin_fmaf(a.beta, o.y, s.y);
-      n.z = __builtin_fmaf(a.beta, o.z, s.z); n.w = __builtin_fmaf(a.beta, o.w, s.w);
+      n.x = a.beta * o.x + s.x; n.y = a.beta * o.y + s.y; n.z = a.beta * o.z + s.z; n.w = a.beta * o.w + s.w;
       m4[k] = n;
       if (a.nesterov) {
-        n.x = __builtin_fmaf(a.beta, n.x, s.x); n.y = __builtin_fmaf(a.beta, n.y, s.y);
-        n.z = __builtin_fmaf(a.beta, n.z, s.z); n.w = __builtin_fmaf(a.beta, n.w, s.w);
+        n.x = a.beta * n.x + s.x; n.y = a.beta * n.y + s.y; n.z = a.beta * n.z + s.z; n.w = a.beta * n.w + s.w;
       }
       u[k] = n;
     }
@@ -732,12 +734,306 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : 2) void ns_product_kernel(NsArgs 
 }
 
 // ---------------------------------------------------------------------------
+// Short sides up to 64
+//
+// The steps' polynomials are polynomials of R = U U^T / (||U||_F + eps)^2 alone,
+// whose trace gives the norm: X = Q U / (||U||_F + eps) with Q the product of the
+// steps' a I + b R + c R^2, and R <- (a I + b R + c R^2)^2 R after each.  So the
+// long side is gone through twice, for R and for Q U, and the steps between run
+// in one workgroup a matrix: three launches instead of 2 + 3 a step, of which
+// each takes 5 us or more here (16 x 4096 291 -> 44 us, 2 x 64 x 128 110 ->
+// 51).  What R's rounding adds to the small directions grows by a^2 = 12 a
+// step, 2e4 in five, and nothing takes it back as X X^T formed anew would: R is
+// held in 64 bits, and its products run on the 64-bit matrix instruction (a
+// product of 64 x 64 x 64 1.3 us; for 128 it would be 10).  The result is fp32's
+// own roundings away from 64 bits.
+// ---------------------------------------------------------------------------
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+
+constexpr int NS_SHORT = 64;               // the longest short side
+constexpr int SB = 16;                     // a matrix instruction's tile
+constexpr int SPITCH = 66;                 // doubles: a row of a staged matrix
+constexpr int STILES = 10;                 // tiles of 16 x 16 on and below a 64 x 64 diagonal
+constexpr int SUPITCH = 68;                // floats: a row of a staged piece of U
+
+struct ShortArgs {
+  MuonIn in;               // mp, np unused
+  int blocks;              // 16-row blocks of the short side
+  int chunks;              // workgroups that share a matrix's long side
+  double* part;            // [batch][chunks][STILES][256]: R's tiles as the instruction holds them
+  float* q;                // [batch][64][64]
+  double* inv;             // [batch]: 1 / (||U||_F + eps)
+  float coef[3 * 64];
+  int steps;
+  void* w;
+  int64_t ldw, sw;
+  int update;
+  float lr, decay, scale;
+  const float* lr_by;
+};
+
+__device__ __forceinline__ void short_tile(int p, int& row, int& col) {
+  row = p < 1 ? 0 : p < 3 ? 1 : p < 6 ? 2 : 3;
+  col = p - row * (row + 1) / 2;
+}
+
+// 64 values of the long side from `at` on: U as [short][64] in LDS.  The tile's
+// own registers hold it as the weight lies.
+template <typename TG, typename TM>
+__device__ __forceinline__ void short_load(const MuonIn& a, int batch, int at, MuonTile<TG, TM>& u, float (*turn)[MPITCH]) {
+  u.load(a, batch, a.tall ? at : 0, a.tall ? 0 : at, turn);
+}
+template <typename TG, typename TM>
+__device__ __forceinline__ void short_stage(const MuonIn& a, const MuonTile<TG, TM>& u, double f, float* lds) {
+  const int t = threadIdx.x, tr = t >> 4, tc = 4 * (t & 15);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float4 v = make_float4((float)(u.u[k].x * f), (float)(u.u[k].y * f), (float)(u.u[k].z * f), (float)(u.u[k].w * f));
+    const int r = tr + 16 * k;
+    if (a.tall) {
+      lds[tc * SUPITCH + r] = v.x;
+      lds[(tc + 1) * SUPITCH + r] = v.y;
+      lds[(tc + 2) * SUPITCH + r] = v.z;
+      lds[(tc + 3) * SUPITCH + r] = v.w;
+    } else {
+      *(float4*)(lds + r * SUPITCH + tc) = v;
+    }
+  }
+}
+
+// Partial sums of U U^T: wave w takes every fourth step of 4 columns.
+template <typename TG, typename TM>
+__global__ __launch_bounds__(256) void short_gram_kernel(ShortArgs a) {
+  __shared__ float turn[MT][MPITCH];
+  __shared__ __align__(16) float u[NS_SHORT * SUPITCH];
+  __shared__ double sums[STILES * 256];
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6, batch = blockIdx.y;
+  const int n = a.in.tall ? a.in.rows : a.in.cols, tiles = a.blocks * (a.blocks + 1) / 2;
+  f64x4 acc[STILES];
+#pragma unroll
+  for (int p = 0; p < STILES; ++p) acc[p] = f64x4{0, 0, 0, 0};
+  for (int at = blockIdx.x * 64; at < n; at += a.chunks * 64) {
+    MuonTile<TG, TM> v;
+    short_load(a.in, batch, at, v, turn);
+    __syncthreads();
+    short_stage(a.in, v, 1.0, u);
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      double x[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) x[b] = (double)u[(SB * b + lane % 16) * SUPITCH + 4 * (4 * s + w) + lane / 16];
+#pragma unroll
+      for (int p = 0; p < STILES; ++p) {
+        int i, j;
+        short_tile(p, i, j);
+        if (i < a.blocks) acc[p] = __builtin_amdgcn_mfma_f64_16x16x4f64(x[i], x[j], acc[p], 0, 0, 0);
+      }
+    }
+  }
+  // the four waves' sums, in their order
+  for (int q = 0; q < 4; ++q) {
+    __syncthreads();
+    if (w == q) {
+#pragma unroll
+      for (int p = 0; p < STILES; ++p)
+        if (p < tiles) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            double* to = sums + p * 256 + 64 * r + lane;
+            *to = q ? *to + acc[p][r] : acc[p][r];
+          }
+        }
+    }
+  }
+  __syncthreads();
+  double* to = a.part + ((int64_t)batch * a.chunks + blockIdx.x) * STILES * 256;
+  for (int i = t; i < tiles * 256; i += 256) to[i] = sums[i];
+}
+
+// Tile (i, j) of x y^T: lane l holds rows 4 r + l / 16, r < 4, of column l % 16.
+// Sixteen columns of both at a time, read ahead of the products.
+__device__ __forceinline__ f64x4 short_product(const double* x, const double* y, int i, int j, int blocks, int lane) {
+  f64x4 c = {0, 0, 0, 0};
+  const double* p = x + (SB * i + lane % 16) * SPITCH + lane / 16;
+  const double* q = y + (SB * j + lane % 16) * SPITCH + lane / 16;
+  double u[2][4], v[2][4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    u[0][k] = p[4 * k];
+    v[0][k] = q[4 * k];
+  }
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    if (b >= blocks) break;
+    if (b + 1 < blocks) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        u[(b + 1) & 1][k] = p[16 * (b + 1) + 4 * k];
+        v[(b + 1) & 1][k] = q[16 * (b + 1) + 4 * k];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c = __builtin_amdgcn_mfma_f64_16x16x4f64(u[b & 1][k], v[b & 1][k], c, 0, 0, 0);
+  }
+  return c;
+}
+
+// The steps, a wave for each tile.  Every matrix is a polynomial of R, symmetric
+// and commuting with the others, so products are formed as X Y^T, by half, and
+// stored twice.
+constexpr int SSTEP_THR = 64 * STILES;
+__global__ __launch_bounds__(SSTEP_THR) void short_steps_kernel(ShortArgs a) {
+  __shared__ double R[NS_SHORT * SPITCH], P[NS_SHORT * SPITCH], Q[NS_SHORT * SPITCH];
+  const int t = threadIdx.x, lane = t & 63, batch = blockIdx.x;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int tiles = a.blocks * (a.blocks + 1) / 2, side = SB * a.blocks;
+  const double* from = a.part + (int64_t)batch * a.chunks * STILES * 256;
+  int ti, tj;
+  short_tile(w, ti, tj);
+  // (of a tile on the diagonal the lower half: the two halves' roundings differ)
+  auto put = [&](double* m, int i, int j, int r, double v) {
+    const int row = SB * i + 4 * r + lane / 16, col = SB * j + lane % 16;
+    if (row < col) return;
+    m[row * SPITCH + col] = v;
+    m[col * SPITCH + row] = v;
+  };
+  for (int e = w; e < 4 * tiles; e += STILES) {           // rows e % 4 of tile e / 4, as the instruction holds them
+    double s = 0.0;
+    for (int c = 0; c < a.chunks; c += 16) {
+      double v[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v[k] = from[(int64_t)(c + k < a.chunks ? c + k : 0) * STILES * 256 + 64 * e + lane];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) s += c + k < a.chunks ? v[k] : 0.0;
+    }
+    int i, j;
+    short_tile(e >> 2, i, j);
+    put(R, i, j, e & 3, s);
+  }
+  __syncthreads();
+  const double norm = sqrt(wave_sum_d(lane < side ? R[lane * (SPITCH + 1)] : 0.0)) + (double)a.in.eps;
+  // a matrix of zeros stays one; one with an infinity or a NaN becomes NaN
+  const double inv = norm == 0.0 ? 0.0 : norm < __builtin_inf() ? 1.0 / norm : __builtin_nan("");
+  __syncthreads();
+  for (int i = t; i < side * side; i += SSTEP_THR) R[i / side * SPITCH + i % side] *= inv * inv;
+  __syncthreads();
+  const bool here = w < tiles;
+  f64x4 acc = {0, 0, 0, 0};
+  auto store = [&](double* m) {
+    if (here)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) put(m, ti, tj, r, acc[r]);
+  };
+  for (int s = 0; s < a.steps; ++s) {
+    const double ca = a.coef[3 * s], cb = a.coef[3 * s + 1], cc = a.coef[3 * s + 2];
+    if (here) {
+      acc = short_product(R, R, ti, tj, a.blocks, lane);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = SB * ti + 4 * r + lane / 16, col = SB * tj + lane % 16;
+        const double v = cb * R[row * SPITCH + col] + cc * acc[r] + (row == col ? ca : 0.0);
+        put(P, ti, tj, r, v);
+        if (s == 0) put(Q, ti, tj, r, v);
+      }
+    }
+    __syncthreads();
+    f64x4 next = {0, 0, 0, 0};
+    if (here && s > 0) next = short_product(P, Q, ti, tj, a.blocks, lane);
+    if (here && s + 1 < a.steps) acc = short_product(P, R, ti, tj, a.blocks, lane);
+    __syncthreads();
+    if (s + 1 < a.steps) store(R);
+    if (s > 0) {
+      acc = next;
+      store(Q);
+    }
+    __syncthreads();
+    if (s + 1 < a.steps) {
+      if (here) acc = short_product(P, R, ti, tj, a.blocks, lane);
+      __syncthreads();
+      store(R);
+      __syncthreads();
+    }
+  }
+  for (int i = t; i < side * side; i += SSTEP_THR)
+    a.q[((int64_t)batch * NS_SHORT + i / side) * NS_SHORT + i % side] = (float)Q[i / side * SPITCH + i % side];
+  if (t == 0) a.inv[batch] = inv;
+}
+
+// X = Q U inv for 64 values of the long side, the momentum's store and the weight.
+template <typename TG, typename TM, typename TW>
+__global__ __launch_bounds__(256) void short_apply_kernel(ShortArgs a) {
+  __shared__ float turn[MT][MPITCH];
+  __shared__ __align__(16) float u[NS_SHORT * SUPITCH], q[NS_SHORT * SUPITCH];
+  const int t = threadIdx.x, tr = t >> 4, tc = 4 * (t & 15), batch = blockIdx.y, side = SB * a.blocks;
+  const MuonIn& in = a.in;
+  const int at = blockIdx.x * 64, r0 = in.tall ? at : 0, c0 = in.tall ? 0 : at;
+  MuonTile<TG, TM> v;
+  short_load(in, batch, at, v, turn);
+  const double inv = a.inv[batch];
+  for (int i = t; i < side * side; i += 256) q[i / side * SUPITCH + i % side] = a.q[((int64_t)batch * NS_SHORT + i / side) * NS_SHORT + i % side];
+  short_stage(in, v, inv, u);
+  const float lr_now = a.lr_by ? a.lr * *a.lr_by : a.lr, keep = 1.0f - lr_now * a.decay, step = lr_now * a.scale;
+  if (in.m) {
+    TM* m = (TM*)in.m + batch * in.sm;
+    const bool vm = muon_vec<TM>(in.m, in.ldm, in.sm);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (r0 + tr + 16 * k < in.rows) muon_put4<TM>(m + (r0 + tr + 16 * k) * in.ldm, c0 + tc, in.cols, vm, v.m4[k]);
+  }
+  __syncthreads();
+  // x[k][e]: the weight's row tr + 16 k, column tc + e of the tile
+  float x[4][4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[k][e] = 0.0f;
+  if (!in.tall) {
+    for (int j = 0; j < side; ++j) {
+      const float4 b = *(const float4*)(u + j * SUPITCH + tc);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float f = k < a.blocks ? q[(tr + 16 * k) * SUPITCH + j] : 0.0f;
+        x[k][0] = __builtin_fmaf(f, b.x, x[k][0]); x[k][1] = __builtin_fmaf(f, b.y, x[k][1]);
+        x[k][2] = __builtin_fmaf(f, b.z, x[k][2]); x[k][3] = __builtin_fmaf(f, b.w, x[k][3]);
+      }
+    }
+  } else if (tc < side) {
+    for (int j = 0; j < side; ++j) {
+      const float4 b = *(const float4*)(q + j * SUPITCH + tc);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float f = u[j * SUPITCH + tr + 16 * k];
+        x[k][0] = __builtin_fmaf(f, b.x, x[k][0]); x[k][1] = __builtin_fmaf(f, b.y, x[k][1]);
+        x[k][2] = __builtin_fmaf(f, b.z, x[k][2]); x[k][3] = __builtin_fmaf(f, b.w, x[k][3]);
+      }
+    }
+  }
+  TW* wp = (TW*)a.w + batch * a.sw;
+  const bool vw = muon_vec<TW>(a.w, a.ldw, a.sw);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int r = r0 + tr + 16 * k;
+    if (r >= in.rows) continue;
+    TW* p = wp + r * a.ldw;
+    float4 o = make_float4(x[k][0], x[k][1], x[k][2], x[k][3]);
+    if (a.update) {
+      const float4 old = muon_get4<TW>(p, c0 + tc, in.cols, vw);
+      o = make_float4(keep * old.x - step * o.x, keep * old.y - step * o.y, keep * old.z - step * o.z, keep * old.w - step * o.w);
+    }
+    muon_put4<TW>(p, c0 + tc, in.cols, vw, o);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
 struct NsPlan {
   int64_t mp, np, x, p;                       // padded sides; bytes of a matrix's X (hi or lo) and of its A or P
   int parts;
   size_t hi[2], lo[2], gram, poly, diag, part, bytes;
+  int chunks;                                 // short sides: workgroups that share the long one; 0: not short
+  size_t q, inv;
 };
 
 static NsPlan ns_plan(int64_t batch, int64_t rows, int64_t cols) {
@@ -754,6 +1050,15 @@ static NsPlan ns_plan(int64_t batch, int64_t rows, int64_t cols) {
     at += (bytes + 255) / 256 * 256;
     return here;
   };
+  if (m <= NS_SHORT) {
+    // fewer where their sums take long to join: of 6 or 10 tiles against 1 or 3
+    h.chunks = (int)std::min<int64_t>(ceil_div(n, 64), m > 32 ? 16 : 32);
+    h.part = take((size_t)(batch * h.chunks) * STILES * 256 * 8);
+    h.q = take((size_t)batch * NS_SHORT * NS_SHORT * 4);
+    h.inv = take((size_t)batch * 8);
+    h.bytes = at;
+    return h;
+  }
   for (int i = 0; i < 2; ++i) {
     h.hi[i] = take((size_t)(batch * h.x));
     h.lo[i] = take((size_t)(batch * h.x));
@@ -864,9 +1169,39 @@ static void muon_begin(const MuonIn& in, int64_t batch, hipStream_t stream) {
                      stream, in);
 }
 
+template <typename TG, typename TM>
+static void short_run(const ShortArgs& a, int64_t batch, bool w_bf16, hipStream_t stream) {
+  const int64_t n = a.in.tall ? a.in.rows : a.in.cols;
+  hipLaunchKernelGGL((short_gram_kernel<TG, TM>), dim3((unsigned)a.chunks, (unsigned)batch), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL(short_steps_kernel, dim3((unsigned)batch), dim3(SSTEP_THR), 0, stream, a);
+  const dim3 grid((unsigned)ceil_div(n, 64), (unsigned)batch);
+  if (w_bf16) hipLaunchKernelGGL((short_apply_kernel<TG, TM, bf16_t>), grid, dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((short_apply_kernel<TG, TM, float>), grid, dim3(256), 0, stream, a);
+}
+
 // X from `in`, the steps, and the last of them into g's weight.
 static void ns_run(const NsPlan& h, MuonIn in, NsArgs g, int64_t batch, const float* coef, int steps, float scale, uint8_t* ws,
                    hipStream_t stream) {
+  if (h.chunks) {
+    ShortArgs a = {};
+    a.in = in;
+    a.in.tall = in.rows > in.cols;
+    a.blocks = (int)ceil_div(std::min(in.rows, in.cols), SB);
+    a.chunks = h.chunks;
+    a.part = (double*)(ws + h.part); a.q = (float*)(ws + h.q); a.inv = (double*)(ws + h.inv);
+    std::copy(coef, coef + 3 * steps, a.coef);
+    a.steps = steps;
+    a.w = g.w; a.ldw = g.ldw; a.sw = g.sw; a.update = g.update;
+    a.lr = g.lr; a.lr_by = g.lr_by; a.decay = g.decay; a.scale = g.scale;
+    if (in.g_bf16) {
+      if (in.m_bf16) short_run<bf16_t, bf16_t>(a, batch, g.w_bf16, stream);
+      else short_run<bf16_t, float>(a, batch, g.w_bf16, stream);
+    } else {
+      if (in.m_bf16) short_run<float, bf16_t>(a, batch, g.w_bf16, stream);
+      else short_run<float, float>(a, batch, g.w_bf16, stream);
+    }
+    return;
+  }
   in.mp = (int)h.mp; in.np = (int)h.np; in.tall = in.rows > in.cols; in.parts = h.parts;
   in.part = (double*)(ws + h.part);
   in.scale = scale;
