@@ -50,7 +50,7 @@ struct KLoad {
 
 // MN-major operand (stored [K][MN]): a stage's 64 K rows of the tile's 64 T
 // values go to LDS as they are, 16-byte chunk c of row k at chunk c ^ 4 (k &
-// 3).  Chunks past the operand's width re-read its last one; K rows past its
+// 3), or, in rows of 8 chunks (T = 1), c ^ 4 (k / 2 & 1).  Chunks past the operand's width re-read its last one; K rows past its
 // end (krows) re-read the last row, whose products the other operand's zeros
 // take away.
 template <int T>
@@ -71,7 +71,7 @@ struct MnLoad {
 #pragma unroll
     for (int i = 0; i < 2 * T; ++i) {
       const int row = RPL * (2 * T * w + i) + lane / CH;
-      int lc = (lane % CH) ^ (4 * (row & 3));
+      int lc = (lane % CH) ^ (4 * (T == 1 ? row >> 1 & 1 : row & 3));
       lc = lc < lastc ? lc : lastc;
       if (i < 2) c[i] = (uint32_t)(lc << 4);
       off[i] = (uint32_t)row * (uint32_t)ld + (uint32_t)(lc << 4);

@@ -375,7 +375,7 @@ __device__ __forceinline__ void ns_triangle(int id, int n, int& row, int& col) {
 }
 
 template <int T, int MODE, typename TW>
-__global__ __launch_bounds__(256, T >= 3 ? 1 : 2) void ns_product_kernel(NsArgs g) {
+__global__ __launch_bounds__(256, T >= 3 ? 1 : T == 2 ? 2 : 4) void ns_product_kernel(NsArgs g) {
   __shared__ __align__(16) uint8_t smem[ns_smem<T>(MODE)];
   constexpr int LDA = MODE >= NS_STEP ? MNMAJ : KMAJ;
   constexpr int TILE = 64 * T;
@@ -430,7 +430,7 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : 2) void ns_product_kernel(NsArgs 
   const int jj = (lr & 15) >> 2;
   const uint32_t kb = (uint32_t)(lr * 128 + ((lg ^ swz_key(lr)) << 4));
   const uint32_t fba = LDA == KMAJ ? kb ^ (uint32_t)(wm << 5)
-                                   : (uint32_t)((8 * lg + jj) * (128 * T) + ((64 * jj) ^ (64 * wm)) + 32 * (lr >> 4) +
+                                   : (uint32_t)((8 * lg + jj) * (128 * T) + ((64 * (T == 1 ? jj >> 1 : jj)) ^ (64 * wm)) + 32 * (lr >> 4) +
                                                 16 * ((lr & 3) >> 1) + 8 * (lr & 1));
   const uint32_t fbb = kb ^ (uint32_t)(wn << 5);
   const int offA = LDA == KMAJ ? wm * 4096 : 0, offB = wn * 4096;
@@ -741,8 +741,8 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : 2) void ns_product_kernel(NsArgs 
 // steps' a I + b R + c R^2, and R <- (a I + b R + c R^2)^2 R after each.  So the
 // long side is gone through twice, for R and for Q U, and the steps between run
 // in one workgroup a matrix: three launches instead of 2 + 3 a step, of which
-// each takes 5 us or more here (16 x 4096 291 -> 44 us, 2 x 64 x 128 110 ->
-// 51).  What R's rounding adds to the small directions grows by a^2 = 12 a
+// each takes 5 us or more here (16 x 4096 291 -> 24 us, 64 x 1000
+// 147 -> 65).  What R's rounding adds to the small directions grows by a^2 = 12 a
 // step, 2e4 in five, and nothing takes it back as X X^T formed anew would: R is
 // held in 64 bits, and its products run on the 64-bit matrix instruction (a
 // product of 64 x 64 x 64 1.3 us; for 128 it would be 10).  The result is fp32's
@@ -989,6 +989,7 @@ __global__ __launch_bounds__(256) void short_apply_kernel(ShortArgs a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[k][e] = 0.0f;
   if (!in.tall) {
+#pragma unroll 4
     for (int j = 0; j < side; ++j) {
       const float4 b = *(const float4*)(u + j * SUPITCH + tc);
 #pragma unroll
@@ -999,6 +1000,7 @@ __global__ __launch_bounds__(256) void short_apply_kernel(ShortArgs a) {
       }
     }
   } else if (tc < side) {
+#pragma unroll 4
     for (int j = 0; j < side; ++j) {
       const float4 b = *(const float4*)(q + j * SUPITCH + tc);
 #pragma unroll
@@ -1132,19 +1134,28 @@ static pbs_status ns_scale(const char* what, const float* coef, int steps, float
   return PBS_OK;
 }
 
-// A product's tile: the one whose rounds of tiles take least.  A round of 256 x
-// 256 tiles, one a compute unit, is 1; of 192 x 192 ones, one a compute unit, or
-// of 128 x 128 ones, two a compute unit, about 0.6.
+// A product's tile: the one that takes least by this account, in us.  A stage of
+// 64 K values takes a compute unit `stage` for each tile that it holds, but a tile
+// no less than `alone`; what a tile takes beside its stages, `fixed`, is behind
+// another tile's stages where several share a compute unit (sides of 64 and 128).
+// Taken from A, A^2 and P X at 4 x 384 x 1100 to 16384 x 4096, with each tile
+// size; measured there in us (A): 1024 x 1024 9.5, 11.9, 17.3 and 27 with tiles
+// of 64, 128, 192 and 256; 2048 x 2048 22.6, 20.2, 28 and 44; 4096 x 4096 122, 95,
+// 74 and 92; three of these 328, 225, 213 and 208.
 constexpr int NS_CUS = 256;
-static int ns_tile(int64_t mp, int64_t np, int64_t batch, bool symmetric) {
+static int ns_tile(int64_t mp, int64_t np, int64_t nk, int64_t batch, bool symmetric) {
+  struct Cost { double stage, alone, fixed; };
+  static const Cost half[5] = {{}, {0.19, 0.40, 3.0}, {0.5, 0.5, 4.0}, {1.06, 1.06, 6.0}, {1.6, 1.6, 9.0}};
+  static const Cost whole[5] = {{}, {0.25, 0.40, 4.0}, {0.5, 0.5, 6.0}, {}, {1.6, 1.6, 20.0}};
   int best = 4;
-  double least = 1e30;
-  for (int t = 4; t >= 2; --t) {
+  double least = 1e300;
+  for (int t = 4; t >= 1; --t) {
     if (t == 3 && !symmetric) continue;
+    const Cost& c = symmetric ? half[t] : whole[t];
     const int64_t a = ceil_div(mp, 64 * t), b = ceil_div(np, 64 * t);
-    const int64_t tiles = batch * (symmetric ? a * (a + 1) / 2 : a * b), slots = t == 2 ? 2 * NS_CUS : NS_CUS;
-    const double cost = (double)ceil_div(tiles, slots) * (t == 4 ? 1.0 : 0.6);
-    if (cost < least - 1e-9) { least = cost; best = t; }
+    const double held = (double)ceil_div(batch * (symmetric ? a * (a + 1) / 2 : a * b), NS_CUS);
+    const double us = t >= 3 ? held * (nk * c.stage + c.fixed) : nk * std::max(c.alone, held * c.stage) + c.fixed;
+    if (us < least) { least = us; best = t; }
   }
   return best;
 }
@@ -1152,13 +1163,14 @@ static int ns_tile(int64_t mp, int64_t np, int64_t batch, bool symmetric) {
 template <int MODE, typename TW = float>
 static void ns_launch(NsArgs g, hipStream_t stream) {
   constexpr bool SYM = MODE <= NS_POLY;
-  const int t = ns_tile(g.mp, g.np, g.batch, SYM);
+  const int t = ns_tile(g.mp, g.np, (MODE == NS_GRAM ? g.np : g.mp) / 64, g.batch, SYM);
   g.tiles_n = (int)ceil_div(g.mp, 64 * t);
   g.tiles_m = SYM ? g.tiles_n : (int)ceil_div(g.np, 64 * t);
   g.per = SYM ? g.tiles_n * (g.tiles_n + 1) / 2 : g.tiles_m * g.tiles_n;
   const dim3 grid((unsigned)(g.per * g.batch)), block(256);
   if (t == 4) hipLaunchKernelGGL((ns_product_kernel<4, MODE, TW>), grid, block, 0, stream, g);
   else if (t == 2) hipLaunchKernelGGL((ns_product_kernel<2, MODE, TW>), grid, block, 0, stream, g);
+  else if (t == 1) hipLaunchKernelGGL((ns_product_kernel<1, MODE, TW>), grid, block, 0, stream, g);
   else if constexpr (SYM) hipLaunchKernelGGL((ns_product_kernel<3, MODE, TW>), grid, block, 0, stream, g);
 }
 
@@ -1275,8 +1287,8 @@ pbs_status pbs_orthogonalize(const void* x, pbs_format x_fmt, int64_t ldx, int64
   in.rows = (int)rows; in.cols = (int)cols; in.eps = eps;
   NsArgs g = {};
   g.w = y; g.ldw = ldy; g.sw = y_batch_stride; g.w_bf16 = 1;
-  log_dispatch("orthogonalize batch=%lld rows=%lld cols=%lld steps=%d tiles=%d,%d scale=%g", (long long)batch, (long long)rows,
-               (long long)cols, steps, 64 * ns_tile(h.mp, h.np, batch, true), 64 * ns_tile(h.mp, h.np, batch, false), scale);
+  log_dispatch("orthogonalize batch=%lld rows=%lld cols=%lld steps=%d scale=%g", (long long)batch, (long long)rows,
+               (long long)cols, steps, scale);
   ns_run(h, in, g, batch, coefficients, steps, scale, (uint8_t*)workspace, stream);
   return check_launch(what);
 }
@@ -1315,8 +1327,8 @@ pbs_status pbs_muon(void* w, pbs_format w_fmt, int64_t ldw, int64_t w_batch_stri
   NsArgs g = {};
   g.w = w; g.ldw = ldw; g.sw = w_batch_stride; g.w_bf16 = w_fmt == PBS_FMT_BF16;
   g.update = 1; g.lr = lr; g.lr_by = lr_factor; g.decay = weight_decay; g.scale = scale;
-  log_dispatch("muon batch=%lld rows=%lld cols=%lld steps=%d tiles=%d,%d scale=%g", (long long)batch, (long long)rows, (long long)cols,
-               steps, 64 * ns_tile(h.mp, h.np, batch, true), 64 * ns_tile(h.mp, h.np, batch, false), hold);
+  log_dispatch("muon batch=%lld rows=%lld cols=%lld steps=%d scale=%g", (long long)batch, (long long)rows, (long long)cols,
+               steps, hold);
   ns_run(h, in, g, batch, coefficients, steps, hold, (uint8_t*)workspace, stream);
   return check_launch(what);
 }
