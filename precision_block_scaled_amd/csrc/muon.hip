@@ -25,6 +25,14 @@
 //
 // A and P are symmetric: the tiles on and below the diagonal are formed and
 // stored twice, once transposed.
+//
+// Where the longer side exceeds the shorter, steps are taken together: with R =
+// X X^T and q = a I + b R + c R^2 of one step, the next step's R is q R q and its X
+// is q' q X, so the long side is gone through once a group and not once a step.  A
+// step alone takes 3 m^2 n + m^3 multiplications (symmetric products by half),
+// two together 3 m^2 n + 5 m^3, three 3 m^2 n + 9 m^3: 16384 x 4096 in five steps,
+// three and two together, 3.05 ms, one by one 4.63.  R's rounding errors grow by
+// q^2 a step until X X^T is formed anew, which is what limits a group (ns_groups).
 #include "device.hpp"
 #include "gemm_common.hpp"
 #include "host.hpp"
@@ -286,17 +294,26 @@ __global__ __launch_bounds__(256) void muon_start_kernel(MuonIn a) {
 // ---------------------------------------------------------------------------
 // The products
 // ---------------------------------------------------------------------------
-enum { NS_GRAM = 0, NS_POLY = 1, NS_STEP = 2, NS_LAST = 3 };
+// The products.  Symmetric, by half: A = X X^T; P from A^2; T = (D + P) R; Q from P
+// Q'.  Whole: the next X, and the last one into the weight.
+enum { NS_GRAM = 0, NS_POLY = 1, NS_TURN = 2, NS_JOIN = 3, NS_STEP = 4, NS_LAST = 5 };
+constexpr bool ns_symmetric(int mode) { return mode < NS_STEP; }
 
 struct NsArgs {
   const uint8_t *hi, *lo;  // X
   uint8_t *hi2, *lo2;      // the next X
-  uint8_t *gram, *poly;    // A, P: [batch][mp][mp] fp16
-  float* diag;             // [batch][mp]: P's diagonal
+  // symmetric products: operands [batch][mp][mp] fp16, of which src1 and src2 enter the
+  // sum by row1 (its row's value, times f1) and col2 (its column's, times f2)
+  const uint8_t *left, *right, *src1, *src2;
+  const float *row1, *col2;
+  float f1, f2, f;         // f: the product's own factor
+  uint8_t* out;
+  float* diag;             // the result's diagonal, [batch][mp]; whole products: Q's
+  const uint8_t* q;        // whole products: Q without its diagonal
   int mp, np, batch;
   int tiles_m, tiles_n, per; // tiles of a matrix
-  float a, b, c;
-  float inv;               // 1 / the power of two that X, A and P are held times
+  float a;
+  float inv;               // 1 / the power of two that X is held times
   // the last step: to y, or into the weight
   void* w;
   int64_t ldw, sw;
@@ -312,7 +329,7 @@ template <int T> constexpr int ns_pitch() { return 128 * T + 16; }      // stage
 template <int T> constexpr int ns_pitch4() { return 256 * T + 16; }     // and of fp32
 constexpr int NS_TALL_PITCH = 68;                                       // floats: staged columns of 64 rows
 template <int T> constexpr int ns_smem(int mode) {
-  return cmax(5 * tile_bytes<T>(), mode == NS_GRAM   ? 64 * T * ns_pitch<T>()
+  return cmax(5 * tile_bytes<T>(), mode == NS_GRAM ? 64 * T * ns_pitch<T>()
                                    : mode == NS_LAST ? 128 * ns_pitch<T>() + 64 * T * NS_TALL_PITCH * 4
                                                      : 256 * ns_pitch<T>());
 }
@@ -418,12 +435,12 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : T == 2 ? 2 : 4) void ns_product_k
   if constexpr (MODE == NS_GRAM) {
     la.init(g.hi + 2 * xs, (int64_t)g.np * 2, m0, g.mp, w);
     lb.init(g.hi + 2 * xs, (int64_t)g.np * 2, n0, g.mp, w);
-  } else if constexpr (MODE == NS_POLY) {
-    la.init(g.gram + 2 * ps, (int64_t)g.mp * 2, m0, g.mp, w);
-    lb.init(g.gram + 2 * ps, (int64_t)g.mp * 2, n0, g.mp, w);
+  } else if constexpr (ns_symmetric(MODE)) {
+    la.init(g.right + 2 * ps, (int64_t)g.mp * 2, m0, g.mp, w);
+    lb.init(g.left + 2 * ps, (int64_t)g.mp * 2, n0, g.mp, w);
   } else {
     la.init(g.hi + 2 * xs, (int64_t)g.np * 2, m0, g.np, g.mp, w);
-    lb.init(g.poly + 2 * ps, (int64_t)g.mp * 2, n0, g.mp, w);
+    lb.init(g.q + 2 * ps, (int64_t)g.mp * 2, n0, g.mp, w);
   }
 
   const int lr = lane & 31, lg = lane >> 5;
@@ -516,8 +533,8 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : T == 2 ? 2 : 4) void ns_product_k
   // The epilogue's sources of 64 rows, A or X's pair, a pass ahead in
   // registers: the first behind the last stage's products.
   constexpr int CHUNKS = 8 * T, PER = 2 * T;                  // 16-byte chunks a row, and a thread in 64 rows
-  const uint8_t* src = MODE == NS_POLY ? g.gram + 2 * ps : g.hi + 2 * xs;
-  const uint8_t* src2 = g.lo + 2 * xs;
+  const uint8_t* src = ns_symmetric(MODE) ? g.src1 + 2 * ps : g.hi + 2 * xs;
+  const uint8_t* src2 = ns_symmetric(MODE) ? g.src2 + 2 * ps : g.lo + 2 * xs;
   u32x4 v1[PER], v2[PER];
   auto fetch = [&](int j) {
 #pragma unroll
@@ -526,17 +543,17 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : T == 2 ? 2 : 4) void ns_product_k
       const int r = n0 + 64 * j + at / CHUNKS, c = m0 + 8 * (at % CHUNKS);
       const int64_t o = 2 * ((int64_t)(r < g.mp ? r : g.mp - 1) * M + (c < M ? c : M - 8));
       v1[k] = *(const u32x4*)(src + o);
-      if constexpr (MODE >= NS_STEP) v2[k] = *(const u32x4*)(src2 + o);
+      if constexpr (MODE >= NS_JOIN) v2[k] = *(const u32x4*)(src2 + o);
     }
   };
   if constexpr (MODE != NS_GRAM) fetch(0);
   const int srow = 32 * wn + lr;                              // the lane's row of 64
-  float own[T];                                               // a + P's diagonal there
-  if constexpr (MODE >= NS_STEP) {
+  float own[T];                                               // Q's or row1's value there
+  if constexpr (MODE >= NS_TURN) {
 #pragma unroll
     for (int j = 0; j < T; ++j) {
       const int row = n0 + 64 * j + srow;
-      own[j] = g.a + g.diag[(int64_t)mat * g.mp + (row < g.mp ? row : g.mp - 1)];
+      own[j] = (ns_symmetric(MODE) ? g.row1 : g.diag)[(int64_t)mat * g.mp + (row < g.mp ? row : g.mp - 1)];
     }
   }
   __builtin_amdgcn_sched_barrier(0);
@@ -590,11 +607,11 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : T == 2 ? 2 : 4) void ns_product_k
         for (int q = 0; q < 4; ++q) {
           f16x4 v;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) v[r] = (f16_t)(acc[i][j][4 * q + r] * g.inv);
+          for (int r = 0; r < 4; ++r) v[r] = (f16_t)(acc[i][j][4 * q + r] * g.f);
           *(f16x4*)(smem + (64 * j + srow) * PITCH + 2 * scol(i, q)) = v;
         }
     lds_barrier();
-    const BufferRows to = rows_of(g.gram + 2 * ps, n0, g.mp, g.mp), over = rows_of(g.gram + 2 * ps, m0, g.mp, g.mp);
+    const BufferRows to = rows_of(g.out + 2 * ps, n0, g.mp, g.mp), over = rows_of(g.out + 2 * ps, m0, g.mp, g.mp);
 #pragma unroll
     for (int j = 0; j < T; ++j) {
       store_rows(smem + 64 * j * PITCH, to, 64 * j, g.mp);
@@ -602,8 +619,8 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : T == 2 ? 2 : 4) void ns_product_k
     }
   } else {
     constexpr int AREA = 64 * PITCH;
-    const BufferRows to1 = MODE == NS_POLY ? rows_of(g.poly + 2 * ps, n0, g.mp, g.mp) : rows_of(g.hi2 + 2 * xs, n0, g.mp, g.np);
-    const BufferRows to2 = MODE == NS_POLY ? rows_of(g.poly + 2 * ps, m0, g.mp, g.mp) : rows_of(g.lo2 + 2 * xs, n0, g.mp, g.np);
+    const BufferRows to1 = ns_symmetric(MODE) ? rows_of(g.out + 2 * ps, n0, g.mp, g.mp) : rows_of(g.hi2 + 2 * xs, n0, g.mp, g.np);
+    const BufferRows to2 = ns_symmetric(MODE) ? rows_of(g.out + 2 * ps, m0, g.mp, g.mp) : rows_of(g.lo2 + 2 * xs, n0, g.mp, g.np);
     // The last step: four values of a row of the weight at a time, QPT a thread
     // and pass.  A tall weight's rows are the tile's columns, which are then
     // staged as rows.  Value 4 of step k in pass j lies k * krows rows on from the
@@ -650,13 +667,13 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : T == 2 ? 2 : 4) void ns_product_k
       for (int k = 0; k < PER; ++k) {
         const int at = t + 256 * k, o = at / CHUNKS * PITCH + 16 * (at % CHUNKS);
         *(u32x4*)(s1 + o) = v1[k];
-        if constexpr (MODE >= NS_STEP) *(u32x4*)(s2 + o) = v2[k];
+        if constexpr (MODE >= NS_JOIN) *(u32x4*)(s2 + o) = v2[k];
       }
       if (j + 1 < T) fetch(j + 1);
       if (MODE == NS_LAST && quads && g.update) fetch_w(j, 0);
       const int row = n0 + 64 * j + srow;
-      // P's diagonal: where the lane's row meets the tile's columns
-      const int dcol = MODE == NS_POLY && tm == tn ? row - m0 : -64 * T;
+      // the diagonal: where the lane's row meets the tile's columns
+      const int dcol = (MODE == NS_POLY || MODE == NS_JOIN) && tm == tn ? row - m0 : -64 * T;
       float dval = 0.0f;
       bool has = false;
       lds_barrier();
@@ -667,12 +684,20 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : T == 2 ? 2 : 4) void ns_product_k
           f16x4* p1 = (f16x4*)(s1 + srow * PITCH + 2 * scol(i, q));
           const f16x4 h = *p1;
           float v[4];
-          if constexpr (MODE == NS_POLY) {
+          if constexpr (ns_symmetric(MODE)) {
             const int at = dcol - scol(i, q);
-            f16x4 o;
+            f16x4 o, h2;
+            float4 c2;
+            if constexpr (MODE == NS_JOIN) {
+              h2 = *(const f16x4*)(s2 + srow * PITCH + 2 * scol(i, q));
+              const int col = m0 + scol(i, q);
+              c2 = *(const float4*)(g.col2 + (int64_t)mat * g.mp + (col < g.mp ? col : g.mp - 4));
+            }
+            const float r1 = MODE == NS_POLY ? g.f1 : own[j] * g.f1;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              v[r] = g.b * (float)h[r] + g.c * (acc[i][j][4 * q + r] * g.inv);
+              v[r] = r1 * (float)h[r] + acc[i][j][4 * q + r] * g.f;
+              if constexpr (MODE == NS_JOIN) v[r] += (r == 0 ? c2.x : r == 1 ? c2.y : r == 2 ? c2.z : c2.w) * g.f2 * (float)h2[r];
               dval = at == r ? v[r] : dval;
               o[r] = (f16_t)(at == r ? 0.0f : v[r]);
             }
@@ -684,7 +709,7 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : T == 2 ? 2 : 4) void ns_product_k
             f16x4 oh, ol;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              v[r] = own[j] * ((float)h[r] + (float)l[r] * (1.0f / NS_LO)) + acc[i][j][4 * q + r] * g.inv;
+              v[r] = own[j] * ((float)h[r] + (float)l[r] * (1.0f / NS_LO)) + acc[i][j][4 * q + r] * g.f;
               f16_t hh, ll;
               ns_split(v[r], hh, ll);
               oh[r] = hh;
@@ -701,9 +726,13 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : T == 2 ? 2 : 4) void ns_product_k
             }
           }
         }
-      if (MODE == NS_POLY && has && row < g.mp) g.diag[(int64_t)mat * g.mp + row] = dval * g.inv;
+      if (has && row < g.mp) {
+        const int64_t at = (int64_t)mat * g.mp + row;
+        if (MODE == NS_POLY) g.diag[at] = g.a + dval * g.inv;
+        if (MODE == NS_JOIN) g.diag[at] = own[j] * g.col2[at] + dval * g.inv;
+      }
       lds_barrier();
-      if constexpr (MODE == NS_POLY) {
+      if constexpr (ns_symmetric(MODE)) {
         store_rows(s1, to1, 64 * j, g.mp);
         if (tm != tn) store_transposed(s1, to2, 64 * j);
       } else if constexpr (MODE == NS_STEP) {
@@ -1030,10 +1059,13 @@ __global__ __launch_bounds__(256) void short_apply_kernel(ShortArgs a) {
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
+// The least short side from which two and three steps go together (see ns_groups).
+constexpr int64_t NS_PAIRS_FROM = 256, NS_THREE_FROM = 1024;
+
 struct NsPlan {
   int64_t mp, np, x, p;                       // padded sides; bytes of a matrix's X (hi or lo) and of its A or P
   int parts;
-  size_t hi[2], lo[2], gram, poly, diag, part, bytes;
+  size_t hi[2], lo[2], gram, poly, turn, poly2, join, diag, part, bytes;
   int chunks;                                 // short sides: workgroups that share the long one; 0: not short
   size_t q, inv;
 };
@@ -1067,7 +1099,12 @@ static NsPlan ns_plan(int64_t batch, int64_t rows, int64_t cols) {
   }
   h.gram = take((size_t)(batch * h.p));
   h.poly = take((size_t)(batch * h.p));
-  h.diag = take((size_t)(batch * h.mp) * 4);
+  if (h.mp >= NS_PAIRS_FROM && h.np > h.mp) {             // several steps together
+    h.turn = take((size_t)(batch * h.p));
+    h.poly2 = take((size_t)(batch * h.p));
+    h.join = take((size_t)(batch * h.p));
+  }
+  h.diag = take((size_t)(3 * batch * h.mp) * 4);
   h.part = take((size_t)(batch * h.parts) * 8);
   h.bytes = at;
   return h;
@@ -1107,24 +1144,27 @@ static pbs_status ns_check_matrix(const char* what, const char* name, const void
 // The power of two that X, A and P are held times: the largest up to 2^14 that
 // keeps all of them below fp16's largest value, 65504, with a third to spare for
 // roundings.  top: the largest singular value ahead of each step, at most 1 at
-// first, then the largest |p(s)| for s up to it (1024 points; between them p
+// first, then the largest |p(s)| for s up to it; qmax: the largest |a + b s^2 + c
+// s^4| of a step (1024 points; between them p
 // differs by less than its largest slope times half the step, which is added).
-static pbs_status ns_scale(const char* what, const float* coef, int steps, float* scale) {
+static pbs_status ns_scale(const char* what, const float* coef, int steps, float* scale, double* qmax) {
   double top = 1.0, most = 1.0;
   for (int k = 0; k < steps; ++k) {
     const double a = coef[3 * k], b = coef[3 * k + 1], c = coef[3 * k + 2];
     PBS_REQUIRE(std::isfinite(a) && std::isfinite(b) && std::isfinite(c), PBS_ERR_INVALID_ARG, "%s: coefficients of step %d are not finite",
                 what, k);
-    double next = 0.0, poly = 0.0;
+    double next = 0.0, poly = 0.0, q = 0.0;
     const double h = top / 1024, t2 = top * top;
     for (int i = 0; i <= 1024; ++i) {
       const double s = h * i, s2 = s * s;
       next = std::max(next, std::fabs(s * (a + s2 * (b + c * s2))));
       poly = std::max(poly, std::fabs(s2 * (b + c * s2)));
+      q = std::max(q, std::fabs(a + s2 * (b + c * s2)));
     }
     next += 0.5 * h * (std::fabs(a) + 3 * std::fabs(b) * t2 + 5 * std::fabs(c) * t2 * t2);
     poly += 0.5 * h * (2 * std::fabs(b) * top + 4 * std::fabs(c) * top * t2);
-    most = std::max({most, t2, poly, next});
+    most = std::max({most, t2, poly, next});              // A, P, X; T, top * next at most, lies between A and the next A
+    qmax[k] = q + 0.5 * h * (2 * std::fabs(b) * top + 4 * std::fabs(c) * top * t2);
     top = next;
     PBS_REQUIRE(most < 4096.0, PBS_ERR_INVALID_ARG, "%s: the coefficients let singular values grow past fp16's range (step %d)", what, k);
   }
@@ -1143,7 +1183,7 @@ static pbs_status ns_scale(const char* what, const float* coef, int steps, float
 // of 64, 128, 192 and 256; 2048 x 2048 22.6, 20.2, 28 and 44; 4096 x 4096 122, 95,
 // 74 and 92; three of these 328, 225, 213 and 208.
 constexpr int NS_CUS = 256;
-static int ns_tile(int64_t mp, int64_t np, int64_t nk, int64_t batch, bool symmetric) {
+static int ns_tile(int64_t mp, int64_t np, int64_t nk, int64_t batch, bool symmetric, double* time = nullptr) {
   struct Cost { double stage, alone, fixed; };
   static const Cost half[5] = {{}, {0.19, 0.40, 3.0}, {0.5, 0.5, 4.0}, {1.06, 1.06, 6.0}, {1.6, 1.6, 9.0}};
   static const Cost whole[5] = {{}, {0.25, 0.40, 4.0}, {0.5, 0.5, 6.0}, {}, {1.6, 1.6, 20.0}};
@@ -1157,12 +1197,13 @@ static int ns_tile(int64_t mp, int64_t np, int64_t nk, int64_t batch, bool symme
     const double us = t >= 3 ? held * (nk * c.stage + c.fixed) : nk * std::max(c.alone, held * c.stage) + c.fixed;
     if (us < least) { least = us; best = t; }
   }
+  if (time) *time = least;
   return best;
 }
 
 template <int MODE, typename TW = float>
 static void ns_launch(NsArgs g, hipStream_t stream) {
-  constexpr bool SYM = MODE <= NS_POLY;
+  constexpr bool SYM = ns_symmetric(MODE);
   const int t = ns_tile(g.mp, g.np, (MODE == NS_GRAM ? g.np : g.mp) / 64, g.batch, SYM);
   g.tiles_n = (int)ceil_div(g.mp, 64 * t);
   g.tiles_m = SYM ? g.tiles_n : (int)ceil_div(g.np, 64 * t);
@@ -1172,6 +1213,48 @@ static void ns_launch(NsArgs g, hipStream_t stream) {
   else if (t == 2) hipLaunchKernelGGL((ns_product_kernel<2, MODE, TW>), grid, block, 0, stream, g);
   else if (t == 1) hipLaunchKernelGGL((ns_product_kernel<1, MODE, TW>), grid, block, 0, stream, g);
   else if constexpr (SYM) hipLaunchKernelGGL((ns_product_kernel<3, MODE, TW>), grid, block, 0, stream, g);
+}
+
+// Steps taken together: `first` of them, then the others two and two where
+// `pairs`.  Each group's factor times which Q is held.
+struct NsGroups {
+  int first;
+  bool pairs;
+};
+
+// A group's time: A, P and the whole product, and for each step after the first
+// T, R, P and Q.
+static double ns_group_us(int64_t mp, int64_t np, int64_t batch, int steps) {
+  double gram, small, whole;
+  ns_tile(mp, np, np / 64, batch, true, &gram);
+  ns_tile(mp, np, mp / 64, batch, true, &small);
+  ns_tile(mp, np, mp / 64, batch, false, &whole);
+  return gram + whole + small * (1 + 4 * (steps - 1));
+}
+
+// How far R = A's rounding errors may grow within a group, by max(a + b s^2 + c
+// s^4)^2 a step: 12 a step for the Muon optimiser's steps.  Errors of the result in
+// emulation (noise; eight directions 30 times above it), one step, groups of 2,
+// a group of 3 and one of 2: 1024 x 2048 0.06, 0.1, 0.06% and 0.02, 0.06, 0.16%;
+// 256 x 1024 0.08, 0.07, 0.15% and 0.06, 0.13, 0.34%; 128 x 512 0.07, 0.06, 0.14%
+// and 0.10, 0.19, 0.47%.  So two steps go together from 256 on and three, at the
+// beginning, from 1024 (where they come later their errors are twice as large).
+constexpr double NS_PAIR_GROWTH = 16.0, NS_THREE_GROWTH = 200.0;
+
+static NsGroups ns_groups(int64_t mp, int64_t np, int64_t batch, int steps, const double* qmax) {
+  NsGroups r = {1, false};
+  if (mp < NS_PAIRS_FROM || np <= mp) return r;
+  const double one = ns_group_us(mp, np, batch, 1), two = ns_group_us(mp, np, batch, 2), three = ns_group_us(mp, np, batch, 3);
+  bool tame = true;
+  for (int k = 0; k + 1 < steps; ++k) tame = tame && qmax[k] * qmax[k] <= NS_PAIR_GROWTH;
+  if (!tame) return r;
+  r.pairs = two < 2 * one;
+  auto rest = [&](int n) { return r.pairs ? n / 2 * two + n % 2 * one : n * one; };
+  double least = one + rest(steps - 1);
+  if (r.pairs && steps >= 2 && two + rest(steps - 2) <= least) { least = two + rest(steps - 2); r.first = 2; }
+  if (mp >= NS_THREE_FROM && steps >= 3 && qmax[0] * qmax[0] * qmax[1] * qmax[1] <= NS_THREE_GROWTH && three + rest(steps - 3) < least)
+    r.first = 3;
+  return r;
 }
 
 template <typename TG, typename TM>
@@ -1192,7 +1275,7 @@ static void short_run(const ShortArgs& a, int64_t batch, bool w_bf16, hipStream_
 }
 
 // X from `in`, the steps, and the last of them into g's weight.
-static void ns_run(const NsPlan& h, MuonIn in, NsArgs g, int64_t batch, const float* coef, int steps, float scale, uint8_t* ws,
+static void ns_run(const NsPlan& h, MuonIn in, NsArgs g, int64_t batch, const float* coef, int steps, float scale, const double* qmax, uint8_t* ws,
                    hipStream_t stream) {
   if (h.chunks) {
     ShortArgs a = {};
@@ -1226,16 +1309,53 @@ static void ns_run(const NsPlan& h, MuonIn in, NsArgs g, int64_t batch, const fl
     else muon_begin<float, float>(in, batch, stream);
   }
   g.mp = (int)h.mp; g.np = (int)h.np; g.batch = (int)batch;
-  g.gram = ws + h.gram; g.poly = ws + h.poly; g.diag = (float*)(ws + h.diag);
   g.inv = 1.0f / scale;
   g.tall = in.tall; g.rows = in.rows; g.cols = in.cols;
-  for (int k = 0; k < steps; ++k) {
-    g.a = coef[3 * k]; g.b = coef[3 * k + 1]; g.c = coef[3 * k + 2];
-    g.hi = ws + h.hi[k & 1]; g.lo = ws + h.lo[k & 1];
-    g.hi2 = ws + h.hi[(k + 1) & 1]; g.lo2 = ws + h.lo[(k + 1) & 1];
+  const NsGroups groups = ns_groups(h.mp, h.np, batch, steps, qmax);
+  uint8_t *R = ws + h.gram, *T = ws + h.turn, *P = ws + h.poly, *P2 = ws + h.poly2, *J = ws + h.join;
+  float* diag[3] = {(float*)(ws + h.diag), (float*)(ws + h.diag) + batch * h.mp, (float*)(ws + h.diag) + 2 * batch * h.mp};
+  int turn = 0;
+  for (int k = 0; k < steps; ++turn) {
+    const int left = steps - k, n = std::min(left, k == 0 ? groups.first : groups.pairs ? 2 : 1);
+    g.hi = ws + h.hi[turn & 1]; g.lo = ws + h.lo[turn & 1];
+    g.hi2 = ws + h.hi[(turn + 1) & 1]; g.lo2 = ws + h.lo[(turn + 1) & 1];
+    g.f = g.inv; g.out = R;
     ns_launch<NS_GRAM>(g, stream);
-    ns_launch<NS_POLY>(g, stream);
-    if (k + 1 < steps) ns_launch<NS_STEP>(g, stream);
+    // the group's Q, held times qs, in q with its diagonal in dq
+    uint8_t* q = P;
+    float *dq = diag[0], qs = scale;
+    double most = qmax[k];
+    for (int i = 0; i < n; ++i, ++k) {
+      const float* c = coef + 3 * k;
+      uint8_t* p = i == 0 ? P : i == 1 ? P2 : P;
+      float* dp = i == 0 ? diag[0] : diag[1];
+      g.a = c[0];
+      g.left = g.right = g.src1 = R; g.f1 = c[1]; g.f = c[2] * g.inv; g.out = p; g.diag = dp;
+      ns_launch<NS_POLY>(g, stream);
+      if (i > 0) {
+        most *= qmax[k];
+        float to = qs;
+        while (to * most > 49152.0) to *= 0.5f;
+        uint8_t* j = i == 1 ? J : P2;
+        float* dj = i == 1 ? diag[2] : diag[0];
+        g.left = p; g.right = q; g.src1 = q; g.row1 = dp; g.f1 = to / qs; g.src2 = p; g.col2 = dq; g.f2 = to / scale;
+        g.f = to / (qs * scale); g.out = j; g.diag = dj;
+        const float inv = g.inv;
+        g.inv = 1.0f / to;
+        ns_launch<NS_JOIN>(g, stream);
+        g.inv = inv;
+        q = j; dq = dj; qs = to;
+      }
+      if (i + 1 < n) {
+        g.left = p; g.row1 = dp; g.f1 = 1.0f; g.f = g.inv;
+        g.right = g.src1 = R; g.out = T;
+        ns_launch<NS_TURN>(g, stream);
+        g.right = g.src1 = T; g.out = R;
+        ns_launch<NS_TURN>(g, stream);
+      }
+    }
+    g.q = q; g.diag = dq; g.f = 1.0f / qs;
+    if (k < steps) ns_launch<NS_STEP>(g, stream);
     else if (g.w_bf16) ns_launch<NS_LAST, bf16_t>(g, stream);
     else ns_launch<NS_LAST, float>(g, stream);
   }
@@ -1276,7 +1396,8 @@ pbs_status pbs_orthogonalize(const void* x, pbs_format x_fmt, int64_t ldx, int64
   const NsPlan h = none ? NsPlan{} : ns_plan(batch, rows, cols);
   if ((st = ns_check_call(what, coefficients, steps, eps, workspace, workspace_bytes, h.bytes)) != PBS_OK) return st;
   float scale;
-  if ((st = ns_scale(what, coefficients, steps, &scale)) != PBS_OK) return st;
+  double qmax[NS_MOST_STEPS];
+  if ((st = ns_scale(what, coefficients, steps, &scale, qmax)) != PBS_OK) return st;
   if (none) return PBS_OK;
   if ((st = ns_check_matrix(what, "x", x, x_fmt, batch, rows, cols, ldx, x_batch_stride, false)) != PBS_OK) return st;
   if ((st = ns_check_matrix(what, "y", y, PBS_FMT_BF16, batch, rows, cols, ldy, y_batch_stride, true)) != PBS_OK) return st;
@@ -1289,7 +1410,7 @@ pbs_status pbs_orthogonalize(const void* x, pbs_format x_fmt, int64_t ldx, int64
   g.w = y; g.ldw = ldy; g.sw = y_batch_stride; g.w_bf16 = 1;
   log_dispatch("orthogonalize batch=%lld rows=%lld cols=%lld steps=%d scale=%g", (long long)batch, (long long)rows,
                (long long)cols, steps, scale);
-  ns_run(h, in, g, batch, coefficients, steps, scale, (uint8_t*)workspace, stream);
+  ns_run(h, in, g, batch, coefficients, steps, scale, qmax, (uint8_t*)workspace, stream);
   return check_launch(what);
 }
 
@@ -1309,7 +1430,8 @@ pbs_status pbs_muon(void* w, pbs_format w_fmt, int64_t ldw, int64_t w_batch_stri
               "%s: lr, weight_decay and scale must be finite", what);
   PBS_REQUIRE(((uintptr_t)lr_factor & 3) == 0, PBS_ERR_INVALID_ARG, "%s: lr_factor is not aligned to its elements", what);
   float hold;
-  if ((st = ns_scale(what, coefficients, steps, &hold)) != PBS_OK) return st;
+  double qmax[NS_MOST_STEPS];
+  if ((st = ns_scale(what, coefficients, steps, &hold, qmax)) != PBS_OK) return st;
   if (none) return PBS_OK;
   if ((st = ns_check_matrix(what, "w", w, w_fmt, batch, rows, cols, ldw, w_batch_stride, true)) != PBS_OK) return st;
   if ((st = ns_check_matrix(what, "momentum", momentum, m_fmt, batch, rows, cols, ldm, m_batch_stride, true)) != PBS_OK) return st;
@@ -1329,7 +1451,7 @@ pbs_status pbs_muon(void* w, pbs_format w_fmt, int64_t ldw, int64_t w_batch_stri
   g.update = 1; g.lr = lr; g.lr_by = lr_factor; g.decay = weight_decay; g.scale = scale;
   log_dispatch("muon batch=%lld rows=%lld cols=%lld steps=%d scale=%g", (long long)batch, (long long)rows, (long long)cols,
                steps, hold);
-  ns_run(h, in, g, batch, coefficients, steps, hold, (uint8_t*)workspace, stream);
+  ns_run(h, in, g, batch, coefficients, steps, hold, qmax, (uint8_t*)workspace, stream);
   return check_launch(what);
 }
 

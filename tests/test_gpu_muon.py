@@ -242,6 +242,22 @@ def test_large_square():
         assert ((got.double() - want).norm() / want.norm()).item() < 2.0 ** -9
 
 
+@pytest.mark.parametrize("kind", ["noise", "low", "lower"])
+@pytest.mark.parametrize("r,c", [(130, 1900), (200, 12000), (2100, 300), (1024, 4096), (4500, 1100), (1030, 2100)])
+def test_long_sides(r, c, kind):
+    """Sides of which the longer is several times the shorter, where steps are taken together: 64 bits on the GPU, within
+    the documented 0.2% and bf16's own rounding (0.17%)."""
+    x = matrix(r, c, kind).cuda()
+    for steps in (PL.MUON_STEPS, PL.MUON_STEPS[:2], PL.MUON_STEPS + PL.MUON_STEPS[:2]):
+        got, want = PL.orthogonalize(x, coefficients=steps), orthogonal(x, steps)
+        off = (got.double() - want).norm() / want.norm()
+        assert off.item() < (0.002 ** 2 + 0.0018 ** 2) ** 0.5, (len(steps), off.item())
+        assert torch.equal(got, PL.orthogonalize(x, coefficients=steps))
+    b = torch.stack([x, 2 * x])
+    got = PL.orthogonalize(b, coefficients=PL.MUON_STEPS[:2], eps=0.0)
+    assert torch.equal(got[0], got[1])
+
+
 def test_a_step_around_the_projection():
     """QKV product, norm and rotation, attention, their gradients with the maximum, the quantized products, the update."""
     torch.manual_seed(0)
