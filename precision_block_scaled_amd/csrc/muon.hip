@@ -546,7 +546,7 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : T == 2 ? 2 : 4) void ns_product_k
       if constexpr (MODE >= NS_JOIN) v2[k] = *(const u32x4*)(src2 + o);
     }
   };
-  if constexpr (MODE != NS_GRAM) fetch(0);
+  if constexpr (MODE != NS_GRAM && MODE != NS_LAST) fetch(0);
   const int srow = 32 * wn + lr;                              // the lane's row of 64
   float own[T];                                               // Q's or row1's value there
   if constexpr (MODE >= NS_TURN) {
@@ -625,9 +625,9 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : T == 2 ? 2 : 4) void ns_product_k
     // and pass.  A tall weight's rows are the tile's columns, which are then
     // staged as rows.  Value 4 of step k in pass j lies k * krows rows on from the
     // thread's first, and j * 64 rows (columns, if tall).
-    constexpr int QUADS = 16 * T, QPT = 64 * QUADS / 256, AHEAD = QPT / 2;
+    constexpr int QUADS = 16 * T, QPT = 64 * QUADS / 256, AHEAD = sizeof(TW) == 2 || QPT < 2 ? QPT : QPT / 2;
     const float lr_now = MODE == NS_LAST && g.lr_by ? g.lr * *g.lr_by : g.lr;
-    const float keep = 1.0f - lr_now * g.decay, step = lr_now * g.scale;
+    const float keep = 1.0f - lr_now * g.decay, step = g.update ? lr_now * g.scale : -1.0f;
     const int row_step = g.tall ? 1 : PITCH4 / 4, col_step = g.tall ? NS_TALL_PITCH : 1;      // of the staged fp32
     const int krows = g.tall ? 16 : 256 / QUADS, kstage = g.tall ? 16 * NS_TALL_PITCH : 256 / QUADS * (PITCH4 / 4);
     const int first = g.tall ? (t >> 4) * NS_TALL_PITCH + 4 * (t & 15) : t / QUADS * (PITCH4 / 4) + 4 * (t % QUADS);
@@ -644,18 +644,18 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : T == 2 ? 2 : 4) void ns_product_k
     const uint32_t ldb32 = (uint32_t)ldb;
     auto w_at = [&](int j, int k) {
       const int c = wcol + (g.tall ? 64 * j : 0), r = qrow + k * krows + (g.tall ? 0 : 64 * j);
-      return c < g.cols && w0 + r < g.rows ? (uint32_t)r * ldb32 + (uint32_t)(c * (int)sizeof(TW)) : NOWHERE;
+      return quads && c < g.cols && w0 + r < g.rows ? (uint32_t)r * ldb32 + (uint32_t)(c * (int)sizeof(TW)) : NOWHERE;
     };
     MuonQuad<TW> old[AHEAD];
     auto fetch_w = [&](int j, int from) {
 #pragma unroll
-      for (int k = 0; k < AHEAD; ++k) old[k].load(wb.r, w_at(j, from + k));
+      for (int k = 0; k < AHEAD; ++k) old[k].load(wb.r, g.update ? w_at(j, from + k) : NOWHERE);
     };
     auto put_w = [&](int j, int from, const float* f) {
 #pragma unroll
       for (int k = 0; k < AHEAD; ++k) {
         float4 v = *(const float4*)(f + first + (from + k) * kstage);
-        if (g.update) v = old[k].moved(keep, step, v);
+        v = old[k].moved(keep, step, v);                       // (no update: 0 and x)
         MuonQuad<TW>::store(wb.r, w_at(j, from + k), v);
       }
     };
@@ -663,14 +663,17 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : T == 2 ? 2 : 4) void ns_product_k
     for (int j = 0; j < T; ++j) {
       uint8_t* s1 = smem + (MODE == NS_LAST ? 0 : (j & 1) * 2 * AREA);
       uint8_t* s2 = s1 + AREA;
+      // (the last step has the weight to fetch ahead: with X's pair a pass ahead too,
+      // registers spill, and a spilled load is waited for, 10 us a pass)
+      if constexpr (MODE == NS_LAST) fetch(j);
 #pragma unroll
       for (int k = 0; k < PER; ++k) {
         const int at = t + 256 * k, o = at / CHUNKS * PITCH + 16 * (at % CHUNKS);
         *(u32x4*)(s1 + o) = v1[k];
         if constexpr (MODE >= NS_JOIN) *(u32x4*)(s2 + o) = v2[k];
       }
-      if (j + 1 < T) fetch(j + 1);
-      if (MODE == NS_LAST && quads && g.update) fetch_w(j, 0);
+      if (MODE != NS_LAST && j + 1 < T) fetch(j + 1);
+      if constexpr (MODE == NS_LAST) fetch_w(j, 0);
       const int row = n0 + 64 * j + srow;
       // the diagonal: where the lane's row meets the tile's columns
       const int dcol = (MODE == NS_POLY || MODE == NS_JOIN) && tm == tn ? row - m0 : -64 * T;
@@ -740,11 +743,12 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : T == 2 ? 2 : 4) void ns_product_k
         store_rows(s2, to2, 64 * j, g.np);
       } else {
         const float* f = (const float*)(smem + 2 * AREA);
-        if (quads) {
-          put_w(j, 0, f);
-          if (g.update) fetch_w(j, AHEAD);
+        put_w(j, 0, f);
+        if constexpr (AHEAD < QPT) {
+          fetch_w(j, AHEAD);
           put_w(j, AHEAD, f);
-        } else {
+        }
+        if (!quads) {
           const int r = w0 + qrow + (g.tall ? 0 : 64 * j), c = wcol + (g.tall ? 64 * j : 0);
           TW* p = weight + (r - w0) * g.ldw;
 #pragma unroll 1
