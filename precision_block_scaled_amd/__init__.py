@@ -11,7 +11,9 @@ succeeds but the first call raises ``PBSError`` -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 __all__ = [
     "PBSError", "lib", "lib_path",
@@ -45,7 +47,7 @@ lib_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpbs.so")
 
 _c = ctypes
 _vp, _i64, _i32, _u64, _f32 = _c.c_void_p, _c.c_int64, _c.c_int, _c.c_uint64, _c.c_float
-_i64p, _f32p = _c.POINTER(_c.c_int64), _c.POINTER(_c.c_float)
+_f32p = _c.POINTER(_c.c_float)
 
 # name -> (restype, argtypes); mirrors include/pbs.h
 SIGNATURES = {
@@ -77,12 +79,12 @@ SIGNATURES = {
                                   _c.c_size_t, _vp]),
     "pbs_linear_distill_grad": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _f32, _vp, _i64, _vp,
                                        _vp, _i32, _vp, _c.c_size_t, _vp]),
-    "pbs_qk_norm_rope": (_i32, [_vp, _i64p, _i64, _vp, _i64p, _i64, _i32, _i64, _i64, _i64, _vp, _vp, _i32, _i32, _f32,
-                                _vp, _i64, _vp, _i64, _i32, _vp, _i64p, _vp, _i64p, _i32, _vp]),
+    "pbs_qk_norm_rope": (_i32, [_vp, _vp, _i64, _vp, _vp, _i64, _i32, _i64, _i64, _i64, _vp, _vp, _i32, _i32, _f32,
+                                _vp, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _i32, _vp]),
     "pbs_qk_norm_rope_grad_bytes": (_i32, [_i64, _i64, _i64, _c.POINTER(_c.c_size_t)]),
-    "pbs_qk_norm_rope_grad": (_i32, [_vp, _i64p, _vp, _i64p, _vp, _i64p, _i32, _vp, _i64p, _i64, _vp, _i64p, _i64, _i32,
+    "pbs_qk_norm_rope_grad": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i64, _vp, _vp, _i64, _i32,
                                      _i64, _i64, _i64, _vp, _vp, _i32, _i32, _f32, _vp, _i64, _vp, _i64, _i32, _vp,
-                                     _i64p, _vp, _i64p, _vp, _i64p, _vp, _vp, _vp, _vp, _c.c_size_t, _vp]),
+                                     _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c.c_size_t, _vp]),
     "pbs_orthogonalize_bytes": (_i32, [_i64, _i64, _i64, _c.POINTER(_c.c_size_t)]),
     "pbs_orthogonalize": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _i64, _f32p, _i32, _f32, _vp, _i64, _i64, _vp,
                                  _c.c_size_t, _vp]),
@@ -126,16 +128,19 @@ def lib():
 
 
 def _ptr(x):
-    if x is None:
-        return None
+    if x is None or type(x) is int:
+        return x
     if isinstance(x, int):
         return x
     return x.data_ptr()
 
 
+_pack3 = struct.Struct("3q").pack
+
+
 def _strides(x):
     """Three int64 (batch, seq, head) as the C side takes them."""
-    return None if x is None else (_i64 * 3)(*x)
+    return None if x is None else _pack3(*x)
 
 
 def _stream(s):
@@ -294,12 +299,17 @@ def pbs_qk_norm_rope_grad(dq, dq_strides, dk, dk_strides, dv, dv_strides, y_fmt,
         _stream(stream)))
 
 
-def _triples(coefficients):
-    """Steps' (a, b, c) as the C side takes them, and their number."""
+@functools.lru_cache(maxsize=64)
+def _floats(coefficients):
     flat = [float(v) for step in coefficients for v in step]
-    if len(flat) != 3 * len(coefficients):
+    if any(len(step) != 3 for step in coefficients):
         raise ValueError("coefficients: want (a, b, c) for each step")
     return (_f32 * max(len(flat), 1))(*flat), len(coefficients)
+
+
+def _triples(coefficients):
+    """Steps' (a, b, c) as the C side takes them (read only), and their number."""
+    return _floats(tuple(map(tuple, coefficients)))
 
 
 def pbs_orthogonalize_bytes(batch, rows, cols):

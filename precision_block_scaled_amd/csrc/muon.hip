@@ -49,7 +49,7 @@ typedef _Float16 f16_t;
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float NS_LO = 2048.0f;           // a pair's lo is held times this
-constexpr int NS_PART = 1024;              // most partial sums of a matrix's norm
+constexpr int NS_PART = 2048;              // most partial sums of a matrix's norm
 
 // ---------------------------------------------------------------------------
 // Momentum, norm and the first X
@@ -137,6 +137,14 @@ __device__ __forceinline__ bool muon_vec(const void* p, int64_t ld, int64_t batc
   return (((uintptr_t)p & (4 * sizeof(T) - 1)) | (uint64_t)(ld & 3) | (uint64_t)(batch_stride & 3)) == 0;
 }
 
+// All waves meet with their LDS work done; loads and stores stay in flight
+// (__syncthreads would wait for them).
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // (Each product and sum is rounded by itself, as the formulas stand: a momentum
 // kept in bf16 then comes out as any fp32 evaluation of them has it.  A value
 // rounded the other way, 2^-8 of it, may move the small directions of the next
@@ -151,16 +159,31 @@ struct MuonTile {
     const int t = threadIdx.x, tr = t >> 4, tc = 4 * (t & 15);
     const TG* g = (const TG*)a.g + batch * a.sg;
     const bool vg = muon_vec<TG>(a.g, a.ldg, a.sg);
-    float4 gv[4];
+    // the momentum's loads first: they are in flight while the gradient is turned
+    float4 gv[4], o4[4];
+    if (a.m) {
+      const TM* m = (const TM*)a.m + batch * a.sm;
+      const bool vm = muon_vec<TM>(a.m, a.ldm, a.sm);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = r0 + tr + 16 * k;
+        o4[k] = r < a.rows ? muon_get4<TM>(m + r * a.ldm, c0 + tc, a.cols, vm) : make_float4(0, 0, 0, 0);
+      }
+    }
     if (a.g_transposed) {
-      __syncthreads();
+      float4 turned[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int c = tr + 16 * k;
-        const float4 v = c0 + c < a.cols ? muon_get4<TG>(g + (c0 + c) * a.ldg, r0 + tc, a.rows, vg) : make_float4(0, 0, 0, 0);
-        lds[tc][c] = v.x; lds[tc + 1][c] = v.y; lds[tc + 2][c] = v.z; lds[tc + 3][c] = v.w;
+        turned[k] = c0 + c < a.cols ? muon_get4<TG>(g + (c0 + c) * a.ldg, r0 + tc, a.rows, vg) : make_float4(0, 0, 0, 0);
       }
-      __syncthreads();
+      lds_barrier();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = tr + 16 * k;
+        lds[tc][c] = turned[k].x; lds[tc + 1][c] = turned[k].y; lds[tc + 2][c] = turned[k].z; lds[tc + 3][c] = turned[k].w;
+      }
+      lds_barrier();
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float* p = &lds[tr + 16 * k][tc];
@@ -178,12 +201,9 @@ struct MuonTile {
       for (int k = 0; k < 4; ++k) u[k] = gv[k];
       return;
     }
-    const TM* m = (const TM*)a.m + batch * a.sm;
-    const bool vm = muon_vec<TM>(a.m, a.ldm, a.sm);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int r = r0 + tr + 16 * k;
-      const float4 o = r < a.rows ? muon_get4<TM>(m + r * a.ldm, c0 + tc, a.cols, vm) : make_float4(0, 0, 0, 0);
+      const float4 o = o4[k];
       const float4 s = make_float4(a.one_less * gv[k].x, a.one_less * gv[k].y, a.one_less * gv[k].z, a.one_less * gv[k].w);
       float4 n;
       n.x = a.beta * o.x + s.x; n.y = a.beta * o.y + s.y; n.z = a.beta * o.z + s.z; n.w = a.beta * o.w + s.w;
@@ -239,6 +259,7 @@ __global__ __launch_bounds__(256) void muon_start_kernel(MuonIn a) {
   const int t = threadIdx.x, tr = t >> 4, tc = 4 * (t & 15);
   const int batch = blockIdx.y;
   double s = 0.0;
+#pragma unroll 8
   for (int i = t; i < a.parts; i += 256) s += a.part[(int64_t)batch * a.parts + i];
   s = wave_sum_d(s);
   if ((t & 63) == 0) sums[t >> 6] = s;
@@ -332,14 +353,6 @@ template <int T> constexpr int ns_smem(int mode) {
   return cmax(5 * tile_bytes<T>(), mode == NS_GRAM ? 64 * T * ns_pitch<T>()
                                    : mode == NS_LAST ? 128 * ns_pitch<T>() + 64 * T * NS_TALL_PITCH * 4
                                                      : 256 * ns_pitch<T>());
-}
-
-// All waves meet with their LDS work done; loads and stores stay in flight
-// (__syncthreads would wait for them).
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
 }
 
 template <int T>

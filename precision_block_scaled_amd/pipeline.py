@@ -614,10 +614,10 @@ def _heads4(name, t, device, shape=None, dtype=None):
         raise ValueError(f"{name}: want {dtype or 'bf16 or fp32'}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, want {device}")
-    s = t.stride()
-    if t.shape[3] > 1 and s[3] != 1:
+    sb, ss, sh, sd = t.stride()
+    if sd != 1 and t.shape[3] > 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
-    return s[:3]
+    return sb, ss, sh
 
 
 def _qk_common(q, k, q_weight, k_weight, positions, freqs, norm, eps):
@@ -691,11 +691,12 @@ def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, positions=None, freqs=
     with _on(dev, stream):
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=out_dtype, device=dev)
-            oq = q_out.stride()[:3]
+            oq = (S * H * D, H * D, D)
         if k is not None and k_out is None:
             k_out = torch.empty(k.shape, dtype=out_dtype, device=dev)
-            ok = k_out.stride()[:3]
-        pbs_qk_norm_rope(q, sq, H, k, sk, kv, x_fmt, B, S, D, *args, interleaved, q_out, oq, k_out, ok,
+            ok = (S * kv * D, kv * D, D)
+        kp, ko = (None, None) if k is None else (k.data_ptr(), k_out.data_ptr())
+        pbs_qk_norm_rope(q.data_ptr(), sq, H, kp, sk, kv, x_fmt, B, S, D, *args, interleaved, q_out.data_ptr(), oq, ko, ok,
                          FMT_OF[out_dtype], _current(dev))
     return q_out, k_out
 
