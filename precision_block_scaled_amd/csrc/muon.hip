@@ -349,8 +349,9 @@ struct NsArgs {
 template <int T> constexpr int ns_pitch() { return 128 * T + 16; }      // staged rows of fp16
 template <int T> constexpr int ns_pitch4() { return 256 * T + 16; }     // and of fp32
 constexpr int NS_TALL_PITCH = 68;                                       // floats: staged columns of 64 rows
-template <int T> constexpr int ns_smem(int mode) {
-  return cmax(5 * tile_bytes<T>(), mode == NS_GRAM ? 64 * T * ns_pitch<T>()
+// D: stages that loads are ahead of the products
+template <int T> constexpr int ns_smem(int mode, int d) {
+  return cmax((2 * d + 1) * tile_bytes<T>(), mode == NS_GRAM ? 64 * T * ns_pitch<T>()
                                    : mode == NS_LAST ? 128 * ns_pitch<T>() + 64 * T * NS_TALL_PITCH * 4
                                                      : 256 * ns_pitch<T>());
 }
@@ -404,9 +405,18 @@ __device__ __forceinline__ void ns_triangle(int id, int n, int& row, int& col) {
   row = col + in;
 }
 
-template <int T, int MODE, typename TW>
-__global__ __launch_bounds__(256, T >= 3 ? 1 : T == 2 ? 2 : 4) void ns_product_kernel(NsArgs g) {
-  __shared__ __align__(16) uint8_t smem[ns_smem<T>(MODE)];
+// The last stages but one.
+template <int LEFT, typename Body>
+__device__ __forceinline__ void ns_tail(int nk, Body& body) {
+  if constexpr (LEFT > 1) {
+    if (nk >= LEFT) body(nk - LEFT, std::integral_constant<int, LEFT>{});
+    ns_tail<LEFT - 1>(nk, body);
+  }
+}
+
+template <int T, int D, int MODE, typename TW>
+__global__ __launch_bounds__(256, T >= 3 ? 1 : (T == 2 ? 4 : 8) / D) void ns_product_kernel(NsArgs g) {
+  __shared__ __align__(16) uint8_t smem[ns_smem<T>(MODE, D)];
   constexpr int LDA = MODE >= NS_STEP ? MNMAJ : KMAJ;
   constexpr int TILE = 64 * T;
   const int t = threadIdx.x, lane = t & 63;
@@ -432,8 +442,8 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : T == 2 ? 2 : 4) void ns_product_k
   // M, the results' contiguous axis, and the contraction's stages
   const int M = MODE >= NS_STEP ? g.np : g.mp, nk = (MODE == NS_GRAM ? g.np : g.mp) / 64;
 
-  auto tileA = [&](int kt) { return smem + (kt & 1) * tile_bytes<T>(); };
-  auto tileB = [&](int kt) { return smem + 2 * tile_bytes<T>() + kt % 3 * tile_bytes<T>(); };
+  auto tileA = [&](int kt) { return smem + kt % D * tile_bytes<T>(); };
+  auto tileB = [&](int kt) { return smem + D * tile_bytes<T>() + kt % (D + 1) * tile_bytes<T>(); };
 
   f32x16 acc[T][T];
 #pragma unroll
@@ -477,29 +487,28 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : T == 2 ? 2 : 4) void ns_product_k
   };
 
 #pragma unroll
-  for (int v = 0; v < NL; ++v) load_a(0, v);
+  for (int k = 0; k < D; ++k)
+    if (k < nk) {
 #pragma unroll
-  for (int v = 0; v < NL; ++v) load_b(0, v);
-  if (nk > 1) {
+      for (int v = 0; v < NL; ++v) load_a(k, v);
 #pragma unroll
-    for (int v = 0; v < NL; ++v) load_a(1, v);
-#pragma unroll
-    for (int v = 0; v < NL; ++v) load_b(1, v);
-    stage_barrier<2 * NL>();
-  } else {
-    stage_barrier<0>();
-  }
+      for (int v = 0; v < NL; ++v) load_b(k, v);
+    }
+  if (nk >= D) stage_barrier<(D - 1) * 2 * NL>();
+  else stage_barrier<0>();
 #pragma unroll
   for (int d = 0; d < RA; ++d) ns_read<0, LDA, T>(a0, d, tileA(0) + offA, fba);
 #pragma unroll
   for (int d = 0; d < RB; ++d) ns_read<0, KMAJ, T>(b0, d, tileB(0) + offB, fbb);
 
-  // A's stages go through two LDS buffers, B's through three, so that the loads
-  // of stage kt + 2 spread over the whole of stage kt; see head.hip's products,
-  // whose schedule this is.
-  auto body = [&](int kt, auto issue_c, auto next_c) {
-    constexpr bool ISSUE = decltype(issue_c)::value;
-    constexpr bool NEXT = decltype(next_c)::value;
+  // A's stages go through D LDS buffers, B's through D + 1, so that the loads of
+  // stage kt + D spread over the whole of stage kt: B's while the first half of
+  // the stage is multiplied, A's, into the buffer that was just read out, while
+  // the second is.  LEFT: stages from this one on, D + 1 if more than D, which
+  // are then loaded ahead.
+  auto body = [&](int kt, auto left_c) {
+    constexpr int LEFT = decltype(left_c)::value;
+    constexpr bool ISSUE = LEFT > D, NEXT = LEFT > 1;
     const uint8_t* curA = tileA(kt) + offA;
     const uint8_t* curB = tileB(kt) + offB;
     const uint8_t* nxtA = tileA(kt + 1) + offA;
@@ -515,12 +524,13 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : T == 2 ? 2 : 4) void ns_product_k
       }
       if (ISSUE) {
 #pragma unroll
-        for (int v = part_lo(NL, NMFMA, m); v < part_hi(NL, NMFMA, m); ++v) load_b(kt + 2, v);
+        for (int v = part_lo(NL, NMFMA, m); v < part_hi(NL, NMFMA, m); ++v) load_b(kt + D, v);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
     // (the last stage's loads were waited for in the one before; what is in flight then is the epilogue's)
-    if constexpr (NEXT) stage_barrier<ISSUE ? NL : 0>();
+    if constexpr (ISSUE) stage_barrier<(D - 2) * 2 * NL + NL>();
+    else if constexpr (NEXT) stage_barrier<(LEFT - 2) * 2 * NL>();
     else lds_barrier();
     constexpr int NDS = NEXT ? RA + RB : 0;
 #pragma unroll
@@ -534,15 +544,13 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : T == 2 ? 2 : 4) void ns_product_k
       }
       if (ISSUE) {
 #pragma unroll
-        for (int v = part_lo(NL, NMFMA, m); v < part_hi(NL, NMFMA, m); ++v) load_a(kt + 2, v);
+        for (int v = part_lo(NL, NMFMA, m); v < part_hi(NL, NMFMA, m); ++v) load_a(kt + D, v);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  using T_ = std::integral_constant<bool, true>;
-  using F_ = std::integral_constant<bool, false>;
-  for (int kt = 0; kt < nk - 2; ++kt) body(kt, T_{}, T_{});
-  if (nk >= 2) body(nk - 2, F_{}, T_{});
+  for (int kt = 0; kt < nk - D; ++kt) body(kt, std::integral_constant<int, D + 1>{});
+  ns_tail<D>(nk, body);
   // The epilogue's sources of 64 rows, A or X's pair, a pass ahead in
   // registers: the first behind the last stage's products.
   constexpr int CHUNKS = 8 * T, PER = 2 * T;                  // 16-byte chunks a row, and a thread in 64 rows
@@ -570,7 +578,7 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : T == 2 ? 2 : 4) void ns_product_k
     }
   }
   __builtin_amdgcn_sched_barrier(0);
-  body(nk - 1, F_{}, F_{});
+  body(nk - 1, std::integral_constant<int, 1>{});
 
   // Every LDS read of the loop finished before its last barrier, and no load to
   // LDS is in flight.  acc[i][j][4 q + r] is row n0 + 32 (2 j + wn) + lr, column m0 + 32
@@ -1077,7 +1085,7 @@ __global__ __launch_bounds__(256) void short_apply_kernel(ShortArgs a) {
 // Host
 // ---------------------------------------------------------------------------
 // The least short side from which two and three steps go together (see ns_groups).
-constexpr int64_t NS_PAIRS_FROM = 256, NS_THREE_FROM = 1024;
+constexpr int64_t NS_PAIRS_FROM = 512, NS_THREE_FROM = 1024;
 
 struct NsPlan {
   int64_t mp, np, x, p;                       // padded sides; bytes of a matrix's X (hi or lo) and of its A or P
@@ -1196,14 +1204,14 @@ static pbs_status ns_scale(const char* what, const float* coef, int steps, float
 // no less than `alone`; what a tile takes beside its stages, `fixed`, is behind
 // another tile's stages where several share a compute unit (sides of 64 and 128).
 // Taken from A, A^2 and P X at 4 x 384 x 1100 to 16384 x 4096, with each tile
-// size; measured there in us (A): 1024 x 1024 9.5, 11.9, 17.3 and 27 with tiles
+// size; measured there in us (A): 1024 x 1024 7.0, 11.9, 17.3 and 27 with tiles
 // of 64, 128, 192 and 256; 2048 x 2048 22.6, 20.2, 28 and 44; 4096 x 4096 122, 95,
 // 74 and 92; three of these 328, 225, 213 and 208.
 constexpr int NS_CUS = 256;
 static int ns_tile(int64_t mp, int64_t np, int64_t nk, int64_t batch, bool symmetric, double* time = nullptr) {
   struct Cost { double stage, alone, fixed; };
-  static const Cost half[5] = {{}, {0.19, 0.40, 3.0}, {0.5, 0.5, 4.0}, {1.06, 1.06, 6.0}, {1.6, 1.6, 9.0}};
-  static const Cost whole[5] = {{}, {0.25, 0.40, 4.0}, {0.5, 0.5, 6.0}, {}, {1.6, 1.6, 20.0}};
+  static const Cost half[5] = {{}, {0.19, 0.27, 3.0}, {0.5, 0.5, 4.0}, {1.06, 1.06, 6.0}, {1.6, 1.6, 9.0}};
+  static const Cost whole[5] = {{}, {0.25, 0.29, 4.0}, {0.5, 0.5, 6.0}, {}, {1.6, 1.6, 20.0}};
   int best = 4;
   double least = 1e300;
   for (int t = 4; t >= 1; --t) {
@@ -1226,10 +1234,17 @@ static void ns_launch(NsArgs g, hipStream_t stream) {
   g.tiles_m = SYM ? g.tiles_n : (int)ceil_div(g.np, 64 * t);
   g.per = SYM ? g.tiles_n * (g.tiles_n + 1) / 2 : g.tiles_m * g.tiles_n;
   const dim3 grid((unsigned)(g.per * g.batch)), block(256);
-  if (t == 4) hipLaunchKernelGGL((ns_product_kernel<4, MODE, TW>), grid, block, 0, stream, g);
-  else if (t == 2) hipLaunchKernelGGL((ns_product_kernel<2, MODE, TW>), grid, block, 0, stream, g);
-  else if (t == 1) hipLaunchKernelGGL((ns_product_kernel<1, MODE, TW>), grid, block, 0, stream, g);
-  else if constexpr (SYM) hipLaunchKernelGGL((ns_product_kernel<3, MODE, TW>), grid, block, 0, stream, g);
+  // Loads further ahead where few tiles leave LDS to spare: 136 tiles of 64 and 16
+  // stages 7.0 us instead of 9.9, but 528 of them and 32 stages 24 instead of 21;
+  // 136 tiles of 128 and 32 stages 19.4 instead of 21.0.  Eight stages ahead gained
+  // nothing over four.
+  const int64_t tiles = (int64_t)g.per * g.batch;
+  if (t == 4) hipLaunchKernelGGL((ns_product_kernel<4, 2, MODE, TW>), grid, block, 0, stream, g);
+  else if (t == 2 && tiles <= NS_CUS) hipLaunchKernelGGL((ns_product_kernel<2, 4, MODE, TW>), grid, block, 0, stream, g);
+  else if (t == 2) hipLaunchKernelGGL((ns_product_kernel<2, 2, MODE, TW>), grid, block, 0, stream, g);
+  else if (t == 1 && tiles <= 2 * NS_CUS) hipLaunchKernelGGL((ns_product_kernel<1, 4, MODE, TW>), grid, block, 0, stream, g);
+  else if (t == 1) hipLaunchKernelGGL((ns_product_kernel<1, 2, MODE, TW>), grid, block, 0, stream, g);
+  else if constexpr (SYM) hipLaunchKernelGGL((ns_product_kernel<3, 2, MODE, TW>), grid, block, 0, stream, g);
 }
 
 // Steps taken together: `first` of them, then the others two and two where
@@ -1254,7 +1269,7 @@ static double ns_group_us(int64_t mp, int64_t np, int64_t batch, int steps) {
 // emulation (noise; eight directions 30 times above it), one step, groups of 2,
 // a group of 3 and one of 2: 1024 x 2048 0.06, 0.1, 0.06% and 0.02, 0.06, 0.16%;
 // 256 x 1024 0.08, 0.07, 0.15% and 0.06, 0.13, 0.34%; 128 x 512 0.07, 0.06, 0.14%
-// and 0.10, 0.19, 0.47%.  So two steps go together from 256 on and three, at the
+// and 0.10, 0.19, 0.47%.  So two steps go together from 512 on and three, at the
 // beginning, from 1024 (where they come later their errors are twice as large).
 constexpr double NS_PAIR_GROWTH = 16.0, NS_THREE_GROWTH = 200.0;
 

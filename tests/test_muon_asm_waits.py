@@ -1,10 +1,10 @@
 """Static check of where the Newton-Schulz products wait for their loads (CPU), as for the linear head's.
 
 In the middle of K stage k a wave waits for its loads of stage k + 1, all but
-those of B's stage k + 2 that it has just issued, and for its LDS reads, then
-meets the others: the counted wait has to leave out exactly the loads issued
-since the loop's start, and nothing else in the loop may wait for loads or move
-scratch memory.
+those of the stages after it up to the one D ahead, of which B's have been
+issued, and for its LDS reads, then meets the others: the counted wait has to
+leave out exactly D - 2 stages' loads and the loop's own so far, and nothing
+else in the loop may wait for loads or move scratch memory.
 """
 import os
 import re
@@ -32,7 +32,7 @@ def kernels():
 
 
 def test_k_loops_wait_at_their_barrier_alone(kernels):
-    assert len(kernels) == 4 * 4 + 3 + 2 * 3        # symmetric products, the next X, the last one in two types
+    assert len(kernels) == 4 * 6 + 5 + 2 * 5        # symmetric products, the next X, the last one in two types
     for name, body in kernels.items():
         loops = [b for _, blocks in loop_blocks(body) for b in blocks if any(_op(l).startswith("v_mfma") for l in b)]
         assert len(loops) == 1, name
@@ -46,4 +46,5 @@ def test_k_loops_wait_at_their_barrier_alone(kernels):
         assert not any(o.startswith(("buffer_load", "ds_")) for o, _ in ops[waits[0]:at[0]]), name
         before = sum(o.startswith("buffer_load") for o, _ in ops[:waits[0]])
         after = sum(o.startswith("buffer_load") for o, _ in ops[at[0]:])
-        assert left == before == after > 0, (name, left, before, after)
+        ahead = int(re.search(r"ILi\d+ELi(\d+)E", name).group(1))
+        assert left == (ahead - 2) * (before + after) + before and before == after > 0, (name, left, before, after)
