@@ -466,7 +466,8 @@ pbs_status pbs_linear_distill_grad(const float* dloss, const void* x, const void
  *    and head in elements (three int64; the last axis is contiguous), so parts
  *    of a packed projection and [batch, heads, seq, head_dim] tensors are taken
  *    as they lie.  An output's rows do not overlap; q_out may be q itself (and
- *    k_out k) with its type and strides, otherwise outputs do not overlap inputs.
+ *    k_out k) with its type and strides, otherwise outputs overlap neither inputs
+ *    nor each other.
  *    heads or kv_heads 0: that tensor is left out (pointers may be NULL).
  *  q_weight, k_weight [head_dim]: w, bf16 or fp32 (w_fmt); NULL is 1.
  *  norm 0: r is 1 (rotation alone; eps unused).
@@ -480,7 +481,7 @@ pbs_status pbs_linear_distill_grad(const float* dloss, const void* x, const void
  *
  * pbs_qk_norm_rope_grad: from dq, dk (y_fmt), and q, k as the forward had them
  * (x_fmt), with g = dy turned back, v = g w, n = x r:
- *   dx = r (v - n mean(v n)),   dw = sum over tokens and heads of g n
+ *   dx = r (v - n mean(v n)),   dw = sum over tokens and heads of g n   (norm 0: dx = v)
  *  dq_out, dk_out: dx in x_fmt.  dv, dv_out (both or neither; kv_heads heads):
  *    dv is copied to dv_out in x_fmt, so that the three outputs may be the parts
  *    of one packed gradient of the projection's output.  An output may be the

@@ -316,7 +316,9 @@ struct QkRows {
 #pragma unroll
             for (int i = 0; i < 2 * CH; ++i) dot = __builtin_fmaf(g[k][i] * w[k][i], v[k][i], dot);
           }
-          const float r = a.norm ? 1.0f / sqrtf(group_sum<G>(sum) * inv + a.eps) : 1.0f;
+          // (a row past the heads adds nothing to dw: with eps 0 its zeros would give 0 / 0)
+          const float squares = group_sum<G>(sum) * inv + a.eps;
+          const float r = a.norm ? there ? 1.0f / sqrtf(squares) : 0.0f : 1.0f;
           const float mean = a.norm ? group_sum<G>(dot) * inv * r : 0.0f;       // mean(v n)
 #pragma unroll
           for (int k = 0; k < NU; ++k)
@@ -324,7 +326,8 @@ struct QkRows {
             for (int i = 0; i < 2 * CH; ++i) {
               const float nrm = v[k][i] * r;
               dw[k][i] = __builtin_fmaf(g[k][i], nrm, dw[k][i]);
-              v[k][i] = r * (g[k][i] * w[k][i] - nrm * mean);
+              // (without the norm dx does not depend on x, whatever x is)
+              v[k][i] = r * (g[k][i] * w[k][i] - (a.norm ? nrm * mean : 0.0f));
             }
           mx = max(mx, store((TX*)p.out.p + o + (h + n * PER) * p.out.sh, there, v));
         }
@@ -338,7 +341,7 @@ template <typename TX, typename TY, int CH, bool INTER, int G, int NU>
 __global__ __launch_bounds__(QK_THR) void qk_norm_rope_kernel(QkArgs a) {
   __shared__ float2 cs[QK_WAVES][QK_MOST_DIM / 2];
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int64_t item = (int64_t)blockIdx.x * QK_WAVES + w;
+  int64_t item = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * QK_WAVES + w;
   if (item >= a.items) return;
   const int64_t queries = a.tokens * a.part[0].blocks;
   const int which = item < queries ? 0 : 1;
@@ -661,6 +664,7 @@ pbs_status pbs_qk_norm_rope(const void* q, const int64_t* q_strides, int64_t hea
                   "pbs_qk_norm_rope: %s is on an input's memory with another type or other strides", names[i][1]);
   }
   if (a.part[0].heads + a.part[1].heads == 0) return PBS_OK;
+  PBS_REQUIRE(a.part[0].out.p != a.part[1].out.p, PBS_ERR_INVALID_ARG, "pbs_qk_norm_rope: q_out and k_out are one tensor");
   a.pos = positions; a.pos_sb = pos_batch_stride; a.freqs = freqs;
   a.seq = (int)seq; a.dim = (int)head_dim; a.rot = (int)rot_dim;
   a.interleaved = c.interleaved; a.norm = c.norm; a.eps = eps; a.w_bf16 = c.w_bf16;
@@ -674,13 +678,14 @@ pbs_status pbs_qk_norm_rope(const void* q, const int64_t* q_strides, int64_t hea
     a.part[i].blocks = (int)ceil_div(a.part[i].heads, a.heads_each);
     a.items += a.tokens * a.part[i].blocks;
   }
-  const int64_t grid = ceil_div(a.items, QK_WAVES);
-  PBS_REQUIRE(grid < (1ll << 31), PBS_ERR_SHAPE, "pbs_qk_norm_rope: too many tokens and heads for one call");
+  // (an axis of a launch holds less than 2^32 threads)
+  const int64_t groups = ceil_div(a.items, QK_WAVES), along = std::min<int64_t>(groups, 1 << 22);
+  const dim3 grid((unsigned)along, (unsigned)ceil_div(groups, along));
   log_dispatch("qk_norm_rope tokens=%lld heads=%d+%d dim=%d rot=%d chunk=%d heads/wave=%d", (long long)a.tokens,
                a.part[0].heads, a.part[1].heads, a.dim, a.rot, ch, a.heads_each);
-  if (ch != 8) PBS_QK_FOUR_OR_ONE(qk_norm_rope_kernel, dim3((unsigned)grid));
-  else if (c.interleaved) PBS_QK_EIGHT(qk_norm_rope_kernel, dim3((unsigned)grid), true);
-  else PBS_QK_EIGHT(qk_norm_rope_kernel, dim3((unsigned)grid), false);
+  if (ch != 8) PBS_QK_FOUR_OR_ONE(qk_norm_rope_kernel, grid);
+  else if (c.interleaved) PBS_QK_EIGHT(qk_norm_rope_kernel, grid, true);
+  else PBS_QK_EIGHT(qk_norm_rope_kernel, grid, false);
   return check_launch("pbs_qk_norm_rope");
 }
 
@@ -741,6 +746,10 @@ pbs_status pbs_qk_norm_rope_grad(const void* dq, const int64_t* dq_strides, cons
     }
   }
   const int all = a.part[0].heads + a.part[1].heads + a.part[2].heads;
+  for (int i = 0; i < 3; ++i)
+    PBS_REQUIRE(!a.part[i].out.p || a.part[i].out.p != a.part[(i + 1) % 3].out.p, PBS_ERR_INVALID_ARG,
+                "pbs_qk_norm_rope_grad: %s and %s are one tensor", names[i][2], names[(i + 1) % 3][2]);
+  PBS_REQUIRE(!dq_weight || dq_weight != dk_weight, PBS_ERR_INVALID_ARG, "pbs_qk_norm_rope_grad: dq_weight and dk_weight are one vector");
   const bool sums = all && (dq_weight || dk_weight);
   if (sums || (all && amax_out)) {
     PBS_REQUIRE(workspace && ((uintptr_t)workspace & 15) == 0, PBS_ERR_INVALID_ARG,

@@ -351,3 +351,49 @@ def test_benchmark_layer_whole():
         assert ((o.double() - want[0]).abs() <= want[1]).all()
         assert ((w.double() - want[2]).abs() <= want[3]).all()
         del want
+
+
+@pytest.mark.parametrize("types", [(BF, BF, BF), (F32, F32, F32)], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("heads,dim,rot", [(1, 128, 128), (3, 64, 32), (5, 96, 96), (9, 256, 128), (1, 37, 36), (2, 512, 512)])
+def test_gradient_with_eps_zero(heads, dim, rot, inter, types):
+    """Rounds of heads that end behind the last head: what is not there adds nothing to the weights' gradients."""
+    tx, ty, tw = types
+    q, _, qw, _, dq, _, _, pos, freqs = make((2, 5, heads, 1, dim, rot), tx, ty, tw, seed=heads + dim)
+    cq, cqw, cdq, cpos, cf = cuda(q, qw, dq, pos, freqs)
+    g = PL.qk_norm_rope_grad(cdq, None, cq, None, cqw, None, cpos, cf, inter, 0.0)
+    check_grad(g[0], g[2], dq, q, qw, pos, freqs, inter, 0.0, True, 1, "q")
+
+
+def test_rotation_alone_and_values_that_are_not_numbers():
+    """Without the norm the gradient of the inputs does not depend on them."""
+    shape = (1, 6, 4, 2, 128, 64)
+    q, k, qw, kw, dq, dk, _, pos, freqs = make(shape, BF, BF, BF, seed=15)
+    cq, ck, cqw, ckw, cdq, cdk, cpos, cf = cuda(q, k, qw, kw, dq, dk, pos, freqs)
+    want = PL.qk_norm_rope_grad(cdq, cdk, cq, ck, cqw, ckw, cpos, cf, norm=False)
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        x = cq.clone()
+        x[0, 2, 1, 5] = bad
+        x[0, 4] = bad
+        got = PL.qk_norm_rope_grad(cdq, cdk, x, ck, cqw, ckw, cpos, cf, norm=False)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(got[3], want[3])
+
+
+def test_more_tokens_than_one_axis_of_a_launch():
+    """2^26 rows of two values: 2^32 threads and more."""
+    B, S = 2, (1 << 24) - 3
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q, k = (torch.randn(B, S, 1, 2, device="cuda", generator=g).to(BF) for _ in range(2))
+    q2, k2 = (torch.randn(B * 4, S, 1, 2, device="cuda", generator=g).to(BF) for _ in range(2))
+    f = torch.tensor([0.01], dtype=torch.float64, device="cuda")
+    for a, b in ((q, k), (q2, k2)):
+        ya, yb = PL.qk_norm_rope(a, b, None, None, None, f)
+        for x, y in ((a, ya), (b, yb)):
+            for i in range(x.shape[0]):
+                # the formula in fp32, angles in 64 bits: a few roundings of 2^-24 beside bf16's own half step, 2^-8
+                t = torch.arange(S, device="cuda").double() * 0.01
+                c, s = t.cos().float(), t.sin().float()
+                v = x[i, :, 0].float()
+                n = v * torch.rsqrt(v.square().mean(-1, keepdim=True) + 1e-6)
+                want = torch.stack((n[:, 0] * c - n[:, 1] * s, n[:, 1] * c + n[:, 0] * s), -1)
+                assert ((y[i, :, 0].float() - want).abs() <= 2.0 ** -8 * want.abs() + 2e-6).all(), i

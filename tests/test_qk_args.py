@@ -99,3 +99,14 @@ def test_python_refusals():
     with pytest.raises(ValueError):
         PL.rope_frequencies(7)
     assert PL.rope_frequencies(4, 100.0, "cpu").tolist() == [1.0, 100.0 ** -0.5]
+
+
+def test_outputs_on_one_tensor():
+    with pytest.raises(P.PBSError, match="q_out and k_out are one tensor") as e:
+        P.pbs_qk_norm_rope(**{**GOOD, "k_out": GOOD["q_out"]})
+    assert e.value.status == 1
+    for change, text in ((dict(dk_out=12 * A), "dq_out and dk_out"), (dict(dv_out=12 * A), "dv_out and dq_out"),
+                         (dict(dv_out=12 * A + 1024), "dk_out and dv_out"), (dict(dk_weight=13 * A), "dq_weight and dk_weight")):
+        with pytest.raises(P.PBSError, match=text + " are one") as e:
+            P.pbs_qk_norm_rope_grad(**{**GRAD, **change})
+        assert e.value.status == 1
