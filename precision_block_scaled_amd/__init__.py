@@ -300,16 +300,17 @@ def pbs_qk_norm_rope_grad(dq, dq_strides, dk, dk_strides, dv, dv_strides, y_fmt,
 
 
 @functools.lru_cache(maxsize=64)
-def _floats(coefficients):
-    flat = [float(v) for step in coefficients for v in step]
-    if any(len(step) != 3 for step in coefficients):
-        raise ValueError("coefficients: want (a, b, c) for each step")
-    return (_f32 * max(len(flat), 1))(*flat), len(coefficients)
+def _floats(values):
+    return (_f32 * max(len(values), 1))(*values)
 
 
 def _triples(coefficients):
     """Steps' (a, b, c) as the C side takes them (read only), and their number."""
-    return _floats(tuple(map(tuple, coefficients)))
+    try:
+        flat = tuple([v for a, b, c in coefficients for v in (float(a), float(b), float(c))])
+    except (TypeError, ValueError):
+        raise ValueError("coefficients: want (a, b, c) for each step") from None
+    return _floats(flat), len(flat) // 3
 
 
 def pbs_orthogonalize_bytes(batch, rows, cols):

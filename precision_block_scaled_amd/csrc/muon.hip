@@ -1434,7 +1434,8 @@ pbs_status pbs_orthogonalize(const void* x, pbs_format x_fmt, int64_t ldx, int64
   if ((st = ns_check_matrix(what, "x", x, x_fmt, batch, rows, cols, ldx, x_batch_stride, false)) != PBS_OK) return st;
   if ((st = ns_check_matrix(what, "y", y, PBS_FMT_BF16, batch, rows, cols, ldy, y_batch_stride, true)) != PBS_OK) return st;
   PBS_REQUIRE(y != workspace && x != workspace, PBS_ERR_INVALID_ARG, "%s: a matrix is on the workspace's memory", what);
-  PBS_REQUIRE(y != x || x_fmt == PBS_FMT_BF16, PBS_ERR_INVALID_ARG, "%s: y is x with another type", what);
+  PBS_REQUIRE(y != x || (x_fmt == PBS_FMT_BF16 && (rows == 1 || ldy == ldx) && (batch == 1 || y_batch_stride == x_batch_stride)),
+              PBS_ERR_INVALID_ARG, "%s: y is x with another type or other strides", what);
   MuonIn in = {};
   in.g = x; in.ldg = ldx; in.sg = x_batch_stride; in.g_bf16 = x_fmt == PBS_FMT_BF16;
   in.rows = (int)rows; in.cols = (int)cols; in.eps = eps;

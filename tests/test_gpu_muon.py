@@ -300,3 +300,32 @@ def test_a_step_around_the_projection():
         # the weight's rounding, half a step of values up to 0.3, over lr; and the orthogonalisation's own error
         assert (moved.cpu() - want).abs().max() <= 2.0 ** -9 * w.float().abs().max().item() * 2 / 0.02 + 0.01
     assert dqw.isfinite().all() and dkw.isfinite().all()
+
+
+@pytest.mark.parametrize("r,c,ld", [(300, 200, 1 << 21), (200, 300, (1 << 23) - 4), (130, 100, (1 << 25) + 4), (100, 130, (1 << 25) + 1)])
+def test_rows_far_apart(r, c, ld):
+    """Weight, momentum and gradient whose rows lie megabytes apart, up to 2^32 bytes and more from the first."""
+    w, m, g = (matrix(r, c, seed=s).to(BF) for s in (1, 2, 3))
+    want_w, want_m = w.cuda(), m.cuda()
+    PL.muon(want_w, want_m, g.cuda(), 0.02)
+    flat = torch.empty((r - 1) * ld + 3 * c + 8, dtype=BF, device="cuda")
+    views = [flat[i * (c + 4):].as_strided((r, c), (ld, 1)) for i in range(3)]
+    for v, t in zip(views, (w, m, g)):
+        v.copy_(t)
+    PL.muon(*views, 0.02)
+    assert torch.equal(views[0], want_w) and torch.equal(views[1], want_m) and torch.equal(views[2].cpu(), g)
+
+
+def test_largest_batch():
+    """65535 matrices, each by itself."""
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(65535, 3, 5, generator=g)
+    got = PL.orthogonalize(x.cuda())
+    want = x.double() / (x.double().flatten(1).norm(dim=1)[:, None, None] + 1e-7)
+    for a, b, c in PL.MUON_STEPS:
+        r = want @ want.transpose(1, 2).contiguous()
+        want = a * want + (b * r + c * r @ r) @ want
+    # bf16's half step, and fp32 roundings of short sums
+    assert ((got.cpu().double() - want).abs() <= half_step(BF) * want.abs() + 1e-5).all()
+    for i in (0, 65534):
+        assert torch.equal(PL.orthogonalize(x[i].cuda()), got[i])

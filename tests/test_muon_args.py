@@ -86,3 +86,26 @@ def test_python_refusals():
         PL.muon(x, x.clone(), x.clone(), 0.1)
     with pytest.raises(ValueError, match="for each step"):
         P.pbs_orthogonalize(**{**ORTHO, "coefficients": ((1.0, 2.0),)})
+
+
+@pytest.mark.parametrize("change", [dict(ldy=128), dict(ldx=128, x_batch_stride=128 * 64), dict(y_batch_stride=96 * 65),
+                                    dict(x_batch_stride=0)], ids=str)
+def test_in_place_with_other_strides(change):
+    """Rows that are written where other rows are still to be read."""
+    same = dict(x_fmt=BF, y=A, y_batch_stride=96 * 64)
+    if "ldy" in change:
+        change = dict(change, y_batch_stride=128 * 64)
+    with pytest.raises(P.PBSError, match="other strides") as e:
+        P.pbs_orthogonalize(**{**ORTHO, **same, **change})
+    assert e.value.status == 1
+
+
+def test_coefficients_that_change_in_place():
+    """A step's numbers are taken as they are at the call, whatever holds them."""
+    a = torch.tensor(1.5)
+    steps = ((a, -0.5, 0.0),)
+    first, n = P._triples(steps)
+    assert n == 1 and list(first) == [1.5, -0.5, 0.0]
+    a.fill_(2.0)
+    assert list(P._triples(steps)[0]) == [2.0, -0.5, 0.0]
+    assert list(P._triples(torch.tensor([[1.0, 2.0, 3.0]]))[0]) == [1.0, 2.0, 3.0]
