@@ -251,13 +251,15 @@ __device__ __forceinline__ void ns_split(float x, f16_t& hi, f16_t& lo) {
   lo = (f16_t)((x - (float)hi) * NS_LO);
 }
 
-// The momentum's store and the first X, zeros past the matrix's end.
+// The momentum's store and the first X, zeros past the matrix's end.  Tiles in
+// reverse, eight at a time (so each stays on its XCD): the norm's pass has left the
+// last ones in the caches (16384 x 4096 193 -> 178 us).
 template <typename TG, typename TM>
 __global__ __launch_bounds__(256) void muon_start_kernel(MuonIn a) {
   __shared__ float lds[MT][MPITCH];
   __shared__ double sums[4];
   const int t = threadIdx.x, tr = t >> 4, tc = 4 * (t & 15);
-  const int batch = blockIdx.y;
+  const int batch = gridDim.y - 1 - blockIdx.y;
   double s = 0.0;
 #pragma unroll 8
   for (int i = t; i < a.parts; i += 256) s += a.part[(int64_t)batch * a.parts + i];
@@ -269,7 +271,9 @@ __global__ __launch_bounds__(256) void muon_start_kernel(MuonIn a) {
   const double f = norm == 0.0 ? 0.0 : norm < __builtin_inf() ? (double)a.scale / norm : __builtin_nan("");
   const int wr = a.tall ? a.np : a.mp, wc = a.tall ? a.mp : a.np;           // the weight's padded shape
   const int tiles_c = wc / MT;
-  const int r0 = (int)(blockIdx.x / tiles_c) * MT, c0 = (int)(blockIdx.x % tiles_c) * MT;
+  const int id = blockIdx.x, whole = gridDim.x / NXCD * NXCD;
+  const int tile = id < whole ? whole - NXCD - id / NXCD * NXCD + id % NXCD : id;
+  const int r0 = tile / tiles_c * MT, c0 = tile % tiles_c * MT;
   if (r0 >= wr) return;
   MuonTile<TG, TM> u;
   u.load(a, batch, r0, c0, lds);
