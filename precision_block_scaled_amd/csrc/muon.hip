@@ -31,7 +31,7 @@
 // is q' q X, so the long side is gone through once a group and not once a step.  A
 // step alone takes 3 m^2 n + m^3 multiplications (symmetric products by half),
 // two together 3 m^2 n + 5 m^3, three 3 m^2 n + 9 m^3: 16384 x 4096 in five steps,
-// three and two together, 3.05 ms, one by one 4.63.  R's rounding errors grow by
+// three and two together, 3.05 ms where one by one took 4.63 (now 2.85).  R's rounding errors grow by
 // q^2 a step until X X^T is formed anew, which is what limits a group (ns_groups).
 #include "device.hpp"
 #include "gemm_common.hpp"
@@ -800,7 +800,7 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : (T == 2 ? 4 : 8) / D) void ns_pro
 // long side is gone through twice, for R and for Q U, and the steps between run
 // in one workgroup a matrix: three launches instead of 2 + 3 a step, of which
 // each takes 5 us or more here (16 x 4096 291 -> 24 us, 64 x 1000
-// 147 -> 65).  What R's rounding adds to the small directions grows by a^2 = 12 a
+// 147 -> 65).  Small ones have a kernel of their own, below.  What R's rounding adds to the small directions grows by a^2 = 12 a
 // step, 2e4 in five, and nothing takes it back as X X^T formed anew would: R is
 // held in 64 bits, and its products run on the 64-bit matrix instruction (a
 // product of 64 x 64 x 64 1.3 us; for 128 it would be 10).  The result is fp32's
@@ -823,6 +823,7 @@ struct ShortArgs {
   double* inv;             // [batch]: 1 / (||U||_F + eps)
   float coef[3 * 64];
   int steps;
+  float hold;              // small matrices: the power of two that X, A and P are held times
   void* w;
   int64_t ldw, sw;
   int update;
@@ -1086,6 +1087,215 @@ __global__ __launch_bounds__(256) void short_apply_kernel(ShortArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// Small matrices: short sides of 33 to 64, long ones up to 256
+//
+// All of X sits in one workgroup's LDS and the steps run there, in one launch that
+// reads the gradient and the momentum once; the three launches above take 42 us for
+// the steps alone of sides over 48 (64 x 64 61 -> 22 us, 64 x 128 64 -> 29, 64 x 256
+// 64 -> 44, 300 of 64 x 64 108 -> 42).  X, A and P are pairs of fp16, hi + lo 2^-11, and
+// each product three of fp16 (hi hi, hi lo, lo hi) with fp32 sums: what is left out is
+// 2^-22 of a value.  Bound by latency, 1.5 us a step for 64 columns where the matrix
+// instructions take 0.3 and the LDS reads as long; the next operands read ahead gained
+// nothing (46 us).
+// ---------------------------------------------------------------------------
+constexpr int TINY_LONG = 256, TINY_TILES = TINY_LONG / 64;
+constexpr int TINY_XP = TINY_LONG + 8, TINY_PP = 64 + 8;      // values a row: 16 rows' 16-byte reads take all banks
+
+struct TinyPair {
+  f16x8 hi, lo;
+};
+// A matrix instruction's operand: rows row0 + lane % 32, 8 values from k0 + 8 (lane / 32) on.
+__device__ __forceinline__ TinyPair tiny_rows(const f16_t* hi, const f16_t* lo, int pitch, int row0, int k0) {
+  const int lane = threadIdx.x & 63, at = (row0 + (lane & 31)) * pitch + k0 + 8 * (lane >> 5);
+  return {*(const f16x8*)(hi + at), *(const f16x8*)(lo + at)};
+}
+// The same of the matrix transposed: columns c0 + lane % 32, 8 rows, by two transposing reads.
+__device__ __forceinline__ f16x8 tiny_turned(const f16_t* m, int pitch, int c0, int k0) {
+  const int lane = threadIdx.x & 63, li = lane & 15;
+  const uint8_t* p = (const uint8_t*)(m + (k0 + 8 * (lane >> 5) + (li >> 2)) * pitch + c0 + 16 * ((lane >> 4) & 1) + 4 * (li & 3));
+  const int2 u = __builtin_bit_cast(int2, read_lds_tr16(p)), v = __builtin_bit_cast(int2, read_lds_tr16(p + 8 * pitch));
+  return __builtin_bit_cast(f16x8, i32x4{u.x, u.y, v.x, v.y});
+}
+// hi hi, and hi lo + lo hi, which counts 2^-11.  (A third sum of their own: 6% slower.)
+struct TinySum {
+  f32x16 big, small;
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) big[r] = small[r] = 0.0f;
+  }
+  __device__ __forceinline__ void add(const TinyPair& a, const TinyPair& b) {
+    big = __builtin_amdgcn_mfma_f32_32x32x16_f16(a.hi, b.hi, big, 0, 0, 0);
+    small = __builtin_amdgcn_mfma_f32_32x32x16_f16(a.hi, b.lo, small, 0, 0, 0);
+    small = __builtin_amdgcn_mfma_f32_32x32x16_f16(a.lo, b.hi, small, 0, 0, 0);
+  }
+  __device__ __forceinline__ float get(int r) const { return big[r] + small[r] * (1.0f / NS_LO); }
+};
+// Four values of a row as a pair.
+__device__ __forceinline__ void tiny_put(f16_t* hi, f16_t* lo, int at, const float (&v)[4]) {
+  f16x4 h, l;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    f16_t x, y;
+    ns_split(v[r], x, y);
+    h[r] = x;
+    l[r] = y;
+  }
+  *(f16x4*)(hi + at) = h;
+  *(f16x4*)(lo + at) = l;
+}
+__device__ __forceinline__ void tiny_get(const f16_t* hi, const f16_t* lo, int at, float (&v)[4]) {
+  const f16x4 h = *(const f16x4*)(hi + at), l = *(const f16x4*)(lo + at);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) v[r] = (float)h[r] + (float)l[r] * (1.0f / NS_LO);
+}
+
+template <typename TG, typename TM, typename TW>
+__global__ __launch_bounds__(256) void tiny_kernel(ShortArgs a) {
+  __shared__ __align__(16) f16_t xh[NS_SHORT * TINY_XP], xl[NS_SHORT * TINY_XP];
+  __shared__ __align__(16) f16_t ah[NS_SHORT * TINY_PP], al[NS_SHORT * TINY_PP], ph[NS_SHORT * TINY_PP], pl[NS_SHORT * TINY_PP];
+  __shared__ float turn[MT][MPITCH];
+  __shared__ double sums[4];
+  const MuonIn& in = a.in;
+  const int t = threadIdx.x, lane = t & 63, tr = t >> 4, tc = 4 * (t & 15), batch = blockIdx.x;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6), lr = lane & 31, lg = lane >> 5;
+  const int tiles = ((in.tall ? in.rows : in.cols) + 63) / 64;         // of the long side
+  // U, the momentum's store and the norm
+  MuonTile<TG, TM> u[TINY_TILES];
+  double s = 0.0;
+#pragma unroll
+  for (int k = 0; k < TINY_TILES; ++k)
+    if (k < tiles) {
+      const int r0 = in.tall ? 64 * k : 0, c0 = in.tall ? 0 : 64 * k;
+      u[k].load(in, batch, r0, c0, turn);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const double x = u[k].u[i].x, y = u[k].u[i].y, z = u[k].u[i].z, v = u[k].u[i].w;
+        s += x * x + y * y + (z * z + v * v);
+      }
+      if (in.m) {
+        TM* m = (TM*)in.m + batch * in.sm;
+        const bool vm = muon_vec<TM>(in.m, in.ldm, in.sm);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (r0 + tr + 16 * i < in.rows) muon_put4<TM>(m + (r0 + tr + 16 * i) * in.ldm, c0 + tc, in.cols, vm, u[k].m4[i]);
+      }
+    }
+  s = wave_sum_d(s);
+  if (lane == 0) sums[w] = s;
+  __syncthreads();
+  const double norm = sqrt(sums[0] + sums[1] + (sums[2] + sums[3])) + (double)in.eps;
+  // a matrix of zeros stays one; one with an infinity or a NaN becomes NaN
+  const double f = norm == 0.0 ? 0.0 : norm < __builtin_inf() ? (double)a.hold / norm : __builtin_nan("");
+#pragma unroll
+  for (int k = 0; k < TINY_TILES; ++k)
+    if (k < tiles) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float v[4] = {(float)(u[k].u[i].x * f), (float)(u[k].u[i].y * f), (float)(u[k].u[i].z * f), (float)(u[k].u[i].w * f)};
+        const int r = tr + 16 * i;
+        if (!in.tall) {
+          tiny_put(xh, xl, r * TINY_XP + 64 * k + tc, v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ns_split(v[e], xh[(tc + e) * TINY_XP + 64 * k + r], xl[(tc + e) * TINY_XP + 64 * k + r]);
+        }
+      }
+    }
+  __syncthreads();
+  const float inv = 1.0f / a.hold;
+  const float lr_now = a.lr_by ? a.lr * *a.lr_by : a.lr, keep = 1.0f - lr_now * a.decay, step = a.update ? lr_now * a.scale : -1.0f;
+  // A and P: wave w's 32 x 32 of them, of which a lane holds row i0 + lr, columns j0 + 8 q + 4 lg on
+  const int i0 = 32 * (w & 1), j0 = 32 * (w >> 1);
+  for (int n = 0; n < a.steps; ++n) {
+    const float ca = a.coef[3 * n], cb = a.coef[3 * n + 1], cc = a.coef[3 * n + 2];
+    TinySum sum;
+    sum.zero();
+    for (int k = 0; k < tiles; ++k)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        sum.add(tiny_rows(xh, xl, TINY_XP, j0, 64 * k + 16 * c), tiny_rows(xh, xl, TINY_XP, i0, 64 * k + 16 * c));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float v[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = sum.get(4 * q + r) * inv;
+      tiny_put(ah, al, (i0 + lr) * TINY_PP + j0 + 8 * q + 4 * lg, v);
+    }
+    __syncthreads();
+    sum.zero();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) sum.add(tiny_rows(ah, al, TINY_PP, j0, 16 * c), tiny_rows(ah, al, TINY_PP, i0, 16 * c));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int at = (i0 + lr) * TINY_PP + j0 + 8 * q + 4 * lg;
+      float v[4];
+      tiny_get(ah, al, at, v);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = cb * v[r] + cc * inv * sum.get(4 * q + r);
+      tiny_put(ph, pl, at, v);
+    }
+    __syncthreads();
+    // P X: rows i0 + lr, columns j0 + 64 k + 8 q + 4 lg on
+    TinyPair p[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) p[c] = tiny_rows(ph, pl, TINY_PP, i0, 16 * c);
+    f32x16 px[TINY_TILES];
+#pragma unroll
+    for (int k = 0; k < TINY_TILES; ++k)
+      if (k < tiles) {
+        sum.zero();
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          sum.add({tiny_turned(xh, TINY_XP, j0 + 64 * k, 16 * c), tiny_turned(xl, TINY_XP, j0 + 64 * k, 16 * c)}, p[c]);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) px[k][r] = sum.get(r);
+      }
+    __syncthreads();                                                   // X is read out
+#pragma unroll
+    for (int k = 0; k < TINY_TILES; ++k)
+      if (k < tiles) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int i = i0 + lr, j = j0 + 64 * k + 8 * q + 4 * lg;
+          float v[4];
+          tiny_get(xh, xl, i * TINY_XP + j, v);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] = ca * v[r] + px[k][4 * q + r] * inv;
+          if (n + 1 < a.steps) {
+            tiny_put(xh, xl, i * TINY_XP + j, v);
+            continue;
+          }
+          TW* wp = (TW*)a.w + batch * a.sw;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] *= inv;
+          if (!in.tall) {
+            if (i < in.rows) {
+              const bool vw = muon_vec<TW>(a.w, a.ldw, a.sw);
+              float4 o = make_float4(v[0], v[1], v[2], v[3]);
+              if (a.update) {
+                const float4 old = muon_get4<TW>(wp + i * a.ldw, j, in.cols, vw);
+                o = make_float4(keep * old.x - step * o.x, keep * old.y - step * o.y, keep * old.z - step * o.z, keep * old.w - step * o.w);
+              }
+              muon_put4<TW>(wp + i * a.ldw, j, in.cols, vw, o);
+            }
+          } else if (i < in.cols) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              if (j + r >= in.rows) continue;
+              TW* at = wp + (j + r) * a.ldw + i;
+              float o = v[r];
+              if (a.update) o = keep * muon_get<TW>(at, 0) - step * o;
+              if constexpr (sizeof(TW) == 4) *at = o;
+              else *at = (bf16_t)pk_bf16(o, o);
+            }
+          }
+        }
+      }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
 // The least short side from which two and three steps go together (see ns_groups).
@@ -1303,6 +1513,12 @@ static void muon_begin(const MuonIn& in, int64_t batch, hipStream_t stream) {
 template <typename TG, typename TM>
 static void short_run(const ShortArgs& a, int64_t batch, bool w_bf16, hipStream_t stream) {
   const int64_t n = a.in.tall ? a.in.rows : a.in.cols;
+  // (of up to 32 the Gram matrix's steps are short themselves: 32 x 256 27 us there and 44 here, 32 x 64 26 and 22)
+  if (n <= TINY_LONG && a.blocks > 2) {
+    if (w_bf16) hipLaunchKernelGGL((tiny_kernel<TG, TM, bf16_t>), dim3((unsigned)batch), dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((tiny_kernel<TG, TM, float>), dim3((unsigned)batch), dim3(256), 0, stream, a);
+    return;
+  }
   hipLaunchKernelGGL((short_gram_kernel<TG, TM>), dim3((unsigned)a.chunks, (unsigned)batch), dim3(256), 0, stream, a);
   hipLaunchKernelGGL(short_steps_kernel, dim3((unsigned)batch), dim3(SSTEP_THR), 0, stream, a);
   const dim3 grid((unsigned)ceil_div(n, 64), (unsigned)batch);
@@ -1322,6 +1538,7 @@ static void ns_run(const NsPlan& h, MuonIn in, NsArgs g, int64_t batch, const fl
     a.part = (double*)(ws + h.part); a.q = (float*)(ws + h.q); a.inv = (double*)(ws + h.inv);
     std::copy(coef, coef + 3 * steps, a.coef);
     a.steps = steps;
+    a.hold = scale;
     a.w = g.w; a.ldw = g.ldw; a.sw = g.sw; a.update = g.update;
     a.lr = g.lr; a.lr_by = g.lr_by; a.decay = g.decay; a.scale = g.scale;
     if (in.g_bf16) {

@@ -329,3 +329,38 @@ def test_largest_batch():
     assert ((got.cpu().double() - want).abs() <= half_step(BF) * want.abs() + 1e-5).all()
     for i in (0, 65534):
         assert torch.equal(PL.orthogonalize(x[i].cuda()), got[i])
+
+
+# around the largest matrix whose steps run in one launch, and short sides of every block count beyond it
+EDGES = [(64, 256), (256, 64), (64, 257), (257, 64), (40, 129), (191, 7), (192, 64), (2, 255), (16, 300), (17, 600), (33, 300),
+         (64, 640), (600, 50), (2, 700), (300, 32)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("r,c", EDGES)
+def test_one_step_of_small_matrices(r, c, dtype):
+    test_one_step(r, c, dtype)
+
+
+@pytest.mark.parametrize("kind", ["noise", "low", "lower"])
+@pytest.mark.parametrize("r,c", EDGES)
+def test_five_steps_of_small_matrices(r, c, kind):
+    test_five_steps(r, c, kind)
+
+
+@pytest.mark.parametrize("turned", [False, True])
+@pytest.mark.parametrize("r,c", [(64, 256), (255, 33), (50, 300), (300, 64), (20, 20)])
+def test_muon_of_small_matrices(r, c, turned):
+    """fp32 throughout: the update to a few fp32 roundings of the steps' slopes, where bf16's store hides nothing."""
+    g0 = torch.Generator().manual_seed(r * c)
+    w, m, g = (torch.randn(3, r, c, generator=g0) for _ in range(3))
+    cw, cm = w.cuda(), m.cuda()
+    cg = g.cuda().transpose(1, 2).contiguous().transpose(1, 2) if turned else g.cuda()
+    PL.muon(cw, cm, cg, 1.0, weight_decay=0.5, scale=1.0)
+    for i in range(3):
+        want, _, u = update_ref(w[i], m[i], g[i], 1.0, 0.95, True, 0.5, 1.0, PL.MUON_STEPS)
+        x = orthogonal(u, PL.MUON_STEPS)
+        # fp16 pairs, 2^-22 of a value, in U, A, P and X of five steps, which grow by the steps' largest slopes: at most
+        # 3.9 each, 902 in all; beside them the weight's fp32 roundings
+        off = (cw[i].cpu().double() - want).norm()
+        assert off <= 20 * 902 * 2.0 ** -22 * x.norm() + 4 * 2.0 ** -24 * w[i].double().norm(), (off / x.norm()).item()
