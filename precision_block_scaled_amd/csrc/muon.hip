@@ -824,6 +824,9 @@ struct ShortArgs {
   float coef[3 * 64];
   int steps;
   float hold;              // small matrices: the power of two that X, A and P are held times
+  double* x;               // step by step: X [batch][short][long], ahead of the first step U
+  double* p;               // step by step: P [batch][64][64]
+  int step;
   void* w;
   int64_t ldw, sw;
   int update;
@@ -860,37 +863,26 @@ __device__ __forceinline__ void short_stage(const MuonIn& a, const MuonTile<TG, 
   }
 }
 
-// Partial sums of U U^T: wave w takes every fourth step of 4 columns.
-template <typename TG, typename TM>
-__global__ __launch_bounds__(256) void short_gram_kernel(ShortArgs a) {
-  __shared__ float turn[MT][MPITCH];
-  __shared__ __align__(16) float u[NS_SHORT * SUPITCH];
-  __shared__ double sums[STILES * 256];
-  const int t = threadIdx.x, lane = t & 63, w = t >> 6, batch = blockIdx.y;
-  const int n = a.in.tall ? a.in.rows : a.in.cols, tiles = a.blocks * (a.blocks + 1) / 2;
-  f64x4 acc[STILES];
+// What 64 staged columns add to U U^T: wave w takes every fourth step of 4 of them.
+template <int PITCH, typename T>
+__device__ __forceinline__ void short_gram_add(const T* u, int blocks, f64x4 (&acc)[STILES]) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
 #pragma unroll
-  for (int p = 0; p < STILES; ++p) acc[p] = f64x4{0, 0, 0, 0};
-  for (int at = blockIdx.x * 64; at < n; at += a.chunks * 64) {
-    MuonTile<TG, TM> v;
-    short_load(a.in, batch, at, v, turn);
-    __syncthreads();
-    short_stage(a.in, v, 1.0, u);
-    __syncthreads();
+  for (int s = 0; s < 4; ++s) {
+    double x[4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      double x[4];
+    for (int b = 0; b < 4; ++b) x[b] = (double)u[(SB * b + lane % 16) * PITCH + 4 * (4 * s + w) + lane / 16];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) x[b] = (double)u[(SB * b + lane % 16) * SUPITCH + 4 * (4 * s + w) + lane / 16];
-#pragma unroll
-      for (int p = 0; p < STILES; ++p) {
-        int i, j;
-        short_tile(p, i, j);
-        if (i < a.blocks) acc[p] = __builtin_amdgcn_mfma_f64_16x16x4f64(x[i], x[j], acc[p], 0, 0, 0);
-      }
+    for (int p = 0; p < STILES; ++p) {
+      int i, j;
+      short_tile(p, i, j);
+      if (i < blocks) acc[p] = __builtin_amdgcn_mfma_f64_16x16x4f64(x[i], x[j], acc[p], 0, 0, 0);
     }
   }
-  // the four waves' sums, in their order
+}
+// The four waves' sums, in their order, to the workgroup's part.
+__device__ __forceinline__ void short_gram_put(const ShortArgs& a, const f64x4 (&acc)[STILES], double* sums) {
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6, tiles = a.blocks * (a.blocks + 1) / 2;
   for (int q = 0; q < 4; ++q) {
     __syncthreads();
     if (w == q) {
@@ -906,8 +898,29 @@ __global__ __launch_bounds__(256) void short_gram_kernel(ShortArgs a) {
     }
   }
   __syncthreads();
-  double* to = a.part + ((int64_t)batch * a.chunks + blockIdx.x) * STILES * 256;
+  double* to = a.part + ((int64_t)blockIdx.y * a.chunks + blockIdx.x) * STILES * 256;
   for (int i = t; i < tiles * 256; i += 256) to[i] = sums[i];
+}
+
+// Partial sums of U U^T.
+template <typename TG, typename TM>
+__global__ __launch_bounds__(256) void short_gram_kernel(ShortArgs a) {
+  __shared__ float turn[MT][MPITCH];
+  __shared__ __align__(16) float u[NS_SHORT * SUPITCH];
+  __shared__ double sums[STILES * 256];
+  const int batch = blockIdx.y, n = a.in.tall ? a.in.rows : a.in.cols;
+  f64x4 acc[STILES];
+#pragma unroll
+  for (int p = 0; p < STILES; ++p) acc[p] = f64x4{0, 0, 0, 0};
+  for (int at = blockIdx.x * 64; at < n; at += a.chunks * 64) {
+    MuonTile<TG, TM> v;
+    short_load(a.in, batch, at, v, turn);
+    __syncthreads();
+    short_stage(a.in, v, 1.0, u);
+    __syncthreads();
+    short_gram_add<SUPITCH>(u, a.blocks, acc);
+  }
+  short_gram_put(a, acc, sums);
 }
 
 // Tile (i, j) of x y^T: lane l holds rows 4 r + l / 16, r < 4, of column l % 16.
@@ -938,25 +951,19 @@ __device__ __forceinline__ f64x4 short_product(const double* x, const double* y,
   return c;
 }
 
-// The steps, a wave for each tile.  Every matrix is a polynomial of R, symmetric
-// and commuting with the others, so products are formed as X Y^T, by half, and
-// stored twice.
+// Row r (of 4) of tile (i, j), as a product's lanes hold it, into a symmetric matrix.  (Of a tile on the diagonal the
+// lower half: the two halves' roundings differ.)
+__device__ __forceinline__ void short_put(double* m, int i, int j, int r, int lane, double v) {
+  const int row = SB * i + 4 * r + lane / 16, col = SB * j + lane % 16;
+  if (row < col) return;
+  m[row * SPITCH + col] = v;
+  m[col * SPITCH + row] = v;
+}
 constexpr int SSTEP_THR = 64 * STILES;
-__global__ __launch_bounds__(SSTEP_THR) void short_steps_kernel(ShortArgs a) {
-  __shared__ double R[NS_SHORT * SPITCH], P[NS_SHORT * SPITCH], Q[NS_SHORT * SPITCH];
-  const int t = threadIdx.x, lane = t & 63, batch = blockIdx.x;
-  const int w = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int tiles = a.blocks * (a.blocks + 1) / 2, side = SB * a.blocks;
+// The parts' sum; wave w of STILES.
+__device__ __forceinline__ void short_gram_join(const ShortArgs& a, int batch, int w, int lane, double* R) {
+  const int tiles = a.blocks * (a.blocks + 1) / 2;
   const double* from = a.part + (int64_t)batch * a.chunks * STILES * 256;
-  int ti, tj;
-  short_tile(w, ti, tj);
-  // (of a tile on the diagonal the lower half: the two halves' roundings differ)
-  auto put = [&](double* m, int i, int j, int r, double v) {
-    const int row = SB * i + 4 * r + lane / 16, col = SB * j + lane % 16;
-    if (row < col) return;
-    m[row * SPITCH + col] = v;
-    m[col * SPITCH + row] = v;
-  };
   for (int e = w; e < 4 * tiles; e += STILES) {           // rows e % 4 of tile e / 4, as the instruction holds them
     double s = 0.0;
     for (int c = 0; c < a.chunks; c += 16) {
@@ -968,15 +975,34 @@ __global__ __launch_bounds__(SSTEP_THR) void short_steps_kernel(ShortArgs a) {
     }
     int i, j;
     short_tile(e >> 2, i, j);
-    put(R, i, j, e & 3, s);
+    short_put(R, i, j, e & 3, lane, s);
   }
-  __syncthreads();
+}
+// U U^T in R becomes that of U / (||U||_F + eps); the factor 1 / (||U||_F + eps) is returned.
+__device__ __forceinline__ double short_normed(const ShortArgs& a, int side, int lane, double* R) {
   const double norm = sqrt(wave_sum_d(lane < side ? R[lane * (SPITCH + 1)] : 0.0)) + (double)a.in.eps;
   // a matrix of zeros stays one; one with an infinity or a NaN becomes NaN
   const double inv = norm == 0.0 ? 0.0 : norm < __builtin_inf() ? 1.0 / norm : __builtin_nan("");
   __syncthreads();
-  for (int i = t; i < side * side; i += SSTEP_THR) R[i / side * SPITCH + i % side] *= inv * inv;
+  for (int i = threadIdx.x; i < side * side; i += SSTEP_THR) R[i / side * SPITCH + i % side] *= inv * inv;
   __syncthreads();
+  return inv;
+}
+
+// The steps, a wave for each tile.  Every matrix is a polynomial of R, symmetric
+// and commuting with the others, so products are formed as X Y^T, by half, and
+// stored twice.
+__global__ __launch_bounds__(SSTEP_THR) void short_steps_kernel(ShortArgs a) {
+  __shared__ double R[NS_SHORT * SPITCH], P[NS_SHORT * SPITCH], Q[NS_SHORT * SPITCH];
+  const int t = threadIdx.x, lane = t & 63, batch = blockIdx.x;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int tiles = a.blocks * (a.blocks + 1) / 2, side = SB * a.blocks;
+  int ti, tj;
+  short_tile(w, ti, tj);
+  auto put = [&](double* m, int i, int j, int r, double v) { short_put(m, i, j, r, lane, v); };
+  short_gram_join(a, batch, w, lane, R);
+  __syncthreads();
+  const double inv = short_normed(a, side, lane, R);
   const bool here = w < tiles;
   f64x4 acc = {0, 0, 0, 0};
   auto store = [&](double* m) {
@@ -1083,6 +1109,141 @@ __global__ __launch_bounds__(256) void short_apply_kernel(ShortArgs a) {
       o = make_float4(keep * old.x - step * o.x, keep * old.y - step * o.y, keep * old.z - step * o.z, keep * old.w - step * o.w);
     }
     muon_put4<TW>(p, c0 + tc, in.cols, vw, o);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Short sides, many steps
+//
+// In directions that U does not have Q grows by a in each step, and what is
+// rounded off Q and off the product Q U with it; and R <- q R q multiplies what 64
+// bits round off R by q^2 a step there, of either sign, where X X^T is never less
+// than 0: once such a value nears -1 the polynomials run away (a matrix of rank 1,
+// Muon's step: 10 times the result after 16, NaN after 20).  Where the steps'
+// growth exceeds SHORT_GROWTH they are therefore taken one by one, with X in 64 bits
+// in the workspace and X X^T formed anew for each: what X's rounding adds to such a
+// direction still grows by a, from 2^-53, but no singular value leaves the
+// polynomials' range.  a X stays apart from P X, so that equal rows stay equal.
+// Three launches a step, 64-bit arithmetic on the vector units, bound by latency.
+// ---------------------------------------------------------------------------
+// Five of Muon's steps grow by 485, six by 1670; the error of a matrix of ones, 64 x 1000, is then 0.03% and 0.12%.
+constexpr double SHORT_GROWTH = 2048.0;
+
+// U, and the momentum's store.
+template <typename TG, typename TM>
+__global__ __launch_bounds__(256) void short_wide_start_kernel(ShortArgs a) {
+  __shared__ float turn[MT][MPITCH];
+  __shared__ __align__(16) float u[NS_SHORT * SUPITCH];
+  const MuonIn& in = a.in;
+  const int t = threadIdx.x, tr = t >> 4, tc = 4 * (t & 15), batch = blockIdx.y, at = blockIdx.x * 64;
+  const int m = in.tall ? in.cols : in.rows, n = in.tall ? in.rows : in.cols;
+  const int r0 = in.tall ? at : 0, c0 = in.tall ? 0 : at;
+  MuonTile<TG, TM> v;
+  short_load(in, batch, at, v, turn);
+  short_stage(in, v, 1.0, u);
+  if (in.m) {
+    TM* p = (TM*)in.m + batch * in.sm;
+    const bool vm = muon_vec<TM>(in.m, in.ldm, in.sm);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (r0 + tr + 16 * k < in.rows) muon_put4<TM>(p + (r0 + tr + 16 * k) * in.ldm, c0 + tc, in.cols, vm, v.m4[k]);
+  }
+  __syncthreads();
+  const int c = t & 63;
+  if (at + c < n)
+    for (int r = t >> 6; r < m; r += 4) a.x[((int64_t)batch * m + r) * n + at + c] = (double)u[r * SUPITCH + c];
+}
+
+// 64 columns of X from `at` on into LDS, zeros behind its rows (up to whole blocks) and columns.
+__device__ __forceinline__ void short_wide_load(const ShortArgs& a, int batch, int at, double* u) {
+  const int m = a.in.tall ? a.in.cols : a.in.rows, n = a.in.tall ? a.in.rows : a.in.cols, c = threadIdx.x & 63;
+  for (int r = threadIdx.x >> 6; r < SB * a.blocks; r += 4)
+    u[r * SPITCH + c] = r < m && at + c < n ? a.x[((int64_t)batch * m + r) * n + at + c] : 0.0;
+}
+
+// Partial sums of X X^T.
+__global__ __launch_bounds__(256) void short_wide_gram_kernel(ShortArgs a) {
+  __shared__ double u[NS_SHORT * SPITCH], sums[STILES * 256];
+  const int batch = blockIdx.y, n = a.in.tall ? a.in.rows : a.in.cols;
+  for (int i = threadIdx.x; i < NS_SHORT * SPITCH; i += 256) u[i] = 0.0;
+  f64x4 acc[STILES];
+#pragma unroll
+  for (int p = 0; p < STILES; ++p) acc[p] = f64x4{0, 0, 0, 0};
+  for (int at = blockIdx.x * 64; at < n; at += a.chunks * 64) {
+    __syncthreads();
+    short_wide_load(a, batch, at, u);
+    __syncthreads();
+    short_gram_add<SPITCH>(u, a.blocks, acc);
+  }
+  short_gram_put(a, acc, sums);
+}
+
+// P = b R + c R^2; ahead of the first step R is U U^T and gives the norm.
+__global__ __launch_bounds__(SSTEP_THR) void short_poly_kernel(ShortArgs a) {
+  __shared__ double R[NS_SHORT * SPITCH], P[NS_SHORT * SPITCH];
+  const int t = threadIdx.x, lane = t & 63, batch = blockIdx.x;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int tiles = a.blocks * (a.blocks + 1) / 2, side = SB * a.blocks;
+  short_gram_join(a, batch, w, lane, R);
+  __syncthreads();
+  if (a.step == 0) {
+    const double inv = short_normed(a, side, lane, R);
+    if (t == 0) a.inv[batch] = inv;
+  }
+  const double cb = a.coef[3 * a.step + 1], cc = a.coef[3 * a.step + 2];
+  if (w < tiles) {
+    int ti, tj;
+    short_tile(w, ti, tj);
+    const f64x4 acc = short_product(R, R, ti, tj, a.blocks, lane);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = SB * ti + 4 * r + lane / 16, col = SB * tj + lane % 16;
+      short_put(P, ti, tj, r, lane, cb * R[row * SPITCH + col] + cc * acc[r]);
+    }
+  }
+  __syncthreads();
+  for (int i = t; i < side * side; i += SSTEP_THR)
+    a.p[((int64_t)batch * NS_SHORT + i / side) * NS_SHORT + i % side] = P[i / side * SPITCH + i % side];
+}
+
+// X' = a X + P X for 64 values of the long side: in place, or of the last step into the weight.
+template <typename TW>
+__global__ __launch_bounds__(256) void short_wide_step_kernel(ShortArgs a) {
+  __shared__ double u[NS_SHORT * SPITCH], p[NS_SHORT * SPITCH];
+  const MuonIn& in = a.in;
+  const int t = threadIdx.x, c = t & 63, w = t >> 6, batch = blockIdx.y, at = blockIdx.x * 64, side = SB * a.blocks;
+  const int m = in.tall ? in.cols : in.rows, n = in.tall ? in.rows : in.cols;
+  short_wide_load(a, batch, at, u);
+  for (int i = t; i < side * side; i += 256) p[i / side * SPITCH + i % side] = a.p[((int64_t)batch * NS_SHORT + i / side) * NS_SHORT + i % side];
+  __syncthreads();
+  if (at + c >= n) return;
+  const double f = a.step == 0 ? a.inv[batch] : 1.0, ca = a.coef[3 * a.step];
+  // rows w + 4 k
+  double x[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) x[k] = 0.0;
+  for (int j = 0; j < side; ++j) {
+    const double v = u[j * SPITCH + c];
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (4 * k < side) x[k] = __builtin_fma(p[(w + 4 * k) * SPITCH + j], v, x[k]);
+  }
+  const float lr_now = a.lr_by ? a.lr * *a.lr_by : a.lr, keep = 1.0f - lr_now * a.decay, step = lr_now * a.scale;
+  TW* wp = (TW*)a.w + batch * a.sw;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const int r = w + 4 * k;
+    if (r >= m) continue;
+    const double v = f * (ca * u[r * SPITCH + c] + x[k]);
+    if (a.step + 1 < a.steps) {
+      a.x[((int64_t)batch * m + r) * n + at + c] = v;
+      continue;
+    }
+    TW* to = in.tall ? wp + (int64_t)(at + c) * a.ldw + r : wp + r * a.ldw + at + c;
+    float o = (float)v;
+    if (a.update) o = keep * muon_get<TW>(to, 0) - step * o;
+    if constexpr (sizeof(TW) == 4) *to = o;
+    else *to = (bf16_t)pk_bf16(o, o);
   }
 }
 
@@ -1306,7 +1467,7 @@ struct NsPlan {
   int parts;
   size_t hi[2], lo[2], gram, poly, turn, poly2, join, diag, part, bytes;
   int chunks;                                 // short sides: workgroups that share the long one; 0: not short
-  size_t q, inv;
+  size_t q, inv, x64;
 };
 
 static NsPlan ns_plan(int64_t batch, int64_t rows, int64_t cols) {
@@ -1327,8 +1488,9 @@ static NsPlan ns_plan(int64_t batch, int64_t rows, int64_t cols) {
     // fewer where their sums take long to join: of 6 or 10 tiles against 1 or 3
     h.chunks = (int)std::min<int64_t>(ceil_div(n, 64), m > 32 ? 16 : 32);
     h.part = take((size_t)(batch * h.chunks) * STILES * 256 * 8);
-    h.q = take((size_t)batch * NS_SHORT * NS_SHORT * 4);
+    h.q = take((size_t)batch * NS_SHORT * NS_SHORT * 8);  // Q, or P in 64 bits
     h.inv = take((size_t)batch * 8);
+    h.x64 = take((size_t)(batch * m * n) * 8);
     h.bytes = at;
     return h;
   }
@@ -1511,7 +1673,7 @@ static void muon_begin(const MuonIn& in, int64_t batch, hipStream_t stream) {
 }
 
 template <typename TG, typename TM>
-static void short_run(const ShortArgs& a, int64_t batch, bool w_bf16, hipStream_t stream) {
+static void short_run(ShortArgs a, int64_t batch, bool w_bf16, bool one_by_one, hipStream_t stream) {
   const int64_t n = a.in.tall ? a.in.rows : a.in.cols;
   // (of up to 32 the Gram matrix's steps are short themselves: 32 x 256 27 us there and 44 here, 32 x 64 26 and 22)
   if (n <= TINY_LONG && a.blocks > 2) {
@@ -1519,9 +1681,19 @@ static void short_run(const ShortArgs& a, int64_t batch, bool w_bf16, hipStream_
     else hipLaunchKernelGGL((tiny_kernel<TG, TM, float>), dim3((unsigned)batch), dim3(256), 0, stream, a);
     return;
   }
-  hipLaunchKernelGGL((short_gram_kernel<TG, TM>), dim3((unsigned)a.chunks, (unsigned)batch), dim3(256), 0, stream, a);
+  const dim3 grid((unsigned)ceil_div(n, 64), (unsigned)batch), parts((unsigned)a.chunks, (unsigned)batch);
+  if (one_by_one) {
+    hipLaunchKernelGGL((short_wide_start_kernel<TG, TM>), grid, dim3(256), 0, stream, a);
+    for (a.step = 0; a.step < a.steps; ++a.step) {
+      hipLaunchKernelGGL(short_wide_gram_kernel, parts, dim3(256), 0, stream, a);
+      hipLaunchKernelGGL(short_poly_kernel, dim3((unsigned)batch), dim3(SSTEP_THR), 0, stream, a);
+      if (w_bf16) hipLaunchKernelGGL((short_wide_step_kernel<bf16_t>), grid, dim3(256), 0, stream, a);
+      else hipLaunchKernelGGL((short_wide_step_kernel<float>), grid, dim3(256), 0, stream, a);
+    }
+    return;
+  }
+  hipLaunchKernelGGL((short_gram_kernel<TG, TM>), parts, dim3(256), 0, stream, a);
   hipLaunchKernelGGL(short_steps_kernel, dim3((unsigned)batch), dim3(SSTEP_THR), 0, stream, a);
-  const dim3 grid((unsigned)ceil_div(n, 64), (unsigned)batch);
   if (w_bf16) hipLaunchKernelGGL((short_apply_kernel<TG, TM, bf16_t>), grid, dim3(256), 0, stream, a);
   else hipLaunchKernelGGL((short_apply_kernel<TG, TM, float>), grid, dim3(256), 0, stream, a);
 }
@@ -1536,17 +1708,24 @@ static void ns_run(const NsPlan& h, MuonIn in, NsArgs g, int64_t batch, const fl
     a.blocks = (int)ceil_div(std::min(in.rows, in.cols), SB);
     a.chunks = h.chunks;
     a.part = (double*)(ws + h.part); a.q = (float*)(ws + h.q); a.inv = (double*)(ws + h.inv);
+    a.x = (double*)(ws + h.x64); a.p = (double*)(ws + h.q);
+    double grown = 1.0, most = 1.0;
+    for (int k = 0; k < steps; ++k) {
+      grown = std::max(grown, 1.0) * qmax[k];
+      most = std::max(most, grown);
+    }
+    const bool one_by_one = most > SHORT_GROWTH;
     std::copy(coef, coef + 3 * steps, a.coef);
     a.steps = steps;
     a.hold = scale;
     a.w = g.w; a.ldw = g.ldw; a.sw = g.sw; a.update = g.update;
     a.lr = g.lr; a.lr_by = g.lr_by; a.decay = g.decay; a.scale = g.scale;
     if (in.g_bf16) {
-      if (in.m_bf16) short_run<bf16_t, bf16_t>(a, batch, g.w_bf16, stream);
-      else short_run<bf16_t, float>(a, batch, g.w_bf16, stream);
+      if (in.m_bf16) short_run<bf16_t, bf16_t>(a, batch, g.w_bf16, one_by_one, stream);
+      else short_run<bf16_t, float>(a, batch, g.w_bf16, one_by_one, stream);
     } else {
-      if (in.m_bf16) short_run<float, bf16_t>(a, batch, g.w_bf16, stream);
-      else short_run<float, float>(a, batch, g.w_bf16, stream);
+      if (in.m_bf16) short_run<float, bf16_t>(a, batch, g.w_bf16, one_by_one, stream);
+      else short_run<float, float>(a, batch, g.w_bf16, one_by_one, stream);
     }
     return;
   }
