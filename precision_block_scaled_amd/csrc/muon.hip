@@ -824,9 +824,10 @@ struct ShortArgs {
   float coef[3 * 64];
   int steps;
   float hold;              // small matrices: the power of two that X, A and P are held times
-  double* x;               // step by step: X [batch][short][long], ahead of the first step U
-  double* p;               // step by step: P [batch][64][64]
-  int step;
+  // in 64 bits:
+  double* x;               // X [batch][short][long], ahead of the first step U
+  double* p;               // P of step `step`, or Q; [batch][64][64]
+  int step;                // -1: all steps together
   void* w;
   int64_t ldw, sw;
   int update;
@@ -1040,8 +1041,11 @@ __global__ __launch_bounds__(SSTEP_THR) void short_steps_kernel(ShortArgs a) {
       __syncthreads();
     }
   }
-  for (int i = t; i < side * side; i += SSTEP_THR)
-    a.q[((int64_t)batch * NS_SHORT + i / side) * NS_SHORT + i % side] = (float)Q[i / side * SPITCH + i % side];
+  for (int i = t; i < side * side; i += SSTEP_THR) {
+    const int64_t to = ((int64_t)batch * NS_SHORT + i / side) * NS_SHORT + i % side;
+    if (a.p) a.p[to] = Q[i / side * SPITCH + i % side];
+    else a.q[to] = (float)Q[i / side * SPITCH + i % side];
+  }
   if (t == 0) a.inv[batch] = inv;
 }
 
@@ -1115,19 +1119,25 @@ __global__ __launch_bounds__(256) void short_apply_kernel(ShortArgs a) {
 // ---------------------------------------------------------------------------
 // Short sides, many steps
 //
-// In directions that U does not have Q grows by a in each step, and what is
-// rounded off Q and off the product Q U with it; and R <- q R q multiplies what 64
+// In directions that U does not have Q grows by a in each step, and with it what is
+// rounded off Q and off the product Q U; and R <- q R q multiplies what 64
 // bits round off R by q^2 a step there, of either sign, where X X^T is never less
 // than 0: once such a value nears -1 the polynomials run away (a matrix of rank 1,
-// Muon's step: 10 times the result after 16, NaN after 20).  Where the steps'
-// growth exceeds SHORT_GROWTH they are therefore taken one by one, with X in 64 bits
-// in the workspace and X X^T formed anew for each: what X's rounding adds to such a
-// direction still grows by a, from 2^-53, but no singular value leaves the
-// polynomials' range.  a X stays apart from P X, so that equal rows stay equal.
-// Three launches a step, 64-bit arithmetic on the vector units, bound by latency.
+// Muon's step: 10 times the result after 16, NaN after 20).  So beyond a growth of
+// SHORT_GROWTH Q U is formed in 64 bits, from a copy of U in the workspace, and beyond
+// SHORT_WIDE_GROWTH the steps are taken one by one, with X in 64 bits and X X^T formed
+// anew for each: what X's rounding adds to such a direction still grows by a, from
+// 2^-53, but no singular value leaves the polynomials' range.  a X stays apart from
+// P X there, so that equal rows stay equal.  Both on the 64-bit matrix instruction,
+// bound by latency: 16 x 4096 six steps 27 us, eight 32, sixteen (one by one) 225;
+// 64 x 1000 72, 98 and 612.
 // ---------------------------------------------------------------------------
-// Five of Muon's steps grow by 485, six by 1670; the error of a matrix of ones, 64 x 1000, is then 0.03% and 0.12%.
+// Five of Muon's steps grow by 485, six by 1670: a matrix of ones, 64 x 1000, is then 0.03% and 0.12% off, and would be
+// 0.5% after eight.
 constexpr double SHORT_GROWTH = 2048.0;
+// Nine steps grow by 68000.  A wave adds at most 4096 products of four to an entry of R one after the other, so R is off by
+// 2^12 2^-53 of its trace, and grown by 2^34 by less than 0.01.
+constexpr double SHORT_WIDE_GROWTH = 131072.0;
 
 // U, and the momentum's store.
 template <typename TG, typename TM>
@@ -1206,45 +1216,50 @@ __global__ __launch_bounds__(SSTEP_THR) void short_poly_kernel(ShortArgs a) {
     a.p[((int64_t)batch * NS_SHORT + i / side) * NS_SHORT + i % side] = P[i / side * SPITCH + i % side];
 }
 
-// X' = a X + P X for 64 values of the long side: in place, or of the last step into the weight.
+// X' = a X + P X, or Q X, for 64 values of the long side: in place, or the last one into the weight.  Wave w takes
+// columns 16 w on.
 template <typename TW>
 __global__ __launch_bounds__(256) void short_wide_step_kernel(ShortArgs a) {
   __shared__ double u[NS_SHORT * SPITCH], p[NS_SHORT * SPITCH];
   const MuonIn& in = a.in;
-  const int t = threadIdx.x, c = t & 63, w = t >> 6, batch = blockIdx.y, at = blockIdx.x * 64, side = SB * a.blocks;
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6, batch = blockIdx.y, at = blockIdx.x * 64, side = SB * a.blocks;
   const int m = in.tall ? in.cols : in.rows, n = in.tall ? in.rows : in.cols;
   short_wide_load(a, batch, at, u);
   for (int i = t; i < side * side; i += 256) p[i / side * SPITCH + i % side] = a.p[((int64_t)batch * NS_SHORT + i / side) * NS_SHORT + i % side];
   __syncthreads();
-  if (at + c >= n) return;
-  const double f = a.step == 0 ? a.inv[batch] : 1.0, ca = a.coef[3 * a.step];
-  // rows w + 4 k
-  double x[16];
+  // U is not divided by its norm yet
+  const double f = a.step <= 0 ? a.inv[batch] : 1.0, ca = a.step < 0 ? 0.0 : (double)a.coef[3 * a.step];
+  const bool last = a.step < 0 || a.step + 1 == a.steps;
+  const int c = SB * w + lane % 16;
+  f64x4 x[4];
 #pragma unroll
-  for (int k = 0; k < 16; ++k) x[k] = 0.0;
-  for (int j = 0; j < side; ++j) {
-    const double v = u[j * SPITCH + c];
+  for (int i = 0; i < 4; ++i) x[i] = f64x4{0, 0, 0, 0};
+  for (int k = lane / 16; k < side; k += 4) {
+    const double v = u[k * SPITCH + c];
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
-      if (4 * k < side) x[k] = __builtin_fma(p[(w + 4 * k) * SPITCH + j], v, x[k]);
+    for (int i = 0; i < 4; ++i)
+      if (i < a.blocks) x[i] = __builtin_amdgcn_mfma_f64_16x16x4f64(p[(SB * i + lane % 16) * SPITCH + k], v, x[i], 0, 0, 0);
   }
+  if (at + c >= n) return;
   const float lr_now = a.lr_by ? a.lr * *a.lr_by : a.lr, keep = 1.0f - lr_now * a.decay, step = lr_now * a.scale;
   TW* wp = (TW*)a.w + batch * a.sw;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const int r = w + 4 * k;
-    if (r >= m) continue;
-    const double v = f * (ca * u[r * SPITCH + c] + x[k]);
-    if (a.step + 1 < a.steps) {
-      a.x[((int64_t)batch * m + r) * n + at + c] = v;
-      continue;
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = SB * i + 4 * r + lane / 16;
+      if (row >= m) continue;
+      const double v = f * (ca * u[row * SPITCH + c] + x[i][r]);
+      if (!last) {
+        a.x[((int64_t)batch * m + row) * n + at + c] = v;
+        continue;
+      }
+      TW* to = in.tall ? wp + (int64_t)(at + c) * a.ldw + row : wp + row * a.ldw + at + c;
+      float o = (float)v;
+      if (a.update) o = keep * muon_get<TW>(to, 0) - step * o;
+      if constexpr (sizeof(TW) == 4) *to = o;
+      else *to = (bf16_t)pk_bf16(o, o);
     }
-    TW* to = in.tall ? wp + (int64_t)(at + c) * a.ldw + r : wp + r * a.ldw + at + c;
-    float o = (float)v;
-    if (a.update) o = keep * muon_get<TW>(to, 0) - step * o;
-    if constexpr (sizeof(TW) == 4) *to = o;
-    else *to = (bf16_t)pk_bf16(o, o);
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -1673,7 +1688,7 @@ static void muon_begin(const MuonIn& in, int64_t batch, hipStream_t stream) {
 }
 
 template <typename TG, typename TM>
-static void short_run(ShortArgs a, int64_t batch, bool w_bf16, bool one_by_one, hipStream_t stream) {
+static void short_run(ShortArgs a, int64_t batch, bool w_bf16, double growth, hipStream_t stream) {
   const int64_t n = a.in.tall ? a.in.rows : a.in.cols;
   // (of up to 32 the Gram matrix's steps are short themselves: 32 x 256 27 us there and 44 here, 32 x 64 26 and 22)
   if (n <= TINY_LONG && a.blocks > 2) {
@@ -1682,16 +1697,27 @@ static void short_run(ShortArgs a, int64_t batch, bool w_bf16, bool one_by_one, 
     return;
   }
   const dim3 grid((unsigned)ceil_div(n, 64), (unsigned)batch), parts((unsigned)a.chunks, (unsigned)batch);
-  if (one_by_one) {
+  if (growth > SHORT_GROWTH) {
+    auto step = [&] {
+      if (w_bf16) hipLaunchKernelGGL((short_wide_step_kernel<bf16_t>), grid, dim3(256), 0, stream, a);
+      else hipLaunchKernelGGL((short_wide_step_kernel<float>), grid, dim3(256), 0, stream, a);
+    };
     hipLaunchKernelGGL((short_wide_start_kernel<TG, TM>), grid, dim3(256), 0, stream, a);
+    if (growth <= SHORT_WIDE_GROWTH) {
+      a.step = -1;
+      hipLaunchKernelGGL(short_wide_gram_kernel, parts, dim3(256), 0, stream, a);
+      hipLaunchKernelGGL(short_steps_kernel, dim3((unsigned)batch), dim3(SSTEP_THR), 0, stream, a);
+      step();
+      return;
+    }
     for (a.step = 0; a.step < a.steps; ++a.step) {
       hipLaunchKernelGGL(short_wide_gram_kernel, parts, dim3(256), 0, stream, a);
       hipLaunchKernelGGL(short_poly_kernel, dim3((unsigned)batch), dim3(SSTEP_THR), 0, stream, a);
-      if (w_bf16) hipLaunchKernelGGL((short_wide_step_kernel<bf16_t>), grid, dim3(256), 0, stream, a);
-      else hipLaunchKernelGGL((short_wide_step_kernel<float>), grid, dim3(256), 0, stream, a);
+      step();
     }
     return;
   }
+  a.p = nullptr;
   hipLaunchKernelGGL((short_gram_kernel<TG, TM>), parts, dim3(256), 0, stream, a);
   hipLaunchKernelGGL(short_steps_kernel, dim3((unsigned)batch), dim3(SSTEP_THR), 0, stream, a);
   if (w_bf16) hipLaunchKernelGGL((short_apply_kernel<TG, TM, bf16_t>), grid, dim3(256), 0, stream, a);
@@ -1709,23 +1735,22 @@ static void ns_run(const NsPlan& h, MuonIn in, NsArgs g, int64_t batch, const fl
     a.chunks = h.chunks;
     a.part = (double*)(ws + h.part); a.q = (float*)(ws + h.q); a.inv = (double*)(ws + h.inv);
     a.x = (double*)(ws + h.x64); a.p = (double*)(ws + h.q);
-    double grown = 1.0, most = 1.0;
+    double grown = 1.0, most = 1.0;             // by any run of steps
     for (int k = 0; k < steps; ++k) {
       grown = std::max(grown, 1.0) * qmax[k];
       most = std::max(most, grown);
     }
-    const bool one_by_one = most > SHORT_GROWTH;
     std::copy(coef, coef + 3 * steps, a.coef);
     a.steps = steps;
     a.hold = scale;
     a.w = g.w; a.ldw = g.ldw; a.sw = g.sw; a.update = g.update;
     a.lr = g.lr; a.lr_by = g.lr_by; a.decay = g.decay; a.scale = g.scale;
     if (in.g_bf16) {
-      if (in.m_bf16) short_run<bf16_t, bf16_t>(a, batch, g.w_bf16, one_by_one, stream);
-      else short_run<bf16_t, float>(a, batch, g.w_bf16, one_by_one, stream);
+      if (in.m_bf16) short_run<bf16_t, bf16_t>(a, batch, g.w_bf16, most, stream);
+      else short_run<bf16_t, float>(a, batch, g.w_bf16, most, stream);
     } else {
-      if (in.m_bf16) short_run<float, bf16_t>(a, batch, g.w_bf16, one_by_one, stream);
-      else short_run<float, float>(a, batch, g.w_bf16, one_by_one, stream);
+      if (in.m_bf16) short_run<float, bf16_t>(a, batch, g.w_bf16, most, stream);
+      else short_run<float, float>(a, batch, g.w_bf16, most, stream);
     }
     return;
   }

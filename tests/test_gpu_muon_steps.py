@@ -66,8 +66,8 @@ SHORT = [(16, 300), (5, 3), (1, 700), (24, 5000), (300, 32), (33, 300), (600, 50
 
 
 @pytest.mark.parametrize("kind", ["ones", "one", "four"])
-@pytest.mark.parametrize("steps", [MUON * 5, MUON * 7, MUON * 10, MUON * 16, CUBIC * 48, QUINTIC * 32, MUON * 4 + CUBIC * 3 + QUINTIC * 8],
-                         ids=["muon5", "muon7", "muon10", "muon16", "cubic48", "quintic32", "mixed"])
+@pytest.mark.parametrize("steps", [MUON * 5, MUON * 7, MUON * 9, MUON * 10, MUON * 16, CUBIC * 48, QUINTIC * 32, MUON * 4 + CUBIC * 3 + QUINTIC * 8],
+                         ids=["muon5", "muon7", "muon9", "muon10", "muon16", "cubic48", "quintic32", "mixed"])
 @pytest.mark.parametrize("r,c", SHORT)
 def test_ranks_of_short_sides(r, c, steps, kind):
     """A long run of steps on a matrix without full rank is the one that 64 bits make of it."""
@@ -147,7 +147,7 @@ def test_update_of_short_sides(r, c, steps, nesterov, turned, types):
         assert off <= (half + 3 * 2.0 ** -24) * (want.norm() + 0.25 * x.norm()) + 0.25 * 485 * 2.0 ** -24 * x.norm()
 
 
-@pytest.mark.parametrize("steps", [MUON * 5, MUON * 9], ids=["muon5", "muon9"])
+@pytest.mark.parametrize("steps", [MUON * 5, MUON * 8, MUON * 10], ids=["muon5", "muon8", "muon10"])
 @pytest.mark.parametrize("r,c,skip,pad", [(16, 300, 0, 0), (30, 261, 3, 5), (300, 41, 1, 2), (64, 270, 2, 3), (7, 20, 1, 1)])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_short_sides_where_they_lie(r, c, skip, pad, dtype, steps):
@@ -198,7 +198,7 @@ def test_short_sides_where_they_lie(r, c, skip, pad, dtype, steps):
         _ = PL.orthogonalize(x, coefficients=steps)
 
 
-@pytest.mark.parametrize("steps", [MUON * 5, MUON * 9], ids=["muon5", "muon9"])
+@pytest.mark.parametrize("steps", [MUON * 5, MUON * 8, MUON * 10], ids=["muon5", "muon8", "muon10"])
 @pytest.mark.parametrize("power", [-38, -20, 20, 37])
 @pytest.mark.parametrize("r,c", [(16, 300), (300, 64)])
 def test_magnitudes_of_short_sides(r, c, power, steps):
