@@ -26,13 +26,13 @@
 // A and P are symmetric: the tiles on and below the diagonal are formed and
 // stored twice, once transposed.
 //
-// Where the longer side exceeds the shorter, steps are taken together: with R =
+// Where the longer side exceeds the shorter, steps are taken two and two: with R =
 // X X^T and q = a I + b R + c R^2 of one step, the next step's R is q R q and its X
-// is q' q X, so the long side is gone through once a group and not once a step.  A
+// is q' q X, so the long side is gone through once a pair and not once a step.  A
 // step alone takes 3 m^2 n + m^3 multiplications (symmetric products by half),
-// two together 3 m^2 n + 5 m^3, three 3 m^2 n + 9 m^3: 16384 x 4096 in five steps,
-// three and two together, 3.05 ms where one by one took 4.63 (now 2.85).  R's rounding errors grow by
-// q^2 a step until X X^T is formed anew, which is what limits a group (ns_groups).
+// two together 3 m^2 n + 5 m^3: 16384 x 4096 in five steps 3.38 ms where one by one
+// takes 4.45.  R's rounding errors grow by
+// q^2 until X X^T is formed anew, which is why no more go together (ns_pairs).
 #include "device.hpp"
 #include "gemm_common.hpp"
 #include "host.hpp"
@@ -1474,8 +1474,8 @@ __global__ __launch_bounds__(256) void tiny_kernel(ShortArgs a) {
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
-// The least short side from which two and three steps go together (see ns_groups).
-constexpr int64_t NS_PAIRS_FROM = 512, NS_THREE_FROM = 1024;
+// The least short side from which two steps go together (see ns_pairs).
+constexpr int64_t NS_PAIRS_FROM = 512;
 
 struct NsPlan {
   int64_t mp, np, x, p;                       // padded sides; bytes of a matrix's X (hi or lo) and of its A or P
@@ -1638,14 +1638,7 @@ static void ns_launch(NsArgs g, hipStream_t stream) {
   else if constexpr (SYM) hipLaunchKernelGGL((ns_product_kernel<3, 2, MODE, TW>), grid, block, 0, stream, g);
 }
 
-// Steps taken together: `first` of them, then the others two and two where
-// `pairs`.  Each group's factor times which Q is held.
-struct NsGroups {
-  int first;
-  bool pairs;
-};
-
-// A group's time: A, P and the whole product, and for each step after the first
+// The time of steps together: A, P and the whole product, and for each step after the first
 // T, R, P and Q.
 static double ns_group_us(int64_t mp, int64_t np, int64_t batch, int steps) {
   double gram, small, whole;
@@ -1655,29 +1648,23 @@ static double ns_group_us(int64_t mp, int64_t np, int64_t batch, int steps) {
   return gram + whole + small * (1 + 4 * (steps - 1));
 }
 
-// How far R = A's rounding errors may grow within a group, by max(a + b s^2 + c
-// s^4)^2 a step: 12 a step for the Muon optimiser's steps.  Errors of the result in
-// emulation (noise; eight directions 30 times above it), one step, groups of 2,
-// a group of 3 and one of 2: 1024 x 2048 0.06, 0.1, 0.06% and 0.02, 0.06, 0.16%;
-// 256 x 1024 0.08, 0.07, 0.15% and 0.06, 0.13, 0.34%; 128 x 512 0.07, 0.06, 0.14%
-// and 0.10, 0.19, 0.47%.  So two steps go together from 512 on and three, at the
-// beginning, from 1024 (where they come later their errors are twice as large).
-constexpr double NS_PAIR_GROWTH = 16.0, NS_THREE_GROWTH = 200.0;
+// Whether steps are taken two and two.  How far R = A's rounding errors may grow
+// within a pair: max(a + b s^2 + c s^4)^2, 12 for the Muon optimiser's step.
+// Errors of the result in emulation, one by one, in pairs, and with three at the
+// beginning, of noise, eight directions 30 times above it, and one (a constant)
+// 100 and 1000 times above it: 1024 x 2048 0.06, 0.1, 0.06%; 0.01, 0.02, 0.08%; 0.01, 0.03,
+// 0.3%; 0.1, 0.2, 1.2%; 256 x 1024 0.08, 0.07, 0.15% and 0.06, 0.13, 0.34%; 128 x 512 0.07,
+// 0.06, 0.14% and 0.10, 0.19, 0.47%.  So two steps go together from 512 on and
+// three nowhere, although they would save another pass over the long side (16384 x
+// 4096 2.88 ms): with R and T as pairs of fp16, as X is, the three's error stays where
+// it is, for P's rounding makes it.
+constexpr double NS_PAIR_GROWTH = 16.0;
 
-static NsGroups ns_groups(int64_t mp, int64_t np, int64_t batch, int steps, const double* qmax) {
-  NsGroups r = {1, false};
-  if (mp < NS_PAIRS_FROM || np <= mp) return r;
-  const double one = ns_group_us(mp, np, batch, 1), two = ns_group_us(mp, np, batch, 2), three = ns_group_us(mp, np, batch, 3);
-  bool tame = true;
-  for (int k = 0; k + 1 < steps; ++k) tame = tame && qmax[k] * qmax[k] <= NS_PAIR_GROWTH;
-  if (!tame) return r;
-  r.pairs = two < 2 * one;
-  auto rest = [&](int n) { return r.pairs ? n / 2 * two + n % 2 * one : n * one; };
-  double least = one + rest(steps - 1);
-  if (r.pairs && steps >= 2 && two + rest(steps - 2) <= least) { least = two + rest(steps - 2); r.first = 2; }
-  if (mp >= NS_THREE_FROM && steps >= 3 && qmax[0] * qmax[0] * qmax[1] * qmax[1] <= NS_THREE_GROWTH && three + rest(steps - 3) < least)
-    r.first = 3;
-  return r;
+static bool ns_pairs(int64_t mp, int64_t np, int64_t batch, int steps, const double* qmax) {
+  if (mp < NS_PAIRS_FROM || np <= mp) return false;
+  for (int k = 0; k + 1 < steps; ++k)
+    if (qmax[k] * qmax[k] > NS_PAIR_GROWTH) return false;
+  return ns_group_us(mp, np, batch, 2) < 2 * ns_group_us(mp, np, batch, 1);
 }
 
 template <typename TG, typename TM>
@@ -1768,24 +1755,24 @@ static void ns_run(const NsPlan& h, MuonIn in, NsArgs g, int64_t batch, const fl
   g.mp = (int)h.mp; g.np = (int)h.np; g.batch = (int)batch;
   g.inv = 1.0f / scale;
   g.tall = in.tall; g.rows = in.rows; g.cols = in.cols;
-  const NsGroups groups = ns_groups(h.mp, h.np, batch, steps, qmax);
+  const bool pairs = ns_pairs(h.mp, h.np, batch, steps, qmax);
   uint8_t *R = ws + h.gram, *T = ws + h.turn, *P = ws + h.poly, *P2 = ws + h.poly2, *J = ws + h.join;
   float* diag[3] = {(float*)(ws + h.diag), (float*)(ws + h.diag) + batch * h.mp, (float*)(ws + h.diag) + 2 * batch * h.mp};
   int turn = 0;
   for (int k = 0; k < steps; ++turn) {
-    const int left = steps - k, n = std::min(left, k == 0 ? groups.first : groups.pairs ? 2 : 1);
+    const int n = pairs && k + 2 <= steps ? 2 : 1;
     g.hi = ws + h.hi[turn & 1]; g.lo = ws + h.lo[turn & 1];
     g.hi2 = ws + h.hi[(turn + 1) & 1]; g.lo2 = ws + h.lo[(turn + 1) & 1];
     g.f = g.inv; g.out = R;
     ns_launch<NS_GRAM>(g, stream);
-    // the group's Q, held times qs, in q with its diagonal in dq
+    // the pair's Q, held times qs, in q with its diagonal in dq
     uint8_t* q = P;
     float *dq = diag[0], qs = scale;
     double most = qmax[k];
     for (int i = 0; i < n; ++i, ++k) {
       const float* c = coef + 3 * k;
-      uint8_t* p = i == 0 ? P : i == 1 ? P2 : P;
-      float* dp = i == 0 ? diag[0] : diag[1];
+      uint8_t* p = i == 0 ? P : P2;
+      float* dp = diag[i];
       g.a = c[0];
       g.left = g.right = g.src1 = R; g.f1 = c[1]; g.f = c[2] * g.inv; g.out = p; g.diag = dp;
       ns_launch<NS_POLY>(g, stream);
@@ -1793,15 +1780,13 @@ static void ns_run(const NsPlan& h, MuonIn in, NsArgs g, int64_t batch, const fl
         most *= qmax[k];
         float to = qs;
         while (to * most > 49152.0) to *= 0.5f;
-        uint8_t* j = i == 1 ? J : P2;
-        float* dj = i == 1 ? diag[2] : diag[0];
         g.left = p; g.right = q; g.src1 = q; g.row1 = dp; g.f1 = to / qs; g.src2 = p; g.col2 = dq; g.f2 = to / scale;
-        g.f = to / (qs * scale); g.out = j; g.diag = dj;
+        g.f = to / (qs * scale); g.out = J; g.diag = diag[2];
         const float inv = g.inv;
         g.inv = 1.0f / to;
         ns_launch<NS_JOIN>(g, stream);
         g.inv = inv;
-        q = j; dq = dj; qs = to;
+        q = J; dq = diag[2]; qs = to;
       }
       if (i + 1 < n) {
         g.left = p; g.row1 = dp; g.f1 = 1.0f; g.f = g.inv;

@@ -206,3 +206,51 @@ def test_magnitudes_of_short_sides(r, c, power, steps):
     x = torch.randn(r, c, generator=torch.Generator().manual_seed(7)) * 10.0 ** power
     got, want = fp32_x(x, steps, eps=0.0).cpu().double(), orthogonal(x.double() * 10.0 ** -power, steps, eps=0.0)
     assert (got - want).norm() <= 485 * 2.0 ** -24 * want.norm()
+
+
+def coherent(r, c, kind, dtype):
+    """A direction that stands far out of the noise of the rest: a constant, or a random one."""
+    g = torch.Generator(device="cuda").manual_seed(r + c)
+    z = torch.randn(r, c, device="cuda", generator=g)
+    if kind == "direction":
+        x = z + 3000 * torch.randn(r, 1, device="cuda", generator=g) @ torch.randn(1, c, device="cuda", generator=g)
+    else:
+        x = 1 + float(kind) * z
+    return x.to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("kind", ["1e-1", "1e-2", "1e-3", "1e-4", "direction"])
+@pytest.mark.parametrize("r,c", [(1024, 2048), (4500, 1100), (1024, 4096), (520, 1300), (1024, 1024), (130, 1900), (64, 200), (64, 300)])
+def test_one_direction_far_out(r, c, kind, dtype):
+    """Documented: 0.2% of the result where the largest direction is up to a few hundred times the others, 1% beyond."""
+    x = coherent(r, c, kind, dtype)
+    got, want = fp32_x(x, MUON * 5).double(), orthogonal(x, MUON * 5)
+    off = ((got - want).norm() / want.norm()).item()
+    assert off <= (0.002 if kind in ("1e-1", "1e-2") else 0.01), off
+
+
+def mixed(*names):
+    """Steps of which no two in a row are alike; d's growth keeps it, and the steps beside it, by themselves."""
+    steps = dict(a=(3.4445, -4.7750, 2.0315), b=(1.875, -1.25, 0.375), c=(1.5, -0.5, 0.0), d=(4.3, -7.0, 3.7), e=(3.0, -3.6, 1.6),
+                 f=(2.5, -2.5, 1.0))
+    return tuple(tuple(torch.tensor(steps[n]).tolist()) for n in names)
+
+
+@pytest.mark.parametrize("names", ["ae", "eaf", "aebf", "feacb", "bcaefb", "aebfcd", "bdcacd", "fcabeba", "facbacb"])
+@pytest.mark.parametrize("shape", [(1024, 4096), (768, 2304), (3000, 700), (2, 640, 1500), (130, 400), (700, 700), (64, 256), (40, 90),
+                                   (16, 300), (33, 300), (600, 50), (2, 24, 700)], ids=str)
+def test_schedules(shape, names):
+    """Steps that differ, by every path: in pairs, one by one, of the small kernel and of the Gram matrix."""
+    steps = mixed(*names)
+    r, c = shape[-2:]
+    g = torch.Generator(device="cuda").manual_seed(r + c)
+    x = torch.randn(shape, device="cuda", generator=g)
+    x = 0.1 * x + torch.randn(*shape[:-1], 4, device="cuda", generator=g) @ torch.randn(*shape[:-2], 4, c, device="cuda", generator=g)
+    got = fp32_x(x, steps).double()
+    for y, z in zip(*(t.reshape(-1, r, c) for t in (got, x))):
+        want = orthogonal(z, steps)
+        off = ((y - want).norm() / want.norm()).item()
+        # documented; and where X is held with 22 bits or more throughout, its roundings and those of short sums in fp32,
+        # a few 2^-22 that grow with the steps
+        assert off <= (0.002 if min(r, c) > 64 else 8 * growth(steps) * 2.0 ** -22), off
