@@ -523,7 +523,10 @@ pbs_status pbs_qk_norm_rope_grad(const void* dq, const int64_t* dq_strides, cons
  *   A = X X^T,  P = b A + c A^2,  X' = a X + P X     for each step (a, b, c)
  * coefficients [host]: `steps` (1 to 64) triples a, b, c; (3.4445, -4.7750,
  * 2.0315) five times are the Muon optimiser's.  They may not let singular values
- * that start within [0, 1], or P's, grow past 4096 (PBS_ERR_INVALID_ARG).
+ * that start within [0, 1], their squares ahead of a step, or P's, grow past 4096
+ * (PBS_ERR_INVALID_ARG), each step's largest taken 2^-10 higher for the roundings: a schedule whose polynomials end
+ * on a steep rise is given with its arguments a little within their ranges (s /
+ * 1.01, say: a / 1.01, b / 1.01^3, c / 1.01^5).
  *
  * pbs_orthogonalize: U = x (bf16 or fp32), y = the last X in bf16.
  * pbs_muon: U = beta M' + (1 - beta) G with nesterov, else M', and
@@ -549,7 +552,8 @@ pbs_status pbs_qk_norm_rope_grad(const void* dq, const int64_t* dq_strides, cons
  *    sums, X carried with 22 bits: within 0.2% after Muon's five steps where the largest singular
  *    value is up to a few hundred times those of the bulk, within 1% where one is thousands of
  *    times them (a matrix that is constant but for 0.1%).  One direction by itself may be
- *    off by more: 0.3% on noise, up to 2% where a few rows stand far out.  Up to 64: X
+ *    off by more: 0.3% on noise, up to 2% where a few rows stand far out.  Other steps' roundings
+ *    grow by their slopes: where a singular value meets a steep rise they show.  Up to 64: X
  *    carried with 22 bits or more throughout, 0.02%.
  *    Directions that U does not have hold what X's roundings leave there, 2^-22 of it (up to 64
  *    beside more than 256, or up to 32: 2^-53 once the steps' growth exceeds 2048), which grows by a

@@ -1557,30 +1557,41 @@ static pbs_status ns_check_matrix(const char* what, const char* name, const void
   return PBS_OK;
 }
 
+// The largest |f(x)| for x in [0, end]: at an end or at one of the roots of f', e0 + e1 x + e2 x^2.
+template <typename F>
+static double ns_largest(F f, double end, double e0, double e1, double e2) {
+  double most = std::max(std::fabs(f(0.0)), std::fabs(f(end)));
+  auto at = [&](double x) {
+    if (x > 0.0 && x < end) most = std::max(most, std::fabs(f(x)));
+  };
+  const double d = e1 * e1 - 4 * e2 * e0;
+  if (d >= 0.0) {
+    const double h = -0.5 * (e1 + std::copysign(std::sqrt(d), e1));     // (no difference of near values)
+    at(h / e2);
+    at(e0 / h);
+  }
+  return most;
+}
+
 // The power of two that X, A and P are held times: the largest up to 2^14 that
 // keeps all of them below fp16's largest value, 65504, with a third to spare for
 // roundings.  top: the largest singular value ahead of each step, at most 1 at
-// first, then the largest |p(s)| for s up to it; qmax: the largest |a + b s^2 + c
-// s^4| of a step (1024 points; between them p
-// differs by less than its largest slope times half the step, which is added).
+// first, then the largest |p(s)| for s up to it and NS_ROUNDING of it, by which
+// A's and P's roundings may move it (2^-12 of each, times slopes of a few): polynomials that
+// rise steeply at the end of their range, as some published schedules have them, would let a matrix of
+// rank 1 run away from there.  qmax: the largest |a + b s^2 + c s^4| of a step.
+constexpr double NS_ROUNDING = 1.0 / 1024;
 static pbs_status ns_scale(const char* what, const float* coef, int steps, float* scale, double* qmax) {
   double top = 1.0, most = 1.0;
   for (int k = 0; k < steps; ++k) {
     const double a = coef[3 * k], b = coef[3 * k + 1], c = coef[3 * k + 2];
     PBS_REQUIRE(std::isfinite(a) && std::isfinite(b) && std::isfinite(c), PBS_ERR_INVALID_ARG, "%s: coefficients of step %d are not finite",
                 what, k);
-    double next = 0.0, poly = 0.0, q = 0.0;
-    const double h = top / 1024, t2 = top * top;
-    for (int i = 0; i <= 1024; ++i) {
-      const double s = h * i, s2 = s * s;
-      next = std::max(next, std::fabs(s * (a + s2 * (b + c * s2))));
-      poly = std::max(poly, std::fabs(s2 * (b + c * s2)));
-      q = std::max(q, std::fabs(a + s2 * (b + c * s2)));
-    }
-    next += 0.5 * h * (std::fabs(a) + 3 * std::fabs(b) * t2 + 5 * std::fabs(c) * t2 * t2);
-    poly += 0.5 * h * (2 * std::fabs(b) * top + 4 * std::fabs(c) * top * t2);
+    const double t2 = top * top;                          // x: s^2
+    const double poly = ns_largest([&](double x) { return x * (b + c * x); }, t2, b, 2 * c, 0.0);
+    const double next = (1.0 + NS_ROUNDING) * ns_largest([&](double x) { return std::sqrt(x) * (a + x * (b + c * x)); }, t2, a, 3 * b, 5 * c);
     most = std::max({most, t2, poly, next});              // A, P, X; T, top * next at most, lies between A and the next A
-    qmax[k] = q + 0.5 * h * (2 * std::fabs(b) * top + 4 * std::fabs(c) * top * t2);
+    qmax[k] = ns_largest([&](double x) { return a + x * (b + c * x); }, t2, b, 2 * c, 0.0);
     top = next;
     PBS_REQUIRE(most < 4096.0, PBS_ERR_INVALID_ARG, "%s: the coefficients let singular values grow past fp16's range (step %d)", what, k);
   }

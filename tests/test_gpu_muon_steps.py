@@ -4,6 +4,8 @@ import torch
 
 from precision_block_scaled_amd import pipeline as PL
 from tests.muon_ref import orthogonal
+from tests.test_gpu_muon import matrix
+from tests.test_muon_coefficients import RISING, within
 
 pytestmark = pytest.mark.gpu
 
@@ -254,3 +256,13 @@ def test_schedules(shape, names):
         # documented; and where X is held with 22 bits or more throughout, its roundings and those of short sums in fp32,
         # a few 2^-22 that grow with the steps
         assert off <= (0.002 if min(r, c) > 64 else 8 * growth(steps) * 2.0 ** -22), off
+
+
+@pytest.mark.parametrize("kind", ["noise", "low"])
+@pytest.mark.parametrize("r,c", [(130, 300), (300, 300), (1024, 2100), (4500, 1100), (64, 200), (16, 300), (1000, 64)])
+def test_polynomials_of_a_shrinking_range(r, c, kind):
+    """Steps that begin steeply, a = 8.2: all else as documented of Muon's."""
+    steps = tuple(tuple(torch.tensor(s).tolist()) for s in within(RISING))
+    x = matrix(r, c, kind).cuda()
+    got, want = fp32_x(x, steps).double(), orthogonal(x, steps)
+    assert ((got - want).norm() / want.norm()).item() <= 0.002
