@@ -817,16 +817,16 @@ constexpr int SUPITCH = 68;                // floats: a row of a staged piece of
 struct ShortArgs {
   MuonIn in;               // mp, np unused
   int blocks;              // 16-row blocks of the short side
-  int chunks;              // workgroups that share a matrix's long side
-  double* part;            // [batch][chunks][STILES][256]: R's tiles as the instruction holds them
-  float* q;                // [batch][64][64]
+  int chunks;              // workgroups that share a matrix's long side; 0: small matrices, all in one launch
+  double* part;            // [batch][chunks][blocks (blocks + 1) / 2][256]: R's tiles as the instruction holds them
+  float* q;                // [batch][side][side], side = 16 blocks
   double* inv;             // [batch]: 1 / (||U||_F + eps)
   float coef[3 * 64];
   int steps;
   float hold;              // small matrices: the power of two that X, A and P are held times
   // in 64 bits:
   double* x;               // X [batch][short][long], ahead of the first step U
-  double* p;               // P of step `step`, or Q; [batch][64][64]
+  double* p;               // P of step `step`, or Q; [batch][side][side]
   int step;                // -1: all steps together
   void* w;
   int64_t ldw, sw;
@@ -899,7 +899,7 @@ __device__ __forceinline__ void short_gram_put(const ShortArgs& a, const f64x4 (
     }
   }
   __syncthreads();
-  double* to = a.part + ((int64_t)blockIdx.y * a.chunks + blockIdx.x) * STILES * 256;
+  double* to = a.part + ((int64_t)blockIdx.y * a.chunks + blockIdx.x) * tiles * 256;
   for (int i = t; i < tiles * 256; i += 256) to[i] = sums[i];
 }
 
@@ -964,13 +964,13 @@ constexpr int SSTEP_THR = 64 * STILES;
 // The parts' sum; wave w of STILES.
 __device__ __forceinline__ void short_gram_join(const ShortArgs& a, int batch, int w, int lane, double* R) {
   const int tiles = a.blocks * (a.blocks + 1) / 2;
-  const double* from = a.part + (int64_t)batch * a.chunks * STILES * 256;
+  const double* from = a.part + (int64_t)batch * a.chunks * tiles * 256;
   for (int e = w; e < 4 * tiles; e += STILES) {           // rows e % 4 of tile e / 4, as the instruction holds them
     double s = 0.0;
     for (int c = 0; c < a.chunks; c += 16) {
       double v[16];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) v[k] = from[(int64_t)(c + k < a.chunks ? c + k : 0) * STILES * 256 + 64 * e + lane];
+      for (int k = 0; k < 16; ++k) v[k] = from[(int64_t)(c + k < a.chunks ? c + k : 0) * tiles * 256 + 64 * e + lane];
 #pragma unroll
       for (int k = 0; k < 16; ++k) s += c + k < a.chunks ? v[k] : 0.0;
     }
@@ -1042,7 +1042,7 @@ __global__ __launch_bounds__(SSTEP_THR) void short_steps_kernel(ShortArgs a) {
     }
   }
   for (int i = t; i < side * side; i += SSTEP_THR) {
-    const int64_t to = ((int64_t)batch * NS_SHORT + i / side) * NS_SHORT + i % side;
+    const int64_t to = (int64_t)batch * side * side + i;
     if (a.p) a.p[to] = Q[i / side * SPITCH + i % side];
     else a.q[to] = (float)Q[i / side * SPITCH + i % side];
   }
@@ -1060,7 +1060,7 @@ __global__ __launch_bounds__(256) void short_apply_kernel(ShortArgs a) {
   MuonTile<TG, TM> v;
   short_load(in, batch, at, v, turn);
   const double inv = a.inv[batch];
-  for (int i = t; i < side * side; i += 256) q[i / side * SUPITCH + i % side] = a.q[((int64_t)batch * NS_SHORT + i / side) * NS_SHORT + i % side];
+  for (int i = t; i < side * side; i += 256) q[i / side * SUPITCH + i % side] = a.q[(int64_t)batch * side * side + i];
   short_stage(in, v, inv, u);
   const float lr_now = a.lr_by ? a.lr * *a.lr_by : a.lr, keep = 1.0f - lr_now * a.decay, step = lr_now * a.scale;
   if (in.m) {
@@ -1213,7 +1213,7 @@ __global__ __launch_bounds__(SSTEP_THR) void short_poly_kernel(ShortArgs a) {
   }
   __syncthreads();
   for (int i = t; i < side * side; i += SSTEP_THR)
-    a.p[((int64_t)batch * NS_SHORT + i / side) * NS_SHORT + i % side] = P[i / side * SPITCH + i % side];
+    a.p[(int64_t)batch * side * side + i] = P[i / side * SPITCH + i % side];
 }
 
 // X' = a X + P X, or Q X, for 64 values of the long side: in place, or the last one into the weight.  Wave w takes
@@ -1225,7 +1225,7 @@ __global__ __launch_bounds__(256) void short_wide_step_kernel(ShortArgs a) {
   const int t = threadIdx.x, lane = t & 63, w = t >> 6, batch = blockIdx.y, at = blockIdx.x * 64, side = SB * a.blocks;
   const int m = in.tall ? in.cols : in.rows, n = in.tall ? in.rows : in.cols;
   short_wide_load(a, batch, at, u);
-  for (int i = t; i < side * side; i += 256) p[i / side * SPITCH + i % side] = a.p[((int64_t)batch * NS_SHORT + i / side) * NS_SHORT + i % side];
+  for (int i = t; i < side * side; i += 256) p[i / side * SPITCH + i % side] = a.p[(int64_t)batch * side * side + i];
   __syncthreads();
   // U is not divided by its norm yet
   const double f = a.step <= 0 ? a.inv[batch] : 1.0, ca = a.step < 0 ? 0.0 : (double)a.coef[3 * a.step];
@@ -1481,7 +1481,8 @@ struct NsPlan {
   int64_t mp, np, x, p;                       // padded sides; bytes of a matrix's X (hi or lo) and of its A or P
   int parts;
   size_t hi[2], lo[2], gram, poly, turn, poly2, join, diag, part, bytes;
-  int chunks;                                 // short sides: workgroups that share the long one; 0: not short
+  int blocks;                                 // short sides: 16-row blocks; else 0
+  int chunks;                                 // and workgroups that share the long one; 0: all in one launch
   size_t q, inv, x64;
 };
 
@@ -1500,10 +1501,17 @@ static NsPlan ns_plan(int64_t batch, int64_t rows, int64_t cols) {
     return here;
   };
   if (m <= NS_SHORT) {
+    h.blocks = (int)ceil_div(m, SB);
+    // (of up to 32 the Gram matrix's steps are short themselves: 32 x 256 27 us there and 44 here, 32 x 64 26 and 22)
+    if (n <= TINY_LONG && h.blocks > 2) {
+      h.bytes = 256;                          // unused: every size's call wants a workspace
+      return h;
+    }
+    const int64_t side = SB * h.blocks;
     // fewer where their sums take long to join: of 6 or 10 tiles against 1 or 3
     h.chunks = (int)std::min<int64_t>(ceil_div(n, 64), m > 32 ? 16 : 32);
-    h.part = take((size_t)(batch * h.chunks) * STILES * 256 * 8);
-    h.q = take((size_t)batch * NS_SHORT * NS_SHORT * 8);  // Q, or P in 64 bits
+    h.part = take((size_t)(batch * h.chunks * (h.blocks * (h.blocks + 1) / 2)) * 256 * 8);
+    h.q = take((size_t)(batch * side * side) * 8);  // Q, or P in 64 bits
     h.inv = take((size_t)batch * 8);
     h.x64 = take((size_t)(batch * m * n) * 8);
     h.bytes = at;
@@ -1688,8 +1696,7 @@ static void muon_begin(const MuonIn& in, int64_t batch, hipStream_t stream) {
 template <typename TG, typename TM>
 static void short_run(ShortArgs a, int64_t batch, bool w_bf16, double growth, hipStream_t stream) {
   const int64_t n = a.in.tall ? a.in.rows : a.in.cols;
-  // (of up to 32 the Gram matrix's steps are short themselves: 32 x 256 27 us there and 44 here, 32 x 64 26 and 22)
-  if (n <= TINY_LONG && a.blocks > 2) {
+  if (a.chunks == 0) {
     if (w_bf16) hipLaunchKernelGGL((tiny_kernel<TG, TM, bf16_t>), dim3((unsigned)batch), dim3(256), 0, stream, a);
     else hipLaunchKernelGGL((tiny_kernel<TG, TM, float>), dim3((unsigned)batch), dim3(256), 0, stream, a);
     return;
@@ -1725,11 +1732,11 @@ static void short_run(ShortArgs a, int64_t batch, bool w_bf16, double growth, hi
 // X from `in`, the steps, and the last of them into g's weight.
 static void ns_run(const NsPlan& h, MuonIn in, NsArgs g, int64_t batch, const float* coef, int steps, float scale, const double* qmax, uint8_t* ws,
                    hipStream_t stream) {
-  if (h.chunks) {
+  if (h.blocks) {
     ShortArgs a = {};
     a.in = in;
     a.in.tall = in.rows > in.cols;
-    a.blocks = (int)ceil_div(std::min(in.rows, in.cols), SB);
+    a.blocks = h.blocks;
     a.chunks = h.chunks;
     a.part = (double*)(ws + h.part); a.q = (float*)(ws + h.q); a.inv = (double*)(ws + h.inv);
     a.x = (double*)(ws + h.x64); a.p = (double*)(ws + h.q);

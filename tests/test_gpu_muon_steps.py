@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import precision_block_scaled_amd as P
 from precision_block_scaled_amd import pipeline as PL
 from tests.muon_ref import orthogonal
 from tests.test_gpu_muon import matrix
@@ -266,3 +267,21 @@ def test_polynomials_of_a_shrinking_range(r, c, kind):
     x = matrix(r, c, kind).cuda()
     got, want = fp32_x(x, steps).double(), orthogonal(x, steps)
     assert ((got - want).norm() / want.norm()).item() <= 0.002
+
+
+@pytest.mark.parametrize("steps", [MUON * 5, MUON * 8, MUON * 12], ids=["muon5", "muon8", "muon12"])
+@pytest.mark.parametrize("shape", [(3, 5), (7, 3, 5), (5, 16, 300), (2, 40, 700), (3, 600, 64), (3, 64, 64), (2, 33, 256), (2, 65, 100),
+                                   (1, 520, 700), (2, 1100, 640)], ids=str)
+def test_workspace_ends_where_it_says(shape, steps):
+    """No byte behind the workspace is written, and what it held before has no part in the result."""
+    b, (r, c) = shape[0] if len(shape) == 3 else 1, shape[-2:]
+    x = torch.randn(b, r, c, generator=torch.Generator().manual_seed(r)).cuda()
+    n = P.pbs_orthogonalize_bytes(b, r, c)
+    got = []
+    for fill in (0, 255):
+        ws = torch.full((n + (1 << 20),), fill, dtype=torch.uint8, device="cuda")
+        y = torch.empty(b, r, c, dtype=BF, device="cuda")
+        P.pbs_orthogonalize(x, P.PBS_FMT_F32, c, r * c, b, r, c, steps, 1e-7, y, c, r * c, ws, n)
+        assert (ws[n:] == fill).all()
+        got.append(y)
+    assert torch.equal(*got) and got[0].isfinite().all()

@@ -109,3 +109,15 @@ def test_coefficients_that_change_in_place():
     a.fill_(2.0)
     assert list(P._triples(steps)[0]) == [2.0, -0.5, 0.0]
     assert list(P._triples(torch.tensor([[1.0, 2.0, 3.0]]))[0]) == [1.0, 2.0, 3.0]
+
+
+def test_workspaces_hold_what_is_used():
+    """Small matrices need none to speak of; short sides their Gram matrices' tiles and a copy in 64 bits; the others two X and a
+    few matrices of the shorter side, 16 bits each."""
+    need = P.pbs_orthogonalize_bytes
+    assert need(65535, 64, 256) <= 256 and need(1, 33, 65) <= 256
+    assert need(65535, 3, 5) <= 65535 * (2 * 16 * 16 * 8 + 3 * 5 * 8 + 8) + 4 * 256
+    assert need(1, 16, 4096) <= 33 * 16 * 16 * 8 + 16 * 4096 * 8 + 4 * 256
+    assert need(1, 64, 1 << 20) <= 16 * 10 * 256 * 8 + 64 * 64 * 8 + (64 << 20) * 8 + 4 * 256
+    assert need(1, 4096, 4096) <= (8 + 2 * 2) * 4096 ** 2 + (1 << 20)
+    assert need(1, 4096, 16384) <= 8 * 4096 * 16384 + 5 * 2 * 4096 ** 2 + (1 << 20)
