@@ -554,7 +554,7 @@ pbs_status pbs_qk_norm_rope_grad(const void* dq, const int64_t* dq_strides, cons
  *    times them (a matrix that is constant but for 0.1%).  One direction by itself may be
  *    off by more: 0.3% on noise, up to 2% where a few rows stand far out.  Other steps' roundings
  *    grow by their slopes: where a singular value meets a steep rise they show.  Up to 64: X
- *    carried with 22 bits or more throughout, 0.02%.
+ *    carried with 22 bits or more throughout, 0.03%.
  *    Directions that U does not have hold what X's roundings leave there, 2^-22 of it (up to 64
  *    beside more than 256, or up to 32: 2^-53 once the steps' growth exceeds 2048), which grows by a
  *    in each step, as in any evaluation of finite precision: it shows after 8 or more of Muon's steps (2^-53:

@@ -90,3 +90,39 @@ def assert_near(got, x, steps, eps=1e-7, scale=SCALE, what="", slack=None):
         bad = ~(off.norm(dim=dim) <= most)
         assert not bad.any(), (f"{what}: {int(bad.sum())} {'columns' if dim == 0 else 'rows'} off, first {int(bad.nonzero()[0])}: "
                                f"{off.norm(dim=dim)[bad][0].item():.3g} of {line[bad][0].item():.3g}, bound {most[bad][0].item():.3g}")
+
+
+def emulated_pairs(x, steps, eps=1e-7, scale=SCALE):
+    """The same with X, A and P as pairs of fp16, three products of their parts and fp32 sums: matrices of 33 to 64 by up to 256."""
+    def pair(v):
+        hi = f16(v, scale)
+        return hi.float(), f16((v - hi) * 2048, scale).float()
+
+    def product(u, v):
+        return (u[0] @ v[0] + (u[0] @ v[1] + u[1] @ v[0]) / 2048).double()
+
+    x = x.double()
+    x = x / (x.norm() + eps)
+    tall = x.shape[0] > x.shape[1]
+    x = x.t() if tall else x
+    for a, b, c in steps:
+        xs = pair(x)
+        g = pair(product(xs, [t.t() for t in xs]))
+        p = pair(b * (g[0].double() + g[1].double() / 2048) + c * product(g, g))
+        x = a * (xs[0].double() + xs[1].double() / 2048) + product(p, xs)
+    return x.t() if tall else x
+
+
+def emulated_gram(x, steps, eps=1e-7):
+    """Shorter sides up to 64, growth up to 2048: polynomials of the Gram matrix in 64 bits, their product Q and Q U in fp32."""
+    x = x.double()
+    tall = x.shape[0] > x.shape[1]
+    x = x.t() if tall else x
+    inv = 1 / (x.norm() + eps)
+    r, one = (x @ x.t()) * inv * inv, torch.eye(len(x), dtype=torch.float64)
+    q = one
+    for a, b, c in steps:
+        p = a * one + b * r + c * (r @ r)
+        q, r = p @ q, p @ r @ p
+    x = (q.float() @ (x * inv).float()).double()
+    return x.t() if tall else x

@@ -4,7 +4,7 @@ import torch
 
 import precision_block_scaled_amd as P
 from precision_block_scaled_amd import pipeline as PL
-from tests.muon_ref import orthogonal
+from tests.muon_ref import emulated, emulated_gram, emulated_pairs, orthogonal
 from tests.test_gpu_muon import matrix
 from tests.test_muon_coefficients import RISING, within
 
@@ -285,3 +285,19 @@ def test_workspace_ends_where_it_says(shape, steps):
         assert (ws[n:] == fill).all()
         got.append(y)
     assert torch.equal(*got) and got[0].isfinite().all()
+
+
+@pytest.mark.parametrize("kind", ["noise", "low", "lower"])
+@pytest.mark.parametrize("r,c", [(64, 256), (256, 64), (64, 64), (33, 65), (255, 40), (48, 100), (16, 300), (300, 16), (33, 300), (64, 257),
+                                 (600, 50), (5, 3), (24, 5000)])
+def test_short_sides_keep_their_bits(r, c, kind):
+    """Shorter sides up to 64 are as exact as their formats' emulation, far from what fp16 operands alone would leave."""
+    x, steps = matrix(r, c, kind), MUON * 5
+    want, got = orthogonal(x, steps), fp32_x(x, steps).cpu().double()
+    small = 32 < min(r, c) and max(r, c) <= 256
+    rough = emulated_pairs(x, steps) if small else emulated_gram(x, steps)
+    # the emulation's roundings fall otherwise than the kernel's; the last one is fp32's
+    bound = 4 * (rough - want).norm() + 2.0 ** -24 * want.norm()
+    assert (got - want).norm() <= bound, ((got - want).norm() / want.norm(), bound / want.norm())
+    if min(r, c) > 16:
+        assert (emulated(x, steps) - want).norm() > 10 * bound
