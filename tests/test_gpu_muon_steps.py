@@ -301,3 +301,23 @@ def test_short_sides_keep_their_bits(r, c, kind):
     assert (got - want).norm() <= bound, ((got - want).norm() / want.norm(), bound / want.norm())
     if min(r, c) > 16:
         assert (emulated(x, steps) - want).norm() > 10 * bound
+
+
+@pytest.mark.parametrize("b,r,c,dtype", [(32, 128, 512, F32), (3, 1537, 1001, BF), (1, 4500, 1500, BF), (300, 64, 64, F32), (40, 16, 700, BF)],
+                         ids=str)
+def test_identical_bytes(b, r, c, dtype):
+    """The same inputs again and again, alone, beside a call on another stream, and through a transposed view."""
+    x = torch.randn(b, r, c, generator=torch.Generator().manual_seed(b)).to(dtype).cuda()
+    other = torch.randn(700, 900, device="cuda")
+    w0, m0 = (0.02 * torch.randn(b, r, c, device="cuda")).to(BF), torch.randn(b, r, c, device="cuda")
+    turned, side = x.transpose(1, 2).contiguous().transpose(1, 2), torch.cuda.Stream()
+    want, first = PL.orthogonalize(x), None
+    for i in range(6):
+        assert torch.equal(PL.orthogonalize(x), want), i
+        side.wait_stream(torch.cuda.current_stream())
+        PL.orthogonalize(other, stream=side)
+        w, m = w0.clone(), m0.clone()
+        PL.muon(w, m, turned if i % 2 else x, 0.02)
+        first = first or (w, m)
+        assert torch.equal(w, first[0]) and torch.equal(m, first[1]), i
+        torch.cuda.synchronize()
