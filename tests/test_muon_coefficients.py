@@ -8,8 +8,8 @@ from precision_block_scaled_amd import pipeline as PL
 
 pytestmark = pytest.mark.skipif(not os.path.exists(P.lib_path), reason="libpbs.so is not built")
 
-# Polynomials of steps whose range shrinks from [1e-3, 1]: largest values 1.99, 1.97, 1.87, 1.56, 1.12, 1.00, 1.00, each reached
-# again at the end of its range, on a rise of 12 times it
+# Polynomials of steps whose range shrinks from [1e-3, 1], as the Polar Express paper (Amsel et al., 2025) tabulates them:
+# largest values 1.99, 1.97, 1.87, 1.56, 1.12, 1.00, 1.00, each reached again at the end of its range, on a rise of 12 times it
 RISING = ((8.28721201814563, -23.595886519098837, 17.300387312530933), (4.107059111542203, -2.9478499167379106, 0.5448431082926601),
           (3.9486908534822946, -2.908902115962949, 0.5518191394370137), (3.3184196573706015, -2.488488024314874, 0.51004894012372),
           (2.300652019954817, -1.6689039845747493, 0.4188073119525673), (1.891301407787398, -1.2679958271945868, 0.37680408948524835),
