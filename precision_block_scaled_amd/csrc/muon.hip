@@ -806,7 +806,8 @@ __global__ __launch_bounds__(256, T >= 3 ? 1 : (T == 2 ? 4 : 8) / D) void ns_pro
 // step, 2e4 in five, and nothing takes it back as X X^T formed anew would: R is
 // held in 64 bits, and its products run on the 64-bit matrix instruction (a
 // product of 64 x 64 x 64 1.3 us; for 128 it would be 10).  The result is fp32's
-// own roundings away from 64 bits.
+// own roundings away from 64 bits, grown by a a step in directions that U lacks; many
+// steps are taken otherwise, below.
 // ---------------------------------------------------------------------------
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 
